@@ -310,6 +310,76 @@ int flce_scale_grads(const float* grad_scale, const void* grad_h_in, void* grad_
                      const float* grad_W_in, void* grad_W_out, int64_t n_W, int w_dtype, hipStream_t stream);
 
 /*
+ * Layer norm over the last dimension, the norm in front of the projection.
+ * For each of M rows x of H values, with weight w (NULL: 1) and bias b
+ * (NULL: 0):
+ *   mean = avg x,  rstd = 1 / sqrt(avg (x - mean)^2 + eps),
+ *   y = (x - mean) rstd w + b.
+ * x and y have row strides of ld_x and ld_y elements (ld_y >= H when M > 1;
+ * ld_x >= 0, so a broadcast row is read with 0) and `dtype`; weight and bias
+ * have H values of `w_dtype`; mean and rstd receive M fp32 values each
+ * (NULL: not written) and are what flce_layer_norm_bwd takes.  Pointers need
+ * the alignment of one element only.  eps > 0, finite.  y may be x itself
+ * (then ld_y == ld_x) and must not overlap it otherwise.  Statistics and
+ * arithmetic are fp32, y is rounded once.  Any H from 1 to 2^21, M < 2^31
+ * (else FLCE_EUNSUPPORTED); M = 0 does nothing.  Enqueued on `stream`;
+ * nothing is allocated, nothing synchronises.  Returns FLCE_OK, FLCE_EINVAL,
+ * FLCE_EUNSUPPORTED or FLCE_EDEVICE.
+ */
+int flce_layer_norm_fwd(const void* x, int64_t ld_x, const void* weight, const void* bias, int64_t M, int64_t H,
+                        float eps, void* y, int64_t ld_y, float* mean, float* rstd,
+                        hipStream_t stream, int dtype, int w_dtype);
+
+/*
+ * Workspace bytes of flce_layer_norm_bwd (per-group sums of the weight and
+ * bias gradients); 0 for sizes it does not take.
+ */
+size_t flce_layer_norm_bwd_workspace_size(int64_t M, int64_t H, int dtype);
+
+/*
+ * Backward pass of layer norm.  With xh = (x - mean) rstd and g = grad_y w:
+ *   grad_x      = rstd (g - avg g - xh avg(g xh))      [M, H] dtype
+ *   grad_weight = sum over rows of grad_y xh           [H] w_dtype
+ *   grad_bias   = sum over rows of grad_y              [H] w_dtype
+ * mean and rstd are those flce_layer_norm_fwd wrote.  Any of the three
+ * outputs may be NULL (not computed); with M = 0 the two parameter gradients
+ * are set to 0.  grad_x must not overlap grad_y or x.  `workspace` (needed
+ * when a parameter gradient is asked for): 256-byte aligned, at least
+ * flce_layer_norm_bwd_workspace_size(M, H, dtype) bytes.  Sums over rows are
+ * fp32 in an order that depends on M, H and dtype alone: the same call gives
+ * the same bits.  Strides, alignment, limits and errors as
+ * flce_layer_norm_fwd, and FLCE_EWORKSPACE.
+ */
+int flce_layer_norm_bwd(const void* grad_y, int64_t ld_gy, const void* x, int64_t ld_x, const void* weight,
+                        const float* mean, const float* rstd, int64_t M, int64_t H,
+                        void* grad_x, int64_t ld_gx, void* grad_weight, void* grad_bias,
+                        hipStream_t stream, int dtype, int w_dtype, void* workspace, size_t workspace_bytes);
+
+/*
+ * Dropout without a stored mask, on n contiguous elements:
+ *   y_i = [residual_i +] (word_i >= floor(p 2^32) ? x_i / (1 - p) : 0)
+ * word_i is word i % 4 of Philox4x32-10 (Salmon et al., SC 2011) on the
+ * counter (i / 4 low, i / 4 high, offset low, offset high) under the key
+ * (seed low, seed high), all 32-bit halves.  Calls with another seed or
+ * another offset draw independent masks; the same three numbers (index,
+ * seed, offset) give the same decision always, so the backward pass is this
+ * call on the upstream gradient without a residual.
+ *   residual    NULL: none; dtype
+ *   p           in [0, 1]; p = 1 drops every element (dropped elements leave
+ *               no trace, also where x is infinite or NaN)
+ *   offset_dev  NULL, or a device pointer to one uint64 that is added to
+ *               `offset` (modulo 2^64): a captured call draws a new mask on
+ *               each replay when the program advances it in between
+ * y may be x or residual itself and must not overlap them otherwise.
+ * Pointers need the alignment of one element only (offset_dev: 8 bytes).
+ * Computed in fp32 and rounded once; n <= 2^33 (else FLCE_EUNSUPPORTED).
+ * Enqueued on `stream`; nothing is allocated, nothing synchronises.  Returns
+ * FLCE_OK, FLCE_EINVAL, FLCE_EUNSUPPORTED or FLCE_EDEVICE.
+ */
+int flce_dropout(const void* x, const void* residual, void* y, int64_t n, double p, uint64_t seed, uint64_t offset,
+                 const uint64_t* offset_dev, hipStream_t stream, int dtype);
+
+/*
  * Synchronise `stream` and return the device-side status of the last
  * flce_fwd_bwd, flce_fwd_bwd_ex, flce_fwd or flce_cross_entropy that used
  * `workspace`: FLCE_OK or FLCE_ELABEL.  Returns
@@ -349,7 +419,11 @@ enum {
   FLCE_KERNEL_LOGITS = 9,       /* flce_logits: logits GEMM + softcap into the caller's buffer */
   FLCE_KERNEL_CROSS_ENTROPY = 10,/* flce_cross_entropy: per-row statistics (+ logit gradient) */
   FLCE_KERNEL_SCALE = 11,       /* flce_scale_grads: upstream-gradient scaling of grad_h / grad_W */
-  FLCE_KERNEL_KINDS = 12
+  FLCE_KERNEL_LAYER_NORM = 12,  /* flce_layer_norm_fwd */
+  FLCE_KERNEL_LAYER_NORM_BWD = 13,/* flce_layer_norm_bwd: grad_x and per-group parameter gradients */
+  FLCE_KERNEL_LAYER_NORM_REDUCE = 14,/* flce_layer_norm_bwd: sum of the groups' parameter gradients */
+  FLCE_KERNEL_DROPOUT = 15,     /* flce_dropout */
+  FLCE_KERNEL_KINDS = 16
 };
 
 /* Turn event timing on (on != 0) or off for subsequent calls.  Returns FLCE_OK. */

@@ -29,11 +29,15 @@ from ._lib import (  # noqa: F401
     FlceError,
     flce_cross_entropy,
     flce_cross_entropy_workspace_size,
+    flce_dropout,
     flce_fwd,
     flce_fwd_bwd,
     flce_fwd_bwd_ex,
     flce_fwd_bwd_noalloc,
     flce_fwd_workspace_size,
+    flce_layer_norm_bwd,
+    flce_layer_norm_bwd_workspace_size,
+    flce_layer_norm_fwd,
     flce_logits,
     flce_options_t,
     flce_profile_enable,
@@ -43,6 +47,15 @@ from ._lib import (  # noqa: F401
     flce_scale_grads,
     flce_strerror,
     flce_workspace_size,
+)
+from .head import (  # noqa: F401
+    LayerNormForward,
+    LayerNormGrads,
+    dropout,
+    layer_norm,
+    layer_norm_bwd,
+    layer_norm_fwd,
+    lm_head_loss,
 )
 from .torch_api import (  # noqa: F401
     CrossEntropyOutputs,

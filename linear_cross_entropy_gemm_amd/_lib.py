@@ -37,11 +37,13 @@ NOALLOC_SCRATCH_BYTES = 256 << 20
 EXPORTED = ("flce_plan", "flce_workspace_size", "flce_fwd_bwd", "flce_fwd_bwd_ex", "flce_fwd_bwd_noalloc",
             "flce_fwd_workspace_size",
             "flce_fwd", "flce_logits", "flce_cross_entropy_workspace_size", "flce_cross_entropy",
-            "flce_scale_grads", "flce_read_status", "flce_strerror", "flce_profile_enable", "flce_profile_read")
+            "flce_scale_grads", "flce_layer_norm_fwd", "flce_layer_norm_bwd_workspace_size",
+            "flce_layer_norm_bwd", "flce_dropout", "flce_read_status", "flce_strerror", "flce_profile_enable", "flce_profile_read")
 
 # Kernel kinds of the per-kernel timing facility (index order of the arrays).
 KERNEL_KINDS = ("label_scan", "fwd_logits", "row_merge", "grad_logits", "grad_h", "grad_h_reduce",
-                "grad_W", "finalize", "zero", "logits", "cross_entropy", "scale")
+                "grad_W", "finalize", "zero", "logits", "cross_entropy", "scale", "layer_norm",
+                "layer_norm_bwd", "layer_norm_reduce", "dropout")
 
 
 class flce_plan_t(ctypes.Structure):
@@ -122,6 +124,15 @@ def _load() -> ctypes.CDLL:
     lib.flce_cross_entropy.restype = i32
     lib.flce_scale_grads.argtypes = [vp, vp, vp, i64, i32, vp, vp, i64, i32, vp]
     lib.flce_scale_grads.restype = i32
+    u64, f64 = ctypes.c_uint64, ctypes.c_double
+    lib.flce_layer_norm_fwd.argtypes = [vp, i64, vp, vp, i64, i64, f32, vp, i64, vp, vp, vp, i32, i32]
+    lib.flce_layer_norm_fwd.restype = i32
+    lib.flce_layer_norm_bwd_workspace_size.argtypes = [i64, i64, i32]
+    lib.flce_layer_norm_bwd_workspace_size.restype = sz
+    lib.flce_layer_norm_bwd.argtypes = [vp, i64, vp, i64, vp, vp, vp, i64, i64, vp, i64, vp, vp, vp, i32, i32, vp, sz]
+    lib.flce_layer_norm_bwd.restype = i32
+    lib.flce_dropout.argtypes = [vp, vp, vp, i64, f64, u64, u64, vp, vp, i32]
+    lib.flce_dropout.restype = i32
     lib.flce_read_status.argtypes = [vp, vp]
     lib.flce_read_status.restype = i32
     lib.flce_strerror.argtypes = [i32]
@@ -218,6 +229,30 @@ def flce_scale_grads(grad_scale: int, grad_h_in, grad_h_out, n_h: int, h_dtype: 
     device address grad_scale); returns the C return code."""
     return int(_lib.flce_scale_grads(grad_scale, grad_h_in, grad_h_out, n_h, h_dtype, grad_W_in, grad_W_out,
                                      n_W, w_dtype, stream))
+
+
+def flce_layer_norm_fwd(x: int, ld_x: int, weight, bias, M: int, H: int, eps: float, y: int, ld_y: int, mean, rstd,
+                        stream: int, dtype: int, w_dtype: int) -> int:
+    """Raw call; returns the C return code."""
+    return _lib.flce_layer_norm_fwd(x, ld_x, weight, bias, M, H, eps, y, ld_y, mean, rstd, stream, dtype, w_dtype)
+
+
+def flce_layer_norm_bwd_workspace_size(M: int, H: int, dtype: int) -> int:
+    return int(_lib.flce_layer_norm_bwd_workspace_size(M, H, dtype))
+
+
+def flce_layer_norm_bwd(grad_y: int, ld_gy: int, x: int, ld_x: int, weight, mean: int, rstd: int, M: int, H: int,
+                        grad_x, ld_gx: int, grad_weight, grad_bias, stream: int, dtype: int, w_dtype: int, workspace,
+                        workspace_bytes: int) -> int:
+    """Raw call; returns the C return code."""
+    return _lib.flce_layer_norm_bwd(grad_y, ld_gy, x, ld_x, weight, mean, rstd, M, H, grad_x, ld_gx, grad_weight,
+                                    grad_bias, stream, dtype, w_dtype, workspace, workspace_bytes)
+
+
+def flce_dropout(x: int, residual, y: int, n: int, p: float, seed: int, offset: int, offset_dev, stream: int,
+                 dtype: int) -> int:
+    """Raw call (seed and offset: unsigned 64-bit); returns the C return code."""
+    return _lib.flce_dropout(x, residual, y, n, p, seed, offset, offset_dev, stream, dtype)
 
 
 def flce_read_status(workspace: int, stream: int) -> int:

@@ -1,0 +1,239 @@
+"""The operators around the vocabulary projection, on torch tensors: dropout
+with its residual add and the final layer norm in front of it, with their
+backward passes.  Every step of the computation runs in the library's HIP
+kernels on torch's current stream of the tensors' device; nothing
+synchronises."""
+from __future__ import annotations
+
+import dataclasses
+from typing import Optional, Union
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import _lib
+from .torch_api import _DTYPES, _ptr, _workspace, linear_cross_entropy
+
+_U64 = (1 << 64) - 1
+
+
+@dataclasses.dataclass
+class LayerNormForward:
+    y: torch.Tensor      # shape and dtype of x
+    mean: torch.Tensor   # [...] fp32, one per row
+    rstd: torch.Tensor   # [...] fp32, one per row
+
+
+@dataclasses.dataclass
+class LayerNormGrads:
+    grad_x: Optional[torch.Tensor]        # shape and dtype of x
+    grad_weight: Optional[torch.Tensor]   # [H] dtype of the weight
+    grad_bias: Optional[torch.Tensor]     # [H] dtype of the weight
+
+
+def _stream(dev) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _rows(x: torch.Tensor) -> torch.Tensor:
+    """x as [M, H] with unit column stride: a view where the strides allow
+    one, so a slice of a wider buffer is read in place."""
+    x2 = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
+    return x2 if x2.stride(1) == 1 or x2.shape[1] == 1 else x2.contiguous()
+
+
+def _check_tensor(name: str, x: torch.Tensor) -> None:
+    if x.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be bfloat16 or float32 (got {x.dtype})")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be on the GPU")
+
+
+def _check_rows(name: str, x: torch.Tensor) -> None:
+    _check_tensor(name, x)
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError(f"{name} must have a last dimension of at least one element")
+
+
+def _check_params(x: torch.Tensor, weight: Optional[torch.Tensor], bias: Optional[torch.Tensor]):
+    """Contiguous weight and bias (None stays None) and their common dtype."""
+    w_dtype = x.dtype
+    out = []
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            if t.dtype not in _DTYPES:
+                raise TypeError(f"{name} must be bfloat16 or float32 (got {t.dtype})")
+            if tuple(t.shape) != (x.shape[-1],):
+                raise ValueError(f"{name} has shape {tuple(t.shape)}, this call needs {(x.shape[-1],)}")
+            if t.device != x.device:
+                raise ValueError(f"{name} is on {t.device}, x is on {x.device}")
+            t = t.contiguous()
+            w_dtype = t.dtype
+        out.append(t)
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise TypeError(f"weight and bias must have one dtype (got {weight.dtype}, {bias.dtype})")
+    return out[0], out[1], w_dtype
+
+
+def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                   eps: float = 1e-5) -> LayerNormForward:
+    """One call of ``flce_layer_norm_fwd`` over the last dimension of ``x``:
+    y and the row statistics that ``layer_norm_bwd`` takes.  ``weight`` and
+    ``bias`` [H] may be absent and may be float32 next to a bfloat16 ``x``."""
+    _check_rows("x", x)
+    w, b, w_dtype = _check_params(x, weight, bias)
+    x2 = _rows(x)
+    M, H = x2.shape
+    dev = x.device
+    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    stats = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=dev)
+    res = LayerNormForward(y, stats[0], stats[1])
+    with torch.cuda.device(dev):
+        rc = _lib.flce_layer_norm_fwd(_ptr(x2), x2.stride(0), _ptr(w), _ptr(b), M, H, eps, _ptr(y), H,
+                                      _ptr(res.mean), _ptr(res.rstd), _stream(dev), _DTYPES[x.dtype],
+                                      _DTYPES[w_dtype])
+    if rc != _lib.FLCE_OK:
+        raise _lib.FlceError(rc, "flce_layer_norm_fwd")
+    return res
+
+
+def layer_norm_bwd(grad_y: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor], mean: torch.Tensor,
+                   rstd: torch.Tensor, workspace: Optional[torch.Tensor] = None, *, need_x: bool = True,
+                   need_params: bool = True) -> LayerNormGrads:
+    """One call of ``flce_layer_norm_bwd``: the gradients of ``x``, of the
+    weight and of the bias (in the weight's dtype; in that of ``x`` without a
+    weight).  ``mean`` and ``rstd`` are those of ``layer_norm_fwd``.  A
+    caller-owned ``workspace`` (uint8, ``flce_layer_norm_bwd_workspace_size``)
+    may be reused by ordered calls."""
+    _check_rows("x", x)
+    w, _, w_dtype = _check_params(x, weight, None)
+    if grad_y.shape != x.shape or grad_y.dtype != x.dtype or grad_y.device != x.device:
+        raise ValueError(f"grad_y must match x: {tuple(x.shape)} {x.dtype} on {x.device} (got "
+                         f"{tuple(grad_y.shape)} {grad_y.dtype} on {grad_y.device})")
+    x2, g2 = _rows(x), _rows(grad_y)
+    M, H = x2.shape
+    dev = x.device
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t.dtype != torch.float32 or t.numel() != M or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{name} must hold one contiguous float32 value per row of x on its device")
+    gx = torch.empty(x.shape, dtype=x.dtype, device=dev) if need_x else None
+    gw = gb = None
+    ws_bytes = 0
+    if need_params:
+        gw = torch.empty(H, dtype=w_dtype, device=dev)
+        gb = torch.empty(H, dtype=w_dtype, device=dev)
+        ws_bytes = _lib.flce_layer_norm_bwd_workspace_size(M, H, _DTYPES[x.dtype])
+        if ws_bytes == 0:
+            raise _lib.FlceError(_lib.FLCE_EUNSUPPORTED, "flce_layer_norm_bwd_workspace_size")
+        workspace = _workspace(workspace, ws_bytes, dev)
+        ws_bytes = workspace.numel()
+    with torch.cuda.device(dev):
+        rc = _lib.flce_layer_norm_bwd(_ptr(g2), g2.stride(0), _ptr(x2), x2.stride(0), _ptr(w), _ptr(mean), _ptr(rstd),
+                                      M, H, _ptr(gx), H, _ptr(gw), _ptr(gb), _stream(dev), _DTYPES[x.dtype],
+                                      _DTYPES[w_dtype], _ptr(workspace) if need_params else None, ws_bytes)
+    if rc != _lib.FLCE_OK:
+        raise _lib.FlceError(rc, "flce_layer_norm_bwd")
+    return LayerNormGrads(gx, gw, gb)
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps):
+        o = layer_norm_fwd(x, weight, bias, eps)
+        ctx.save_for_backward(x, weight, o.mean, o.rstd)
+        ctx.b_dtype = None if bias is None else bias.dtype
+        return o.y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_y):
+        x, weight, mean, rstd = ctx.saved_tensors
+        need_x, need_w, need_b, _ = ctx.needs_input_grad
+        g = layer_norm_bwd(grad_y, x, weight, mean, rstd, need_x=need_x, need_params=need_w or need_b)
+        gb = g.grad_bias if need_b else None
+        if gb is not None and gb.dtype != ctx.b_dtype:   # a bias without a weight
+            gb = gb.to(ctx.b_dtype)
+        return g.grad_x, g.grad_weight if need_w else None, gb, None
+
+
+def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+               eps: float = 1e-5) -> torch.Tensor:
+    """Differentiable layer norm over the last dimension of ``x``.  A row's
+    statistics are kept for the backward pass, the normalised values are not:
+    they are formed again from ``x``."""
+    return _LayerNorm.apply(x, weight, bias, eps)
+
+
+def _dropout(x, p, seed, offset, residual) -> torch.Tensor:
+    xc = x.contiguous()
+    rc_ = None if residual is None else residual.contiguous()
+    dev = x.device
+    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    tensor = torch.is_tensor(offset)
+    with torch.cuda.device(dev):
+        rc = _lib.flce_dropout(_ptr(xc), _ptr(rc_), _ptr(y), xc.numel(), p, seed, 0 if tensor else offset,
+                               _ptr(offset) if tensor else None, _stream(dev), _DTYPES[x.dtype])
+    if rc != _lib.FLCE_OK:
+        raise _lib.FlceError(rc, "flce_dropout")
+    return y
+
+
+class _Dropout(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, p, seed, offset):
+        tensor = torch.is_tensor(offset)
+        # kept as autograd state: changing it in place before the backward
+        # pass raises there instead of drawing another mask
+        ctx.save_for_backward(offset if tensor else None)
+        ctx.args = (p, seed, None if tensor else offset)
+        return _dropout(x, p, seed, offset, residual)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_y):
+        need_x, need_r = ctx.needs_input_grad[:2]
+        p, seed, offset = ctx.args
+        gx = _dropout(grad_y, p, seed, ctx.saved_tensors[0] if offset is None else offset, None) if need_x else None
+        return gx, grad_y if need_r else None, None, None, None
+
+
+def dropout(x: torch.Tensor, p: float, seed: int, offset: Union[int, torch.Tensor] = 0,
+            residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Differentiable dropout, ``[residual +] keep * x / (1 - p)``
+    (``flce_dropout``); the mask is a function of the element's position in
+    row-major order, of ``seed`` and of ``offset`` and is formed again in the
+    backward pass.  Draw each layer's and step's mask with a (seed, offset) of
+    its own.  ``offset`` may be an int64 tensor of one element on the device
+    of ``x``: a captured graph draws a new mask on each replay when the
+    program advances it in between."""
+    _check_tensor("x", x)
+    if not 0.0 <= p <= 1.0:
+        raise ValueError(f"p must lie in [0, 1] (got {p})")
+    if not 0 <= seed <= _U64:
+        raise ValueError("seed must be an unsigned 64-bit integer")
+    if torch.is_tensor(offset):
+        if offset.dtype != torch.int64 or offset.numel() != 1 or offset.device != x.device:
+            raise ValueError("a tensor offset must be one int64 on the device of x")
+    elif not 0 <= offset <= _U64:
+        raise ValueError("offset must be an unsigned 64-bit integer")
+    if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype
+                                 or residual.device != x.device):
+        raise ValueError(f"residual must match x: {tuple(x.shape)} {x.dtype} on {x.device} (got "
+                         f"{tuple(residual.shape)} {residual.dtype} on {residual.device})")
+    return _Dropout.apply(x, residual, float(p), seed, offset)
+
+
+def lm_head_loss(x: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, norm_weight: Optional[torch.Tensor],
+                 norm_bias: Optional[torch.Tensor] = None, eps: float = 1e-5, *,
+                 residual: Optional[torch.Tensor] = None, dropout_p: float = 0.0, seed: int = 0,
+                 offset: Union[int, torch.Tensor] = 0, ignore_index: int = -100, softcap: Optional[float] = None,
+                 multiplier: float = 1.0, reduction: str = "mean", workspace: Optional[torch.Tensor] = None,
+                 check: bool = False):
+    """The whole head of a training step, differentiable: the last block's
+    output ``x`` through dropout onto the ``residual`` stream (when either is
+    asked for), the final layer norm, and the fused linear cross-entropy.
+    Returns (loss, n_correct) as ``linear_cross_entropy`` does."""
+    if dropout_p != 0.0 or residual is not None:
+        x = dropout(x, dropout_p, seed, offset, residual)
+    y = layer_norm(x, norm_weight, norm_bias, eps)
+    return linear_cross_entropy(y, W, labels, ignore_index, softcap, multiplier, reduction, workspace, check)
