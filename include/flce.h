@@ -380,6 +380,56 @@ int flce_dropout(const void* x, const void* residual, void* y, int64_t n, double
                  const uint64_t* offset_dev, hipStream_t stream, int dtype);
 
 /*
+ * Parameters of flce_sample: one value for every row, or (pointer not NULL)
+ * a device array with one value per row.  Zero-initialise the struct and set
+ * temperature, top_p and what else is needed.
+ */
+typedef struct {
+  float temperature;              /* t >= 0, finite; 0: the lowest index of the maximum */
+  float top_p;                    /* 0 < p <= 1; 1: off */
+  float min_p;                    /* 0 <= q <= 1; 0: off */
+  int64_t top_k;                  /* k >= 0; 0 (or k >= V): off */
+  const float* temperature_rows;
+  const float* top_p_rows;
+  const float* min_p_rows;
+  const int64_t* top_k_rows;
+} flce_sample_params_t;
+
+/* Workspace bytes of flce_sample; 0 for sizes it does not take. */
+size_t flce_sample_workspace_size(int64_t N, int64_t V, int dtype);
+
+/*
+ * Draw one token from each row z of logits (as flce_logits writes them) with
+ * the caller's random number u.  With max = max z, w_i = exp((z_i - max) / t)
+ * and tokens ordered by descending z, equal logits by ascending index:
+ *   S_k   the first k tokens
+ *   S_p   the shortest prefix of S_k that holds at least p of S_k's weight
+ *   S_q   the tokens with w_i >= q
+ *   S = S_k n S_p n S_q (never empty: it holds the first token)
+ *   token = the lowest i in S with sum_{j in S, j <= i} w_j > u sum_{j in S} w_j
+ *   logprob = log(w_token / sum_{j in S} w_j)
+ * A logit of -inf is masked: it is never drawn (nor is NaN, which counts as
+ * -inf, or a weight below 2^-39 of the largest).  Logits of +inf share the
+ * whole weight.  A row without a logit above -inf, with a per-row parameter
+ * out of its range or with u outside [0, 1) gets token -1 and logprob -inf.
+ *   logits     [N, V] dtype, row stride ld_logits >= 0 elements (rows may
+ *              overlap: they are only read), aligned to one element
+ *   u          [N] fp32 in [0, 1)
+ *   tokens     [N] int64 out
+ *   logprobs   [N] fp32 out, or NULL
+ *   workspace  256-byte aligned, flce_sample_workspace_size bytes
+ * Decisions are taken on 64-bit exponentials rounded to integers, so they do
+ * not depend on the order of any sum: the same call gives the same tokens.
+ * N <= 2^22 and V <= 2^24 (else FLCE_EUNSUPPORTED).  Enqueued on `stream`;
+ * nothing is allocated, nothing synchronises.  Returns FLCE_OK, FLCE_EINVAL
+ * (also for a scalar parameter out of its range), FLCE_EUNSUPPORTED,
+ * FLCE_EWORKSPACE or FLCE_EDEVICE.
+ */
+int flce_sample(const void* logits, int64_t ld_logits, const float* u, int64_t N, int64_t V,
+                const flce_sample_params_t* params, int64_t* tokens, float* logprobs,
+                hipStream_t stream, int dtype, void* workspace, size_t workspace_bytes);
+
+/*
  * Synchronise `stream` and return the device-side status of the last
  * flce_fwd_bwd, flce_fwd_bwd_ex, flce_fwd or flce_cross_entropy that used
  * `workspace`: FLCE_OK or FLCE_ELABEL.  Returns
@@ -423,7 +473,8 @@ enum {
   FLCE_KERNEL_LAYER_NORM_BWD = 13,/* flce_layer_norm_bwd: grad_x and per-group parameter gradients */
   FLCE_KERNEL_LAYER_NORM_REDUCE = 14,/* flce_layer_norm_bwd: sum of the groups' parameter gradients */
   FLCE_KERNEL_DROPOUT = 15,     /* flce_dropout */
-  FLCE_KERNEL_KINDS = 16
+  FLCE_KERNEL_SAMPLE = 16,      /* flce_sample */
+  FLCE_KERNEL_KINDS = 17
 };
 
 /* Turn event timing on (on != 0) or off for subsequent calls.  Returns FLCE_OK. */

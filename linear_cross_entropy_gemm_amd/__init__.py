@@ -44,6 +44,9 @@ from ._lib import (  # noqa: F401
     flce_profile_read,
     flce_plan,
     flce_read_status,
+    flce_sample,
+    flce_sample_params_t,
+    flce_sample_workspace_size,
     flce_scale_grads,
     flce_strerror,
     flce_workspace_size,
@@ -51,11 +54,14 @@ from ._lib import (  # noqa: F401
 from .head import (  # noqa: F401
     LayerNormForward,
     LayerNormGrads,
+    SampleOutputs,
     dropout,
     layer_norm,
     layer_norm_bwd,
     layer_norm_fwd,
     lm_head_loss,
+    lm_head_sample,
+    sample,
 )
 from .torch_api import (  # noqa: F401
     CrossEntropyOutputs,

@@ -38,12 +38,12 @@ EXPORTED = ("flce_plan", "flce_workspace_size", "flce_fwd_bwd", "flce_fwd_bwd_ex
             "flce_fwd_workspace_size",
             "flce_fwd", "flce_logits", "flce_cross_entropy_workspace_size", "flce_cross_entropy",
             "flce_scale_grads", "flce_layer_norm_fwd", "flce_layer_norm_bwd_workspace_size",
-            "flce_layer_norm_bwd", "flce_dropout", "flce_read_status", "flce_strerror", "flce_profile_enable", "flce_profile_read")
+            "flce_layer_norm_bwd", "flce_dropout", "flce_sample_workspace_size", "flce_sample", "flce_read_status", "flce_strerror", "flce_profile_enable", "flce_profile_read")
 
 # Kernel kinds of the per-kernel timing facility (index order of the arrays).
 KERNEL_KINDS = ("label_scan", "fwd_logits", "row_merge", "grad_logits", "grad_h", "grad_h_reduce",
                 "grad_W", "finalize", "zero", "logits", "cross_entropy", "scale", "layer_norm",
-                "layer_norm_bwd", "layer_norm_reduce", "dropout")
+                "layer_norm_bwd", "layer_norm_reduce", "dropout", "sample")
 
 
 class flce_plan_t(ctypes.Structure):
@@ -71,6 +71,20 @@ class flce_options_t(ctypes.Structure):
         ("grad_scale", ctypes.c_float),
         ("accumulate_grad_W", ctypes.c_int),
         ("use_grad_scale", ctypes.c_int),
+    ]
+
+
+class flce_sample_params_t(ctypes.Structure):
+    """Parameters of flce_sample (device addresses as ints, 0 = none)."""
+    _fields_ = [
+        ("temperature", ctypes.c_float),
+        ("top_p", ctypes.c_float),
+        ("min_p", ctypes.c_float),
+        ("top_k", ctypes.c_int64),
+        ("temperature_rows", ctypes.c_void_p),
+        ("top_p_rows", ctypes.c_void_p),
+        ("min_p_rows", ctypes.c_void_p),
+        ("top_k_rows", ctypes.c_void_p),
     ]
 
 
@@ -133,6 +147,10 @@ def _load() -> ctypes.CDLL:
     lib.flce_layer_norm_bwd.restype = i32
     lib.flce_dropout.argtypes = [vp, vp, vp, i64, f64, u64, u64, vp, vp, i32]
     lib.flce_dropout.restype = i32
+    lib.flce_sample_workspace_size.argtypes = [i64, i64, i32]
+    lib.flce_sample_workspace_size.restype = sz
+    lib.flce_sample.argtypes = [vp, i64, vp, i64, i64, ctypes.POINTER(flce_sample_params_t), vp, vp, vp, i32, vp, sz]
+    lib.flce_sample.restype = i32
     lib.flce_read_status.argtypes = [vp, vp]
     lib.flce_read_status.restype = i32
     lib.flce_strerror.argtypes = [i32]
@@ -253,6 +271,17 @@ def flce_dropout(x: int, residual, y: int, n: int, p: float, seed: int, offset: 
                  dtype: int) -> int:
     """Raw call (seed and offset: unsigned 64-bit); returns the C return code."""
     return _lib.flce_dropout(x, residual, y, n, p, seed, offset, offset_dev, stream, dtype)
+
+
+def flce_sample_workspace_size(N: int, V: int, dtype: int) -> int:
+    return int(_lib.flce_sample_workspace_size(N, V, dtype))
+
+
+def flce_sample(logits: int, ld_logits: int, u: int, N: int, V: int, params: flce_sample_params_t, tokens: int,
+                logprobs, stream: int, dtype: int, workspace: int, workspace_bytes: int) -> int:
+    """Raw call; returns the C return code."""
+    return _lib.flce_sample(logits, ld_logits, u, N, V, None if params is None else ctypes.byref(params), tokens,
+                            logprobs, stream, dtype, workspace, workspace_bytes)
 
 
 def flce_read_status(workspace: int, stream: int) -> int:

@@ -1,6 +1,6 @@
 """The operators around the vocabulary projection, on torch tensors: dropout
 with its residual add and the final layer norm in front of it, with their
-backward passes.  Every step of the computation runs in the library's HIP
+backward passes, and drawing tokens from the logits behind it.  Every step of the computation runs in the library's HIP
 kernels on torch's current stream of the tensors' device; nothing
 synchronises."""
 from __future__ import annotations
@@ -12,7 +12,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib
-from .torch_api import _DTYPES, _ptr, _workspace, linear_cross_entropy
+from .torch_api import _DTYPES, _ptr, _workspace, linear_cross_entropy, logits as _logits
 
 _U64 = (1 << 64) - 1
 
@@ -29,6 +29,12 @@ class LayerNormGrads:
     grad_x: Optional[torch.Tensor]        # shape and dtype of x
     grad_weight: Optional[torch.Tensor]   # [H] dtype of the weight
     grad_bias: Optional[torch.Tensor]     # [H] dtype of the weight
+
+
+@dataclasses.dataclass
+class SampleOutputs:
+    tokens: torch.Tensor                     # [...] int64; -1: nothing to draw
+    logprobs: Optional[torch.Tensor] = None  # [...] fp32, of the filtered distribution
 
 
 def _stream(dev) -> int:
@@ -237,3 +243,72 @@ def lm_head_loss(x: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, norm_we
         x = dropout(x, dropout_p, seed, offset, residual)
     y = layer_norm(x, norm_weight, norm_bias, eps)
     return linear_cross_entropy(y, W, labels, ignore_index, softcap, multiplier, reduction, workspace, check)
+
+
+def _sample_param(name: str, v, dtype, N: int, dev, prm) -> Optional[torch.Tensor]:
+    """A scalar goes into the parameter block, a tensor's address into its
+    per-row field; the tensor is returned to be kept alive for the call."""
+    if not torch.is_tensor(v):
+        setattr(prm, name, v)
+        return None
+    if v.dtype != dtype or v.device != dev or v.numel() != N:
+        raise ValueError(f"{name} must be a number or one {dtype} per row on {dev}")
+    v = v.contiguous()
+    setattr(prm, name + "_rows", _ptr(v))
+    return v
+
+
+def sample(logits: torch.Tensor, u: torch.Tensor, temperature: Union[float, torch.Tensor] = 1.0,
+           top_k: Union[int, torch.Tensor] = 0, top_p: Union[float, torch.Tensor] = 1.0,
+           min_p: Union[float, torch.Tensor] = 0.0, *, logprobs: bool = False,
+           workspace: Optional[torch.Tensor] = None) -> SampleOutputs:
+    """One call of ``flce_sample``: a token for every row of ``logits``
+    [..., V] (which may be a row-padded view) from the random numbers ``u``
+    [...], float32 in [0, 1).  ``temperature`` (0: the first maximum),
+    ``top_k`` (0: off), ``top_p`` (1: off) and ``min_p`` (0: off) are numbers,
+    or tensors with one value per row (float32; int64 for ``top_k``) on the
+    device of ``logits``; they apply in that order, min-p relative to the
+    largest probability.  A row without a logit above -inf, or with a per-row
+    value out of range, gets token -1."""
+    _check_rows("logits", logits)
+    z = _rows(logits)
+    N, V = z.shape
+    dev = logits.device
+    shape = logits.shape[:-1]
+    if u.dtype != torch.float32 or u.device != dev or u.numel() != N:
+        raise ValueError(f"u must hold one float32 per row of logits on {dev}")
+    u = u.contiguous()
+    prm = _lib.flce_sample_params_t()
+    keep = [_sample_param(n, v, d, N, dev, prm) for n, v, d in (
+        ("temperature", temperature, torch.float32), ("top_k", top_k, torch.int64),
+        ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32))]
+    dtype = _DTYPES[logits.dtype]
+    ws_bytes = _lib.flce_sample_workspace_size(N, V, dtype)
+    if ws_bytes == 0:
+        raise _lib.FlceError(_lib.FLCE_EUNSUPPORTED, "flce_sample_workspace_size")
+    workspace = _workspace(workspace, ws_bytes, dev)
+    res = SampleOutputs(torch.empty(shape, dtype=torch.int64, device=dev),
+                        torch.empty(shape, dtype=torch.float32, device=dev) if logprobs else None)
+    with torch.cuda.device(dev):
+        rc = _lib.flce_sample(_ptr(z), z.stride(0), _ptr(u), N, V, prm, _ptr(res.tokens), _ptr(res.logprobs),
+                              _stream(dev), dtype, _ptr(workspace), workspace.numel())
+    del keep
+    if rc != _lib.FLCE_OK:
+        raise _lib.FlceError(rc, "flce_sample")
+    return res
+
+
+def lm_head_sample(x: torch.Tensor, W: torch.Tensor, u: torch.Tensor, norm_weight: Optional[torch.Tensor],
+                   norm_bias: Optional[torch.Tensor] = None, eps: float = 1e-5, *, softcap: Optional[float] = None,
+                   multiplier: float = 1.0, temperature: Union[float, torch.Tensor] = 1.0,
+                   top_k: Union[int, torch.Tensor] = 0, top_p: Union[float, torch.Tensor] = 1.0,
+                   min_p: Union[float, torch.Tensor] = 0.0, logprobs: bool = False) -> SampleOutputs:
+    """The whole head of a decoding step: the final layer norm of the hidden
+    states ``x`` [..., H], the materialised logits (``logits``), and one token
+    per row (``sample``)."""
+    y = layer_norm_fwd(x, norm_weight, norm_bias, eps).y
+    H = x.shape[-1]
+    z = _logits(y.reshape(-1, H), W, softcap, multiplier)
+    o = sample(z, u, temperature, top_k, top_p, min_p, logprobs=logprobs)
+    shape = x.shape[:-1]
+    return SampleOutputs(o.tokens.reshape(shape), o.logprobs.reshape(shape) if logprobs else None)

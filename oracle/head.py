@@ -65,3 +65,35 @@ def dropout(x, p, seed, offset, residual=None):
     if p < 1.0:
         y[keep] = x[keep] / (1.0 - p)
     return y if residual is None else y + np.asarray(residual, dtype=np.float64)
+
+
+def sample_row(z, u, t=1.0, k=0, p=1.0, q=0.0):
+    """(token, logprob, border) of one row of logits: the definition step by
+    step.  `border` is the distance of u from the nearest end of the token's
+    interval, for tests that must stay clear of it."""
+    z = np.asarray(z, dtype=np.float64).copy()
+    z[np.isnan(z)] = -np.inf
+    zm = z.max()
+    if zm == -np.inf:
+        return -1, -np.inf, 1.0
+    if t == 0.0:
+        return int(np.flatnonzero(z == zm)[0]), 0.0, 1.0
+    with np.errstate(invalid="ignore"):
+        w = np.where(z == zm, 1.0, np.exp((z - zm) / t))
+    order = sorted(range(z.size), key=lambda i: (-z[i], i))
+    if k > 0:
+        order = order[:k]
+    if p < 1.0:
+        total, run, prefix = float(np.cumsum(w[order])[-1]), 0.0, []
+        for i in order:
+            prefix.append(i)
+            run += w[i]
+            if run >= p * total:
+                break
+        order = prefix
+    kept = sorted(i for i in order if w[i] >= q and w[i] > 0.0)
+    c = np.cumsum(w[kept])
+    j = min(int(np.searchsorted(c, u * c[-1], side="right")), len(kept) - 1)
+    lo, hi = (c[j - 1] if j else 0.0) / c[-1], c[j] / c[-1]
+    border = min(u - lo if j else 1.0, hi - u if j + 1 < len(kept) else 1.0)
+    return kept[j], float(np.log(w[kept[j]] / c[-1])), border

@@ -89,3 +89,42 @@ def test_wrappers_refuse_bad_tensors():
     for f in (lambda: L.layer_norm_fwd(x.half()), lambda: L.dropout(x.long(), 0.5, 1)):
         with pytest.raises(TypeError):
             f()
+
+
+def _sample(prm=None, rows=None, **kw):
+    p = L.flce_sample_params_t(temperature=1.0, top_p=1.0)
+    for k, v in (prm or {}).items():
+        setattr(p, k, v)
+    a = dict(logits=16, ld=8, u=16, N=2, V=8, params=p, tokens=16, logprobs=16, stream=0, dtype=0, workspace=256,
+             workspace_bytes=0)   # no workspace bytes: refused last
+    a.update(kw)
+    return L.flce_sample(*a.values())
+
+
+@pytest.mark.parametrize("prm,kw,code", [
+    ({}, dict(dtype=2), L.FLCE_EINVAL), ({}, dict(N=-1), L.FLCE_EINVAL), ({}, dict(V=0), L.FLCE_EINVAL),
+    ({}, dict(params=None), L.FLCE_EINVAL), (dict(temperature=-1.0), {}, L.FLCE_EINVAL),
+    (dict(temperature=float("nan")), {}, L.FLCE_EINVAL), (dict(temperature=float("inf")), {}, L.FLCE_EINVAL),
+    (dict(top_k=-1), {}, L.FLCE_EINVAL), (dict(top_p=0.0), {}, L.FLCE_EINVAL), (dict(top_p=1.5), {}, L.FLCE_EINVAL),
+    (dict(top_p=float("nan")), {}, L.FLCE_EINVAL), (dict(min_p=-0.5), {}, L.FLCE_EINVAL),
+    (dict(min_p=1.5), {}, L.FLCE_EINVAL), (dict(temperature_rows=18), {}, L.FLCE_EINVAL),
+    (dict(top_k_rows=20), {}, L.FLCE_EINVAL), (dict(top_p_rows=18), {}, L.FLCE_EINVAL),
+    (dict(min_p_rows=18), {}, L.FLCE_EINVAL), ({}, dict(logits=None), L.FLCE_EINVAL),
+    ({}, dict(u=None), L.FLCE_EINVAL), ({}, dict(tokens=None), L.FLCE_EINVAL),
+    ({}, dict(workspace=None), L.FLCE_EINVAL), ({}, dict(logits=17), L.FLCE_EINVAL),
+    ({}, dict(logits=18, dtype=1), L.FLCE_EINVAL), ({}, dict(u=18), L.FLCE_EINVAL),
+    ({}, dict(tokens=20), L.FLCE_EINVAL), ({}, dict(logprobs=18), L.FLCE_EINVAL),
+    ({}, dict(workspace=128), L.FLCE_EINVAL), ({}, dict(ld=-1), L.FLCE_EINVAL),
+    ({}, dict(N=(1 << 22) + 1), L.FLCE_EUNSUPPORTED), ({}, dict(V=(1 << 24) + 1), L.FLCE_EUNSUPPORTED),
+    ({}, {}, L.FLCE_EWORKSPACE), ({}, dict(N=0, logits=None, u=None, tokens=None, workspace=None), L.FLCE_OK),
+])
+def test_sample_rejects_before_launch(prm, kw, code):
+    assert _sample(prm, **kw) == code
+
+
+def test_sample_workspace_size():
+    for N, V, dt in [(1, 1, 0), (64, 129280, 1), (256, 202048, 0), (0, 8, 0), (1 << 22, 8, 1), (1, 1 << 24, 0)]:
+        b = L.flce_sample_workspace_size(N, V, dt)
+        assert b >= 256 and b % 256 == 0
+    assert L.flce_sample_workspace_size(-1, 8, 0) == 0 and L.flce_sample_workspace_size(1, 0, 0) == 0
+    assert L.flce_sample_workspace_size(1, 8, 2) == 0 and L.flce_sample_workspace_size(1, (1 << 24) + 1, 0) == 0

@@ -55,3 +55,32 @@ def test_layer_norm_gradients_against_differences(M, H):
 def test_layer_norm_closed_form():
     y, mean, rstd = O.layer_norm([[1.0, 3.0]], [2.0, 2.0], [0.5, 0.5], 3.0)
     assert mean[0] == 2.0 and rstd[0] == 0.5 and y.tolist() == [[-0.5, 1.5]]
+
+
+def test_sample_row_by_hand():
+    """Weights 1, 1/2, 1/4, 1/4 (base-2 logits at t = 1 / ln 2)."""
+    z, t = np.array([-1.0, 0.0, -2.0, -2.0]), 1.0 / np.log(2.0)
+    pick = lambda u, **kw: O.sample_row(z, u, t, **kw)[0]
+    # index order: token 0 holds [0, 1/4), 1 [1/4, 3/4), 2 [3/4, 7/8), 3 the rest
+    assert [pick(u) for u in (0.0, 0.24, 0.26, 0.74, 0.76, 0.87, 0.88, 0.99)] == [0, 0, 1, 1, 2, 2, 3, 3]
+    assert abs(O.sample_row(z, 0.0, t)[1] - np.log(0.25)) < 1e-15
+    assert pick(0.99, k=1) == 1 and pick(0.99, k=2) == 1 and pick(0.99, k=3) == 2   # ties: lowest index stays
+    assert pick(0.99, p=0.5) == 1 and pick(0.01, p=0.51) == 0 and pick(0.99, p=0.8) == 2 and pick(0.99, p=0.9) == 3
+    assert pick(0.01, q=0.6) == 1 and pick(0.01, q=0.5) == 0 and pick(0.99, q=0.2) == 3
+    # top-p counts within the top-k: 2/3 of (1, 1/2) is the first alone
+    assert pick(0.01, k=2, p=0.66) == 1 and pick(0.01, k=2, p=0.67) == 0
+    assert O.sample_row(z, 0.5, 0.0)[:2] == (1, 0.0)
+    assert O.sample_row([-np.inf] * 3, 0.5)[:2] == (-1, -np.inf)
+    assert O.sample_row([np.inf, 0.0, np.inf], 0.6)[0] == 2
+    assert O.sample_row([np.nan, 0.0], 0.0)[0] == 1
+
+
+def test_sample_row_frequencies():
+    """Over evenly spaced random numbers a token is drawn in proportion to its
+    probability, to one draw."""
+    r = np.random.default_rng(9)
+    z = r.normal(size=20)
+    n = 4000
+    drawn = np.bincount([O.sample_row(z, (i + 0.5) / n, 0.7)[0] for i in range(n)], minlength=20)
+    w = np.exp(z / 0.7)
+    assert np.abs(drawn - n * w / w.sum()).max() <= 1.0
