@@ -420,7 +420,8 @@ size_t flce_sample_workspace_size(int64_t N, int64_t V, int dtype);
  *   workspace  256-byte aligned, flce_sample_workspace_size bytes
  * Decisions are taken on 64-bit exponentials rounded to integers, so they do
  * not depend on the order of any sum: the same call gives the same tokens.
- * N <= 2^22 and V <= 2^24 (else FLCE_EUNSUPPORTED).  Enqueued on `stream`;
+ * N <= 2^21, V <= 2^24 and N ceil(V / 8192) <= 2^23 (else
+ * FLCE_EUNSUPPORTED).  Enqueued on `stream`;
  * nothing is allocated, nothing synchronises.  Returns FLCE_OK, FLCE_EINVAL
  * (also for a scalar parameter out of its range), FLCE_EUNSUPPORTED,
  * FLCE_EWORKSPACE or FLCE_EDEVICE.
@@ -473,8 +474,9 @@ enum {
   FLCE_KERNEL_LAYER_NORM_BWD = 13,/* flce_layer_norm_bwd: grad_x and per-group parameter gradients */
   FLCE_KERNEL_LAYER_NORM_REDUCE = 14,/* flce_layer_norm_bwd: sum of the groups' parameter gradients */
   FLCE_KERNEL_DROPOUT = 15,     /* flce_dropout */
-  FLCE_KERNEL_SAMPLE = 16,      /* flce_sample */
-  FLCE_KERNEL_KINDS = 17
+  FLCE_KERNEL_SAMPLE_SCAN = 16, /* flce_sample: maxima and weights of each row's pieces */
+  FLCE_KERNEL_SAMPLE_PICK = 17, /* flce_sample: the filters' cut and the token */
+  FLCE_KERNEL_KINDS = 18
 };
 
 /* Turn event timing on (on != 0) or off for subsequent calls.  Returns FLCE_OK. */

@@ -115,15 +115,15 @@ def _sample(prm=None, rows=None, **kw):
     ({}, dict(logits=18, dtype=1), L.FLCE_EINVAL), ({}, dict(u=18), L.FLCE_EINVAL),
     ({}, dict(tokens=20), L.FLCE_EINVAL), ({}, dict(logprobs=18), L.FLCE_EINVAL),
     ({}, dict(workspace=128), L.FLCE_EINVAL), ({}, dict(ld=-1), L.FLCE_EINVAL),
-    ({}, dict(N=(1 << 22) + 1), L.FLCE_EUNSUPPORTED), ({}, dict(V=(1 << 24) + 1), L.FLCE_EUNSUPPORTED),
-    ({}, {}, L.FLCE_EWORKSPACE), ({}, dict(N=0, logits=None, u=None, tokens=None, workspace=None), L.FLCE_OK),
+    ({}, dict(N=(1 << 21) + 1), L.FLCE_EUNSUPPORTED), ({}, dict(V=(1 << 24) + 1), L.FLCE_EUNSUPPORTED),
+    ({}, dict(N=1 << 20, V=1 << 20), L.FLCE_EUNSUPPORTED), ({}, {}, L.FLCE_EWORKSPACE), ({}, dict(N=0, logits=None, u=None, tokens=None, workspace=None), L.FLCE_OK),
 ])
 def test_sample_rejects_before_launch(prm, kw, code):
     assert _sample(prm, **kw) == code
 
 
 def test_sample_workspace_size():
-    for N, V, dt in [(1, 1, 0), (64, 129280, 1), (256, 202048, 0), (0, 8, 0), (1 << 22, 8, 1), (1, 1 << 24, 0)]:
+    for N, V, dt in [(1, 1, 0), (64, 129280, 1), (256, 202048, 0), (0, 8, 0), (0, 1 << 20, 0), (1 << 21, 8, 1), (1, 1 << 24, 0)]:
         b = L.flce_sample_workspace_size(N, V, dt)
         assert b >= 256 and b % 256 == 0
     assert L.flce_sample_workspace_size(-1, 8, 0) == 0 and L.flce_sample_workspace_size(1, 0, 0) == 0
