@@ -11,9 +11,10 @@
 // reason: an fp32 one moves the borders between tokens of a flat row by more
 // than their spacing warrants.
 //
-// A row passes through the chip once, in pieces of 8192 logits spread over
-// the work-groups of sample_scan_kernel, which leaves behind what decides
-// where the answer lies:
+// Rows of up to 1024 logits stay in one wave's registers
+// (sample_small_kernel).  A longer row passes through the chip once, in pieces of 8192 logits spread over the
+// work-groups of sample_scan_kernel, which leaves behind what decides where
+// the answer lies:
 //   * the maximum of each 64 logits and of the piece;
 //   * with top-p alone: the piece's weight by bins of z, 1/8 of min(t, 1) wide,
 //     counted down from the piece's maximum (bins are aligned in z, so bins
@@ -25,9 +26,11 @@
 //     from below, so every candidate lies in a group whose maximum reaches it;
 //   * min-p: the candidates reach the maximum + t ln q;
 //   * top-p alone: the bin in which the weight from above reaches p of the
-//     row's; only that bin's logits decide where the cut falls;
-//   * then a search in the list of candidates (LDS), or, where the kept set
-//     is most of a flat row, one piece whose weights are summed in order.
+//     row's: the candidates are the logits from that bin up where those are
+//     few, and the bin's own logits where the kept set is most of a flat row;
+//   * then a sort of the candidates (1024 of them) or a search among them
+//     (8192, in LDS), or, in a flat row, one piece whose weights are summed
+//     in index order.
 // Rows for which that does not work out (a list that overflows, a cut below
 // the bins) take the searches over the whole row at the end of the kernel.
 //
@@ -44,18 +47,21 @@ namespace flce {
 
 namespace {
 
-typedef unsigned long long u64;
-
 constexpr int kRowThreads = 1024;
 constexpr int kRowWaves = kRowThreads / 64;
 constexpr int kBins = 2048;          // 11 bits of a key per search pass
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;
+constexpr int kSmall = 1024;         // rows one wave holds, lists that are sorted
 constexpr int kPiece = 8192;         // logits per work-group of the scan
 constexpr int kGroup = 64;           // logits per stored maximum
 constexpr int kPieceGroups = kPiece / kGroup;
+constexpr int kMaxPieces = (1 << 24) / kPiece;
 constexpr int kSlots = 128;          // bins of z per piece; the last holds the rest
 constexpr int kList = 8192;          // candidates per row (64 KB of LDS)
+constexpr int kGroupBatch = 4096;    // groups looked through at a time
 constexpr int kScanThreads = 256;
+
+constexpr double kInfMax = 1e300;   // stands for an infinite maximum
 
 struct SampleArgs {
   const void* z;
@@ -66,7 +72,7 @@ struct SampleArgs {
   int s;           // weights are multiples of 2^-s
   int64_t* tokens;
   float* logprobs;
-  // left by the scan (rows longer than one piece)
+  // left by the scan (rows longer than kSmall)
   int pieces;
   uint32_t* pmax;   // [N][pieces] key of the piece's maximum
   double* psum;     // [N][pieces] its weight relative to that maximum
@@ -86,10 +92,12 @@ __device__ __forceinline__ float value_of(uint32_t k) {
 
 // A row's parameters and the weights they define.
 struct RowParams {
-  double t, p, q, zmax;
+  double t, p, q, zmax, rate;   // rate = log2(e) / t
   int64_t k;
   float u;
   bool ok;
+
+  __device__ __forceinline__ void set_max(float m) { zmax = m < __builtin_inff() ? (double)m : kInfMax; }
 };
 
 __device__ __forceinline__ RowParams row_params(const SampleArgs& a, int64_t row) {
@@ -105,6 +113,7 @@ __device__ __forceinline__ RowParams row_params(const SampleArgs& a, int64_t row
   r.p = p;
   r.q = q;
   r.zmax = 0.0;
+  r.rate = 1.4426950408889634074 / r.t;
   return r;
 }
 
@@ -117,18 +126,36 @@ __device__ __forceinline__ Mode mode_of(const RowParams& r, int64_t V) {
   return r.p < 1.0 ? kTopP : kAll;
 }
 
-// Bins of z: 1/8 of min(t, 1) wide, ascending with z.
+// Bins of z, 1/8 of min(t, 1) wide, by whole-number floats ascending with z.
+// Differences of two are exact below kBinLimit.
+constexpr float kBinLimit = 8388608.0f;   // 2^23
 __device__ __forceinline__ float bin_scale(const RowParams& r) {
   return r.t < 1.0 ? (float)(8.0 / r.t < 1e30 ? 8.0 / r.t : 1e30) : 8.0f;
 }
-__device__ __forceinline__ int bin_of(float x, float alpha) {
-  return (int)__builtin_floorf(__builtin_fminf(__builtin_fmaxf(x * alpha, -0x1p30f), 0x1p30f));
-}
+__device__ __forceinline__ float bin_of(float x, float alpha) { return __builtin_floorf(x * alpha); }
 
-// exp((z - max) / t); 1 for the maximum itself, also where it is infinite.
+// exp((z - max) / t) as 2^(n + f), |f| <= 1/2: 2^f by the polynomial of
+// degree 9 through the Chebyshev nodes with its constant term put to 1
+// (relative error 2^-45), n put into the exponent.  The maximum itself weighs
+// exactly 1 (y = 0; where it is infinite, zmax is 1e300 and y is clamped),
+// and weights stop falling at 2^-1000, which is nothing to every use of
+// them.  The coefficients are loaded, not literal: in scalar registers they
+// feed the multiply-adds directly, where literals would each take two moves
+// more.
+__constant__ double exp2_coef[9] = {0x1.62e42fefa39f7p-1,  0x1.ebfbdff8149f2p-3,  0x1.c6b08d7044115p-5,
+                                    0x1.3b2ab72b175f8p-7,  0x1.5d87fe908fed1p-10, 0x1.43088e257e65bp-13,
+                                    0x1.ffcb7677a5f5cp-17, 0x1.63ef969b0e64ep-20, 0x1.b6571ea79d565p-24};
+
+__device__ __forceinline__ double exp2_of(double y) {
+  const double n = __builtin_rint(y), f = y - n;
+  double v = __builtin_fma(exp2_coef[8], f, exp2_coef[7]);
+#pragma unroll
+  for (int i = 6; i >= 0; --i) v = __builtin_fma(v, f, exp2_coef[i]);
+  return __builtin_amdgcn_ldexp(__builtin_fma(v, f, 1.0), (int)n);
+}
 __device__ __forceinline__ double weight(float x, const RowParams& r) {
-  const double z = (double)x;
-  return z == r.zmax ? 1.0 : exp((z - r.zmax) / r.t);
+  const double y = ((double)x - r.zmax) * r.rate;
+  return exp2_of(__builtin_fmin(__builtin_fmax(y, -1000.0), 0.0));
 }
 
 // round(w 2^s) for w <= 1, s <= 51: adding 2^52 leaves the integer in the
@@ -137,168 +164,286 @@ __device__ __forceinline__ u64 fixed(double w, double scale) {
   return __builtin_bit_cast(u64, __builtin_fma(w, scale, 0x1p52)) - __builtin_bit_cast(u64, 0x1p52);
 }
 
-__device__ __forceinline__ u64 wave_sum_u64(u64 x) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
+__device__ __forceinline__ double scale_of(const SampleArgs& a) {
+  return __builtin_bit_cast(double, (u64)(1023 + a.s) << 52);
+}
+
+// The least integer weight that min-p keeps (a weight of 0 is never drawn).
+__device__ __forceinline__ u64 floor_weight(const RowParams& r, double scale) {
+  const u64 f = (u64)ceil(r.q * scale);
+  return f < 1 ? 1 : f;
+}
+
+// The share of a sum that u (or p) asks for, as a running-sum target.
+__device__ __forceinline__ u64 draw_target(float u, u64 sum) {
+  const u64 t = (u64)((double)u * (double)sum);
+  return t < sum ? t : sum - 1;
+}
+__device__ __forceinline__ u64 share(double p, u64 sum) {
+  const u64 n = (u64)ceil(p * (double)sum);
+  return n < 1 ? 1 : n > sum ? sum : n;
+}
+
+// A row's result; `weight_sum` is the kept set's.  Its logarithm starts
+// from the hardware's fp32 one and takes one step of log s = log a + log(1 +
+// (s / a - 1)), where the rest is below 1e-6.
+__device__ __forceinline__ void emit(const SampleArgs& a, int64_t row, int64_t tok, float x, const RowParams& r,
+                                     double weight_sum) {
+  a.tokens[row] = tok;
+  if (!a.logprobs) return;
+  const double l2 = (double)__builtin_amdgcn_logf((float)weight_sum);
+  const double e = __builtin_fma(weight_sum, exp2_of(-l2), -1.0);
+  const double ls = __builtin_fma(l2, 0.69314718055994530942, e - 0.5 * e * e);
+  const double y = __builtin_fmin(((double)x - r.zmax) * r.rate, 0.0);
+  a.logprobs[row] = (float)(__builtin_fma(y, 0.69314718055994530942, -ls));
+}
+__device__ __forceinline__ void emit_none(const SampleArgs& a, int64_t row) {
+  a.tokens[row] = -1;
+  if (a.logprobs) a.logprobs[row] = kNegInf;
+}
+
+__device__ __forceinline__ int bits_of(u64 x) { return x ? 64 - __builtin_clzll(x) : 0; }
+
+// Sums over a work-group of TH threads.
+template <int TH>
+struct GroupScratch {
+  u64 wsum[TH / 64];
+};
+
+// Exclusive sum of x over the threads in order; `all` gets the whole sum.
+template <int TH>
+__device__ __forceinline__ u64 group_scan(u64 x, u64& all, GroupScratch<TH>& sh) {
+  u64 sum;
+  const u64 inc = wave_scan_u64(x, sum);
+  if (TH > 64) {
+    const int w = threadIdx.x >> 6;
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) sh.wsum[w] = sum;
+    __syncthreads();
+    // every wave scans the waves' sums
+    const int lane = threadIdx.x & 63;
+    const u64 inc_w = wave_scan_u64(lane < TH / 64 ? sh.wsum[lane] : 0, sum);
+    all = sum;
+    return (w ? lane_u64(inc_w, w - 1) : 0) + inc - x;
+  }
+  all = sum;
+  return inc - x;
+}
+
+// LDS written by a wave is read by others of the group (or by the wave
+// itself where it is the group).
+template <int TH> __device__ __forceinline__ void group_sync() {
+  if (TH == 64) {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  } else {
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Up to kSmall candidates, one per thread: composites that order them by
+// descending logit, then ascending index.
+
+__device__ __forceinline__ u64 composite(uint32_t key, int64_t i) { return (u64)key << 32 | (uint32_t)~(uint32_t)i; }
+__device__ __forceinline__ uint32_t key_in(u64 c) { return (uint32_t)(c >> 32); }
+__device__ __forceinline__ int64_t index_in(u64 c) { return (int64_t)(uint32_t)~(uint32_t)c; }
+__device__ __forceinline__ float value_in(u64 c) { return value_of(key_in(c)); }
+
+template <int TH>
+struct SortShared {
+  GroupScratch<TH> scratch;
+  u64 x[TH];   // exchange between waves, then the candidates' weights
+  u64 c[TH];
+};
+
+// Bitonic sort of the first P threads' values (P a power of two, at least
+// 64), largest first; strides within a wave are exchanged between lanes.
+template <int TH>
+__device__ __forceinline__ u64 sort_down(u64 x, int P, u64* lds) {
+  const int t = threadIdx.x;
+#pragma unroll 1
+  for (int size = 2; size <= P; size <<= 1)
+#pragma unroll 1
+    for (int d = size >> 1; d > 0; d >>= 1) {
+      u64 y;
+      if (TH == 64 || d < 64) {
+        y = lane_xor_u64(x, d);
+      } else {
+        __syncthreads();
+        lds[t] = x;
+        __syncthreads();
+        y = lds[t ^ d];
+      }
+      const bool keep_max = ((t & size) == 0) == ((t & d) == 0);
+      if ((y > x) == keep_max) x = y;
+    }
   return x;
 }
 
-// Inclusive sum over the wave's lanes.
-__device__ __forceinline__ u64 wave_scan_u64(u64 x) {
+__device__ __forceinline__ int pow2_from_64(int n) { return n <= 64 ? 64 : 1 << bits_of((u64)(n - 1)); }
+
+// Draws from n candidates (c = this thread's, 0 beyond them) that hold every
+// token at least as likely as the least of them.  top-p is a share of the
+// candidates' weight after top-k, or of `row_sum` where that is not 0.
+template <int TH>
+__device__ __forceinline__ void pick_sorted(const SampleArgs& a, int64_t row, u64 c, int n, const RowParams& r, bool top_k,
+                            u64 row_sum, SortShared<TH>& sh) {
+  const int t = threadIdx.x;
+  const double scale = scale_of(a);
+  c = sort_down<TH>(c, pow2_from_64(n), sh.x);
+  u64 f = t < n && (!top_k || (int64_t)t < r.k) ? fixed(weight(value_in(c), r), scale) : 0, all;
+  if (r.p < 1.0) {
+    const u64 before = group_scan<TH>(f, all, sh.scratch);
+    if (before >= share(r.p, row_sum ? row_sum : all)) f = 0;
+  }
+  if (f < floor_weight(r, scale)) f = 0;
+  // the kept ones are the first m threads'; now by ascending index
+  u64 m = 64;
+  if (TH > 64) group_scan<TH>(f ? 1 : 0, m, sh.scratch);
+  group_sync<TH>();
+  sh.c[t] = c;
+  group_sync<TH>();
+  const int P = pow2_from_64((int)m);
+  const u64 o = sort_down<TH>(f ? (c << 32) | (u64)t : 0, P, sh.x);
+  const u64 hit = sh.c[(uint32_t)o & (TH - 1)];
+  const u64 mine = o && t < P ? fixed(weight(value_in(hit), r), scale) : 0;
+  u64 sum;
+  const u64 before = group_scan<TH>(mine, sum, sh.scratch);
+  const u64 target = draw_target(r.u, sum);
+  if (before <= target && target < before + mine)   // one thread
+    emit(a, row, index_in(hit), value_in(hit), r, (double)sum / scale);
+}
+
+// Rows of up to 64 kPer logits, any parameters: one wave per row, lane l
+// holding the logits [l kPer, (l + 1) kPer).  Every cut is found bit by bit
+// of its key, from counts and sums over the wave.
+template <typename T, int kPer>
+__global__ __launch_bounds__(256) void sample_small_kernel(SampleArgs a) {
+  constexpr int low = sizeof(T) == 2 ? 16 : 0, E = RowVec<T>::E;
   const int lane = threadIdx.x & 63;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (row >= a.N) return;
+  RowParams r = row_params(a, row);
+  const T* z = static_cast<const T*>(a.z) + row * a.ld;
+  float x[kPer];
+  if (kPer == 1) {
+    x[0] = lane < a.V ? clean(to_f32(z[lane])) : kNegInf;
+  } else {
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const u64 y = __shfl_up(x, o);
-    if (lane >= o) x += y;
+    for (int j = 0; j < kPer; j += E) {
+      const typename RowVec<T>::type v = load_row(z, lane * kPer + j, a.V, kNegInf);
+#pragma unroll
+      for (int e = 0; e < E && j + e < kPer; ++e) x[j + e] = clean(to_f32(v[e]));
+    }
   }
-  return x;
+  float m = x[0];
+#pragma unroll
+  for (int j = 1; j < kPer; ++j) m = __builtin_fmaxf(m, x[j]);
+  m = wave_max(m);
+  if (!r.ok || m == kNegInf) {
+    if (lane == 0) emit_none(a, row);
+    return;
+  }
+  r.set_max(m);
+  if (r.t == 0.0) {   // the first maximum
+    int at = kPer;
+#pragma unroll
+    for (int j = kPer - 1; j >= 0; --j) at = x[j] == m ? j : at;
+    const int l = __builtin_ctzll(__builtin_amdgcn_ballot_w64(at < kPer));
+    if (lane == l) emit(a, row, lane * kPer + at, m, r, 1.0);
+    return;
+  }
+  uint32_t key[kPer];
+  uint32_t keep = 0;   // bit j: x[j] is kept
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    key[j] = key_of(x[j]);
+    keep |= (x[j] > kNegInf ? 1u : 0u) << j;
+  }
+  // Of the kept logits with key K, only the first `n` in index order stay;
+  // smaller keys go.
+  auto cut_at = [&](uint32_t K, u64 n) {
+    uint32_t tie = 0, over = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      tie |= (key[j] == K ? 1u : 0u) << j;
+      over |= (key[j] > K ? 1u : 0u) << j;
+    }
+    tie &= keep;
+    u64 all;
+    u64 rank = wave_scan_u64((u64)__builtin_popcount(tie), all) - (u64)__builtin_popcount(tie);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const bool is = tie >> j & 1;
+      if (is && rank >= n) tie &= ~(1u << j);
+      rank += is ? 1 : 0;
+    }
+    keep &= over | tie;
+  };
+  if (r.k > 0 && r.k < a.V) {
+    auto count = [&](uint32_t from) {
+      int n = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) n += __builtin_popcountll(__builtin_amdgcn_ballot_w64(x[j] > kNegInf && key[j] >= from));
+      return n;
+    };
+    if (count(0) > r.k) {
+      const int k = (int)r.k;
+      uint32_t K = 0;
+#pragma unroll 1
+      for (int b = 31; b >= low; --b)
+        if (count(K | 1u << b) >= k) K |= 1u << b;
+      K |= low && !(K >> 31) ? 0xFFFFu : 0u;   // a bf16 key's last 16 bits follow from its first
+      cut_at(K, (u64)(k - count(K + 1)));
+    }
+  }
+  const double scale = scale_of(a);
+  u64 w[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) w[j] = keep >> j & 1 ? fixed(weight(x[j], r), scale) : 0;
+  if (r.p < 1.0) {
+    auto mass = [&](uint32_t from) {
+      u64 s = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) s += key[j] >= from ? w[j] : 0;
+      return wave_sum_u64(s);
+    };
+    const u64 need = share(r.p, mass(0));
+    uint32_t K = 0;
+#pragma unroll 1
+    for (int b = 31; b >= low; --b)
+      if (mass(K | 1u << b) >= need) K |= 1u << b;
+    K |= low && !(K >> 31) ? 0xFFFFu : 0u;
+    const u64 rest = need - mass(K + 1), each = fixed(weight(value_of(K), r), scale);
+    cut_at(K, (rest + each - 1) / each);
+  }
+  const u64 least = floor_weight(r, scale);
+  u64 own = 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    w[j] = (keep >> j & 1) && w[j] >= least ? w[j] : 0;
+    own += w[j];
+  }
+  u64 sum;
+  u64 run = wave_scan_u64(own, sum) - own;
+  const u64 target = draw_target(r.u, sum);
+  if (run <= target && target < run + own) {   // one lane
+    int at = 0;
+    float xt = x[0];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      if (run <= target) {
+        at = j;
+        xt = x[j];
+      }
+      run += w[j];
+    }
+    emit(a, row, lane * kPer + at, xt, r, (double)sum / scale);
+  }
 }
 
-struct RowShared {
-  u64 hist[kBins];
-  u64 wsum[kRowWaves];
-  u64 above, total;
-  uint32_t digit;
-  uint32_t kmax[kRowWaves];
-  int64_t idx;
-};
-
-// A row of V logits: every wave of the work-group owns a consecutive part of
-// it, so sums over waves are sums in index order.
-template <typename T>
-struct Row {
-  static constexpr int E = RowVec<T>::E;
-  const T* z;
-  int64_t V, begin, end;
-
-  __device__ __forceinline__ Row(const T* p, int64_t v) : z(p), V(v) {
-    const int64_t per = (v + kRowWaves * 64 * E - 1) / (kRowWaves * 64 * E) * (64 * E);
-    begin = (int64_t)(threadIdx.x >> 6) * per;
-    end = begin + per < v ? begin + per : v;
-  }
-
-  // f(index, value) over this thread's elements of its wave's part.
-  template <typename F> __device__ __forceinline__ void each(F f) const {
-    for (int64_t c = begin + (threadIdx.x & 63) * E; c < end; c += 64 * E) {
-      const typename RowVec<T>::type v = load_row(z, c, V);
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (c + e < V) f(c + e, clean(to_f32(v[e])));
-    }
-  }
-
-  // The first index at which the running sum of f (u64, in index order)
-  // exceeds `target`, or -1.  All threads get it.
-  template <typename F> __device__ int64_t locate(F f, u64 target, RowShared& sh) const {
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    u64 s = 0;
-    each([&](int64_t i, float x) { s += f(i, x); });
-    s = wave_sum_u64(s);
-    __syncthreads();
-    if (lane == 0) sh.wsum[w] = s;
-    if (threadIdx.x == 0) sh.idx = -1;
-    __syncthreads();
-    u64 before = 0;
-    for (int i = 0; i < w; ++i) before += sh.wsum[i];
-    if (before <= target && target < before + s) {   // one wave
-      for (int64_t b = begin; b < end; b += 64 * E) {
-        const int64_t c = b + lane * E;
-        u64 own[E], sum = 0;
-        const typename RowVec<T>::type v = load_row(z, c, V);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          own[e] = c + e < V ? f(c + e, clean(to_f32(v[e]))) : 0;
-          sum += own[e];
-        }
-        const u64 inc = wave_scan_u64(sum);
-        const u64 all = __shfl(inc, 63);
-        if (target < before + all) {
-          u64 run = before + inc - sum;
-          if (run <= target && target < run + sum) {   // one lane
-            int64_t at = c;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-              run += own[e];
-              if (run <= target) at = c + e + 1;
-            }
-            sh.idx = at;
-          }
-          break;
-        }
-        before += all;
-      }
-    }
-    __syncthreads();
-    return sh.idx;
-  }
-
-  // The key K at which the sum of f over keys above K is below `need` and
-  // the sum with K reaches it; `above` receives the former.  `need_of` maps
-  // the sum over everything to `need` (1 <= need <= that sum).  One pass of
-  // 11 key bits after another, the passes after the first over the keys that
-  // share K's leading bits.
-  template <typename F, typename G> __device__ uint32_t search(F f, G need_of, u64& above, RowShared& sh) const {
-    constexpr int low = sizeof(T) == 2 ? 16 : 0;   // a bf16 key's last 16 bits follow from its first
-    uint32_t prefix = 0;
-    u64 over = 0, need = 0;
-    int hi = 32;
-    while (hi > low) {
-      const int bits = hi - low < 11 ? hi - low : 11, lo = hi - bits;
-      for (int i = threadIdx.x; i < kBins; i += kRowThreads) sh.hist[i] = 0;
-      __syncthreads();
-      each([&](int64_t i, float x) {
-        const uint32_t k = key_of(x);
-        if (hi == 32 || (k >> hi) == prefix) {
-          const u64 w = f(i, x);
-          if (w) atomicAdd(&sh.hist[(k >> lo) & ((1u << bits) - 1)], w);
-        }
-      });
-      __syncthreads();
-      // running sums from the highest bin down: thread i holds the bins
-      // kBins - 1 - 2 i and the one below it
-      const int top = kBins - 1 - 2 * threadIdx.x;
-      const u64 a = sh.hist[top], b = sh.hist[top - 1];
-      u64 inc = wave_scan_u64(a + b);
-      if ((threadIdx.x & 63) == 63) sh.wsum[threadIdx.x >> 6] = inc;
-      __syncthreads();
-      u64 before = 0, all = 0;
-      for (int i = 0; i < kRowWaves; ++i) {
-        if (i < (int)(threadIdx.x >> 6)) before += sh.wsum[i];
-        all += sh.wsum[i];
-      }
-      if (hi == 32) need = need_of(all);
-      inc += before + over;
-      const u64 exc = inc - a - b;
-      if (exc < need && need <= inc) {   // one thread
-        const bool first = need <= exc + a;
-        sh.digit = (uint32_t)(first ? top : top - 1);
-        sh.above = first ? exc : exc + a;
-      }
-      __syncthreads();
-      prefix = (hi == 32 ? 0u : prefix << bits) | sh.digit;
-      over = sh.above;
-      __syncthreads();
-      hi = lo;
-    }
-    above = over;
-    if (low == 0) return prefix;
-    return prefix << 16 | ((prefix & 0x8000u) ? 0u : 0xFFFFu);
-  }
-};
-
-// Kept by a filter: keys above `key`, and `key` itself up to index `idx`.
-struct Cut {
-  uint32_t key;
-  int64_t idx;
-  __device__ __forceinline__ bool keeps(int64_t i, uint32_t k) const { return k > key || (k == key && i <= idx); }
-};
-
-__device__ __forceinline__ double wave_sum_f64(double x) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
-  return x;
-}
-
+// ---------------------------------------------------------------------------
 // Maximum over aligned groups of 8 or 16 lanes.
 template <int kLanes> __device__ __forceinline__ float lanes_max(float x) {
   x = __builtin_fmaxf(x, dpp_f32<0xB1>(x));
@@ -336,8 +481,7 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a)
     if (t % kLanes == 0) a.gmax[out * kPieceGroups + (j * kScanThreads + t) / kLanes] = key_of(g);
     m = __builtin_fmaxf(m, g);
   }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) m = __builtin_fmaxf(m, __shfl_xor(m, o));
+  m = wave_max(m);
   if (lane == 0) wmax[w] = m;
   const Mode mode = mode_of(r, a.V);
   if (mode == kTopP)
@@ -353,7 +497,7 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a)
     if (mode == kTopP && t < kSlots) a.hist[out * kSlots + t] = 0;
     return;
   }
-  r.zmax = (double)m;
+  r.set_max(m);
   if (mode != kTopP) {
     double sum = 0.0;
 #pragma unroll
@@ -366,99 +510,265 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a)
     if (t == 0) a.psum[out] = ((wsum[0] + wsum[1]) + wsum[2]) + wsum[3];
     return;
   }
-  const double scale = __builtin_bit_cast(double, (u64)(1023 + a.s) << 52);
+  const double scale = scale_of(a);
   const float alpha = bin_scale(r);
-  const int top = bin_of(m, alpha);
+  const float top = bin_of(m, alpha);
 #pragma unroll
   for (int j = 0; j < kVec; ++j)
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const float x = clean(to_f32(v[j][e]));
       const u64 f = fixed(weight(x, r), scale);
-      const int d = top - bin_of(x, alpha);
-      if (f) atomicAdd(&hist[w][d < kSlots ? d : kSlots - 1], f);
+      // (an undefined difference of infinities counts as the rest)
+      const int d = (int)__builtin_fminf(top - bin_of(x, alpha), (float)(kSlots - 1));
+      if (f) atomicAdd(&hist[w][d], f);
     }
   __syncthreads();
-  u64 h = 0;
   if (t < kSlots) {
+    u64 h = 0;
 #pragma unroll
     for (int i = 0; i < kWaves; ++i) h += hist[i][t];
     a.hist[out * kSlots + t] = h;
   }
-  const u64 all = wave_sum_u64(h);
-  __syncthreads();
-  if (lane == 0) hist[0][w] = all;
-  __syncthreads();
-  if (t == 0) a.psum[out] = (double)(hist[0][0] + hist[0][1]) / scale;
 }
+
+// ---------------------------------------------------------------------------
+struct RowShared {
+  u64 hist[kBins];
+  GroupScratch<kRowThreads> scratch;
+  u64 above;
+  uint32_t digit;
+  uint32_t kmax[kRowWaves];
+  int64_t idx;
+};
 
 struct PickShared {
   RowShared row;
-  u64 list[kList];                  // composites, see Candidates
   union {
-    u64 cmass[kPiece / 4];          // kept list weight per piece (at most 2^24 / 8192 = 2048)
-    double dmass[kPiece / 4];
+    u64 list[kList];                  // composites
+    SortShared<kRowThreads> sort;     // after each thread has taken its own
+    SortShared<64> sort1;
   };
-  double factor[kPiece / 4];        // weight of each piece's maximum
-  double slot[kSlots];
-  double dsum[kRowWaves];
-  u64 usum[kRowWaves];
+  u64 cmass[kMaxPieces];              // kept weight per piece
+  double factor[kMaxPieces];          // weight of each piece's maximum
+  u64 slot[kSlots];
+  u64 sum;
+  uint16_t glist[kGroupBatch];        // accepted groups of a batch
+  int groups;
   int count;
   int found;
 };
 
-__device__ __forceinline__ int bits_of(u64 x) { return x ? 64 - __builtin_clzll(x) : 0; }
-
-// Sum over the work-group, all threads get it.
-__device__ __forceinline__ u64 group_sum_u64(u64 x, PickShared& sh) {
-  x = wave_sum_u64(x);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) sh.usum[threadIdx.x >> 6] = x;
-  __syncthreads();
-  x = 0;
-  for (int i = 0; i < kRowWaves; ++i) x += sh.usum[i];
-  return x;
+__device__ __forceinline__ u64 group_sum(u64 x, RowShared& sh) {
+  u64 all;
+  group_scan<kRowThreads>(x, all, sh.scratch);
+  return all;
 }
 
-// The candidates of a row: composites that order them by descending logit,
-// then ascending index (a larger composite comes first).
+// The bin, from the highest down, at which the running sum reaches `need`
+// (1 <= need <= the sum); `above` gets the sum of the bins over it, plus what
+// it held.  `need_of` maps the whole sum to `need`.
+template <typename G>
+__device__ __forceinline__ uint32_t find_bin(G need_of, u64& above, RowShared& sh) {
+  const int top = kBins - 1 - 2 * threadIdx.x;
+  const u64 a = sh.hist[top], b = sh.hist[top - 1];
+  u64 all;
+  const u64 exc = group_scan<kRowThreads>(a + b, all, sh.scratch) + above, inc = exc + a + b;
+  const u64 need = need_of(all);
+  if (exc < need && need <= inc) {   // one thread
+    const bool first = need <= exc + a;
+    sh.digit = (uint32_t)(first ? top : top - 1);
+    sh.above = first ? exc : exc + a;
+  }
+  __syncthreads();
+  above = sh.above;
+  return sh.digit;
+}
+
+__device__ __forceinline__ void clear_bins(RowShared& sh) {
+  __syncthreads();
+  sh.hist[threadIdx.x] = 0;
+  sh.hist[threadIdx.x + kRowThreads] = 0;
+  __syncthreads();
+}
+
+// A row of V logits: every wave of the work-group owns a consecutive part of
+// it, so sums over waves are sums in index order.
+template <typename T>
+struct Row {
+  static constexpr int E = RowVec<T>::E;
+  const T* z;
+  int64_t V, begin, end;
+
+  __device__ __forceinline__ Row(const T* p, int64_t v) : z(p), V(v) {
+    const int64_t per = (v + kRowWaves * 64 * E - 1) / (kRowWaves * 64 * E) * (64 * E);
+    begin = (int64_t)(threadIdx.x >> 6) * per;
+    end = begin + per < v ? begin + per : v;
+  }
+
+  // f(index, value) over this thread's elements of its wave's part, four
+  // loads under way.
+  template <typename F> __device__ __forceinline__ void each(F f) const {
+    constexpr int kUnroll = 4;
+    for (int64_t c = begin + (threadIdx.x & 63) * E; c < end; c += 64 * E * kUnroll) {
+      typename RowVec<T>::type v[kUnroll];
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j)
+        if (c + j * 64 * E < end) v[j] = load_row(z, c + j * 64 * E, V);
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j)
+        if (c + j * 64 * E < end) {
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if (c + j * 64 * E + e < V) f(c + j * 64 * E + e, clean(to_f32(v[j][e])));
+        }
+    }
+  }
+
+  // The first index at which the running sum of f (u64, in index order)
+  // exceeds the target that `target_of` makes of the whole sum; `sum` gets
+  // that.  -1 if there is none.
+  template <typename F, typename G> __device__ __forceinline__ int64_t locate(F f, G target_of, u64& sum, RowShared& sh) const {
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    u64 s = 0;
+    each([&](int64_t i, float x) { s += f(i, x); });
+    s = wave_sum_u64(s);
+    __syncthreads();
+    if (lane == 0) sh.scratch.wsum[w] = s;
+    if (threadIdx.x == 0) sh.idx = -1;
+    __syncthreads();
+    u64 before = 0;
+    sum = 0;
+    for (int i = 0; i < kRowWaves; ++i) {
+      if (i < w) before += sh.scratch.wsum[i];
+      sum += sh.scratch.wsum[i];
+    }
+    const u64 target = target_of(sum);
+    if (before <= target && target < before + s) {   // one wave
+      for (int64_t b = begin; b < end; b += 64 * E) {
+        const int64_t c = b + lane * E;
+        u64 own[E], part = 0;
+        const typename RowVec<T>::type v = load_row(z, c, V);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          own[e] = c + e < V ? f(c + e, clean(to_f32(v[e]))) : 0;
+          part += own[e];
+        }
+        u64 all;
+        const u64 inc = wave_scan_u64(part, all);
+        if (target < before + all) {
+          u64 run = before + inc - part;
+          if (run <= target && target < run + part) {   // one lane
+            int64_t at = c;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+              run += own[e];
+              if (run <= target) at = c + e + 1;
+            }
+            sh.idx = at;
+          }
+          break;
+        }
+        before += all;
+      }
+    }
+    __syncthreads();
+    return sh.idx;
+  }
+
+  // The key K at which the sum of f over keys above K is below `need` and
+  // the sum with K reaches it; `above` receives the former.  `need_of` maps
+  // the sum over everything to `need` (1 <= need <= that sum).  One pass of
+  // 11 key bits after another, the passes after the first over the keys that
+  // share K's leading bits.
+  template <typename F, typename G> __device__ __forceinline__ uint32_t search(F f, G need_of, u64& above, RowShared& sh) const {
+    constexpr int low = sizeof(T) == 2 ? 16 : 0;   // a bf16 key's last 16 bits follow from its first
+    uint32_t prefix = 0;
+    u64 need = 0;
+    above = 0;
+    int hi = 32;
+    while (hi > low) {
+      const int bits = hi - low < 11 ? hi - low : 11, lo = hi - bits;
+      clear_bins(sh);
+      each([&](int64_t i, float x) {
+        const uint32_t k = key_of(x);
+        if (hi == 32 || (k >> hi) == prefix) {
+          const u64 w = f(i, x);
+          if (w) atomicAdd(&sh.hist[(k >> lo) & ((1u << bits) - 1)], w);
+        }
+      });
+      __syncthreads();
+      const uint32_t d = find_bin([&](u64 all) { return hi == 32 ? need = need_of(all) : need; }, above, sh);
+      prefix = (hi == 32 ? 0u : prefix << bits) | d;
+      hi = lo;
+    }
+    if (low == 0) return prefix;
+    return prefix << 16 | ((prefix & 0x8000u) ? 0u : 0xFFFFu);
+  }
+};
+
+// Kept by a filter: keys above `key`, and `key` itself up to index `idx`.
+struct Cut {
+  uint32_t key;
+  int64_t idx;
+  __device__ __forceinline__ bool keeps(int64_t i, uint32_t k) const { return k > key || (k == key && i <= idx); }
+};
+
+// The candidates of a row in LDS.
 template <typename T>
 struct Candidates {
   static constexpr int low = sizeof(T) == 2 ? 16 : 0;
   PickShared& sh;
-  uint32_t kmin;     // lower bound of the keys, without their last `low` bits
-  int ib;            // bits of an index
-  int bits;          // bits of a composite
   int n;
-
-  __device__ __forceinline__ u64 pack(uint32_t key, int64_t i) const {
-    return (u64)((key >> low) - kmin) << ib | (((u64)1 << ib) - 1 - (u64)i);
-  }
-  __device__ __forceinline__ int64_t index(u64 c) const { return (int64_t)(((u64)1 << ib) - 1 - (c & (((u64)1 << ib) - 1))); }
-  __device__ __forceinline__ uint32_t key(u64 c) const {
-    const uint32_t k = (uint32_t)(c >> ib) + kmin;
-    if (low == 0) return k;
-    return k << 16 | ((k & 0x8000u) ? 0u : 0xFFFFu);
-  }
-  __device__ __forceinline__ float value(u64 c) const { return value_of(key(c)); }
+  uint32_t kmin;   // of the listed keys, without their last `low` bits
+  int ib, bits;    // bits of an index, and of a packed composite
 
   template <typename F> __device__ __forceinline__ void each(F f) const {
     for (int i = threadIdx.x; i < n; i += kRowThreads) f(sh.list[i]);
   }
 
+  // Packs composites into as few bits as the listed keys and the row's
+  // indices need.
+  __device__ __forceinline__ void measure(int64_t V) {
+    uint32_t lo = 0xFFFFFFFFu, hi = 0;
+    each([&](u64 c) {
+      const uint32_t k = key_in(c) >> low;
+      lo = k < lo ? k : lo;
+      hi = k > hi ? k : hi;
+    });
+    lo = ~wave_max_u32(~lo);
+    hi = wave_max_u32(hi);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) sh.row.scratch.wsum[threadIdx.x >> 6] = (u64)hi << 32 | lo;
+    __syncthreads();
+    for (int i = 0; i < kRowWaves; ++i) {
+      const u64 v = sh.row.scratch.wsum[i];
+      lo = (uint32_t)v < lo ? (uint32_t)v : lo;
+      hi = (uint32_t)(v >> 32) > hi ? (uint32_t)(v >> 32) : hi;
+    }
+    kmin = lo;
+    ib = bits_of((u64)V);
+    bits = bits_of(hi - lo) + ib;
+  }
+  __device__ __forceinline__ u64 mask() const { return ((u64)1 << ib) - 1; }
+  __device__ __forceinline__ u64 pack(u64 c) const {
+    return (u64)((key_in(c) >> low) - kmin) << ib | (mask() - (u64)index_in(c));
+  }
+  __device__ __forceinline__ u64 unpack(u64 p) const {
+    uint32_t k = (uint32_t)(p >> ib) + kmin;
+    if (low) k = k << 16 | ((k & 0x8000u) ? 0u : 0xFFFFu);
+    return composite(k, (int64_t)(mask() - (p & mask())));
+  }
+
   // The value X of `part` (`width` bits) at which the sum of f over
   // candidates with a larger part is below `need` and the sum with X reaches
   // it; 11 bits per pass.
-  template <typename P, typename F> __device__ u64 search(P part, int width, F f, u64 need) const {
+  template <typename P, typename F> __device__ __forceinline__ u64 search(P part, int width, F f, u64 need) const {
     RowShared& r = sh.row;
-    u64 prefix = 0, over = 0;
-    int hi = width;
-    while (hi > 0) {
+    u64 prefix = 0, above = 0;
+    for (int hi = width; hi > 0;) {
       const int b = hi < 11 ? hi : 11, lo = hi - b;
-      __syncthreads();
-      r.hist[threadIdx.x] = 0;
-      r.hist[threadIdx.x + kRowThreads] = 0;
-      __syncthreads();
+      clear_bins(r);
       each([&](u64 c) {
         const u64 x = part(c);
         if (x >> hi == prefix) {
@@ -467,72 +777,83 @@ struct Candidates {
         }
       });
       __syncthreads();
-      const int top = kBins - 1 - 2 * threadIdx.x;
-      const u64 u = r.hist[top], v = r.hist[top - 1];
-      u64 inc = wave_scan_u64(u + v);
-      if ((threadIdx.x & 63) == 63) r.wsum[threadIdx.x >> 6] = inc;
-      __syncthreads();
-      for (int i = 0; i < (int)(threadIdx.x >> 6); ++i) inc += r.wsum[i];
-      inc += over;
-      const u64 exc = inc - u - v;
-      if (exc < need && need <= inc) {   // one thread
-        const bool first = need <= exc + u;
-        r.digit = (uint32_t)(first ? top : top - 1);
-        r.above = first ? exc : exc + u;
-      }
-      __syncthreads();
-      prefix = prefix << b | r.digit;
-      over = r.above;
+      prefix = prefix << b | find_bin([=](u64) { return need; }, above, r);
       hi = lo;
     }
-    __syncthreads();
     return prefix;
   }
 
   // Collects the logits that `take(key, value)` accepts out of the groups
   // whose maximum `group(key)` accepts; false if they overflow the list.
   template <typename G, typename F>
-  __device__ bool collect(const T* z, int64_t V, const uint32_t* gmax, G group, F take) {
-    constexpr int E = RowVec<T>::E, kUnroll = 4;
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  __device__ __forceinline__ bool collect(const T* z, int64_t V, const uint32_t* gmax, G group, F take) {
+    constexpr int E = RowVec<T>::E, kLanes = kGroup / E, kPass = kRowThreads / kLanes, kUnroll = 4;
+    const int t = threadIdx.x, lane = t & 63;
+    const int groups = (int)((V + kGroup - 1) / kGroup);
     __syncthreads();
-    if (threadIdx.x == 0) sh.count = 0;
-    __syncthreads();
-    const int64_t stride = (int64_t)kRowThreads * E;
-    for (int64_t b = (int64_t)w * 64 * E; b < V; b += stride * kUnroll) {
-      bool live[kUnroll];
-      typename RowVec<T>::type v[kUnroll];
+    if (t == 0) sh.count = 0;
+    for (int g0 = 0; g0 < groups; g0 += kGroupBatch) {
+      // the accepted groups of a batch, in any order
+      __syncthreads();
+      if (t == 0) sh.groups = 0;
+      __syncthreads();
+      bool live[kGroupBatch / kRowThreads];
+      u64 hit[kGroupBatch / kRowThreads];
+      int total = 0;
 #pragma unroll
-      for (int j = 0; j < kUnroll; ++j) {
-        const int64_t c = b + j * stride + lane * E;
-        live[j] = c < V && (!gmax || group(gmax[c / kGroup]));
+      for (int j = 0; j < kGroupBatch / kRowThreads; ++j) {
+        const int g = g0 + j * kRowThreads + t;
+        live[j] = g < groups && group(gmax[g]);
       }
 #pragma unroll
-      for (int j = 0; j < kUnroll; ++j)
-        if (live[j]) v[j] = load_row(z, b + j * stride + lane * E, V);
-#pragma unroll
-      for (int j = 0; j < kUnroll; ++j) {
-        if (!__builtin_amdgcn_ballot_w64(live[j])) continue;
-        const int64_t c = b + j * stride + lane * E;
-        uint32_t k[E];
-        u64 hit[E];
-        int total = 0;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float x = live[j] && c + e < V ? clean(to_f32(v[j][e])) : kNegInf;
-          k[e] = key_of(x);
-          hit[e] = __builtin_amdgcn_ballot_w64(live[j] && c + e < V && take(k[e], x));
-          total += __builtin_popcountll(hit[e]);
-        }
-        if (!total) continue;
+      for (int j = 0; j < kGroupBatch / kRowThreads; ++j) {
+        hit[j] = __builtin_amdgcn_ballot_w64(live[j]);
+        total += __builtin_popcountll(hit[j]);
+      }
+      if (total) {
         int at = 0;
-        if (lane == 0) at = atomicAdd(&sh.count, total);
+        if (lane == 0) at = atomicAdd(&sh.groups, total);
         at = __builtin_amdgcn_readfirstlane(at);
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const int pos = at + __builtin_amdgcn_mbcnt_hi((uint32_t)(hit[e] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)hit[e], 0));
-          if ((hit[e] >> lane & 1) && pos < kList) sh.list[pos] = pack(k[e], c + e);
-          at += __builtin_popcountll(hit[e]);
+        for (int j = 0; j < kGroupBatch / kRowThreads; ++j) {
+          if (live[j]) sh.glist[at + lane_rank(hit[j])] = (uint16_t)(j * kRowThreads + t);
+          at += __builtin_popcountll(hit[j]);
+        }
+      }
+      __syncthreads();
+      const int ng = sh.groups;
+      for (int i0 = 0; i0 < ng; i0 += kPass * kUnroll) {
+        typename RowVec<T>::type v[kUnroll];
+        int64_t c[kUnroll];
+#pragma unroll
+        for (int j = 0; j < kUnroll; ++j) {
+          const int i = i0 + j * kPass + t / kLanes;
+          c[j] = i < ng ? (int64_t)(g0 + sh.glist[i]) * kGroup + (t % kLanes) * E : V;
+          if (c[j] < V) v[j] = load_row(z, c[j], V, kNegInf);
+        }
+#pragma unroll
+        for (int j = 0; j < kUnroll; ++j) {
+          if (!__builtin_amdgcn_ballot_w64(c[j] < V)) break;
+          uint32_t k[E];
+          u64 ok[E];
+          int n_ok = 0;
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const float x = c[j] + e < V ? clean(to_f32(v[j][e])) : kNegInf;
+            k[e] = key_of(x);
+            ok[e] = __builtin_amdgcn_ballot_w64(c[j] + e < V && take(k[e], x));
+            n_ok += __builtin_popcountll(ok[e]);
+          }
+          if (!n_ok) continue;
+          int at = 0;
+          if (lane == 0) at = atomicAdd(&sh.count, n_ok);
+          at = __builtin_amdgcn_readfirstlane(at);
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const int pos = at + lane_rank(ok[e]);
+            if ((ok[e] >> lane & 1) && pos < kList) sh.list[pos] = composite(k[e], c[j] + e);
+            at += __builtin_popcountll(ok[e]);
+          }
         }
       }
     }
@@ -546,43 +867,34 @@ struct Candidates {
 // (in index order) exceeds `target`; a target at or past the piece's sum is
 // taken as its last counted element.  -1 if the piece counts nothing.
 template <typename T, typename F>
-__device__ int64_t locate_in_piece(const T* z, int64_t V, int64_t base, F f, u64 target, PickShared& sh) {
+__device__ __forceinline__ int64_t locate_in_piece(const T* z, int64_t V, int64_t base, F f, u64 target, RowShared& sh) {
   constexpr int E = RowVec<T>::E, kVec = kPiece / (kRowThreads * E);
   const int64_t c = base + (int64_t)threadIdx.x * E * kVec;
-  u64 own[kVec * E], sum = 0;
+  u64 own[kVec * E], part = 0;
 #pragma unroll
   for (int j = 0; j < kVec; ++j) {
     const typename RowVec<T>::type v = load_row(z, c + j * E, V, kNegInf);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       own[j * E + e] = c + j * E + e < V ? f(c + j * E + e, clean(to_f32(v[e]))) : 0;
-      sum += own[j * E + e];
+      part += own[j * E + e];
     }
   }
-  const u64 inc = wave_scan_u64(sum);
-  const int w = threadIdx.x >> 6;
-  __syncthreads();
-  if ((threadIdx.x & 63) == 63) sh.usum[w] = inc;
-  __syncthreads();
-  u64 before = 0, all = 0;
-  for (int i = 0; i < kRowWaves; ++i) {
-    if (i < w) before += sh.usum[i];
-    all += sh.usum[i];
-  }
+  u64 all;
+  u64 run = group_scan<kRowThreads>(part, all, sh.scratch);
   if (all == 0) return -1;
   if (target >= all) target = all - 1;
-  u64 run = before + inc - sum;
-  if (run <= target && target < run + sum) {   // one thread
+  if (run <= target && target < run + part) {   // one thread
     int64_t at = c;
 #pragma unroll
     for (int e = 0; e < kVec * E; ++e) {
       run += own[e];
       if (run <= target) at = c + e + 1;
     }
-    sh.row.idx = at;
+    sh.idx = at;
   }
   __syncthreads();
-  return sh.row.idx;
+  return sh.idx;
 }
 
 // sh.factor[i] = weight of piece i's maximum (0 where the piece is masked).
@@ -595,332 +907,316 @@ __device__ __forceinline__ void piece_factors(const SampleArgs& a, int64_t row_i
   __syncthreads();
 }
 
-// Top-k, min-p, or any filter on a row of one piece: the candidates in a
-// list.  False if they overflow it.
+// An integer weight relative to a piece's maximum, relative to the row's.
+__device__ __forceinline__ u64 rescale(u64 h, double factor) {
+  return factor == 1.0 ? h : (u64)((double)h * factor + 0.5);
+}
+__device__ __forceinline__ u64 piece_weight(double psum, double factor, double scale) {
+  return (u64)(psum * factor * scale + 0.5);
+}
+
+// The listed candidates (which hold every token at least as likely as the
+// least of them): sorted, or searched where they are too many for that.
 template <typename T>
-__device__ bool pick_from_list(const SampleArgs& a, const T* z, int64_t row_i, const RowParams& r, uint32_t km,
-                               double scale, Mode mode, const uint32_t* gmax, PickShared& sh, int64_t& tok,
-                               double& total) {
-  constexpr int low = sizeof(T) == 2 ? 16 : 0;
-  const int ib = bits_of((u64)a.V);
+__device__ __forceinline__ void pick_from_list(const SampleArgs& a, int64_t row_i, Candidates<T>& list, const RowParams& r, bool top_k,
+                               u64 row_sum, PickShared& sh) {
+  top_k = top_k && r.k < list.n;
+  if (list.n <= 64) {   // one wave, without barriers
+    if (threadIdx.x < 64) {
+      const u64 c = (int)threadIdx.x < list.n ? sh.list[threadIdx.x] : 0;
+      group_sync<64>();
+      pick_sorted<64>(a, row_i, c, list.n, r, top_k, row_sum, sh.sort1);
+    }
+    return;
+  }
+  if (list.n <= kSmall) {
+    const u64 c = (int)threadIdx.x < list.n ? sh.list[threadIdx.x] : 0;
+    __syncthreads();   // the sort takes the list's place
+    pick_sorted<kRowThreads>(a, row_i, c, list.n, r, top_k, row_sum, sh.sort);
+    return;
+  }
+  const double scale = scale_of(a);
+  list.measure(a.V);
+  auto wt = [&](u64 c) { return weight(value_in(c), r); };
+  auto pack = [&](u64 c) { return list.pack(c); };
+  u64 cut = 0;   // composites from here on are kept
+  if (top_k) cut = list.unpack(list.search(pack, list.bits, [](u64) { return (u64)1; }, (u64)r.k));
+  if (r.p < 1.0) {
+    auto f = [&](u64 c) { return c >= cut ? fixed(wt(c), scale) : 0; };
+    u64 s = 0;
+    list.each([&](u64 c) { s += f(c); });
+    s = group_sum(s, sh.row);
+    const u64 need = share(r.p, row_sum ? row_sum : s);
+    if (need <= s) {   // else the share reaches below the list
+      const u64 c = list.unpack(list.search(pack, list.bits, f, need));
+      cut = c > cut ? c : cut;
+    }
+  }
+  const u64 least = floor_weight(r, scale);
+  auto mass = [&](u64 c) {
+    const u64 w = c >= cut ? fixed(wt(c), scale) : 0;
+    return w >= least ? w : (u64)0;
+  };
+  u64 s = 0;
+  list.each([&](u64 c) { s += mass(c); });
+  s = group_sum(s, sh.row);
+  // in index order: the larger its complement, the earlier an index
+  const u64 at = list.search([&](u64 c) { return list.mask() - (u64)index_in(c); }, list.ib, mass,
+                             draw_target(r.u, s) + 1);
+  const int64_t tok = (int64_t)(list.mask() - at);
+  if (threadIdx.x == 0)
+    emit(a, row_i, tok, clean(to_f32(static_cast<const T*>(a.z)[row_i * a.ld + tok])), r, (double)s / scale);
+}
+
+// Top-k or min-p: false if the candidates overflow the list.
+template <typename T>
+__device__ __forceinline__ bool pick_bounded(const SampleArgs& a, const T* z, int64_t row_i, const RowParams& r, uint32_t km, Mode mode,
+                             PickShared& sh) {
+  const uint32_t* gmax = a.gmax + row_i * a.pieces * kPieceGroups;
   uint32_t bound = kKeyNegInf + 1;   // candidates' keys from here on
-  if (gmax && mode == kTopK) {
-    // the k-th largest group maximum, to the first 11 bits of its key
-    const int groups = a.pieces * kPieceGroups;
-    if (r.k > groups - groups / 8) return false;
-    RowShared& s = sh.row;
-    __syncthreads();
-    s.hist[threadIdx.x] = 0;
-    s.hist[threadIdx.x + kRowThreads] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < groups; i += kRowThreads) atomicAdd(&s.hist[gmax[i] >> 21], (u64)1);
-    __syncthreads();
-    const int top = kBins - 1 - 2 * threadIdx.x;
-    const u64 u = s.hist[top], v = s.hist[top - 1];
-    u64 inc = wave_scan_u64(u + v);
-    if ((threadIdx.x & 63) == 63) s.wsum[threadIdx.x >> 6] = inc;
-    __syncthreads();
-    for (int i = 0; i < (int)(threadIdx.x >> 6); ++i) inc += s.wsum[i];
-    const u64 exc = inc - u - v, k = (u64)r.k;
-    if (exc < k && k <= inc) s.digit = (uint32_t)(k <= exc + u ? top : top - 1);
-    __syncthreads();
-    const uint32_t b = s.digit << 21;
-    bound = b > bound ? b : bound;
-  } else if (gmax) {
+  u64 row_sum = 0;
+  if (mode == kTopK) {
+    // the k-th largest group maximum, by its key's distance from the row's:
+    // in steps of 2^13 (a thousandth of a binade) over two binades, or to the
+    // first 11 bits.  With as many tokens wanted as there are groups, all of
+    // the row may be listed.
+    const int groups = (int)((a.V + kGroup - 1) / kGroup);
+    if (r.k <= groups) {
+      uint32_t* bins = reinterpret_cast<uint32_t*>(sh.row.hist);
+      for (int step = 13; step <= 21; step += 8) {
+        clear_bins(sh.row);
+        for (int i = threadIdx.x; i < groups; i += kRowThreads) {
+          const uint32_t d = (km - gmax[i]) >> step;
+          atomicAdd(&bins[d < kBins - 1 ? d : kBins - 1], 1u);
+        }
+        __syncthreads();
+        u64 all;
+        const uint32_t x = bins[2 * threadIdx.x], y = bins[2 * threadIdx.x + 1];
+        const u64 exc = group_scan<kRowThreads>(x + y, all, sh.row.scratch);
+        if (exc < (u64)r.k && (u64)r.k <= exc + x + y)   // one thread
+          sh.found = 2 * threadIdx.x + ((u64)r.k <= exc + x ? 0 : 1);
+        __syncthreads();
+        const uint32_t d = (uint32_t)sh.found;
+        if (d == kBins - 1) continue;   // further down: coarser steps
+        const uint32_t reach = ((d + 1) << step) - 1;
+        if (km - (kKeyNegInf + 1) > reach) bound = km - reach;
+        break;
+      }
+    }
+  } else {
     // w >= q: a little below max + t ln q in fp32, the exact test follows
     const double zq = r.zmax + r.t * log(r.q);
     const float x = (float)(zq - 1e-6 * (__builtin_fabs(zq) + __builtin_fabs(r.zmax)));
     const uint32_t b = key_of(clean(x));
     bound = b > bound ? b : bound;
+    if (r.p < 1.0) {
+      piece_factors(a, row_i, r, sh);
+      const double scale = scale_of(a);
+      for (int i = 0; i < a.pieces; ++i)
+        row_sum += piece_weight(a.psum[row_i * a.pieces + i], sh.factor[i], scale);
+    }
   }
-  Candidates<T> list{sh, bound >> low, ib, 0, 0};
-  list.bits = bits_of((km >> low) - list.kmin) + ib;
+  Candidates<T> list{sh, 0, 0, 0, 0};
   if (!list.collect(z, a.V, gmax, [=](uint32_t k) { return k >= bound; },
                     [=](uint32_t k, float) { return k >= bound; }))
     return false;
-  auto wt = [&](u64 c) { return weight(list.value(c), r); };
-  auto self = [](u64 c) { return c; };
-  u64 cut = 0;
-  if (mode == kTopK && (u64)r.k < (u64)list.n)
-    cut = list.search(self, list.bits, [](u64) { return (u64)1; }, (u64)r.k);
-  if (r.p < 1.0) {
-    u64 s = 0;
-    list.each([&](u64 c) { s += c >= cut ? fixed(wt(c), scale) : 0; });
-    s = group_sum_u64(s, sh);
-    // the weight that p is a share of: the top-k's, or the whole row's
-    double all = (double)s;
-    if (mode == kMinP && gmax) {
-      piece_factors(a, row_i, r, sh);
-      all = 0.0;
-      for (int i = 0; i < a.pieces; ++i) all += a.psum[row_i * a.pieces + i] * sh.factor[i];
-      all *= scale;
-    }
-    u64 need = (u64)ceil(r.p * all);
-    if (need < 1) need = 1;
-    if (need < s || (need == s && !(mode == kMinP && gmax))) {
-      const u64 c2 = list.search(self, list.bits, [&](u64 c) { return c >= cut ? fixed(wt(c), scale) : 0; }, need);
-      cut = c2 > cut ? c2 : cut;
-    }
-  }
-  auto mass = [&](u64 c) {
-    if (c < cut) return (u64)0;
-    const double w = wt(c);
-    return w >= r.q ? fixed(w, scale) : (u64)0;
-  };
-  u64 s = 0;
-  list.each([&](u64 c) { s += mass(c); });
-  s = group_sum_u64(s, sh);
-  u64 target = (u64)((double)r.u * (double)s);
-  if (target >= s) target = s - 1;
-  // in index order: the larger its complement, the earlier an index
-  const u64 mask = ((u64)1 << ib) - 1;
-  const u64 at = list.search([=](u64 c) { return c & mask; }, ib, mass, target + 1);
-  tok = (int64_t)(mask - at);
-  total = (double)s / scale;
+  pick_from_list(a, row_i, list, r, mode == kTopK, row_sum, sh);
   return true;
 }
 
-// No filter, or top-p alone on a long row: the pieces' weights above the cut,
-// then the piece that holds the answer.  False if the cut lies below the bins
-// or its bin overflows the list.
+// No filter, or top-p alone: the pieces' weights above the cut, then the
+// piece that holds the answer; a short list where the kept set is small.
+// False if the cut lies below the bins or its bin overflows the list.
 template <typename T>
-__device__ bool pick_by_pieces(const SampleArgs& a, const T* z, int64_t row_i, const RowParams& r, uint32_t km,
-                               double scale, Mode mode, PickShared& sh, int64_t& tok, double& total) {
-  constexpr int low = sizeof(T) == 2 ? 16 : 0;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+__device__ __forceinline__ bool pick_by_pieces(const SampleArgs& a, const T* z, int64_t row_i, const RowParams& r, uint32_t km,
+                               Mode mode, PickShared& sh) {
+  const double scale = scale_of(a);
   const uint32_t* pmax = a.pmax + row_i * a.pieces;
-  const double* psum = a.psum + row_i * a.pieces;
   Cut cut{0u, a.V};
-  auto mass = [&](int64_t i, float x) { return cut.keeps(i, key_of(x)) ? fixed(weight(x, r), scale) : (u64)0; };
-  if (a.pieces == 1) {   // no scan ran: the row is the piece
-    u64 s = 0;
-    for (int64_t c = threadIdx.x; c < a.V; c += kRowThreads) s += mass(c, clean(to_f32(z[c])));
-    s = group_sum_u64(s, sh);
-    tok = locate_in_piece(z, a.V, 0, mass, (u64)((double)r.u * (double)s), sh);
-    total = (double)s / scale;
-    return true;
-  }
   piece_factors(a, row_i, r, sh);
-  int border = 0;
-  const float alpha = bin_scale(r);
-  const int top = bin_of(value_of(km), alpha);
-  const u64* hist = a.hist + row_i * a.pieces * kSlots;
   if (mode == kTopP) {
-    double all = 0.0;
-    for (int i = 0; i < a.pieces; ++i) all += psum[i] * sh.factor[i];
-    // the row's bins: slot j of piece i is bin (top - its top) + j
-    if (threadIdx.x < kSlots) {
-      double s = 0.0;
-      if (threadIdx.x < kSlots - 1)
-        for (int i = 0; i < a.pieces; ++i) {
-          if (pmax[i] <= kKeyNegInf) continue;
-          const int64_t j = (int64_t)threadIdx.x - ((int64_t)top - bin_of(value_of(pmax[i]), alpha));
-          if (j >= 0) s += (double)hist[i * kSlots + j] / scale * sh.factor[i];
-        }
-      sh.slot[threadIdx.x] = s;
-    }
-    __syncthreads();
-    const double need = r.p * all;
-    if (threadIdx.x == 0) {
-      double run = 0.0;
-      int b = 0;
-      for (; b < kSlots - 1; ++b) {
-        if (run + sh.slot[b] >= need) break;
-        run += sh.slot[b];
+    const float alpha = bin_scale(r), top = bin_of(value_of(km), alpha);
+    if (!(__builtin_fabsf(top) < kBinLimit)) return false;
+    const uint32_t* gmax = a.gmax + row_i * a.pieces * kPieceGroups;
+    // f(piece, row's bin, weight) over the pieces' bins; slot j of a piece is
+    // the row's bin j + (row's top - piece's top), kSlots - 1 is the rest
+    auto each_slot = [&](auto f) {
+      const int j = threadIdx.x % kSlots;
+#pragma unroll 4
+      for (int i = threadIdx.x / kSlots; i < a.pieces; i += kRowThreads / kSlots) {
+        const u64 h = a.hist[(row_i * a.pieces + i) * kSlots + j];
+        const float d = (float)j + (top - bin_of(value_of(pmax[i]), alpha));
+        const int slot = j < kSlots - 1 ? (int)__builtin_fminf(d, (float)(kSlots - 1)) : kSlots - 1;
+        f(i, slot, rescale(h, sh.factor[i]));
       }
-      sh.found = b;
-      sh.dsum[0] = run;
+    };
+    for (int i = threadIdx.x; i < kSlots; i += kRowThreads) sh.slot[i] = 0;
+    __syncthreads();
+    each_slot([&](int, int slot, u64 w) {
+      if (w) atomicAdd(&sh.slot[slot], w);
+    });
+    __syncthreads();
+    // the bin at which the sum from above reaches p of the whole
+    u64 all;
+    const int t = threadIdx.x;
+    const u64 own = t < kSlots ? sh.slot[t] : 0;
+    const u64 exc = group_scan<kRowThreads>(own, all, sh.row.scratch);
+    const u64 need = share(r.p, all);
+    if (exc < need && need <= exc + own) {   // one thread
+      sh.found = t;
+      sh.sum = exc;
     }
     __syncthreads();
-    border = sh.found;
-    const double above = sh.dsum[0];
+    const int border = sh.found;
+    const u64 above = sh.sum;
     if (border == kSlots - 1) return false;
-    Candidates<T> list{sh, 0, bits_of((u64)a.V), 0, 0};
-    list.kmin = 0;
-    list.bits = 32 - low + list.ib;
-    const int64_t bin = (int64_t)top - border;
-    if (!list.collect(z, a.V, a.gmax + row_i * a.pieces * kPieceGroups,
-                      [=](uint32_t k) { return bin_of(value_of(k), alpha) >= bin; },
-                      [=](uint32_t, float x) { return bin_of(x, alpha) == bin; }))
-      return false;
-    auto wt = [&](u64 c) { return fixed(weight(list.value(c), r), scale); };
+    const float bin = top - (float)border;
+    auto group = [=](uint32_t k) { return bin_of(value_of(k), alpha) >= bin; };
+    Candidates<T> list{sh, 0, 0, 0, 0};
+    // every logit above the border bin weighs at least what its upper edge
+    // does: few of them make a short list together with the bin
+    const double edge = weight((bin + 1.0f) / alpha, r) * 0.99;
+    if ((double)above <= edge * scale * kSmall &&
+        list.collect(z, a.V, gmax, group, [=](uint32_t, float x) { return bin_of(x, alpha) >= bin; })) {
+      pick_from_list(a, row_i, list, r, false, all, sh);
+      return true;
+    }
+    if (!list.collect(z, a.V, gmax, group, [=](uint32_t, float x) { return bin_of(x, alpha) == bin; })) return false;
+    auto wt = [&](u64 c) { return fixed(weight(value_in(c), r), scale); };
     u64 s = 0;
     list.each([&](u64 c) { s += wt(c); });
-    s = group_sum_u64(s, sh);
+    s = group_sum(s, sh.row);
     if (s == 0) return false;
-    const double rest = ceil((need - above) * scale);
-    u64 n = rest < 1.0 ? 1 : (u64)rest;
-    if (n > s) n = s;
-    const u64 c = list.search([](u64 x) { return x; }, list.bits, wt, n);
-    cut = Cut{list.key(c), list.index(c)};
-    // the kept part of the border bin, by pieces
-    __syncthreads();
+    const u64 rest = need - above;
+    list.measure(a.V);
+    const u64 c =
+        list.unpack(list.search([&](u64 x) { return list.pack(x); }, list.bits, wt, rest < s ? rest : s));
+    cut = Cut{key_in(c), index_in(c)};
+    // the kept weight by pieces
     for (int i = threadIdx.x; i < a.pieces; i += kRowThreads) sh.cmass[i] = 0;
     __syncthreads();
     list.each([&](u64 x) {
-      if (x >= c) atomicAdd(&sh.cmass[list.index(x) / kPiece], wt(x));
+      if (x >= c) atomicAdd(&sh.cmass[index_in(x) / kPiece], wt(x));
     });
-    __syncthreads();
-    for (int i = w; i < a.pieces; i += kRowWaves) {
-      const double f = sh.factor[i];
-      double s2 = 0.0;
-      if (f != 0.0) {
-        const int64_t shift = (int64_t)top - bin_of(value_of(pmax[i]), alpha);
-        for (int j = lane; j < kSlots - 1; j += 64)
-          if (shift + j < border) s2 += (double)hist[i * kSlots + j];
-      }
-      s2 = wave_sum_f64(s2);
-      if (lane == 0) sh.dmass[i] = ((double)sh.cmass[i] + s2 * f) / scale;
-    }
+    each_slot([&](int i, int slot, u64 w) {
+      if (slot < border && w) atomicAdd(&sh.cmass[i], w);
+    });
   } else {
-    for (int i = threadIdx.x; i < a.pieces; i += kRowThreads) sh.dmass[i] = psum[i] * sh.factor[i];
+    for (int i = threadIdx.x; i < a.pieces; i += kRowThreads)
+      sh.cmass[i] = piece_weight(a.psum[row_i * a.pieces + i], sh.factor[i], scale);
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    double s = 0.0;
-    for (int i = 0; i < a.pieces; ++i) s += sh.dmass[i];
-    const double target = (double)r.u * s;
-    double run = 0.0;
-    int at = -1, last = 0;
-    for (int i = 0; i < a.pieces; ++i) {
-      if (sh.dmass[i] > 0.0) last = i;
-      if (at < 0) {
-        if (run + sh.dmass[i] > target) at = i;
-        else run += sh.dmass[i];
-      }
-    }
-    if (at < 0) {   // rounding at the very end: the last counted element
-      at = last;
-      run = 0.0;
-      sh.dsum[1] = s;
-    } else {
-      sh.dsum[1] = target - run;
-    }
-    sh.dsum[0] = s;
-    sh.found = at;
+  const int i2 = 2 * threadIdx.x;
+  const u64 m0 = i2 < a.pieces ? sh.cmass[i2] : 0, m1 = i2 + 1 < a.pieces ? sh.cmass[i2 + 1] : 0;
+  u64 sum;
+  const u64 exc = group_scan<kRowThreads>(m0 + m1, sum, sh.row.scratch);
+  u64 target = draw_target(r.u, sum);
+  if (exc <= target && target < exc + m0 + m1) {   // one thread
+    const bool first = target < exc + m0;
+    sh.found = first ? i2 : i2 + 1;
+    sh.sum = target - (first ? exc : exc + m0);
   }
   __syncthreads();
-  total = sh.dsum[0];
-  u64 target = (u64)(sh.dsum[1] * scale);
-  tok = -1;
-  // a piece whose weights all round to nothing passes on to the next
+  target = sh.sum;
+  int64_t tok = -1;
+  auto mass = [&](int64_t i, float x) { return cut.keeps(i, key_of(x)) ? fixed(weight(x, r), scale) : (u64)0; };
+  // (a piece whose logits all round to nothing passes on to the next)
   for (int i = sh.found; i < a.pieces && tok < 0; ++i, target = 0)
-    tok = locate_in_piece(z, a.V, (int64_t)i * kPiece, mass, target, sh);
-  return tok >= 0;
+    tok = locate_in_piece(z, a.V, (int64_t)i * kPiece, mass, target, sh.row);
+  if (tok < 0) return false;
+  if (threadIdx.x == 0) emit(a, row_i, tok, clean(to_f32(z[tok])), r, (double)sum / scale);
+  return true;
+}
+
+// Any parameters, by passes over the whole row.  A function of its own, with
+// its arguments by value: inlined or by reference it would put what the
+// common paths hold in registers on the stack.
+template <typename T>
+__device__ __attribute__((noinline)) void pick_whole_row(SampleArgs a, const T* z, int64_t row_i, RowParams r,
+                                                         RowShared& sh) {
+  const Row<T> row(z, a.V);
+  const double scale = scale_of(a);
+  Cut cut{0u, a.V};
+  // the ties at the border go to the lowest indices
+  auto tie_index = [&](uint32_t key, u64 count) {
+    u64 n;
+    const int64_t i = row.locate([&](int64_t, float x) { return (u64)(key_of(x) == key); },
+                                 [=](u64) { return count - 1; }, n, sh);
+    return i < 0 ? a.V : i;
+  };
+  if (r.k > 0 && r.k < a.V) {
+    const u64 k = (u64)r.k;
+    u64 above;
+    cut.key = row.search([](int64_t, float) { return (u64)1; }, [=](u64) { return k; }, above, sh);
+    cut.idx = tie_index(cut.key, k - above);
+  }
+  if (r.p < 1.0) {
+    u64 above, need = 0;
+    const Cut in = cut;
+    const uint32_t key =
+        row.search([&](int64_t i, float x) { return in.keeps(i, key_of(x)) ? fixed(weight(x, r), scale) : 0; },
+                   [&](u64 all) { return need = share(r.p, all); }, above, sh);
+    const u64 each = fixed(weight(value_of(key), r), scale);
+    const int64_t i = tie_index(key, (need - above + each - 1) / each);
+    cut.idx = key == cut.key && cut.idx < i ? cut.idx : i;
+    cut.key = key;
+  }
+  const u64 least = floor_weight(r, scale);
+  u64 sum;
+  const int64_t tok = row.locate(
+      [&](int64_t i, float x) {
+        const u64 w = cut.keeps(i, key_of(x)) ? fixed(weight(x, r), scale) : 0;
+        return w >= least ? w : (u64)0;
+      },
+      [&](u64 s) { return draw_target(r.u, s); }, sum, sh);
+  if (threadIdx.x == 0) emit(a, row_i, tok, clean(to_f32(z[tok])), r, (double)sum / scale);
 }
 
 // One row per work-group.
 template <typename T>
 __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleArgs a) {
-  __shared__ PickShared ps;
-  RowShared& sh = ps.row;
+  __shared__ PickShared sh;
   const int64_t row_i = blockIdx.x;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   RowParams r = row_params(a, row_i);
-  const Row<T> row(static_cast<const T*>(a.z) + row_i * a.ld, a.V);
-
+  const T* z = static_cast<const T*>(a.z) + row_i * a.ld;
   const uint32_t* pmax = a.pmax + row_i * a.pieces;
-  const uint32_t* gmax = a.pieces > 1 ? a.gmax + row_i * a.pieces * kPieceGroups : nullptr;
   uint32_t km = 0;
-  if (a.pieces > 1) {
-    for (int i = threadIdx.x; i < a.pieces; i += kRowThreads) km = pmax[i] > km ? pmax[i] : km;
-  } else {
-    row.each([&](int64_t, float x) {
-      const uint32_t k = key_of(x);
-      km = k > km ? k : km;
-    });
-  }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const uint32_t y = __shfl_xor(km, o);
-    km = y > km ? y : km;
-  }
-  if (lane == 0) sh.kmax[w] = km;
+  for (int i = threadIdx.x; i < a.pieces; i += kRowThreads) km = pmax[i] > km ? pmax[i] : km;
+  km = wave_max_u32(km);
+  if ((threadIdx.x & 63) == 0) sh.row.kmax[threadIdx.x >> 6] = km;
+  if (threadIdx.x == 0) sh.found = a.pieces;
   __syncthreads();
-  km = 0;
-  for (int i = 0; i < kRowWaves; ++i) km = sh.kmax[i] > km ? sh.kmax[i] : km;
+  for (int i = 0; i < kRowWaves; ++i) km = sh.row.kmax[i] > km ? sh.row.kmax[i] : km;
+  if (!r.ok || km <= kKeyNegInf) {
+    if (threadIdx.x == 0) emit_none(a, row_i);
+    return;
+  }
+  r.set_max(value_of(km));
+  const Mode mode = mode_of(r, a.V);
+  bool done;
+  if (mode == kGreedy) {
+    // the first piece that holds the maximum, then the first index in it
+    for (int i = threadIdx.x; i < a.pieces; i += kRowThreads)
+      if (pmax[i] == km) atomicMin(&sh.found, i);
+    __syncthreads();
+    const int64_t tok = locate_in_piece(z, a.V, (int64_t)sh.found * kPiece,
+                                        [&](int64_t, float x) { return (u64)(key_of(x) == km); }, 0, sh.row);
+    if (threadIdx.x == 0) emit(a, row_i, tok, value_of(km), r, 1.0);
+    done = true;
+  } else if (mode == kTopK || mode == kMinP) {
+    done = pick_bounded(a, z, row_i, r, km, mode, sh);
+  } else {
+    done = pick_by_pieces(a, z, row_i, r, km, mode, sh);
+  }
+  if (!done) pick_whole_row(a, z, row_i, r, sh.row);
+}
 
-  int64_t tok = -1;
-  double lp = -__builtin_inf();
-  if (r.ok && km > kKeyNegInf) {
-    const double scale = __builtin_bit_cast(double, (u64)(1023 + a.s) << 52);
-    r.zmax = (double)value_of(km);
-    const Mode mode = mode_of(r, a.V);
-    double total = 0.0;   // weight of the kept set
-    bool done = false;
-    if (mode == kGreedy) {
-      // the first piece that holds the maximum, then the first index in it
-      if (threadIdx.x == 0) ps.found = a.pieces;
-      __syncthreads();
-      if (a.pieces > 1)
-        for (int i = threadIdx.x; i < a.pieces; i += kRowThreads)
-          if (pmax[i] == km) atomicMin(&ps.found, i);
-      __syncthreads();
-      const int64_t at = a.pieces > 1 ? ps.found : 0;
-      tok = locate_in_piece(row.z, a.V, at * kPiece, [&](int64_t, float x) { return (u64)(key_of(x) == km); }, 0, ps);
-      done = true;
-    } else if (mode == kAll || (mode == kTopP && a.pieces > 1)) {
-      done = pick_by_pieces(a, row.z, row_i, r, km, scale, mode, ps, tok, total);
-    } else {
-      done = pick_from_list(a, row.z, row_i, r, km, scale, mode, gmax, ps, tok, total);
-    }
-    if (mode == kGreedy) {
-      lp = 0.0;
-    } else if (done) {
-      const double z = (double)clean(to_f32(row.z[tok]));
-      lp = (z == r.zmax ? 0.0 : (z - r.zmax) / r.t) - log(total);
-    } else {
-      Cut cut{0u, a.V};
-      // the ties at the border go to the lowest indices
-      auto tie_index = [&](uint32_t key, u64 count) {
-        const int64_t i = row.locate([&](int64_t, float x) { return (u64)(key_of(x) == key); }, count - 1, sh);
-        return i < 0 ? a.V : i;
-      };
-      if (r.k > 0 && r.k < a.V) {
-        const u64 k = (u64)r.k;
-        u64 above;
-        cut.key = row.search([](int64_t, float) { return (u64)1; }, [=](u64) { return k; }, above, sh);
-        cut.idx = tie_index(cut.key, k - above);
-      }
-      if (r.p < 1.0) {
-        u64 above, need = 0;
-        const Cut in = cut;
-        const uint32_t key = row.search(
-            [&](int64_t i, float x) { return in.keeps(i, key_of(x)) ? fixed(weight(x, r), scale) : 0; },
-            [&](u64 all) {
-              const u64 n = (u64)ceil(r.p * (double)all);
-              return need = n < 1 ? 1 : n > all ? all : n;
-            },
-            above, sh);
-        const u64 each = fixed(weight(value_of(key), r), scale);
-        const int64_t i = tie_index(key, (need - above + each - 1) / each);
-        cut.idx = key == cut.key && cut.idx < i ? cut.idx : i;
-        cut.key = key;
-      }
-      auto mass = [&](int64_t i, float x) {
-        if (!cut.keeps(i, key_of(x))) return (u64)0;
-        const double wt = weight(x, r);
-        return wt >= r.q ? fixed(wt, scale) : (u64)0;
-      };
-      u64 s = 0;
-      row.each([&](int64_t i, float x) { s += mass(i, x); });
-      s = wave_sum_u64(s);
-      __syncthreads();
-      if (lane == 0) sh.wsum[w] = s;
-      __syncthreads();
-      s = 0;
-      for (int i = 0; i < kRowWaves; ++i) s += sh.wsum[i];
-      u64 target = (u64)((double)r.u * (double)s);
-      if (target >= s) target = s - 1;
-      tok = row.locate(mass, target, sh);
-      const double z = (double)clean(to_f32(row.z[tok]));
-      lp = (z == r.zmax ? 0.0 : (z - r.zmax) / r.t) - log((double)s / scale);
-    }
-  }
-  if (threadIdx.x == 0) {
-    a.tokens[row_i] = tok;
-    if (a.logprobs) a.logprobs[row_i] = (float)lp;
-  }
+template <typename T>
+void launch_small(const SampleArgs& a, hipStream_t st) {
+  const unsigned g = (unsigned)((a.N + 3) / 4);
+  if (a.V <= 64) sample_small_kernel<T, 1><<<g, 256, 0, st>>>(a);
+  else if (a.V <= 512) sample_small_kernel<T, 8><<<g, 256, 0, st>>>(a);
+  else sample_small_kernel<T, 16><<<g, 256, 0, st>>>(a);
 }
 
 // Workspace: what the scan leaves, for rows longer than one piece.
@@ -933,7 +1229,7 @@ SampleLayout sample_layout(int64_t N, int64_t V) {
   SampleLayout l{(V + kPiece - 1) / kPiece, 0, 0, 0, 0};
   // launches of fewer than 2^32 threads
   if (N > (int64_t(1) << 21) || V > (int64_t(1) << 24) || N * l.pieces > (int64_t(1) << 23)) return l;
-  if (l.pieces == 1) {
+  if (V <= kSmall) {
     l.total = 256;
     return l;
   }
@@ -997,7 +1293,15 @@ extern "C" int flce_sample(const void* logits, int64_t ld_logits, const float* u
   a.psum = reinterpret_cast<double*>(ws + l.psum);
   a.hist = reinterpret_cast<u64*>(ws + l.hist);
   a.gmax = reinterpret_cast<uint32_t*>(ws + l.gmax);
-  if (a.pieces > 1) {
+  if (V <= kSmall) {
+    ProfileScope ps(FLCE_KERNEL_SAMPLE_PICK, stream);
+    if (dtype == FLCE_DTYPE_BF16)
+      launch_small<bf16>(a, stream);
+    else
+      launch_small<float>(a, stream);
+    return hipGetLastError() == hipSuccess ? FLCE_OK : FLCE_EDEVICE;
+  }
+  {
     ProfileScope ps(FLCE_KERNEL_SAMPLE_SCAN, stream);
     const unsigned g = (unsigned)(N * l.pieces);
     if (dtype == FLCE_DTYPE_BF16)

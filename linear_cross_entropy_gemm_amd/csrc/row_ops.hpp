@@ -70,4 +70,94 @@ __device__ __forceinline__ float wave_sum(float x) {
   return (lane_f32(x, 0) + lane_f32(x, 16)) + (lane_f32(x, 32) + lane_f32(x, 48));
 }
 
+__device__ __forceinline__ float wave_max(float x) {   // no NaN
+  x = __builtin_fmaxf(x, dpp_f32<0xB1>(x));
+  x = __builtin_fmaxf(x, dpp_f32<0x4E>(x));
+  x = __builtin_fmaxf(x, dpp_f32<0x141>(x));
+  x = __builtin_fmaxf(x, dpp_f32<0x140>(x));
+  return __builtin_fmaxf(__builtin_fmaxf(lane_f32(x, 0), lane_f32(x, 16)),
+                         __builtin_fmaxf(lane_f32(x, 32), lane_f32(x, 48)));
+}
+
+template <int ctrl>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, ctrl, 0xf, 0xf, true);
+}
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t x) {
+  auto larger = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
+  x = larger(x, dpp_u32<0xB1>(x));
+  x = larger(x, dpp_u32<0x4E>(x));
+  x = larger(x, dpp_u32<0x141>(x));
+  x = larger(x, dpp_u32<0x140>(x));
+  auto lane = [=](int l) { return (uint32_t)__builtin_amdgcn_readlane((int)x, l); };
+  return larger(larger(lane(0), lane(16)), larger(lane(32), lane(48)));
+}
+
+// How many lower lanes are set in `mask`.
+__device__ __forceinline__ int lane_rank(unsigned long long mask) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+}
+
+// The same on 64-bit values, moved by halves.
+typedef unsigned long long u64;
+template <int ctrl>
+__device__ __forceinline__ u64 dpp_u64(u64 x) {
+  return (u64)dpp_u32<ctrl>((uint32_t)(x >> 32)) << 32 | dpp_u32<ctrl>((uint32_t)x);
+}
+__device__ __forceinline__ u64 lane_u64(u64 x, int lane) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)x, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(x >> 32), lane);
+  return (u64)hi << 32 | lo;
+}
+__device__ __forceinline__ u64 wave_sum_u64(u64 x) {
+  x += dpp_u64<0xB1>(x);
+  x += dpp_u64<0x4E>(x);
+  x += dpp_u64<0x141>(x);
+  x += dpp_u64<0x140>(x);
+  return (lane_u64(x, 0) + lane_u64(x, 16)) + (lane_u64(x, 32) + lane_u64(x, 48));
+}
+__device__ __forceinline__ double wave_sum_f64(double x) {
+  auto bits = [](double v) { return __builtin_bit_cast(u64, v); };
+  auto val = [](u64 v) { return __builtin_bit_cast(double, v); };
+  x += val(dpp_u64<0xB1>(bits(x)));
+  x += val(dpp_u64<0x4E>(bits(x)));
+  x += val(dpp_u64<0x141>(bits(x)));
+  x += val(dpp_u64<0x140>(bits(x)));
+  return (val(lane_u64(bits(x), 0)) + val(lane_u64(bits(x), 16))) +
+         (val(lane_u64(bits(x), 32)) + val(lane_u64(bits(x), 48)));
+}
+// Inclusive sum over the lanes in order; `all` gets the whole sum.
+__device__ __forceinline__ u64 wave_scan_u64(u64 x, u64& all) {
+  x += dpp_u64<0x111>(x);   // from 1, 2, 4, 8 lanes below within 16
+  x += dpp_u64<0x112>(x);
+  x += dpp_u64<0x114>(x);
+  x += dpp_u64<0x118>(x);
+  const u64 a = lane_u64(x, 15), b = a + lane_u64(x, 31), c = b + lane_u64(x, 47);
+  const int lane = threadIdx.x & 63;
+  x += lane < 16 ? 0 : lane < 32 ? a : lane < 48 ? b : c;
+  all = lane_u64(x, 63);
+  return x;
+}
+
+// The value of lane ^ d, d a power of two below 64.
+__device__ __forceinline__ uint32_t lane_xor_u32(uint32_t x, int d) {
+  switch (d) {
+    case 1: return dpp_u32<0xB1>(x);
+    case 2: return dpp_u32<0x4E>(x);
+    case 4: return dpp_u32<0x1B>(dpp_u32<0x141>(x));   // mirrored within 8 (^ 7), then within 4 (^ 3)
+    case 8: return dpp_u32<0x128>(x);   // rotated by 8 of 16
+    case 16: {
+      const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+      return (threadIdx.x & 16) ? r[0] : r[1];
+    }
+    default: {
+      const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+      return (threadIdx.x & 32) ? r[0] : r[1];
+    }
+  }
+}
+__device__ __forceinline__ u64 lane_xor_u64(u64 x, int d) {
+  return (u64)lane_xor_u32((uint32_t)(x >> 32), d) << 32 | lane_xor_u32((uint32_t)x, d);
+}
+
 }  // namespace flce
