@@ -28,9 +28,9 @@
 //   * top-p alone: the bin in which the weight from above reaches p of the
 //     row's: the candidates are the logits from that bin up where those are
 //     few, and the bin's own logits where the kept set is most of a flat row;
-//   * then a sort of the candidates (1024 of them) or a search among them
-//     (8192, in LDS), or, in a flat row, one piece whose weights are summed
-//     in index order.
+//   * then one wave compares up to 64 candidates with each other, or a search
+//     in LDS finds the cuts among up to 8192, or, in a flat row, the weights
+//     of one piece are summed in index order.
 // Rows for which that does not work out (a list that overflows, a cut below
 // the bins) take the searches over the whole row at the end of the kernel.
 //
@@ -51,7 +51,7 @@ constexpr int kRowThreads = 1024;
 constexpr int kRowWaves = kRowThreads / 64;
 constexpr int kBins = 2048;          // 11 bits of a key per search pass
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;
-constexpr int kSmall = 1024;         // rows one wave holds, lists that are sorted
+constexpr int kSmall = 1024;         // rows one wave holds
 constexpr int kPiece = 8192;         // logits per work-group of the scan
 constexpr int kGroup = 64;           // logits per stored maximum
 constexpr int kPieceGroups = kPiece / kGroup;
@@ -133,13 +133,17 @@ __device__ __forceinline__ float bin_scale(const RowParams& r) {
   return r.t < 1.0 ? (float)(8.0 / r.t < 1e30 ? 8.0 / r.t : 1e30) : 8.0f;
 }
 __device__ __forceinline__ float bin_of(float x, float alpha) { return __builtin_floorf(x * alpha); }
+// The least float in bin b or above: within a few steps of b / alpha.
+__device__ __forceinline__ float bin_edge(float b, float alpha) {
+  uint32_t k = key_of(clean(b / alpha)) + 8;
+  for (int i = 0; i < 32 && bin_of(value_of(k - 1), alpha) >= b; ++i) --k;
+  return value_of(k);
+}
 
 // exp((z - max) / t) as 2^(n + f), |f| <= 1/2: 2^f by the polynomial of
 // degree 9 through the Chebyshev nodes with its constant term put to 1
 // (relative error 2^-45), n put into the exponent.  The maximum itself weighs
-// exactly 1 (y = 0; where it is infinite, zmax is 1e300 and y is clamped),
-// and weights stop falling at 2^-1000, which is nothing to every use of
-// them.  The coefficients are loaded, not literal: in scalar registers they
+// exactly 1 (y = 0).  The coefficients are loaded, not literal: in scalar registers they
 // feed the multiply-adds directly, where literals would each take two moves
 // more.
 __constant__ double exp2_coef[9] = {0x1.62e42fefa39f7p-1,  0x1.ebfbdff8149f2p-3,  0x1.c6b08d7044115p-5,
@@ -153,15 +157,24 @@ __device__ __forceinline__ double exp2_of(double y) {
   for (int i = 6; i >= 0; --i) v = __builtin_fma(v, f, exp2_coef[i]);
   return __builtin_amdgcn_ldexp(__builtin_fma(v, f, 1.0), (int)n);
 }
-__device__ __forceinline__ double weight(float x, const RowParams& r) {
+// Any row: the maximum may be infinite (zmax is 1e300 then, and y clamped).
+__device__ __forceinline__ double weight_any(float x, const RowParams& r) {
   const double y = ((double)x - r.zmax) * r.rate;
   return exp2_of(__builtin_fmin(__builtin_fmax(y, -1000.0), 0.0));
+}
+// Ordinary rows, with fewer clamps: NaN and -inf count as -1e30, far below
+// any weight there.
+__device__ __forceinline__ bool ordinary(float m, const RowParams& r) {
+  return __builtin_fabsf(m) < 1e29f && r.t < 1e20;
+}
+__device__ __forceinline__ double weight(float x, const RowParams& r) {
+  return exp2_of(((double)__builtin_fmaxf(x, -1e30f) - r.zmax) * r.rate);
 }
 
 // round(w 2^s) for w <= 1, s <= 51: adding 2^52 leaves the integer in the
 // mantissa.
 __device__ __forceinline__ u64 fixed(double w, double scale) {
-  return __builtin_bit_cast(u64, __builtin_fma(w, scale, 0x1p52)) - __builtin_bit_cast(u64, 0x1p52);
+  return __builtin_bit_cast(u64, __builtin_fma(w, scale, 0x1p52)) & 0xFFFFFFFFFFFFFull;
 }
 
 __device__ __forceinline__ double scale_of(const SampleArgs& a) {
@@ -230,89 +243,49 @@ __device__ __forceinline__ u64 group_scan(u64 x, u64& all, GroupScratch<TH>& sh)
   return inc - x;
 }
 
-// LDS written by a wave is read by others of the group (or by the wave
-// itself where it is the group).
-template <int TH> __device__ __forceinline__ void group_sync() {
-  if (TH == 64) {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-  } else {
-    __syncthreads();
-  }
-}
-
 // ---------------------------------------------------------------------------
-// Up to kSmall candidates, one per thread: composites that order them by
-// descending logit, then ascending index.
+// Candidates as composites that order them by descending logit, then
+// ascending index.
 
 __device__ __forceinline__ u64 composite(uint32_t key, int64_t i) { return (u64)key << 32 | (uint32_t)~(uint32_t)i; }
 __device__ __forceinline__ uint32_t key_in(u64 c) { return (uint32_t)(c >> 32); }
 __device__ __forceinline__ int64_t index_in(u64 c) { return (int64_t)(uint32_t)~(uint32_t)c; }
 __device__ __forceinline__ float value_in(u64 c) { return value_of(key_in(c)); }
 
-template <int TH>
-struct SortShared {
-  GroupScratch<TH> scratch;
-  u64 x[TH];   // exchange between waves, then the candidates' weights
-  u64 c[TH];
-};
-
-// Bitonic sort of the first P threads' values (P a power of two, at least
-// 64), largest first; strides within a wave are exchanged between lanes.
-template <int TH>
-__device__ __forceinline__ u64 sort_down(u64 x, int P, u64* lds) {
-  const int t = threadIdx.x;
-#pragma unroll 1
-  for (int size = 2; size <= P; size <<= 1)
-#pragma unroll 1
-    for (int d = size >> 1; d > 0; d >>= 1) {
-      u64 y;
-      if (TH == 64 || d < 64) {
-        y = lane_xor_u64(x, d);
-      } else {
-        __syncthreads();
-        lds[t] = x;
-        __syncthreads();
-        y = lds[t ^ d];
-      }
-      const bool keep_max = ((t & size) == 0) == ((t & d) == 0);
-      if ((y > x) == keep_max) x = y;
-    }
-  return x;
-}
-
-__device__ __forceinline__ int pow2_from_64(int n) { return n <= 64 ? 64 : 1 << bits_of((u64)(n - 1)); }
-
-// Draws from n candidates (c = this thread's, 0 beyond them) that hold every
-// token at least as likely as the least of them.  top-p is a share of the
-// candidates' weight after top-k, or of `row_sum` where that is not 0.
-template <int TH>
-__device__ __forceinline__ void pick_sorted(const SampleArgs& a, int64_t row, u64 c, int n, const RowParams& r, bool top_k,
-                            u64 row_sum, SortShared<TH>& sh) {
-  const int t = threadIdx.x;
+// Draws from n <= 64 candidates, one per lane of a wave (c = 0 beyond them),
+// that hold every token at least as likely as the least of them.  top-p is a
+// share of the candidates' weight after top-k, or of `row_sum` where that is
+// not 0.  A candidate's rank and the weights before it come from comparing it
+// with every other one.
+__device__ __forceinline__ void pick_in_wave(const SampleArgs& a, int64_t row, u64 c, int n, const RowParams& r,
+                                             bool top_k, u64 row_sum) {
   const double scale = scale_of(a);
-  c = sort_down<TH>(c, pow2_from_64(n), sh.x);
-  u64 f = t < n && (!top_k || (int64_t)t < r.k) ? fixed(weight(value_in(c), r), scale) : 0, all;
+  u64 f = c ? fixed(weight(value_in(c), r), scale) : 0;
+  int rank = 0;
+  u64 above = 0;
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    const bool more = lane_u64(c, i) > c;
+    rank += more ? 1 : 0;
+    above += more ? lane_u64(f, i) : 0;
+  }
+  if (top_k && rank >= r.k) f = 0;
   if (r.p < 1.0) {
-    const u64 before = group_scan<TH>(f, all, sh.scratch);
-    if (before >= share(r.p, row_sum ? row_sum : all)) f = 0;
+    const u64 all = wave_sum_u64(f);
+    if (above >= share(r.p, row_sum ? row_sum : all)) f = 0;
   }
   if (f < floor_weight(r, scale)) f = 0;
-  // the kept ones are the first m threads'; now by ascending index
-  u64 m = 64;
-  if (TH > 64) group_scan<TH>(f ? 1 : 0, m, sh.scratch);
-  group_sync<TH>();
-  sh.c[t] = c;
-  group_sync<TH>();
-  const int P = pow2_from_64((int)m);
-  const u64 o = sort_down<TH>(f ? (c << 32) | (u64)t : 0, P, sh.x);
-  const u64 hit = sh.c[(uint32_t)o & (TH - 1)];
-  const u64 mine = o && t < P ? fixed(weight(value_in(hit), r), scale) : 0;
-  u64 sum;
-  const u64 before = group_scan<TH>(mine, sum, sh.scratch);
+  u64 before = 0, sum = 0;   // in index order
+#pragma unroll 1
+  for (u64 left = __builtin_amdgcn_ballot_w64(f != 0); left; left &= left - 1) {
+    const int i = __builtin_ctzll(left);
+    const u64 w = lane_u64(f, i);
+    sum += w;
+    before += (uint32_t)lane_u64(c, i) > (uint32_t)c ? w : 0;   // indices are complemented
+  }
   const u64 target = draw_target(r.u, sum);
-  if (before <= target && target < before + mine)   // one thread
-    emit(a, row, index_in(hit), value_in(hit), r, (double)sum / scale);
+  if (before <= target && target < before + f)   // one lane
+    emit(a, row, index_in(c), value_in(c), r, (double)sum / scale);
 }
 
 // Rows of up to 64 kPer logits, any parameters: one wave per row, lane l
@@ -401,7 +374,7 @@ __global__ __launch_bounds__(256) void sample_small_kernel(SampleArgs a) {
   const double scale = scale_of(a);
   u64 w[kPer];
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) w[j] = keep >> j & 1 ? fixed(weight(x[j], r), scale) : 0;
+  for (int j = 0; j < kPer; ++j) w[j] = keep >> j & 1 ? fixed(weight_any(x[j], r), scale) : 0;
   if (r.p < 1.0) {
     auto mass = [&](uint32_t from) {
       u64 s = 0;
@@ -415,7 +388,7 @@ __global__ __launch_bounds__(256) void sample_small_kernel(SampleArgs a) {
     for (int b = 31; b >= low; --b)
       if (mass(K | 1u << b) >= need) K |= 1u << b;
     K |= low && !(K >> 31) ? 0xFFFFu : 0u;
-    const u64 rest = need - mass(K + 1), each = fixed(weight(value_of(K), r), scale);
+    const u64 rest = need - mass(K + 1), each = fixed(weight_any(value_of(K), r), scale);
     cut_at(K, (rest + each - 1) / each);
   }
   const u64 least = floor_weight(r, scale);
@@ -474,10 +447,10 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a)
   float m = kNegInf;
 #pragma unroll
   for (int j = 0; j < kVec; ++j) {
-    float g = clean(to_f32(v[j][0]));
+    float g = to_f32(v[j][0]);   // the maximum passes over NaN
 #pragma unroll
-    for (int e = 1; e < E; ++e) g = __builtin_fmaxf(g, clean(to_f32(v[j][e])));
-    g = lanes_max<kLanes>(g);
+    for (int e = 1; e < E; ++e) g = __builtin_fmaxf(g, to_f32(v[j][e]));
+    g = clean(lanes_max<kLanes>(g));
     if (t % kLanes == 0) a.gmax[out * kPieceGroups + (j * kScanThreads + t) / kLanes] = key_of(g);
     m = __builtin_fmaxf(m, g);
   }
@@ -492,7 +465,7 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a)
   for (int i = 1; i < kWaves; ++i) m = __builtin_fmaxf(m, wmax[i]);
   if (t == 0) a.pmax[out] = key_of(m);
   if (!r.ok || mode == kGreedy || mode == kTopK || (mode == kMinP && r.p >= 1.0)) return;
-  if (m == kNegInf) {
+  if (!ordinary(m, r)) {   // nothing beside the rest of an ordinary row
     if (t == 0) a.psum[out] = 0.0;
     if (mode == kTopP && t < kSlots) a.hist[out * kSlots + t] = 0;
     return;
@@ -503,7 +476,7 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a)
 #pragma unroll
     for (int j = 0; j < kVec; ++j)
 #pragma unroll
-      for (int e = 0; e < E; ++e) sum += weight(clean(to_f32(v[j][e])), r);
+      for (int e = 0; e < E; ++e) sum += weight(to_f32(v[j][e]), r);
     sum = wave_sum_f64(sum);
     if (lane == 0) wsum[w] = sum;
     __syncthreads();
@@ -513,16 +486,22 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a)
   const double scale = scale_of(a);
   const float alpha = bin_scale(r);
   const float top = bin_of(m, alpha);
+  u64 rest = 0;   // what lies below the bins
 #pragma unroll
   for (int j = 0; j < kVec; ++j)
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const float x = clean(to_f32(v[j][e]));
+      const float x = to_f32(v[j][e]);
       const u64 f = fixed(weight(x, r), scale);
-      // (an undefined difference of infinities counts as the rest)
-      const int d = (int)__builtin_fminf(top - bin_of(x, alpha), (float)(kSlots - 1));
-      if (f) atomicAdd(&hist[w][d], f);
+      const float d = top - bin_of(x, alpha);
+      if (d < (float)(kSlots - 1)) {
+        if (f) atomicAdd(&hist[w][(int)d], f);
+      } else {
+        rest += f;
+      }
     }
+  rest = wave_sum_u64(rest);
+  if (lane == 0) hist[w][kSlots - 1] = rest;
   __syncthreads();
   if (t < kSlots) {
     u64 h = 0;
@@ -544,11 +523,7 @@ struct RowShared {
 
 struct PickShared {
   RowShared row;
-  union {
-    u64 list[kList];                  // composites
-    SortShared<kRowThreads> sort;     // after each thread has taken its own
-    SortShared<64> sort1;
-  };
+  u64 list[kList];                    // composites
   u64 cmass[kMaxPieces];              // kept weight per piece
   double factor[kMaxPieces];          // weight of each piece's maximum
   u64 slot[kSlots];
@@ -783,10 +758,12 @@ struct Candidates {
     return prefix;
   }
 
-  // Collects the logits that `take(key, value)` accepts out of the groups
-  // whose maximum `group(key)` accepts; false if they overflow the list.
-  template <typename G, typename F>
-  __device__ __forceinline__ bool collect(const T* z, int64_t V, const uint32_t* gmax, G group, F take) {
+  // Collects the logits from `from` up to (not including) `to` (+inf: no
+  // limit) out of the groups whose maximum reaches `from`; false if they
+  // overflow the list.
+  __device__ __forceinline__ bool collect(const T* z, int64_t V, const uint32_t* gmax, float from, float to) {
+    const uint32_t least = key_of(clean(from));
+    const bool open = to == __builtin_inff();
     constexpr int E = RowVec<T>::E, kLanes = kGroup / E, kPass = kRowThreads / kLanes, kUnroll = 4;
     const int t = threadIdx.x, lane = t & 63;
     const int groups = (int)((V + kGroup - 1) / kGroup);
@@ -803,7 +780,7 @@ struct Candidates {
 #pragma unroll
       for (int j = 0; j < kGroupBatch / kRowThreads; ++j) {
         const int g = g0 + j * kRowThreads + t;
-        live[j] = g < groups && group(gmax[g]);
+        live[j] = g < groups && gmax[g] >= least;
       }
 #pragma unroll
       for (int j = 0; j < kGroupBatch / kRowThreads; ++j) {
@@ -821,45 +798,57 @@ struct Candidates {
         }
       }
       __syncthreads();
+      // kLanes lanes take a group, kUnroll groups in a row; a lane's accepted
+      // logits are the bits of a mask, and their indices go into the list
       const int ng = sh.groups;
-      for (int i0 = 0; i0 < ng; i0 += kPass * kUnroll) {
+      for (int i0 = t / kLanes; i0 - t / kLanes < ng; i0 += kPass * kUnroll) {
         typename RowVec<T>::type v[kUnroll];
-        int64_t c[kUnroll];
+        int c[kUnroll];
 #pragma unroll
         for (int j = 0; j < kUnroll; ++j) {
-          const int i = i0 + j * kPass + t / kLanes;
-          c[j] = i < ng ? (int64_t)(g0 + sh.glist[i]) * kGroup + (t % kLanes) * E : V;
+          const int i = i0 + j * kPass;
+          c[j] = i < ng ? (g0 + (int)sh.glist[i]) * kGroup + (t % kLanes) * E : (int)V;
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[j][e] = (T)kNegInf;
           if (c[j] < V) v[j] = load_row(z, c[j], V, kNegInf);
         }
+        uint32_t mask = 0;
 #pragma unroll
-        for (int j = 0; j < kUnroll; ++j) {
-          if (!__builtin_amdgcn_ballot_w64(c[j] < V)) break;
-          uint32_t k[E];
-          u64 ok[E];
-          int n_ok = 0;
+        for (int j = 0; j < kUnroll; ++j)
 #pragma unroll
           for (int e = 0; e < E; ++e) {
-            const float x = c[j] + e < V ? clean(to_f32(v[j][e])) : kNegInf;
-            k[e] = key_of(x);
-            ok[e] = __builtin_amdgcn_ballot_w64(c[j] + e < V && take(k[e], x));
-            n_ok += __builtin_popcountll(ok[e]);
+            const float x = to_f32(v[j][e]);   // NaN fails both comparisons
+            mask |= (x >= from && (open || x < to) ? 1u : 0u) << (j * E + e);
           }
-          if (!n_ok) continue;
-          int at = 0;
-          if (lane == 0) at = atomicAdd(&sh.count, n_ok);
-          at = __builtin_amdgcn_readfirstlane(at);
+        u64 all;
+        const int mine = __builtin_popcount(mask);
+        int pos = (int)wave_scan_u64((u64)mine, all) - mine;
+        if (!all) continue;
+        int at = 0;
+        if (lane == 0) at = atomicAdd(&sh.count, (int)all);
+        pos += __builtin_amdgcn_readfirstlane(at);
+        while (__builtin_amdgcn_ballot_w64(mask != 0)) {
+          const int b = __builtin_ctz(mask | 0x80000000u);
+          int base = c[0];
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const int pos = at + lane_rank(ok[e]);
-            if ((ok[e] >> lane & 1) && pos < kList) sh.list[pos] = composite(k[e], c[j] + e);
-            at += __builtin_popcountll(ok[e]);
-          }
+          for (int j = 1; j < kUnroll; ++j) base = b >= j * E ? c[j] : base;
+          if (mask && pos < kList) sh.list[pos] = (u64)(base + b % E);
+          ++pos;
+          mask &= mask - 1;
         }
       }
     }
     __syncthreads();
     n = sh.count;
-    return n <= kList;
+    if (n > kList) return false;
+    // indices to composites
+#pragma unroll 4
+    for (int i = t; i < n; i += kRowThreads) {
+      const int64_t at = (int64_t)sh.list[i];
+      sh.list[i] = composite(key_of(clean(to_f32(z[at]))), at);
+    }
+    __syncthreads();
+    return true;
   }
 };
 
@@ -916,23 +905,14 @@ __device__ __forceinline__ u64 piece_weight(double psum, double factor, double s
 }
 
 // The listed candidates (which hold every token at least as likely as the
-// least of them): sorted, or searched where they are too many for that.
+// least of them): by one wave, or searched where they are more.
 template <typename T>
-__device__ __forceinline__ void pick_from_list(const SampleArgs& a, int64_t row_i, Candidates<T>& list, const RowParams& r, bool top_k,
-                               u64 row_sum, PickShared& sh) {
+__device__ __forceinline__ void pick_from_list(const SampleArgs& a, int64_t row_i, Candidates<T>& list,
+                                               const RowParams& r, bool top_k, u64 row_sum, PickShared& sh) {
   top_k = top_k && r.k < list.n;
-  if (list.n <= 64) {   // one wave, without barriers
-    if (threadIdx.x < 64) {
-      const u64 c = (int)threadIdx.x < list.n ? sh.list[threadIdx.x] : 0;
-      group_sync<64>();
-      pick_sorted<64>(a, row_i, c, list.n, r, top_k, row_sum, sh.sort1);
-    }
-    return;
-  }
-  if (list.n <= kSmall) {
-    const u64 c = (int)threadIdx.x < list.n ? sh.list[threadIdx.x] : 0;
-    __syncthreads();   // the sort takes the list's place
-    pick_sorted<kRowThreads>(a, row_i, c, list.n, r, top_k, row_sum, sh.sort);
+  if (list.n <= 64) {
+    if (threadIdx.x < 64)
+      pick_in_wave(a, row_i, (int)threadIdx.x < list.n ? sh.list[threadIdx.x] : 0, list.n, r, top_k, row_sum);
     return;
   }
   const double scale = scale_of(a);
@@ -976,32 +956,34 @@ __device__ __forceinline__ bool pick_bounded(const SampleArgs& a, const T* z, in
   uint32_t bound = kKeyNegInf + 1;   // candidates' keys from here on
   u64 row_sum = 0;
   if (mode == kTopK) {
-    // the k-th largest group maximum, by its key's distance from the row's:
-    // in steps of 2^13 (a thousandth of a binade) over two binades, or to the
-    // first 11 bits.  With as many tokens wanted as there are groups, all of
-    // the row may be listed.
+    // the k-th largest of the group maxima, or of all logits where there are
+    // fewer groups, by its key's distance from the row's maximum: in steps of
+    // 2^13 (a thousandth of a binade) over two binades, or to the first 11 bits
     const int groups = (int)((a.V + kGroup - 1) / kGroup);
-    if (r.k <= groups) {
-      uint32_t* bins = reinterpret_cast<uint32_t*>(sh.row.hist);
-      for (int step = 13; step <= 21; step += 8) {
-        clear_bins(sh.row);
-        for (int i = threadIdx.x; i < groups; i += kRowThreads) {
-          const uint32_t d = (km - gmax[i]) >> step;
-          atomicAdd(&bins[d < kBins - 1 ? d : kBins - 1], 1u);
-        }
-        __syncthreads();
-        u64 all;
-        const uint32_t x = bins[2 * threadIdx.x], y = bins[2 * threadIdx.x + 1];
-        const u64 exc = group_scan<kRowThreads>(x + y, all, sh.row.scratch);
-        if (exc < (u64)r.k && (u64)r.k <= exc + x + y)   // one thread
-          sh.found = 2 * threadIdx.x + ((u64)r.k <= exc + x ? 0 : 1);
-        __syncthreads();
-        const uint32_t d = (uint32_t)sh.found;
-        if (d == kBins - 1) continue;   // further down: coarser steps
-        const uint32_t reach = ((d + 1) << step) - 1;
-        if (km - (kKeyNegInf + 1) > reach) bound = km - reach;
-        break;
+    uint32_t* bins = reinterpret_cast<uint32_t*>(sh.row.hist);
+    for (int step = 13; step <= 21; step += 8) {
+      auto count = [&](uint32_t key) {
+        const uint32_t d = (km - key) >> step;
+        if (d < kBins - 1) atomicAdd(&bins[d], 1u);
+      };
+      clear_bins(sh.row);
+      if (r.k <= groups) {
+        for (int i = threadIdx.x; i < groups; i += kRowThreads) count(gmax[i]);
+      } else {
+        Row<T>(z, a.V).each([&](int64_t, float x) { count(key_of(x)); });
       }
+      __syncthreads();
+      u64 all;
+      const uint32_t x = bins[2 * threadIdx.x], y = bins[2 * threadIdx.x + 1];
+      const u64 exc = group_scan<kRowThreads>(x + y, all, sh.row.scratch);
+      if ((u64)r.k > all) continue;   // further down: coarser steps
+      if (exc < (u64)r.k && (u64)r.k <= exc + x + y)   // one thread
+        sh.found = 2 * threadIdx.x + ((u64)r.k <= exc + x ? 0 : 1);
+      __syncthreads();
+      const uint32_t d = (uint32_t)sh.found;
+      const uint32_t reach = ((d + 1) << step) - 1;
+      if (km - (kKeyNegInf + 1) > reach) bound = km - reach;
+      break;
     }
   } else {
     // w >= q: a little below max + t ln q in fp32, the exact test follows
@@ -1017,9 +999,7 @@ __device__ __forceinline__ bool pick_bounded(const SampleArgs& a, const T* z, in
     }
   }
   Candidates<T> list{sh, 0, 0, 0, 0};
-  if (!list.collect(z, a.V, gmax, [=](uint32_t k) { return k >= bound; },
-                    [=](uint32_t k, float) { return k >= bound; }))
-    return false;
+  if (!list.collect(z, a.V, gmax, value_of(bound), __builtin_inff())) return false;
   pick_from_list(a, row_i, list, r, mode == kTopK, row_sum, sh);
   return true;
 }
@@ -1071,17 +1051,15 @@ __device__ __forceinline__ bool pick_by_pieces(const SampleArgs& a, const T* z, 
     const u64 above = sh.sum;
     if (border == kSlots - 1) return false;
     const float bin = top - (float)border;
-    auto group = [=](uint32_t k) { return bin_of(value_of(k), alpha) >= bin; };
+    const float from = bin_edge(bin, alpha), to = bin_edge(bin + 1.0f, alpha);
     Candidates<T> list{sh, 0, 0, 0, 0};
     // every logit above the border bin weighs at least what its upper edge
     // does: few of them make a short list together with the bin
-    const double edge = weight((bin + 1.0f) / alpha, r) * 0.99;
-    if ((double)above <= edge * scale * kSmall &&
-        list.collect(z, a.V, gmax, group, [=](uint32_t, float x) { return bin_of(x, alpha) >= bin; })) {
+    if ((double)above <= weight(to, r) * scale * (kList / 4) && list.collect(z, a.V, gmax, from, __builtin_inff())) {
       pick_from_list(a, row_i, list, r, false, all, sh);
       return true;
     }
-    if (!list.collect(z, a.V, gmax, group, [=](uint32_t, float x) { return bin_of(x, alpha) == bin; })) return false;
+    if (!list.collect(z, a.V, gmax, from, to)) return false;
     auto wt = [&](u64 c) { return fixed(weight(value_in(c), r), scale); };
     u64 s = 0;
     list.each([&](u64 c) { s += wt(c); });
@@ -1095,11 +1073,22 @@ __device__ __forceinline__ bool pick_by_pieces(const SampleArgs& a, const T* z, 
     // the kept weight by pieces
     for (int i = threadIdx.x; i < a.pieces; i += kRowThreads) sh.cmass[i] = 0;
     __syncthreads();
-    list.each([&](u64 x) {
-      if (x >= c) atomicAdd(&sh.cmass[index_in(x) / kPiece], wt(x));
-    });
-    each_slot([&](int i, int slot, u64 w) {
-      if (slot < border && w) atomicAdd(&sh.cmass[i], w);
+    // (one addition per wave and piece: neighbours in the list share pieces)
+    for (int i0 = 0; i0 < list.n; i0 += kRowThreads) {
+      const int i = i0 + (int)threadIdx.x;
+      const u64 x = i < list.n ? sh.list[i] : 0;
+      const u64 wx = x >= c ? wt(x) : 0;
+      const int piece = (int)(index_in(x) / kPiece);
+      for (u64 left = __builtin_amdgcn_ballot_w64(wx != 0); left;) {
+        const int p = __builtin_amdgcn_readlane(piece, __builtin_ctzll(left));
+        const u64 sum = wave_sum_u64(piece == p ? wx : 0);
+        if ((threadIdx.x & 63) == 0) atomicAdd(&sh.cmass[p], sum);
+        left &= ~__builtin_amdgcn_ballot_w64(piece == p);
+      }
+    }
+    each_slot([&](int i, int slot, u64 w) {   // a wave's slots are of one piece
+      const u64 sum = wave_sum_u64(slot < border ? w : 0);
+      if (sum && (threadIdx.x & 63) == 0) atomicAdd(&sh.cmass[i], sum);
     });
   } else {
     for (int i = threadIdx.x; i < a.pieces; i += kRowThreads)
@@ -1154,9 +1143,9 @@ __device__ __attribute__((noinline)) void pick_whole_row(SampleArgs a, const T* 
     u64 above, need = 0;
     const Cut in = cut;
     const uint32_t key =
-        row.search([&](int64_t i, float x) { return in.keeps(i, key_of(x)) ? fixed(weight(x, r), scale) : 0; },
+        row.search([&](int64_t i, float x) { return in.keeps(i, key_of(x)) ? fixed(weight_any(x, r), scale) : 0; },
                    [&](u64 all) { return need = share(r.p, all); }, above, sh);
-    const u64 each = fixed(weight(value_of(key), r), scale);
+    const u64 each = fixed(weight_any(value_of(key), r), scale);
     const int64_t i = tie_index(key, (need - above + each - 1) / each);
     cut.idx = key == cut.key && cut.idx < i ? cut.idx : i;
     cut.key = key;
@@ -1165,7 +1154,7 @@ __device__ __attribute__((noinline)) void pick_whole_row(SampleArgs a, const T* 
   u64 sum;
   const int64_t tok = row.locate(
       [&](int64_t i, float x) {
-        const u64 w = cut.keeps(i, key_of(x)) ? fixed(weight(x, r), scale) : 0;
+        const u64 w = cut.keeps(i, key_of(x)) ? fixed(weight_any(x, r), scale) : 0;
         return w >= least ? w : (u64)0;
       },
       [&](u64 s) { return draw_target(r.u, s); }, sum, sh);
@@ -1193,7 +1182,7 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleArgs a) 
   }
   r.set_max(value_of(km));
   const Mode mode = mode_of(r, a.V);
-  bool done;
+  bool done = false;
   if (mode == kGreedy) {
     // the first piece that holds the maximum, then the first index in it
     for (int i = threadIdx.x; i < a.pieces; i += kRowThreads)
@@ -1203,6 +1192,7 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleArgs a) 
                                         [&](int64_t, float x) { return (u64)(key_of(x) == km); }, 0, sh.row);
     if (threadIdx.x == 0) emit(a, row_i, tok, value_of(km), r, 1.0);
     done = true;
+  } else if (!ordinary(value_of(km), r)) {
   } else if (mode == kTopK || mode == kMinP) {
     done = pick_bounded(a, z, row_i, r, km, mode, sh);
   } else {
