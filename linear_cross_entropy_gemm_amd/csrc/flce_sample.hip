@@ -90,14 +90,34 @@ __device__ __forceinline__ float value_of(uint32_t k) {
   return __builtin_bit_cast(float, k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
 
+// Coefficients of P, held in scalar registers: they feed the multiply-adds
+// directly there, where literals take two moves each.  The empty asm keeps
+// the compiler from seeing their values.
+struct ExpCoef {
+  double c[8];
+  __device__ __forceinline__ void load() {
+    const double v[8] = {0x1.62e42fef9cc69p-1,  0x1.ebfbdff82a733p-3,  0x1.c6b08da70cce5p-5,  0x1.3b2ab70ad2596p-7,
+                         0x1.5d87759834f12p-10, 0x1.4308c7183804ap-13, 0x1.00c0e4e161930p-16, 0x1.63b2d79cc14d7p-20};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      c[i] = v[i];
+      asm("" : "+s"(c[i]));
+    }
+  }
+};
+
 // A row's parameters and the weights they define.
 struct RowParams {
   double t, p, q, zmax, rate;   // rate = log2(e) / t
+  ExpCoef coef;
   int64_t k;
-  float u;
+  float u, xmin;
   bool ok;
 
-  __device__ __forceinline__ void set_max(float m) { zmax = m < __builtin_inff() ? (double)m : kInfMax; }
+  __device__ __forceinline__ void set_max(float m) {
+    zmax = m < __builtin_inff() ? (double)m : kInfMax;
+    xmin = (float)((double)m - t * (0.69314718055994530942 * 0.8 * 0x1p30));
+  }
 };
 
 __device__ __forceinline__ RowParams row_params(const SampleArgs& a, int64_t row) {
@@ -112,8 +132,9 @@ __device__ __forceinline__ RowParams row_params(const SampleArgs& a, int64_t row
   r.t = t;
   r.p = p;
   r.q = q;
-  r.zmax = 0.0;
+  r.set_max(0.0f);
   r.rate = 1.4426950408889634074 / r.t;
+  r.coef.load();
   return r;
 }
 
@@ -140,35 +161,30 @@ __device__ __forceinline__ float bin_edge(float b, float alpha) {
   return value_of(k);
 }
 
-// exp((z - max) / t) as 2^(n + f), |f| <= 1/2: 2^f by the polynomial of
-// degree 9 through the Chebyshev nodes with its constant term put to 1
-// (relative error 2^-45), n put into the exponent.  The maximum itself weighs
-// exactly 1 (y = 0).  The coefficients are loaded, not literal: in scalar registers they
-// feed the multiply-adds directly, where literals would each take two moves
-// more.
-__constant__ double exp2_coef[9] = {0x1.62e42fefa39f7p-1,  0x1.ebfbdff8149f2p-3,  0x1.c6b08d7044115p-5,
-                                    0x1.3b2ab72b175f8p-7,  0x1.5d87fe908fed1p-10, 0x1.43088e257e65bp-13,
-                                    0x1.ffcb7677a5f5cp-17, 0x1.63ef969b0e64ep-20, 0x1.b6571ea79d565p-24};
-
-__device__ __forceinline__ double exp2_of(double y) {
-  const double n = __builtin_rint(y), f = y - n;
-  double v = __builtin_fma(exp2_coef[8], f, exp2_coef[7]);
+// 2^(d rate) as 2^(n + f), |f| <= 1/2 and |d rate| < 2^31: adding 1.5 2^52
+// leaves n in the low bits, 2^f = 1 + f P(f) with P through the Chebyshev
+// nodes (relative error 2^-38.8; exactly 1 at d = 0), n put into the exponent.
+__device__ __forceinline__ double exp2_of(double d, double rate, const ExpCoef& k) {
+  const double big = __builtin_fma(d, rate, 0x1.8p52);
+  const double f = __builtin_fma(d, rate, -(big - 0x1.8p52));
+  double v = k.c[7];
 #pragma unroll
-  for (int i = 6; i >= 0; --i) v = __builtin_fma(v, f, exp2_coef[i]);
-  return __builtin_amdgcn_ldexp(__builtin_fma(v, f, 1.0), (int)n);
+  for (int i = 6; i >= 0; --i) v = __builtin_fma(v, f, k.c[i]);
+  return __builtin_amdgcn_ldexp(__builtin_fma(v, f, 1.0), (int)(uint32_t)__builtin_bit_cast(u64, big));
 }
-// Any row: the maximum may be infinite (zmax is 1e300 then, and y clamped).
+// exp((x - max) / t) in any row: the maximum may be infinite (zmax is 1e300
+// then), so the exponent is clamped.
 __device__ __forceinline__ double weight_any(float x, const RowParams& r) {
   const double y = ((double)x - r.zmax) * r.rate;
-  return exp2_of(__builtin_fmin(__builtin_fmax(y, -1000.0), 0.0));
+  return exp2_of(__builtin_fmin(__builtin_fmax(y, -1000.0), 0.0), 1.0, r.coef);
 }
-// Ordinary rows, with fewer clamps: NaN and -inf count as -1e30, far below
-// any weight there.
+// In ordinary rows the clamp is one fp32 maximum: xmin lies 0.8 2^30 in the
+// exponent below the row's maximum, and takes NaN and -inf too.
 __device__ __forceinline__ bool ordinary(float m, const RowParams& r) {
-  return __builtin_fabsf(m) < 1e29f && r.t < 1e20;
+  return (double)__builtin_fabsf(m) < r.t * 0x1p48 && r.t < 1e20;
 }
 __device__ __forceinline__ double weight(float x, const RowParams& r) {
-  return exp2_of(((double)__builtin_fmaxf(x, -1e30f) - r.zmax) * r.rate);
+  return exp2_of((double)__builtin_fmaxf(x, r.xmin) - r.zmax, r.rate, r.coef);
 }
 
 // round(w 2^s) for w <= 1, s <= 51: adding 2^52 leaves the integer in the
@@ -205,7 +221,7 @@ __device__ __forceinline__ void emit(const SampleArgs& a, int64_t row, int64_t t
   a.tokens[row] = tok;
   if (!a.logprobs) return;
   const double l2 = (double)__builtin_amdgcn_logf((float)weight_sum);
-  const double e = __builtin_fma(weight_sum, exp2_of(-l2), -1.0);
+  const double e = __builtin_fma(weight_sum, exp2_of(-l2, 1.0, r.coef), -1.0);
   const double ls = __builtin_fma(l2, 0.69314718055994530942, e - 0.5 * e * e);
   const double y = __builtin_fmin(((double)x - r.zmax) * r.rate, 0.0);
   a.logprobs[row] = (float)(__builtin_fma(y, 0.69314718055994530942, -ls));
@@ -433,7 +449,8 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a)
   constexpr int kWaves = kScanThreads / 64;
   __shared__ float wmax[kWaves];
   __shared__ double wsum[kWaves];
-  __shared__ u64 hist[kWaves][kSlots];
+  constexpr int kRest = 16;
+  __shared__ u64 hist[kWaves][kSlots + kRest - 1];
   const int64_t row_i = blockIdx.x / a.pieces;
   const int piece = blockIdx.x % a.pieces;
   const int t = threadIdx.x, lane = t & 63, w = t >> 6;
@@ -458,7 +475,7 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a)
   if (lane == 0) wmax[w] = m;
   const Mode mode = mode_of(r, a.V);
   if (mode == kTopP)
-    for (int i = t; i < kWaves * kSlots; i += kScanThreads) hist[i / kSlots][i % kSlots] = 0;
+    for (int i = lane; i < kSlots + kRest - 1; i += 64) hist[w][i] = 0;
   __syncthreads();
   m = wmax[0];
 #pragma unroll
@@ -486,27 +503,26 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a)
   const double scale = scale_of(a);
   const float alpha = bin_scale(r);
   const float top = bin_of(m, alpha);
-  u64 rest = 0;   // what lies below the bins
+  // what lies below the bins is most of a peaked row: 16 places share it
+  const float spread = (float)(kSlots - 1 + lane % kRest);
 #pragma unroll
   for (int j = 0; j < kVec; ++j)
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const float x = to_f32(v[j][e]);
       const u64 f = fixed(weight(x, r), scale);
-      const float d = top - bin_of(x, alpha);
-      if (d < (float)(kSlots - 1)) {
-        if (f) atomicAdd(&hist[w][(int)d], f);
-      } else {
-        rest += f;
-      }
+      const int d = (int)__builtin_fminf(top - bin_of(x, alpha), spread);
+      if (f) atomicAdd(&hist[w][d], f);
     }
-  rest = wave_sum_u64(rest);
-  if (lane == 0) hist[w][kSlots - 1] = rest;
   __syncthreads();
   if (t < kSlots) {
     u64 h = 0;
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) h += hist[i][t];
+    for (int i = 0; i < kWaves; ++i) {
+      h += hist[i][t];
+      if (t == kSlots - 1)
+        for (int j = 1; j < kRest; ++j) h += hist[i][t + j];
+    }
     a.hist[out * kSlots + t] = h;
   }
 }
@@ -689,6 +705,67 @@ struct Cut {
   __device__ __forceinline__ bool keeps(int64_t i, uint32_t k) const { return k > key || (k == key && i <= idx); }
 };
 
+// The values from `from` up to (not including) `to`, +inf for no limit; NaN
+// is none of them.  accepted() turns vectors into a mask of their elements;
+// bit() gives the element (vector and position) of a mask's bit.
+template <typename T> struct Interval;
+template <> struct Interval<float> {
+  float from, to;
+  bool open;
+  __device__ __forceinline__ Interval(float f, float t) : from(f), to(t), open(t == __builtin_inff()) {}
+  template <int N> __device__ __forceinline__ uint32_t accepted(const typename RowVec<float>::type (&v)[N]) const {
+    uint32_t mask = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = v[j][e];
+        mask |= (x >= from && (open || x < to) ? 1u : 0u) << (j * 4 + e);
+      }
+    return mask;
+  }
+  static __device__ __forceinline__ int bit(int b, int) { return b; }
+};
+// bf16 pairs as 16-bit keys: with d = key - least, d < width where the
+// saturating difference width - d is not 0; two elements per instruction.
+template <> struct Interval<bf16> {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
+  u16x2 least, width;
+  // the first 16-bit key whose value is at least x (zeros of both signs are
+  // one value: the lower key of the two)
+  static __device__ __forceinline__ uint32_t ceil_key(float x) {
+    const uint32_t k = key_of(clean(x));
+    const uint32_t k16 = k >> 31 ? (uint32_t)(((u64)k + 0xFFFFu) >> 16) : k >> 16;
+    return k16 == 0x8000u ? 0x7FFFu : k16;
+  }
+  __device__ __forceinline__ Interval(float from, float to) {
+    const uint32_t a = ceil_key(from), b = to == __builtin_inff() ? 0xFF81u : ceil_key(to);
+    least = (uint16_t)a;
+    width = (uint16_t)(b > a ? b - a : 0);
+  }
+  template <int N> __device__ __forceinline__ uint32_t accepted(const typename RowVec<bf16>::type (&v)[N]) const {
+    uint32_t mask = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const u32x4 w = __builtin_bit_cast(u32x4, v[j]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const i16x2 s = __builtin_bit_cast(i16x2, (uint32_t)w[q]);
+        const u16x2 key = __builtin_bit_cast(u16x2, s) ^ (__builtin_bit_cast(u16x2, (i16x2)(s >> 15)) | (uint16_t)0x8000);
+        const u16x2 d = key - least;
+        uint32_t in;   // (spelled out: the compiler would make two compares and selects of it)
+        asm("v_pk_sub_u16 %0, %1, %2 clamp\n\tv_pk_min_u16 %0, %0, 1 op_sel_hi:[1,0]" : "=v"(in) : "v"(width), "v"(d));
+        mask = mask << 1 | in;
+      }
+    }
+    return mask;
+  }
+  // bit 15 - p (first of a pair) or 31 - p (second) of a full mask of four
+  // vectors is pair p
+  static __device__ __forceinline__ int bit(int b, int n) { return 2 * (4 * n - 1 - (b & 15)) + (b >> 4); }
+};
+
 // The candidates of a row in LDS.
 template <typename T>
 struct Candidates {
@@ -763,7 +840,7 @@ struct Candidates {
   // overflow the list.
   __device__ __forceinline__ bool collect(const T* z, int64_t V, const uint32_t* gmax, float from, float to) {
     const uint32_t least = key_of(clean(from));
-    const bool open = to == __builtin_inff();
+    const Interval<T> in(from, to);
     constexpr int E = RowVec<T>::E, kLanes = kGroup / E, kPass = kRowThreads / kLanes, kUnroll = 4;
     const int t = threadIdx.x, lane = t & 63;
     const int groups = (int)((V + kGroup - 1) / kGroup);
@@ -799,53 +876,52 @@ struct Candidates {
       }
       __syncthreads();
       // kLanes lanes take a group, kUnroll groups in a row; a lane's accepted
-      // logits are the bits of a mask, and their indices go into the list
-      const int ng = sh.groups;
-      for (int i0 = t / kLanes; i0 - t / kLanes < ng; i0 += kPass * kUnroll) {
-        typename RowVec<T>::type v[kUnroll];
-        int c[kUnroll];
+      // logits are the bits of a mask, and the list first holds where they are
+      const int ng = sh.groups, before = sh.count;
+      __syncthreads();
+      typename RowVec<T>::type v[kUnroll], next[kUnroll];
+      auto load = [&](typename RowVec<T>::type (&to)[kUnroll], int i0) {
 #pragma unroll
         for (int j = 0; j < kUnroll; ++j) {
           const int i = i0 + j * kPass;
-          c[j] = i < ng ? (g0 + (int)sh.glist[i]) * kGroup + (t % kLanes) * E : (int)V;
+          const int c = i < ng ? (g0 + (int)sh.glist[i]) * kGroup + (t % kLanes) * E : (int)V;
 #pragma unroll
-          for (int e = 0; e < E; ++e) v[j][e] = (T)kNegInf;
-          if (c[j] < V) v[j] = load_row(z, c[j], V, kNegInf);
+          for (int e = 0; e < E; ++e) to[j][e] = (T)kNegInf;
+          if (c < V) to[j] = load_row(z, c, V, kNegInf);
         }
-        uint32_t mask = 0;
+      };
+      load(next, t / kLanes);
+      for (int i0 = t / kLanes; i0 - t / kLanes < ng; i0 += kPass * kUnroll) {
 #pragma unroll
-        for (int j = 0; j < kUnroll; ++j)
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const float x = to_f32(v[j][e]);   // NaN fails both comparisons
-            mask |= (x >= from && (open || x < to) ? 1u : 0u) << (j * E + e);
-          }
-        u64 all;
-        const int mine = __builtin_popcount(mask);
-        int pos = (int)wave_scan_u64((u64)mine, all) - mine;
+        for (int j = 0; j < kUnroll; ++j) v[j] = next[j];
+        if (i0 - t / kLanes + kPass * kUnroll < ng) load(next, i0 + kPass * kUnroll);
+        uint32_t mask = in.template accepted<kUnroll>(v);
+        uint32_t all;
+        const uint32_t mine = (uint32_t)__builtin_popcount(mask);
+        int pos = (int)(wave_scan_u32(mine, all) - mine);
         if (!all) continue;
         int at = 0;
         if (lane == 0) at = atomicAdd(&sh.count, (int)all);
         pos += __builtin_amdgcn_readfirstlane(at);
+        const uint32_t code = (uint32_t)i0 << 16 | (uint32_t)(t % kLanes) << 8;
         while (__builtin_amdgcn_ballot_w64(mask != 0)) {
-          const int b = __builtin_ctz(mask | 0x80000000u);
-          int base = c[0];
-#pragma unroll
-          for (int j = 1; j < kUnroll; ++j) base = b >= j * E ? c[j] : base;
-          if (mask && pos < kList) sh.list[pos] = (u64)(base + b % E);
+          if (mask && pos < kList) sh.list[pos] = code + (uint32_t)__builtin_ctz(mask);
           ++pos;
           mask &= mask - 1;
         }
       }
-    }
-    __syncthreads();
-    n = sh.count;
-    if (n > kList) return false;
-    // indices to composites
+      __syncthreads();
+      n = sh.count;
+      if (n > kList) return false;
+      // places to composites
 #pragma unroll 4
-    for (int i = t; i < n; i += kRowThreads) {
-      const int64_t at = (int64_t)sh.list[i];
-      sh.list[i] = composite(key_of(clean(to_f32(z[at]))), at);
+      for (int i = before + t; i < n; i += kRowThreads) {
+        const uint32_t code = (uint32_t)sh.list[i];
+        const int b = Interval<T>::bit((int)(code & 255u), kUnroll);
+        const int g = sh.glist[(int)(code >> 16) + b / E * kPass];
+        const int64_t at = (int64_t)(g0 + g) * kGroup + (int)(code >> 8 & 255u) * E + b % E;
+        sh.list[i] = composite(key_of(clean(to_f32(z[at]))), at);
+      }
     }
     __syncthreads();
     return true;
@@ -1073,19 +1149,9 @@ __device__ __forceinline__ bool pick_by_pieces(const SampleArgs& a, const T* z, 
     // the kept weight by pieces
     for (int i = threadIdx.x; i < a.pieces; i += kRowThreads) sh.cmass[i] = 0;
     __syncthreads();
-    // (one addition per wave and piece: neighbours in the list share pieces)
-    for (int i0 = 0; i0 < list.n; i0 += kRowThreads) {
-      const int i = i0 + (int)threadIdx.x;
-      const u64 x = i < list.n ? sh.list[i] : 0;
-      const u64 wx = x >= c ? wt(x) : 0;
-      const int piece = (int)(index_in(x) / kPiece);
-      for (u64 left = __builtin_amdgcn_ballot_w64(wx != 0); left;) {
-        const int p = __builtin_amdgcn_readlane(piece, __builtin_ctzll(left));
-        const u64 sum = wave_sum_u64(piece == p ? wx : 0);
-        if ((threadIdx.x & 63) == 0) atomicAdd(&sh.cmass[p], sum);
-        left &= ~__builtin_amdgcn_ballot_w64(piece == p);
-      }
-    }
+    list.each([&](u64 x) {
+      if (x >= c) atomicAdd(&sh.cmass[index_in(x) / kPiece], wt(x));
+    });
     each_slot([&](int i, int slot, u64 w) {   // a wave's slots are of one piece
       const u64 sum = wave_sum_u64(slot < border ? w : 0);
       if (sum && (threadIdx.x & 63) == 0) atomicAdd(&sh.cmass[i], sum);

@@ -139,25 +139,17 @@ __device__ __forceinline__ u64 wave_scan_u64(u64 x, u64& all) {
   return x;
 }
 
-// The value of lane ^ d, d a power of two below 64.
-__device__ __forceinline__ uint32_t lane_xor_u32(uint32_t x, int d) {
-  switch (d) {
-    case 1: return dpp_u32<0xB1>(x);
-    case 2: return dpp_u32<0x4E>(x);
-    case 4: return dpp_u32<0x1B>(dpp_u32<0x141>(x));   // mirrored within 8 (^ 7), then within 4 (^ 3)
-    case 8: return dpp_u32<0x128>(x);   // rotated by 8 of 16
-    case 16: {
-      const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
-      return (threadIdx.x & 16) ? r[0] : r[1];
-    }
-    default: {
-      const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
-      return (threadIdx.x & 32) ? r[0] : r[1];
-    }
-  }
-}
-__device__ __forceinline__ u64 lane_xor_u64(u64 x, int d) {
-  return (u64)lane_xor_u32((uint32_t)(x >> 32), d) << 32 | lane_xor_u32((uint32_t)x, d);
+__device__ __forceinline__ uint32_t wave_scan_u32(uint32_t x, uint32_t& all) {
+  x += dpp_u32<0x111>(x);
+  x += dpp_u32<0x112>(x);
+  x += dpp_u32<0x114>(x);
+  x += dpp_u32<0x118>(x);
+  auto lane = [](uint32_t v, int l) { return (uint32_t)__builtin_amdgcn_readlane((int)v, l); };
+  const uint32_t a = lane(x, 15), b = a + lane(x, 31), c = b + lane(x, 47);
+  const int l = threadIdx.x & 63;
+  x += l < 16 ? 0 : l < 32 ? a : l < 48 ? b : c;
+  all = lane(x, 63);
+  return x;
 }
 
 }  // namespace flce
