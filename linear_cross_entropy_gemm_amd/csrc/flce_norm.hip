@@ -71,83 +71,130 @@ __device__ __forceinline__ void load_param(float (&out)[E], const void* p, int c
   }
 }
 
-// Sum of a and b over the kRow threads of a row (every thread gets both).
+// Sums of N values over the kRow threads of a row (every thread gets them).
 // Rows wider than a wave go through LDS; `buf` alternates between calls so
 // that one barrier per call is enough.
-template <int kRow>
-__device__ __forceinline__ void row_sum2(float& a, float& b, float (&lds)[2][2][16], int& buf) {
-  a = wave_sum(a);
-  b = wave_sum(b);
+template <int N> using SumLds = float[2][N][16];
+template <int kRow, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], SumLds<N>& lds, int& buf) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
   if (kRow == 64) return;
   const int w = threadIdx.x >> 6;
   if ((threadIdx.x & 63) == 0) {
-    lds[buf][0][w] = a;
-    lds[buf][1][w] = b;
+#pragma unroll
+    for (int i = 0; i < N; ++i) lds[buf][i][w] = v[i];
   }
   __syncthreads();
-  a = 0.0f;
-  b = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kRow / 64; ++i) {
-    a += lds[buf][0][i];
-    b += lds[buf][1][i];
+  for (int i = 0; i < N; ++i) {
+    v[i] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kRow / 64; ++k) v[i] += lds[buf][i][k];
   }
   buf ^= 1;
 }
 
+// Mean and 1 / standard deviation of a row from its waves' own: a wave's mean
+// and sum of squared deviations from it need no barrier, and
+//   mean = sum n_w mean_w / H,  sum of squares = sum (q_w + n_w (mean_w - mean)^2)
+// joins them behind one.  Neither a far mean nor an outlier costs accuracy.
 // kRow threads hold a row in kVec vectors each; a work-group holds kRows
 // rows (more than one only where a row is one wave) and walks over the rows
 // in steps of the grid, the next row's loads issued before the current row's
 // sums.
-template <typename T, typename WT, int kRow, int kVec, int kRows>
-__global__ __launch_bounds__(kRow* kRows) void ln_fwd_kernel(LnFwdArgs p) {
+template <typename T, typename WT, int kRow, int kVec, int kRows, int kEu>
+__global__ __launch_bounds__(kRow* kRows) __attribute__((amdgpu_waves_per_eu(kEu))) void ln_fwd_kernel(LnFwdArgs p) {
   static_assert(kRow == 64 || kRows == 1, "a work-group barrier must see one row");
-  constexpr int E = RowVec<T>::E;
+  constexpr int E = RowVec<T>::E, kWaves = kRow / 64;
   typedef typename RowVec<T>::type vec_t;
-  __shared__ float lds[2][2][16];
+  __shared__ float lds[2][2][kWaves];
   int buf = 0;
-  const int t = threadIdx.x % kRow;
+  const int t = threadIdx.x % kRow, wave = t >> 6;
   const int64_t step = (int64_t)gridDim.x * kRows;
   int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / kRow;
   if (row >= p.M) return;   // whole waves (kRow = 64) or the whole work-group
   vec_t cur[kVec], nxt[kVec];
+  auto load = [&](vec_t (&to)[kVec], int64_t from) {
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) cur[i] = load_row(static_cast<const T*>(p.x) + row * p.ldx, (t + i * kRow) * E, p.H);
+    for (int i = 0; i < kVec; ++i)
+      to[i] = load_clamped(static_cast<const T*>(p.x) + from * p.ldx, (t + i * kRow) * E, p.H);
+  };
+  // elements that wave w holds
+  auto count = [&](int w) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const int left = p.H - (w * 64 + i * kRow) * E;
+      n += left < 0 ? 0 : left < 64 * E ? left : 64 * E;
+    }
+    return (float)n;
+  };
+  load(cur, row);
   float w[kVec][E], b[kVec][E];
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
     load_param<WT>(w[i], p.weight, (t + i * kRow) * E, p.H, 1.0f);
     load_param<WT>(b[i], p.bias, (t + i * kRow) * E, p.H, 0.0f);
   }
-  const float inv = 1.0f / (float)p.H;
+  const float inv = 1.0f / (float)p.H, mine = count(wave), inv_mine = mine > 0.0f ? 1.0f / mine : 0.0f;
   for (; row < p.M; row += step) {
-    const bool more = row + step < p.M;
-    if (more) {
+    if (row + step < p.M) load(nxt, row + step);
+    float s = 0.0f;
 #pragma unroll
-      for (int i = 0; i < kVec; ++i)
-        nxt[i] = load_row(static_cast<const T*>(p.x) + (row + step) * p.ldx, (t + i * kRow) * E, p.H);
-    }
-    float s = 0.0f, zero = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kVec; ++i)
+    for (int i = 0; i < kVec; ++i) {
+      row_tail<T>(cur[i], (t + i * kRow) * E, p.H);
 #pragma unroll
       for (int e = 0; e < E; ++e) s += to_f32(cur[i][e]);
-    row_sum2<kRow>(s, zero, lds, buf);
-    const float mean0 = s * inv;
+    }
+    const float m0 = wave_sum(s) * inv_mine;
     // squares of the deviations, and the deviations' own sum: what the
-    // rounding of the first mean left over is taken out of both results
+    // rounding of m0 left over is taken out of both results
     float d1 = 0.0f, d2 = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kVec; ++i)
+    for (int i = 0; i < kVec; ++i) {
+      const int left = p.H - (t + i * kRow) * E;
+      if (__builtin_amdgcn_ballot_w64(left < E)) {   // the row ends in this wave's vectors
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float d = (t + i * kRow) * E + e < p.H ? to_f32(cur[i][e]) - mean0 : 0.0f;
-        d1 += d;
-        d2 = __builtin_fmaf(d, d, d2);
+        for (int e = 0; e < E; ++e) {
+          const float x = e < left ? to_f32(cur[i][e]) - m0 : 0.0f;
+          d1 += x;
+          d2 = __builtin_fmaf(x, x, d2);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float x = to_f32(cur[i][e]) - m0;
+          d1 += x;
+          d2 = __builtin_fmaf(x, x, d2);
+        }
       }
-    row_sum2<kRow>(d1, d2, lds, buf);
-    const float rest = d1 * inv;
-    const float var = __builtin_fmaf(-rest, rest, d2 * inv);
+    }
+    d1 = wave_sum(d1);
+    d2 = wave_sum(d2);
+    const float rest0 = d1 * inv_mine, q0 = __builtin_fmaf(-rest0, d1, d2);
+    // the row's mean is m + rest
+    float m = m0, rest = rest0, q = q0;
+    if (kRow > 64) {
+      if ((threadIdx.x & 63) == 0) {
+        lds[buf][0][wave] = m0 + rest0;
+        lds[buf][1][wave] = q0;
+      }
+      __syncthreads();
+      m = lds[buf][0][0];   // deviations of the waves' means from the first
+      rest = 0.0f;
+#pragma unroll
+      for (int i = 1; i < kWaves; ++i) rest = __builtin_fmaf(count(i), lds[buf][0][i] - m, rest);
+      rest *= inv;
+      q = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kWaves; ++i) {
+        const float d = (lds[buf][0][i] - m) - rest, n = count(i);
+        q += n > 0.0f ? __builtin_fmaf(n * d, d, lds[buf][1][i]) : 0.0f;
+      }
+      buf ^= 1;
+    }
+    const float var = q * inv;
     const float rstd = 1.0f / sqrtf((var > 0.0f ? var : var == var ? 0.0f : var) + p.eps);
     T* yr = static_cast<T*>(p.y) + row * p.ldy;
 #pragma unroll
@@ -155,19 +202,17 @@ __global__ __launch_bounds__(kRow* kRows) void ln_fwd_kernel(LnFwdArgs p) {
       vec_t o;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const float xh = ((to_f32(cur[i][e]) - mean0) - rest) * rstd;
+        const float xh = ((to_f32(cur[i][e]) - m) - rest) * rstd;
         o[e] = (T)__builtin_fmaf(xh, w[i][e], b[i][e]);
       }
       store_row(yr, (t + i * kRow) * E, p.H, o);
     }
     if (t == 0) {
-      if (p.mean) p.mean[row] = mean0 + rest;
+      if (p.mean) p.mean[row] = m + rest;
       if (p.rstd) p.rstd[row] = rstd;
     }
-    if (more) {
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) cur[i] = nxt[i];
-    }
+    for (int i = 0; i < kVec; ++i) cur[i] = nxt[i];
   }
 }
 
@@ -179,32 +224,33 @@ template <typename T, typename WT>
 __global__ __launch_bounds__(kWide) void ln_fwd_wide_kernel(LnFwdArgs p) {
   constexpr int E = RowVec<T>::E;
   typedef typename RowVec<T>::type vec_t;
-  __shared__ float lds[2][2][16];
-  int buf = 0;
+  __shared__ SumLds<1> lds1;
+  __shared__ SumLds<2> lds2;
+  int buf = 0, buf2 = 0;
   const float inv = 1.0f / (float)p.H;
   for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
     const T* xr = static_cast<const T*>(p.x) + row * p.ldx;
-    float s = 0.0f, zero = 0.0f;
+    float s[1] = {0.0f};
     for (int c = threadIdx.x * E; c < p.H; c += kWide * E) {
       const vec_t v = load_row(xr, c, p.H);
 #pragma unroll
-      for (int e = 0; e < E; ++e) s += to_f32(v[e]);
+      for (int e = 0; e < E; ++e) s[0] += to_f32(v[e]);
     }
-    row_sum2<kWide>(s, zero, lds, buf);
-    const float mean0 = s * inv;
-    float d1 = 0.0f, d2 = 0.0f;
+    row_sums<kWide>(s, lds1, buf);
+    const float mean0 = s[0] * inv;
+    float dev[2] = {0.0f, 0.0f};
     for (int c = threadIdx.x * E; c < p.H; c += kWide * E) {
       const vec_t v = load_row(xr, c, p.H);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const float d = c + e < p.H ? to_f32(v[e]) - mean0 : 0.0f;
-        d1 += d;
-        d2 = __builtin_fmaf(d, d, d2);
+        dev[0] += d;
+        dev[1] = __builtin_fmaf(d, d, dev[1]);
       }
     }
-    row_sum2<kWide>(d1, d2, lds, buf);
-    const float rest = d1 * inv;
-    const float var = __builtin_fmaf(-rest, rest, d2 * inv);
+    row_sums<kWide>(dev, lds2, buf2);
+    const float rest = dev[0] * inv;
+    const float var = __builtin_fmaf(-rest, rest, dev[1] * inv);
     const float rstd = 1.0f / sqrtf((var > 0.0f ? var : var == var ? 0.0f : var) + p.eps);
     T* yr = static_cast<T*>(p.y) + row * p.ldy;
     for (int c = threadIdx.x * E; c < p.H; c += kWide * E) {
@@ -225,27 +271,30 @@ __global__ __launch_bounds__(kWide) void ln_fwd_wide_kernel(LnFwdArgs p) {
   }
 }
 
-template <typename T, typename WT, int kRow, int kVec, int kRows>
-__global__ __launch_bounds__(kRow* kRows) void ln_bwd_kernel(LnBwdArgs p) {
+template <typename T, typename WT, int kRow, int kVec, int kRows, int kEu>
+__global__ __launch_bounds__(kRow* kRows) __attribute__((amdgpu_waves_per_eu(kEu))) void ln_bwd_kernel(LnBwdArgs p) {
   static_assert(kRow == 64 || kRows == 1, "a work-group barrier must see one row");
   constexpr int E = RowVec<T>::E;
   typedef typename RowVec<T>::type vec_t;
-  __shared__ float lds[2][2][16];
+  __shared__ SumLds<2> lds;
   int buf = 0;
   const int t = threadIdx.x % kRow, sub = threadIdx.x / kRow;
   const int64_t step = (int64_t)gridDim.x * kRows;
   int64_t row = (int64_t)blockIdx.x * kRows + sub;
-  vec_t cx[kVec], cd[kVec], nx[kVec], nd[kVec];
-  float mean = 0.0f, rstd = 0.0f, nmean = 0.0f, nrstd = 0.0f;
-  if (row < p.M) {
+  struct Rows {
+    vec_t x[kVec], d[kVec];
+    float mean, rstd;
+  } cur, nxt;
+  auto load = [&](Rows& to, int64_t from) {
+    to.mean = p.mean[from];
+    to.rstd = p.rstd[from];
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-      cx[i] = load_row(static_cast<const T*>(p.x) + row * p.ldx, (t + i * kRow) * E, p.H);
-      cd[i] = load_row(static_cast<const T*>(p.dy) + row * p.ldy, (t + i * kRow) * E, p.H);
+      to.x[i] = load_clamped(static_cast<const T*>(p.x) + from * p.ldx, (t + i * kRow) * E, p.H);
+      to.d[i] = load_clamped(static_cast<const T*>(p.dy) + from * p.ldy, (t + i * kRow) * E, p.H);
     }
-    mean = p.mean[row];
-    rstd = p.rstd[row];
-  }
+  };
+  if (row < p.M) load(cur, row);
   float w[kVec][E], dw[kVec][E], db[kVec][E];
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
@@ -255,52 +304,39 @@ __global__ __launch_bounds__(kRow* kRows) void ln_bwd_kernel(LnBwdArgs p) {
   }
   const float inv = 1.0f / (float)p.H;
   for (; row < p.M; row += step) {
-    const bool more = row + step < p.M;
-    if (more) {
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        nx[i] = load_row(static_cast<const T*>(p.x) + (row + step) * p.ldx, (t + i * kRow) * E, p.H);
-        nd[i] = load_row(static_cast<const T*>(p.dy) + (row + step) * p.ldy, (t + i * kRow) * E, p.H);
-      }
-      nmean = p.mean[row + step];
-      nrstd = p.rstd[row + step];
-    }
+    if (row + step < p.M) load(nxt, row + step);
     // columns past the row's end hold dy = 0 and add nothing to any sum
-    float s1 = 0.0f, s2 = 0.0f;
+    float s[2] = {0.0f, 0.0f}, xh[kVec][E];
 #pragma unroll
-    for (int i = 0; i < kVec; ++i)
+    for (int i = 0; i < kVec; ++i) {
+      row_tail<T>(cur.x[i], (t + i * kRow) * E, p.H);
+      row_tail<T>(cur.d[i], (t + i * kRow) * E, p.H);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const float d = to_f32(cd[i][e]), xh = (to_f32(cx[i][e]) - mean) * rstd, g = d * w[i][e];
-        s1 += g;
-        s2 = __builtin_fmaf(g, xh, s2);
-        dw[i][e] = __builtin_fmaf(d, xh, dw[i][e]);
+        const float d = to_f32(cur.d[i][e]), g = d * w[i][e];
+        xh[i][e] = (to_f32(cur.x[i][e]) - cur.mean) * cur.rstd;
+        s[0] += g;
+        s[1] = __builtin_fmaf(g, xh[i][e], s[1]);
+        dw[i][e] = __builtin_fmaf(d, xh[i][e], dw[i][e]);
         db[i][e] += d;
       }
+    }
     if (p.dx) {
-      row_sum2<kRow>(s1, s2, lds, buf);
-      const float m1 = s1 * inv, m2 = s2 * inv;
+      row_sums<kRow>(s, lds, buf);
+      const float m1 = s[0] * inv, m2 = s[1] * inv * cur.rstd;
       T* gr = static_cast<T*>(p.dx) + row * p.ldg;
 #pragma unroll
       for (int i = 0; i < kVec; ++i) {
         vec_t o;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          const float xh = (to_f32(cx[i][e]) - mean) * rstd;
-          o[e] = (T)((__builtin_fmaf(to_f32(cd[i][e]), w[i][e], -m1) - xh * m2) * rstd);
+          const float g = __builtin_fmaf(to_f32(cur.d[i][e]), w[i][e], -m1);
+          o[e] = (T)__builtin_fmaf(g, cur.rstd, -(xh[i][e] * m2));
         }
         store_row(gr, (t + i * kRow) * E, p.H, o);
       }
     }
-    if (more) {
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        cx[i] = nx[i];
-        cd[i] = nd[i];
-      }
-      mean = nmean;
-      rstd = nrstd;
-    }
+    cur = nxt;
   }
   if (!p.partial) return;
   float* out = p.partial + (int64_t)blockIdx.x * 2 * p.H;
@@ -342,14 +378,14 @@ template <typename T, typename WT>
 __global__ __launch_bounds__(kWide) void ln_bwd_wide_kernel(LnBwdArgs p) {
   constexpr int E = RowVec<T>::E;
   typedef typename RowVec<T>::type vec_t;
-  __shared__ float lds[2][2][16];
+  __shared__ SumLds<2> lds;
   int buf = 0;
   const float inv = 1.0f / (float)p.H;
   for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
     const T* xr = static_cast<const T*>(p.x) + row * p.ldx;
     const T* dr = static_cast<const T*>(p.dy) + row * p.ldy;
     const float mean = p.mean[row], rstd = p.rstd[row];
-    float s1 = 0.0f, s2 = 0.0f;
+    float s[2] = {0.0f, 0.0f};
     for (int c = threadIdx.x * E; c < p.H; c += kWide * E) {
       const vec_t x = load_row(xr, c, p.H), d = load_row(dr, c, p.H);
       float w[E];
@@ -357,12 +393,12 @@ __global__ __launch_bounds__(kWide) void ln_bwd_wide_kernel(LnBwdArgs p) {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const float g = to_f32(d[e]) * w[e];
-        s1 += g;
-        s2 = __builtin_fmaf(g, (to_f32(x[e]) - mean) * rstd, s2);
+        s[0] += g;
+        s[1] = __builtin_fmaf(g, (to_f32(x[e]) - mean) * rstd, s[1]);
       }
     }
-    row_sum2<kWide>(s1, s2, lds, buf);
-    const float m1 = s1 * inv, m2 = s2 * inv;
+    row_sums<kWide>(s, lds, buf);
+    const float m1 = s[0] * inv, m2 = s[1] * inv;
     T* gr = static_cast<T*>(p.dx) + row * p.ldg;
     for (int c = threadIdx.x * E; c < p.H; c += kWide * E) {
       const vec_t x = load_row(xr, c, p.H), d = load_row(dr, c, p.H);
@@ -428,30 +464,43 @@ constexpr int64_t kMaxRegVecs = 2048;
 
 int64_t row_vecs(int64_t H, int dtype) { return ceil_div(H, dtype == FLCE_DTYPE_BF16 ? 8 : 4); }
 
+// Work-groups for `sets` of rows, at most `most`: as few as leave every one
+// the same number of steps.
+int64_t even_grid(int64_t sets, int64_t most) {
+  if (sets <= most) return sets;
+  return ceil_div(sets, ceil_div(sets, most));
+}
+
 // Groups of rows that ln_bwd_kernel (or ln_param_grad_kernel) sums dw and db
 // over, one partial each.
 int64_t bwd_groups(int64_t M, int64_t H, int dtype) {
   const int64_t v = row_vecs(H, dtype);
-  int64_t g;
-  if (v <= 128) g = ceil_div(M, 4);            // four one-wave rows per work-group
-  else g = M;
-  const int64_t most = v <= 128 ? 1024 : v <= 512 ? 1024 : v <= kMaxRegVecs ? 512 : 64;
-  return g < most ? g : most;
+  if (v <= 64) return even_grid(ceil_div(M, 4), 1024);
+  if (v <= 128) return even_grid(ceil_div(M, 4), 512);
+  if (v <= 256) return even_grid(ceil_div(M, 4), 256);
+  if (v <= 512) return even_grid(M, 512);
+  if (v <= kMaxRegVecs) return even_grid(M, 256);
+  return M < 64 ? M : 64;
 }
 
+// Threads, vectors per thread and resident work-groups by the row's length,
+// as measured at 218 MB of rows in and out (bf16 rows, fp32 parameters; TB/s,
+// the next best shape in brackets; a plain copy of as much reaches 5.4):
+//   H      512       1024      2048      4096      6656      16384
+//   fwd    4.9       5.1       5.1       5.0       4.2       4.0
+//          [4.4]     [4.6]     [5.0]     [4.8]     [3.9]     [4.1 at 1024 threads]
+//   bwd    5.2       5.4       5.1       4.9       4.1       4.1
+//          [4.8]     [4.8]     [4.9]     [4.9]     [4.0]     [3.0]
 template <typename T, typename WT>
 void launch_fwd(const LnFwdArgs& p, int dtype, hipStream_t st) {
   const int64_t v = row_vecs(p.H, dtype);
-  auto grid = [&](int rows, int64_t most) {
-    const int64_t g = ceil_div(p.M, rows);
-    return (unsigned)(g < most ? g : most);
-  };
-  if (v <= 64) ln_fwd_kernel<T, WT, 64, 1, 4><<<grid(4, 2048), 256, 0, st>>>(p);
-  else if (v <= 128) ln_fwd_kernel<T, WT, 64, 2, 4><<<grid(4, 2048), 256, 0, st>>>(p);
-  else if (v <= 256) ln_fwd_kernel<T, WT, 256, 1, 1><<<grid(1, 2048), 256, 0, st>>>(p);
-  else if (v <= 512) ln_fwd_kernel<T, WT, 512, 1, 1><<<grid(1, 1024), 512, 0, st>>>(p);
-  else if (v <= 1024) ln_fwd_kernel<T, WT, 1024, 1, 1><<<grid(1, 512), 1024, 0, st>>>(p);
-  else if (v <= kMaxRegVecs) ln_fwd_kernel<T, WT, 1024, 2, 1><<<grid(1, 512), 1024, 0, st>>>(p);
+  auto grid = [&](int rows, int64_t most) { return (unsigned)even_grid(ceil_div(p.M, rows), most); };
+  if (v <= 64) ln_fwd_kernel<T, WT, 64, 1, 4, 1><<<grid(4, 4096), 256, 0, st>>>(p);
+  else if (v <= 128) ln_fwd_kernel<T, WT, 64, 2, 4, 1><<<grid(4, 1024), 256, 0, st>>>(p);
+  else if (v <= 256) ln_fwd_kernel<T, WT, 64, 4, 4, 1><<<grid(4, 512), 256, 0, st>>>(p);
+  else if (v <= 512) ln_fwd_kernel<T, WT, 128, 4, 1, 1><<<grid(1, 1536), 128, 0, st>>>(p);
+  else if (v <= 1024) ln_fwd_kernel<T, WT, 256, 4, 1, 3><<<grid(1, 768), 256, 0, st>>>(p);
+  else if (v <= kMaxRegVecs) ln_fwd_kernel<T, WT, 512, 4, 1, 1><<<grid(1, 256), 512, 0, st>>>(p);
   else ln_fwd_wide_kernel<T, WT><<<grid(1, 65536), kWide, 0, st>>>(p);
 }
 
@@ -459,12 +508,12 @@ template <typename T, typename WT>
 void launch_bwd(const LnBwdArgs& p, int dtype, hipStream_t st) {
   const int64_t v = row_vecs(p.H, dtype);
   const unsigned g = (unsigned)bwd_groups(p.M, p.H, dtype);
-  if (v <= 64) ln_bwd_kernel<T, WT, 64, 1, 4><<<g, 256, 0, st>>>(p);
-  else if (v <= 128) ln_bwd_kernel<T, WT, 64, 2, 4><<<g, 256, 0, st>>>(p);
-  else if (v <= 256) ln_bwd_kernel<T, WT, 256, 1, 1><<<g, 256, 0, st>>>(p);
-  else if (v <= 512) ln_bwd_kernel<T, WT, 512, 1, 1><<<g, 512, 0, st>>>(p);
-  else if (v <= 1024) ln_bwd_kernel<T, WT, 1024, 1, 1><<<g, 1024, 0, st>>>(p);
-  else if (v <= kMaxRegVecs) ln_bwd_kernel<T, WT, 1024, 2, 1><<<g, 1024, 0, st>>>(p);
+  if (v <= 64) ln_bwd_kernel<T, WT, 64, 1, 4, 1><<<g, 256, 0, st>>>(p);
+  else if (v <= 128) ln_bwd_kernel<T, WT, 64, 2, 4, 1><<<g, 256, 0, st>>>(p);
+  else if (v <= 256) ln_bwd_kernel<T, WT, 64, 4, 4, 1><<<g, 256, 0, st>>>(p);
+  else if (v <= 512) ln_bwd_kernel<T, WT, 256, 2, 1, 1><<<g, 256, 0, st>>>(p);
+  else if (v <= 1024) ln_bwd_kernel<T, WT, 512, 2, 1, 1><<<g, 512, 0, st>>>(p);
+  else if (v <= kMaxRegVecs) ln_bwd_kernel<T, WT, 512, 4, 1, 1><<<g, 512, 0, st>>>(p);
   else {
     if (p.dx) ln_bwd_wide_kernel<T, WT><<<(unsigned)(p.M < 65536 ? p.M : 65536), kWide, 0, st>>>(p);
     if (p.partial) ln_param_grad_kernel<T><<<dim3((unsigned)ceil_div(p.H, 256), g), 256, 0, st>>>(p);

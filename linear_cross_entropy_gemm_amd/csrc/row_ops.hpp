@@ -41,12 +41,36 @@ __device__ __forceinline__ typename RowVec<T>::type load_row(const T* p, int64_t
   return v;
 }
 
+// The same in two steps, for loads that stay under way: load_clamped reads a
+// whole vector at `col`, or the row's last whole one where that would cross or
+// lie past the row's end (rows of at least one vector); row_tail, at the
+// vector's use, moves the elements that belong to it down and clears the rest.
+template <typename T>
+__device__ __forceinline__ typename RowVec<T>::type load_clamped(const T* p, int col, int n) {
+  constexpr int E = RowVec<T>::E;
+  if (n < E) return load_row(p, col, n);
+  return *reinterpret_cast<const typename RowVec<T>::mem*>(p + (col + E <= n ? col : n - E));
+}
+template <typename T>
+__device__ __forceinline__ void row_tail(typename RowVec<T>::type& v, int col, int n) {
+  constexpr int E = RowVec<T>::E;
+  const int over = n < E ? 0 : col + E - n;   // (shorter rows were read element by element)
+  if (!__builtin_amdgcn_ballot_w64(over > 0)) return;
+  u32x4 x = __builtin_bit_cast(u32x4, v);
+  if (over >= E) x = u32x4{0, 0, 0, 0};
+  const int k = over > 0 ? over * (8 / E) : 0;   // in halves of 2 bytes (bf16: elements)
+  if (k & 4) x = u32x4{x[2], x[3], 0, 0};
+  if (k & 2) x = u32x4{x[1], x[2], x[3], 0};
+  if (k & 1) x = u32x4{x[0] >> 16 | x[1] << 16, x[1] >> 16 | x[2] << 16, x[2] >> 16 | x[3] << 16, x[3] >> 16};
+  v = __builtin_bit_cast(typename RowVec<T>::type, x);
+}
+
 template <typename T>
 __device__ __forceinline__ void store_row(T* p, int64_t col, int64_t n, typename RowVec<T>::type v) {
   constexpr int E = RowVec<T>::E;
   if (col + E <= n) {
     *reinterpret_cast<typename RowVec<T>::mem*>(p + col) = v;
-  } else {
+  } else if (col < n) {
 #pragma unroll
     for (int e = 0; e < E; ++e)
       if (col + e < n) p[col + e] = v[e];
