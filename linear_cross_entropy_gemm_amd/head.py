@@ -37,8 +37,14 @@ class SampleOutputs:
     logprobs: Optional[torch.Tensor] = None  # [...] fp32, of the filtered distribution
 
 
-def _stream(dev) -> int:
-    return torch.cuda.current_stream(dev).cuda_stream
+def _enqueue(dev, call) -> int:
+    """call(stream) with the tensors' device current, on torch's current
+    stream there (the raw handle: a stream object costs as much as a launch)."""
+    index = dev.index
+    if index == torch.cuda.current_device():
+        return call(torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.device(dev):
+        return call(torch._C._cuda_getCurrentRawStream(index))
 
 
 def _rows(x: torch.Tensor) -> torch.Tensor:
@@ -63,22 +69,25 @@ def _check_rows(name: str, x: torch.Tensor) -> None:
 
 def _check_params(x: torch.Tensor, weight: Optional[torch.Tensor], bias: Optional[torch.Tensor]):
     """Contiguous weight and bias (None stays None) and their common dtype."""
+    def one(name, t):
+        if t.dtype not in _DTYPES:
+            raise TypeError(f"{name} must be bfloat16 or float32 (got {t.dtype})")
+        if t.dim() != 1 or t.shape[0] != x.shape[-1]:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, this call needs {(x.shape[-1],)}")
+        if t.device != x.device:
+            raise ValueError(f"{name} is on {t.device}, x is on {x.device}")
+        return t.contiguous()
+
     w_dtype = x.dtype
-    out = []
-    for name, t in (("weight", weight), ("bias", bias)):
-        if t is not None:
-            if t.dtype not in _DTYPES:
-                raise TypeError(f"{name} must be bfloat16 or float32 (got {t.dtype})")
-            if tuple(t.shape) != (x.shape[-1],):
-                raise ValueError(f"{name} has shape {tuple(t.shape)}, this call needs {(x.shape[-1],)}")
-            if t.device != x.device:
-                raise ValueError(f"{name} is on {t.device}, x is on {x.device}")
-            t = t.contiguous()
-            w_dtype = t.dtype
-        out.append(t)
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
-        raise TypeError(f"weight and bias must have one dtype (got {weight.dtype}, {bias.dtype})")
-    return out[0], out[1], w_dtype
+    if bias is not None:
+        bias = one("bias", bias)
+        w_dtype = bias.dtype
+    if weight is not None:
+        weight = one("weight", weight)
+        if bias is not None and weight.dtype != w_dtype:
+            raise TypeError(f"weight and bias must have one dtype (got {weight.dtype}, {w_dtype})")
+        w_dtype = weight.dtype
+    return weight, bias, w_dtype
 
 
 def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
@@ -92,15 +101,13 @@ def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias:
     M, H = x2.shape
     dev = x.device
     y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    stats = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=dev)
-    res = LayerNormForward(y, stats[0], stats[1])
-    with torch.cuda.device(dev):
-        rc = _lib.flce_layer_norm_fwd(_ptr(x2), x2.stride(0), _ptr(w), _ptr(b), M, H, eps, _ptr(y), H,
-                                      _ptr(res.mean), _ptr(res.rstd), _stream(dev), _DTYPES[x.dtype],
-                                      _DTYPES[w_dtype])
+    mean, rstd = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=dev).unbind(0)
+    rc = _enqueue(dev, lambda stream: _lib.flce_layer_norm_fwd(
+        x2.data_ptr(), x2.stride(0), _ptr(w), _ptr(b), M, H, eps, y.data_ptr(), H, mean.data_ptr(), rstd.data_ptr(),
+        stream, _DTYPES[x.dtype], _DTYPES[w_dtype]))
     if rc != _lib.FLCE_OK:
         raise _lib.FlceError(rc, "flce_layer_norm_fwd")
-    return res
+    return LayerNormForward(y, mean, rstd)
 
 
 def layer_norm_bwd(grad_y: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor], mean: torch.Tensor,
@@ -133,13 +140,17 @@ def layer_norm_bwd(grad_y: torch.Tensor, x: torch.Tensor, weight: Optional[torch
             raise _lib.FlceError(_lib.FLCE_EUNSUPPORTED, "flce_layer_norm_bwd_workspace_size")
         workspace = _workspace(workspace, ws_bytes, dev)
         ws_bytes = workspace.numel()
-    with torch.cuda.device(dev):
-        rc = _lib.flce_layer_norm_bwd(_ptr(g2), g2.stride(0), _ptr(x2), x2.stride(0), _ptr(w), _ptr(mean), _ptr(rstd),
-                                      M, H, _ptr(gx), H, _ptr(gw), _ptr(gb), _stream(dev), _DTYPES[x.dtype],
-                                      _DTYPES[w_dtype], _ptr(workspace) if need_params else None, ws_bytes)
+    rc = _enqueue(dev, lambda stream: _lib.flce_layer_norm_bwd(
+        g2.data_ptr(), g2.stride(0), x2.data_ptr(), x2.stride(0), _ptr(w), mean.data_ptr(), rstd.data_ptr(), M, H,
+        _ptr(gx), H, _ptr(gw), _ptr(gb), stream, _DTYPES[x.dtype], _DTYPES[w_dtype],
+        _ptr(workspace) if need_params else None, ws_bytes))
     if rc != _lib.FLCE_OK:
         raise _lib.FlceError(rc, "flce_layer_norm_bwd")
     return LayerNormGrads(gx, gw, gb)
+
+
+def _needs_grad(*tensors) -> bool:
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
 
 
 class _LayerNorm(torch.autograd.Function):
@@ -167,18 +178,20 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     """Differentiable layer norm over the last dimension of ``x``.  A row's
     statistics are kept for the backward pass, the normalised values are not:
     they are formed again from ``x``."""
+    if not _needs_grad(x, weight, bias):
+        return layer_norm_fwd(x, weight, bias, eps).y
     return _LayerNorm.apply(x, weight, bias, eps)
 
 
 def _dropout(x, p, seed, offset, residual) -> torch.Tensor:
     xc = x.contiguous()
-    rc_ = None if residual is None else residual.contiguous()
+    res = None if residual is None else residual.contiguous()
     dev = x.device
     y = torch.empty(x.shape, dtype=x.dtype, device=dev)
     tensor = torch.is_tensor(offset)
-    with torch.cuda.device(dev):
-        rc = _lib.flce_dropout(_ptr(xc), _ptr(rc_), _ptr(y), xc.numel(), p, seed, 0 if tensor else offset,
-                               _ptr(offset) if tensor else None, _stream(dev), _DTYPES[x.dtype])
+    rc = _enqueue(dev, lambda stream: _lib.flce_dropout(
+        xc.data_ptr(), _ptr(res), y.data_ptr(), xc.numel(), p, seed, 0 if tensor else offset,
+        offset.data_ptr() if tensor else None, stream, _DTYPES[x.dtype]))
     if rc != _lib.FLCE_OK:
         raise _lib.FlceError(rc, "flce_dropout")
     return y
@@ -226,6 +239,8 @@ def dropout(x: torch.Tensor, p: float, seed: int, offset: Union[int, torch.Tenso
                                  or residual.device != x.device):
         raise ValueError(f"residual must match x: {tuple(x.shape)} {x.dtype} on {x.device} (got "
                          f"{tuple(residual.shape)} {residual.dtype} on {residual.device})")
+    if not _needs_grad(x, residual):
+        return _dropout(x, float(p), seed, offset, residual)
     return _Dropout.apply(x, residual, float(p), seed, offset)
 
 
@@ -289,9 +304,9 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature: Union[float, torc
     workspace = _workspace(workspace, ws_bytes, dev)
     res = SampleOutputs(torch.empty(shape, dtype=torch.int64, device=dev),
                         torch.empty(shape, dtype=torch.float32, device=dev) if logprobs else None)
-    with torch.cuda.device(dev):
-        rc = _lib.flce_sample(_ptr(z), z.stride(0), _ptr(u), N, V, prm, _ptr(res.tokens), _ptr(res.logprobs),
-                              _stream(dev), dtype, _ptr(workspace), workspace.numel())
+    rc = _enqueue(dev, lambda stream: _lib.flce_sample(
+        z.data_ptr(), z.stride(0), u.data_ptr(), N, V, prm, res.tokens.data_ptr(), _ptr(res.logprobs), stream, dtype,
+        workspace.data_ptr(), workspace.numel()))
     del keep
     if rc != _lib.FLCE_OK:
         raise _lib.FlceError(rc, "flce_sample")
