@@ -321,7 +321,8 @@ int flce_scale_grads(const float* grad_scale, const void* grad_h_in, void* grad_
  * (NULL: not written) and are what flce_layer_norm_bwd takes.  Pointers need
  * the alignment of one element only.  eps > 0, finite.  y may be x itself
  * (then ld_y == ld_x) and must not overlap it otherwise.  Statistics and
- * arithmetic are fp32, y is rounded once.  Any H from 1 to 2^21, M < 2^31
+ * arithmetic are fp32, y is rounded once.  (A row whose deviations from
+ * the mean exceed 2^63 overflows their squares: rstd is 0 there.)  Any H from 1 to 2^21, M < 2^31
  * (else FLCE_EUNSUPPORTED); M = 0 does nothing.  Enqueued on `stream`;
  * nothing is allocated, nothing synchronises.  Returns FLCE_OK, FLCE_EINVAL,
  * FLCE_EUNSUPPORTED or FLCE_EDEVICE.

@@ -725,6 +725,7 @@ template <> struct Interval<float> {
     return mask;
   }
   static __device__ __forceinline__ int bit(int b, int) { return b; }
+  static __device__ __forceinline__ uint32_t bits_of_vector(int j) { return 0xFu << (4 * j); }
 };
 // bf16 pairs as 16-bit keys: with d = key - least, d < width where the
 // saturating difference width - d is not 0; two elements per instruction.
@@ -764,6 +765,7 @@ template <> struct Interval<bf16> {
   // bit 15 - p (first of a pair) or 31 - p (second) of a full mask of four
   // vectors is pair p
   static __device__ __forceinline__ int bit(int b, int n) { return 2 * (4 * n - 1 - (b & 15)) + (b >> 4); }
+  static __device__ __forceinline__ uint32_t bits_of_vector(int j) { return 0x000F000Fu << (12 - 4 * j); }
 };
 
 // The candidates of a row in LDS.
@@ -879,23 +881,39 @@ struct Candidates {
       // logits are the bits of a mask, and the list first holds where they are
       const int ng = sh.groups, before = sh.count;
       __syncthreads();
-      typename RowVec<T>::type v[kUnroll], next[kUnroll];
-      auto load = [&](typename RowVec<T>::type (&to)[kUnroll], int i0) {
+      // (loads without a branch stay under way: lanes past the last group read
+      // the first again, and a vector across the row's end is read once more)
+      struct Batch {
+        typename RowVec<T>::type v[kUnroll];
+        uint32_t ok;   // mask bits of the vectors that are groups
+        bool edge;
+      } cur, nxt;
+      auto place = [&](int i) { return (g0 + (int)sh.glist[i < ng ? i : 0]) * kGroup + (t % kLanes) * E; };
+      auto load = [&](Batch& to, int i0) {
+        to.ok = 0;
+        to.edge = false;
 #pragma unroll
         for (int j = 0; j < kUnroll; ++j) {
-          const int i = i0 + j * kPass;
-          const int c = i < ng ? (g0 + (int)sh.glist[i]) * kGroup + (t % kLanes) * E : (int)V;
-#pragma unroll
-          for (int e = 0; e < E; ++e) to[j][e] = (T)kNegInf;
-          if (c < V) to[j] = load_row(z, c, V, kNegInf);
+          const int i = i0 + j * kPass, c = place(i);
+          to.ok |= i < ng ? Interval<T>::bits_of_vector(j) : 0u;
+          to.edge |= c + E > V;
+          to.v[j] = *reinterpret_cast<const typename RowVec<T>::mem*>(z + (c + E <= V ? c : V - E));
         }
       };
-      load(next, t / kLanes);
+      if (ng > 0) load(nxt, t / kLanes);
       for (int i0 = t / kLanes; i0 - t / kLanes < ng; i0 += kPass * kUnroll) {
+        cur = nxt;
+        if (i0 - t / kLanes + kPass * kUnroll < ng) load(nxt, i0 + kPass * kUnroll);
+        if (__builtin_amdgcn_ballot_w64(cur.edge)) {
+#pragma unroll 1
+          for (int j = 0; j < kUnroll; ++j) {
+            const typename RowVec<T>::type x = load_row(z, place(i0 + j * kPass), V, kNegInf);
 #pragma unroll
-        for (int j = 0; j < kUnroll; ++j) v[j] = next[j];
-        if (i0 - t / kLanes + kPass * kUnroll < ng) load(next, i0 + kPass * kUnroll);
-        uint32_t mask = in.template accepted<kUnroll>(v);
+            for (int q = 0; q < kUnroll; ++q)
+              if (q == j) cur.v[q] = x;
+          }
+        }
+        uint32_t mask = in.template accepted<kUnroll>(cur.v) & cur.ok;
         uint32_t all;
         const uint32_t mine = (uint32_t)__builtin_popcount(mask);
         int pos = (int)(wave_scan_u32(mine, all) - mine);
@@ -1062,8 +1080,11 @@ __device__ __forceinline__ bool pick_bounded(const SampleArgs& a, const T* z, in
       break;
     }
   } else {
-    // w >= q: a little below max + t ln q in fp32, the exact test follows
-    const double zq = r.zmax + r.t * log(r.q);
+    // w >= q: a little below max + t ln q, by what the weights' rounding lets
+    // through (2^-37 of a weight, one unit of an integer) and then by fp32's;
+    // the exact test follows
+    const double unit = 1.0 / scale_of(a), q = r.q > unit ? r.q : unit;
+    const double zq = r.zmax + r.t * (log(q) - 0x1p-37 - unit / q);
     const float x = (float)(zq - 1e-6 * (__builtin_fabs(zq) + __builtin_fabs(r.zmax)));
     const uint32_t b = key_of(clean(x));
     bound = b > bound ? b : bound;

@@ -97,6 +97,7 @@ def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias:
     ``bias`` [H] may be absent and may be float32 next to a bfloat16 ``x``."""
     _check_rows("x", x)
     w, b, w_dtype = _check_params(x, weight, bias)
+    eps = float(eps)
     x2 = _rows(x)
     M, H = x2.shape
     dev = x.device
@@ -228,13 +229,16 @@ def dropout(x: torch.Tensor, p: float, seed: int, offset: Union[int, torch.Tenso
     _check_tensor("x", x)
     if not 0.0 <= p <= 1.0:
         raise ValueError(f"p must lie in [0, 1] (got {p})")
+    seed = int(seed)
     if not 0 <= seed <= _U64:
         raise ValueError("seed must be an unsigned 64-bit integer")
     if torch.is_tensor(offset):
         if offset.dtype != torch.int64 or offset.numel() != 1 or offset.device != x.device:
             raise ValueError("a tensor offset must be one int64 on the device of x")
-    elif not 0 <= offset <= _U64:
-        raise ValueError("offset must be an unsigned 64-bit integer")
+    else:
+        offset = int(offset)
+        if not 0 <= offset <= _U64:
+            raise ValueError("offset must be an unsigned 64-bit integer")
     if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype
                                  or residual.device != x.device):
         raise ValueError(f"residual must match x: {tuple(x.shape)} {x.dtype} on {x.device} (got "
@@ -264,7 +268,7 @@ def _sample_param(name: str, v, dtype, N: int, dev, prm) -> Optional[torch.Tenso
     """A scalar goes into the parameter block, a tensor's address into its
     per-row field; the tensor is returned to be kept alive for the call."""
     if not torch.is_tensor(v):
-        setattr(prm, name, v)
+        setattr(prm, name, int(v) if dtype == torch.int64 else float(v))
         return None
     if v.dtype != dtype or v.device != dev or v.numel() != N:
         raise ValueError(f"{name} must be a number or one {dtype} per row on {dev}")

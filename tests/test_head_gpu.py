@@ -233,7 +233,7 @@ def test_dropout(n, p, seed, offset, dtype):
         assert np.array_equal(np.isnan(got[keep]), np.isnan(ref[keep]))
         assert np.array_equal(np.isinf(got[keep]), np.isinf(ref[keep]))
         tol = HALF[dtype] * (1 + 4 * U) * np.abs(ref) + 3 * U * (np.abs(xn) / max(1 - p, 1e-9) + np.abs(ref))
-        assert (np.abs(got - ref)[fin] <= tol[fin]).all()
+        assert (np.abs(got[fin] - ref[fin]) <= tol[fin]).all()
         y2 = L.dropout(x, p, seed, torch.tensor([offset - 2 ** 64 if offset >= 2 ** 63 else offset], device="cuda"), r)
         assert torch.equal(y2.view(torch.int16 if dtype == "bf16" else torch.int32),
                            y.view(torch.int16 if dtype == "bf16" else torch.int32))
@@ -407,3 +407,62 @@ def test_lm_head_loss_runs_the_operators_together(reduction):
     # more than twice the largest of those
     la = 0.5 * (np.abs(yr) @ np.abs(_np(W)).T).max()
     assert abs(mine - ref["loss"]) <= 2 * 3 * 2.0 ** -8 * la * (1 if reduction == "mean" else N) and rel < 0.05
+
+
+def test_layer_norm_rows_far_apart():
+    """Row offsets past 2^31 elements, in every tensor."""
+    import torch
+    import linear_cross_entropy_gemm_amd as L
+    ld, H = (1 << 31) + 8191, 700
+    st = torch.cuda.current_stream().cuda_stream
+    bufs = [torch.empty(ld + H, dtype=torch.bfloat16, device="cuda").as_strided((2, H), (ld, 1)) for _ in range(4)]
+    x, dy, y, gx = bufs
+    x.copy_(_rand((2, H), "bf16", 80))
+    dy.copy_(_rand((2, H), "bf16", 81))
+    want = L.layer_norm_fwd(x.contiguous())
+    g = L.layer_norm_bwd(dy.contiguous(), x.contiguous(), None, want.mean, want.rstd)
+    log("[ln] rows far apart")
+    assert L.flce_layer_norm_fwd(x.data_ptr(), ld, None, None, 2, H, EPS, y.data_ptr(), ld, None, None, st, 0,
+                                 0) == L.FLCE_OK
+    assert L.flce_layer_norm_bwd(dy.data_ptr(), ld, x.data_ptr(), ld, None, want.mean.data_ptr(), want.rstd.data_ptr(),
+                                 2, H, gx.data_ptr(), ld, None, None, st, 0, 0, None, 0) == L.FLCE_OK
+    o = L.layer_norm_fwd(x)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want.y) and torch.equal(gx, g.grad_x) and torch.equal(o.y, want.y)
+
+
+def test_dropout_past_2_to_the_32_elements():
+    """The last elements of a tensor of more than 2^32: their words come from
+    counters past 2^30 (elements / 4)."""
+    import torch
+    import linear_cross_entropy_gemm_amd as L
+    n, tail = (1 << 32) + 1001, 4001
+    x = torch.ones(n, dtype=torch.bfloat16, device="cuda")
+    log("[dropout] 2^32 + 1001 elements")
+    y = L.dropout(x, 0.25, 5, 6)
+    torch.cuda.synchronize()
+    first = (n - tail) // 4
+    blk = np.arange(first, (n + 3) // 4, dtype=np.uint64)
+    ctr = np.zeros((blk.size, 4), dtype=np.uint64)
+    ctr[:, 0], ctr[:, 1], ctr[:, 2] = blk & np.uint64(0xFFFFFFFF), blk >> np.uint64(32), 6
+    keep = (O.philox4x32_10(ctr, (5, 0)).reshape(-1) >= np.uint64(1 << 30))[:n - first * 4]
+    got = _np(y[first * 4:])
+    assert np.array_equal(got != 0, keep) and set(got[keep]) == {float(torch.tensor(4 / 3).bfloat16())}
+    assert 0.745 < float((y[::4099] != 0).float().mean()) < 0.755
+
+
+def test_operators_take_numpy_scalars_and_empty_batches():
+    import torch
+    import linear_cross_entropy_gemm_amd as L
+    x = _rand((4, 96), "bf16", 90)
+    assert torch.equal(L.dropout(x, np.float32(0.5), np.int64(3), np.uint32(2)), L.dropout(x, 0.5, 3, 2))
+    u = torch.rand(4, device="cuda")
+    a = L.sample(x, u, np.float32(0.5), np.int32(7), np.float64(0.5), np.float32(0.25)).tokens
+    assert torch.equal(a, L.sample(x, u, 0.5, 7, 0.5, 0.25).tokens)
+    assert torch.equal(L.layer_norm(x, eps=np.float32(0.5)), L.layer_norm(x, eps=0.5))
+    W = _rand((50, 96), "bf16", 91).clone()
+    w = torch.ones(96, device="cuda")
+    o = L.lm_head_sample(x[:0], W, u[:0], w)
+    assert o.tokens.shape == (0,)
+    loss, n = L.lm_head_loss(x[:0], W, torch.zeros(0, dtype=torch.int64, device="cuda"), w)
+    assert loss.item() == 0.0 and n.item() == 0

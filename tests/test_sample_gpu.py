@@ -157,6 +157,55 @@ def test_sample_special_values(dtype, V):
     assert o.tokens.tolist()[2:8] == [3, 1, 0, 5, 0, V - 1]
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_sample_masked_pieces_and_extreme_temperatures(dtype):
+    """Long stretches without a candidate, and temperatures at which every
+    weight is the same or all but the largest vanish."""
+    import torch
+    import linear_cross_entropy_gemm_amd as L
+    V = 41000
+    z = _logits(6, V, dtype, "peaked", 31)
+    z[0, :8192 * 4] = float("-inf")
+    z[1, 8192:] = float("-inf")
+    z[2, 9000:40000] = float("-inf")
+    z[3] *= 1e30
+    z[4] *= 1e-30
+    z[5, ::2] = torch.finfo(z.dtype).min
+    u = _u(6, 32)
+    for t in (1e-30, 1e-5, 1e25, 3e38):
+        for name in ("plain", "k5", "k300", "p90", "q5", "all"):
+            prm = dict(PARAMS[name], temperature=t)
+            log(f"[sample] masked pieces {dtype} {name} t={t}")
+            _compare(z, u, L.sample(z, u, **prm, logprobs=True), **_kw(prm))
+    for name, prm in PARAMS.items():
+        log(f"[sample] masked pieces {dtype} {name}")
+        _compare(z, u, L.sample(z, u, **prm, logprobs=True), **_kw(prm))
+
+
+def test_sample_many_short_rows():
+    import linear_cross_entropy_gemm_amd as L
+    z, u = _logits(70001, 5, "f32", "flat", 33), _u(70001, 34)
+    o = L.sample(z, u, 0.9, 3, 0.8, logprobs=True)
+    _compare(z[::997], u[::997], L.SampleOutputs(o.tokens[::997], o.logprobs[::997]), 0.9, 3, 0.8)
+    # the lowest logit of five is never among the first three
+    assert not (o.tokens == z.argmin(1)).any()
+
+
+@pytest.mark.parametrize("V", [700, 20000])
+def test_sample_rows_far_apart(V):
+    """Row offsets past 2^32 bytes and past 2^31 elements."""
+    import torch
+    import linear_cross_entropy_gemm_amd as L
+    ld = (1 << 31) + 12345
+    buf = torch.empty(ld + V, dtype=torch.bfloat16, device="cuda")
+    z = buf.as_strided((2, V), (ld, 1))
+    z.copy_(_logits(2, V, "bf16", "peaked", 35))
+    u = _u(2, 36)
+    for prm in ({}, dict(top_k=40, top_p=0.9), dict(top_p=0.9), dict(temperature=0.0)):
+        log(f"[sample] rows far apart V={V} {prm}")
+        _compare(z, u, L.sample(z, u, **prm, logprobs=True), **_kw(prm))
+
+
 def test_sample_bad_row_values_give_no_token():
     import torch
     import linear_cross_entropy_gemm_amd as L
