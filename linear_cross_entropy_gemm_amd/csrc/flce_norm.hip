@@ -363,12 +363,10 @@ __global__ __launch_bounds__(kRow* kRows) __attribute__((amdgpu_waves_per_eu(kEu
 #pragma unroll
     for (int i = 0; i < kVec; ++i)
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
+      for (int e = 0; e < E; e += 4) {
         const int col = (t + i * kRow) * E + e;
-        if (col < p.H) {
-          out[col] = dw[i][e];
-          out[p.H + col] = db[i][e];
-        }
+        store_row<float>(out, col, p.H, f32x4{dw[i][e], dw[i][e + 1], dw[i][e + 2], dw[i][e + 3]});
+        store_row<float>(out + p.H, col, p.H, f32x4{db[i][e], db[i][e + 1], db[i][e + 2], db[i][e + 3]});
       }
   }
 }
@@ -478,19 +476,23 @@ int64_t bwd_groups(int64_t M, int64_t H, int dtype) {
   if (v <= 64) return even_grid(ceil_div(M, 4), 1024);
   if (v <= 128) return even_grid(ceil_div(M, 4), 512);
   if (v <= 256) return even_grid(ceil_div(M, 4), 256);
-  if (v <= 512) return even_grid(M, 512);
+  if (v <= 1024) return even_grid(M, 512);
   if (v <= kMaxRegVecs) return even_grid(M, 256);
   return M < 64 ? M : 64;
 }
 
-// Threads, vectors per thread and resident work-groups by the row's length,
-// as measured at 218 MB of rows in and out (bf16 rows, fp32 parameters; TB/s,
-// the next best shape in brackets; a plain copy of as much reaches 5.4):
-//   H      512       1024      2048      4096      6656      16384
-//   fwd    4.9       5.1       5.1       5.0       4.2       4.0
-//          [4.4]     [4.6]     [5.0]     [4.8]     [3.9]     [4.1 at 1024 threads]
-//   bwd    5.2       5.4       5.1       4.9       4.1       4.1
-//          [4.8]     [4.8]     [4.9]     [4.9]     [4.0]     [3.0]
+// Threads, vectors per thread and resident work-groups by the row's length in
+// vectors of 16 bytes, as measured on 134 MB of bf16 rows with fp32 parameters
+// (kernel alone, TB/s of rows read and written; next best shape in brackets; a
+// plain copy reaches 5.3; H = 5003 is fp32, 82 MB):
+//   H      512       1024      2048      4096      6656      5003      16384
+//   fwd    4.9       5.1       5.1       5.0       4.3       4.3       4.0
+//          [4.7]     [4.6]     [5.0]     [4.8]     [3.9]     [4.3]     [4.1, 1024 threads]
+//   bwd    5.2       5.4       5.1       4.9       4.5       4.6       4.1
+//          [4.8]     [4.8]     [4.9]     [4.9]     [4.3]     [4.1]     [3.0]
+// What they lose to the copy is the wait between a row's last load and its
+// first store, which the registers for more rows in flight would hide; asking
+// the compiler for more resident waves spills and costs more (fwd 4.3 to 2.4).
 template <typename T, typename WT>
 void launch_fwd(const LnFwdArgs& p, int dtype, hipStream_t st) {
   const int64_t v = row_vecs(p.H, dtype);
@@ -500,6 +502,7 @@ void launch_fwd(const LnFwdArgs& p, int dtype, hipStream_t st) {
   else if (v <= 256) ln_fwd_kernel<T, WT, 64, 4, 4, 1><<<grid(4, 512), 256, 0, st>>>(p);
   else if (v <= 512) ln_fwd_kernel<T, WT, 128, 4, 1, 1><<<grid(1, 1536), 128, 0, st>>>(p);
   else if (v <= 1024) ln_fwd_kernel<T, WT, 256, 4, 1, 3><<<grid(1, 768), 256, 0, st>>>(p);
+  else if (v <= 1536) ln_fwd_kernel<T, WT, 512, 3, 1, 1><<<grid(1, 512), 512, 0, st>>>(p);
   else if (v <= kMaxRegVecs) ln_fwd_kernel<T, WT, 512, 4, 1, 1><<<grid(1, 256), 512, 0, st>>>(p);
   else ln_fwd_wide_kernel<T, WT><<<grid(1, 65536), kWide, 0, st>>>(p);
 }
@@ -512,7 +515,8 @@ void launch_bwd(const LnBwdArgs& p, int dtype, hipStream_t st) {
   else if (v <= 128) ln_bwd_kernel<T, WT, 64, 2, 4, 1><<<g, 256, 0, st>>>(p);
   else if (v <= 256) ln_bwd_kernel<T, WT, 64, 4, 4, 1><<<g, 256, 0, st>>>(p);
   else if (v <= 512) ln_bwd_kernel<T, WT, 256, 2, 1, 1><<<g, 256, 0, st>>>(p);
-  else if (v <= 1024) ln_bwd_kernel<T, WT, 512, 2, 1, 1><<<g, 512, 0, st>>>(p);
+  else if (v <= 1024) ln_bwd_kernel<T, WT, 256, 4, 1, 2><<<g, 256, 0, st>>>(p);
+  else if (v <= 1536) ln_bwd_kernel<T, WT, 512, 3, 1, 1><<<g, 512, 0, st>>>(p);
   else if (v <= kMaxRegVecs) ln_bwd_kernel<T, WT, 512, 4, 1, 1><<<g, 512, 0, st>>>(p);
   else {
     if (p.dx) ln_bwd_wide_kernel<T, WT><<<(unsigned)(p.M < 65536 ? p.M : 65536), kWide, 0, st>>>(p);
