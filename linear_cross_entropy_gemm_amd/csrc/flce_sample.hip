@@ -51,7 +51,7 @@ constexpr int kRowThreads = 1024;
 constexpr int kRowWaves = kRowThreads / 64;
 constexpr int kBins = 2048;          // 11 bits of a key per search pass
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;
-constexpr int kSmall = 1024;         // rows one wave holds
+constexpr int kSmall = 2048;         // rows one wave holds
 constexpr int kPiece = 8192;         // logits per work-group of the scan
 constexpr int kGroup = 64;           // logits per stored maximum
 constexpr int kPieceGroups = kPiece / kGroup;
@@ -306,7 +306,7 @@ __device__ __forceinline__ void pick_in_wave(const SampleArgs& a, int64_t row, u
 
 // Rows of up to 64 kPer logits, any parameters: one wave per row, lane l
 // holding the logits [l kPer, (l + 1) kPer).  Every cut is found bit by bit
-// of its key, from counts and sums over the wave.
+// of its key, from counts and sums over the wave, until one key is left.
 template <typename T, int kPer>
 __global__ __launch_bounds__(256) void sample_small_kernel(SampleArgs a) {
   constexpr int low = sizeof(T) == 2 ? 16 : 0, E = RowVec<T>::E;
@@ -343,54 +343,64 @@ __global__ __launch_bounds__(256) void sample_small_kernel(SampleArgs a) {
     if (lane == l) emit(a, row, lane * kPer + at, m, r, 1.0);
     return;
   }
-  uint32_t key[kPer];
-  uint32_t keep = 0;   // bit j: x[j] is kept
+  uint32_t key[kPer];   // 0: not kept
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    key[j] = key_of(x[j]);
-    keep |= (x[j] > kNegInf ? 1u : 0u) << j;
-  }
+  for (int j = 0; j < kPer; ++j) key[j] = x[j] > kNegInf ? key_of(x[j]) : 0;
+  auto count = [&](uint32_t from) {
+    uint32_t n = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) n += key[j] >= from ? 1u : 0u;
+    return wave_sum_u32(n);
+  };
+  // the largest kept key K for which reaches(K, count from K) holds (it holds
+  // for all keys below, and for the least); where the test is the count, the
+  // search ends when one key is left (counting beside the sums of weights
+  // costs as much as the passes it saves: 19 against 18 us at V = 1000, fp32)
+  auto search = [&](auto reaches, bool counted) {
+    uint32_t K = 0, top = 0, at_least = 2, above = 0;   // K <= result < top (0: no bound)
+    if (counted) at_least = count(1);
+#pragma unroll 1
+    for (int b = 31; b >= low && at_least - above > 1; --b) {
+      const uint32_t c = K | 1u << b, n = counted ? count(c) : above + 2;
+      if (reaches(c, n)) {
+        K = c;
+        at_least = n;
+      } else {
+        top = c;
+        above = counted ? n : above;
+      }
+    }
+    uint32_t best = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const bool in = key[j] >= K && (top == 0 || key[j] < top);
+      best = in && key[j] > best ? key[j] : best;
+    }
+    return wave_max_u32(best);
+  };
   // Of the kept logits with key K, only the first `n` in index order stay;
   // smaller keys go.
   auto cut_at = [&](uint32_t K, u64 n) {
-    uint32_t tie = 0, over = 0;
+    uint32_t ties = 0, before;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) ties += key[j] == K ? 1u : 0u;
+    before = wave_scan_u32(ties, before) - ties;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      tie |= (key[j] == K ? 1u : 0u) << j;
-      over |= (key[j] > K ? 1u : 0u) << j;
+      const bool tie = key[j] == K;
+      key[j] = key[j] < K || (tie && before >= n) ? 0 : key[j];
+      before += tie ? 1u : 0u;
     }
-    tie &= keep;
-    u64 all;
-    u64 rank = wave_scan_u64((u64)__builtin_popcount(tie), all) - (u64)__builtin_popcount(tie);
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const bool is = tie >> j & 1;
-      if (is && rank >= n) tie &= ~(1u << j);
-      rank += is ? 1 : 0;
-    }
-    keep &= over | tie;
   };
-  if (r.k > 0 && r.k < a.V) {
-    auto count = [&](uint32_t from) {
-      int n = 0;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) n += __builtin_popcountll(__builtin_amdgcn_ballot_w64(x[j] > kNegInf && key[j] >= from));
-      return n;
-    };
-    if (count(0) > r.k) {
-      const int k = (int)r.k;
-      uint32_t K = 0;
-#pragma unroll 1
-      for (int b = 31; b >= low; --b)
-        if (count(K | 1u << b) >= k) K |= 1u << b;
-      K |= low && !(K >> 31) ? 0xFFFFu : 0u;   // a bf16 key's last 16 bits follow from its first
-      cut_at(K, (u64)(k - count(K + 1)));
-    }
+  if (r.k > 0 && r.k < a.V && count(1) > (u64)r.k) {
+    const uint32_t k = (uint32_t)r.k;
+    const uint32_t K = search([=](uint32_t, uint32_t n) { return n >= k; }, true);
+    cut_at(K, k - count(K + 1));
   }
   const double scale = scale_of(a);
   u64 w[kPer];
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) w[j] = keep >> j & 1 ? fixed(weight_any(x[j], r), scale) : 0;
+  for (int j = 0; j < kPer; ++j) w[j] = key[j] ? fixed(weight_any(x[j], r), scale) : 0;
   if (r.p < 1.0) {
     auto mass = [&](uint32_t from) {
       u64 s = 0;
@@ -398,12 +408,8 @@ __global__ __launch_bounds__(256) void sample_small_kernel(SampleArgs a) {
       for (int j = 0; j < kPer; ++j) s += key[j] >= from ? w[j] : 0;
       return wave_sum_u64(s);
     };
-    const u64 need = share(r.p, mass(0));
-    uint32_t K = 0;
-#pragma unroll 1
-    for (int b = 31; b >= low; --b)
-      if (mass(K | 1u << b) >= need) K |= 1u << b;
-    K |= low && !(K >> 31) ? 0xFFFFu : 0u;
+    const u64 need = share(r.p, mass(1));
+    const uint32_t K = search([&](uint32_t c, uint32_t) { return mass(c) >= need; }, false);
     const u64 rest = need - mass(K + 1), each = fixed(weight_any(value_of(K), r), scale);
     cut_at(K, (rest + each - 1) / each);
   }
@@ -411,7 +417,7 @@ __global__ __launch_bounds__(256) void sample_small_kernel(SampleArgs a) {
   u64 own = 0;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
-    w[j] = (keep >> j & 1) && w[j] >= least ? w[j] : 0;
+    w[j] = key[j] && w[j] >= least ? w[j] : 0;
     own += w[j];
   }
   u64 sum;
@@ -1051,9 +1057,12 @@ __device__ __forceinline__ bool pick_bounded(const SampleArgs& a, const T* z, in
   u64 row_sum = 0;
   if (mode == kTopK) {
     // the k-th largest of the group maxima, or of all logits where there are
-    // fewer groups, by its key's distance from the row's maximum: in steps of
-    // 2^13 (a thousandth of a binade) over two binades, or to the first 11 bits
+    // too few groups or a short row's bound would be loose (with k above a
+    // quarter of the groups, more than 1.15 k logits reach it), by its key's
+    // distance from the row's maximum: in steps of 2^13 (a thousandth of a
+    // binade) over two binades, or to the first 11 bits
     const int groups = (int)((a.V + kGroup - 1) / kGroup);
+    const bool by_group = r.k <= (a.V <= 4 * kPiece ? groups / 4 : groups);
     uint32_t* bins = reinterpret_cast<uint32_t*>(sh.row.hist);
     for (int step = 13; step <= 21; step += 8) {
       auto count = [&](uint32_t key) {
@@ -1061,7 +1070,7 @@ __device__ __forceinline__ bool pick_bounded(const SampleArgs& a, const T* z, in
         if (d < kBins - 1) atomicAdd(&bins[d], 1u);
       };
       clear_bins(sh.row);
-      if (r.k <= groups) {
+      if (by_group) {
         for (int i = threadIdx.x; i < groups; i += kRowThreads) count(gmax[i]);
       } else {
         Row<T>(z, a.V).each([&](int64_t, float x) { count(key_of(x)); });
@@ -1293,7 +1302,8 @@ void launch_small(const SampleArgs& a, hipStream_t st) {
   const unsigned g = (unsigned)((a.N + 3) / 4);
   if (a.V <= 64) sample_small_kernel<T, 1><<<g, 256, 0, st>>>(a);
   else if (a.V <= 512) sample_small_kernel<T, 8><<<g, 256, 0, st>>>(a);
-  else sample_small_kernel<T, 16><<<g, 256, 0, st>>>(a);
+  else if (a.V <= 1024) sample_small_kernel<T, 16><<<g, 256, 0, st>>>(a);
+  else sample_small_kernel<T, 32><<<g, 256, 0, st>>>(a);
 }
 
 // Workspace: what the scan leaves, for rows longer than one piece.

@@ -117,6 +117,15 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t x) {
   return larger(larger(lane(0), lane(16)), larger(lane(32), lane(48)));
 }
 
+__device__ __forceinline__ uint32_t wave_sum_u32(uint32_t x) {
+  x += dpp_u32<0xB1>(x);
+  x += dpp_u32<0x4E>(x);
+  x += dpp_u32<0x141>(x);
+  x += dpp_u32<0x140>(x);
+  auto lane = [=](int l) { return (uint32_t)__builtin_amdgcn_readlane((int)x, l); };
+  return (lane(0) + lane(16)) + (lane(32) + lane(48));
+}
+
 // How many lower lanes are set in `mask`.
 __device__ __forceinline__ int lane_rank(unsigned long long mask) {
   return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));

@@ -82,7 +82,7 @@ def _kw(prm):
 @pytest.mark.parametrize("kind", ["flat", "peaked", "masked", "ties"])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("N,V", [(2, 1), (3, 2), (5, 37), (4, 64), (3, 65), (4, 256), (3, 257),
-                                 (6, 1000), (3, 1024), (3, 1025), (3, 3001), (3, 8191), (2, 8193), (2, 33001)])
+                                 (6, 1000), (3, 1024), (3, 1025), (3, 2048), (3, 2049), (3, 3001), (3, 8191), (2, 8193), (2, 33001)])
 def test_sample(N, V, dtype, kind):
     import linear_cross_entropy_gemm_amd as L
     z = _logits(N, V, dtype, kind, N * V, pad=V % 5, off=1)
