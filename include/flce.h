@@ -409,8 +409,9 @@ size_t flce_sample_workspace_size(int64_t N, int64_t V, int dtype);
  *   S = S_k n S_p n S_q (never empty: it holds the first token)
  *   token = the lowest i in S with sum_{j in S, j <= i} w_j > u sum_{j in S} w_j
  *   logprob = log(w_token / sum_{j in S} w_j)
- * A logit of -inf is masked: it is never drawn (nor is NaN, which counts as
- * -inf, or a weight below 2^-39 of the largest).  Logits of +inf share the
+ * A logit of -inf is masked: it is never drawn, nor is NaN, which counts as
+ * -inf, nor a weight that rounds to 0 in the unit of the sums (2^-38 of the
+ * largest weight at V = 2^24, 2^-44 at V = 2^18).  Logits of +inf share the
  * whole weight.  A row without a logit above -inf, with a per-row parameter
  * out of its range or with u outside [0, 1) gets token -1 and logprob -inf.
  *   logits     [N, V] dtype, row stride ld_logits >= 0 elements (rows may

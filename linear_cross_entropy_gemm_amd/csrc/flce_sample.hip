@@ -7,14 +7,14 @@
 // the order of atomics nor the split of a row changes a decision; the
 // rounding, 2^-(s+1) per token next to the largest token's 1, is far below
 // what a 24-bit random number or an fp32 probability resolves (s is 44 at a
-// vocabulary of 2^18).  The exponential is taken in 64 bits for the same
-// reason: an fp32 one moves the borders between tokens of a flat row by more
-// than their spacing warrants.
+// vocabulary of 2^18).  The exponential is taken in 64 bits (relative error
+// 2^-38.8) for the same reason: an fp32 one moves the borders between tokens
+// of a flat row by more than their spacing warrants.
 //
-// Rows of up to 1024 logits stay in one wave's registers
-// (sample_small_kernel).  A longer row passes through the chip once, in pieces of 8192 logits spread over the
-// work-groups of sample_scan_kernel, which leaves behind what decides where
-// the answer lies:
+// Rows of up to 2048 logits stay in one wave's registers
+// (sample_small_kernel).  A longer row passes through the chip once, in
+// pieces of 8192 logits spread over the work-groups of sample_scan_kernel,
+// which leaves behind what decides where the answer lies:
 //   * the maximum of each 64 logits and of the piece;
 //   * with top-p alone: the piece's weight by bins of z, 1/8 of min(t, 1) wide,
 //     counted down from the piece's maximum (bins are aligned in z, so bins
@@ -31,6 +31,13 @@
 //   * then one wave compares up to 64 candidates with each other, or a search
 //     in LDS finds the cuts among up to 8192, or, in a flat row, the weights
 //     of one piece are summed in index order.
+// What bounds them: the scan the memory where no weights are needed (256 rows
+// of 202048 bf16 logits, 103 MB, in 19 us: 5.4 TB/s, a plain copy's rate) and
+// the 64-bit arithmetic where they are (17 multiply-adds or their like per
+// logit: 46 us, 58 with the bins); the pick the latency of one row's steps (11
+// to 17 us on a short list, of which a third is waiting for memory and a third
+// for instructions that no earlier work-group fetched; 45 us in a flat row,
+// half of it reading the row once more).
 // Rows for which that does not work out (a list that overflows, a cut below
 // the bins) take the searches over the whole row at the end of the kernel.
 //
@@ -47,18 +54,12 @@ namespace flce {
 
 namespace {
 
-constexpr int kRowThreads = 1024;
-constexpr int kRowWaves = kRowThreads / 64;
-constexpr int kBins = 2048;          // 11 bits of a key per search pass
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;
 constexpr int kSmall = 2048;         // rows one wave holds
 constexpr int kPiece = 8192;         // logits per work-group of the scan
 constexpr int kGroup = 64;           // logits per stored maximum
 constexpr int kPieceGroups = kPiece / kGroup;
-constexpr int kMaxPieces = (1 << 24) / kPiece;
 constexpr int kSlots = 128;          // bins of z per piece; the last holds the rest
-constexpr int kList = 8192;          // candidates per row (64 KB of LDS)
-constexpr int kGroupBatch = 4096;    // groups looked through at a time
 constexpr int kScanThreads = 256;
 
 constexpr double kInfMax = 1e300;   // stands for an infinite maximum
@@ -304,8 +305,9 @@ __device__ __forceinline__ void pick_in_wave(const SampleArgs& a, int64_t row, u
     emit(a, row, index_in(c), value_in(c), r, (double)sum / scale);
 }
 
-// Rows of up to 64 kPer logits, any parameters: one wave per row, lane l
-// holding the logits [l kPer, (l + 1) kPer).  Every cut is found bit by bit
+// Rows of up to 64 kPer logits, any parameters: one wave per row, no LDS (1024
+// rows of 1000 bf16 logits: 8 us without filters, 14 with top-p, 18 with top-k
+// and top-p, bound by the searches' instructions), lane l holding the logits [l kPer, (l + 1) kPer).  Every cut is found bit by bit
 // of its key, from counts and sums over the wave, until one key is left.
 template <typename T, int kPer>
 __global__ __launch_bounds__(256) void sample_small_kernel(SampleArgs a) {
@@ -534,176 +536,6 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a)
 }
 
 // ---------------------------------------------------------------------------
-struct RowShared {
-  u64 hist[kBins];
-  GroupScratch<kRowThreads> scratch;
-  u64 above;
-  uint32_t digit;
-  uint32_t kmax[kRowWaves];
-  int64_t idx;
-};
-
-struct PickShared {
-  RowShared row;
-  u64 list[kList];                    // composites
-  u64 cmass[kMaxPieces];              // kept weight per piece
-  double factor[kMaxPieces];          // weight of each piece's maximum
-  u64 slot[kSlots];
-  u64 sum;
-  uint16_t glist[kGroupBatch];        // accepted groups of a batch
-  int groups;
-  int count;
-  int found;
-};
-
-__device__ __forceinline__ u64 group_sum(u64 x, RowShared& sh) {
-  u64 all;
-  group_scan<kRowThreads>(x, all, sh.scratch);
-  return all;
-}
-
-// The bin, from the highest down, at which the running sum reaches `need`
-// (1 <= need <= the sum); `above` gets the sum of the bins over it, plus what
-// it held.  `need_of` maps the whole sum to `need`.
-template <typename G>
-__device__ __forceinline__ uint32_t find_bin(G need_of, u64& above, RowShared& sh) {
-  const int top = kBins - 1 - 2 * threadIdx.x;
-  const u64 a = sh.hist[top], b = sh.hist[top - 1];
-  u64 all;
-  const u64 exc = group_scan<kRowThreads>(a + b, all, sh.scratch) + above, inc = exc + a + b;
-  const u64 need = need_of(all);
-  if (exc < need && need <= inc) {   // one thread
-    const bool first = need <= exc + a;
-    sh.digit = (uint32_t)(first ? top : top - 1);
-    sh.above = first ? exc : exc + a;
-  }
-  __syncthreads();
-  above = sh.above;
-  return sh.digit;
-}
-
-__device__ __forceinline__ void clear_bins(RowShared& sh) {
-  __syncthreads();
-  sh.hist[threadIdx.x] = 0;
-  sh.hist[threadIdx.x + kRowThreads] = 0;
-  __syncthreads();
-}
-
-// A row of V logits: every wave of the work-group owns a consecutive part of
-// it, so sums over waves are sums in index order.
-template <typename T>
-struct Row {
-  static constexpr int E = RowVec<T>::E;
-  const T* z;
-  int64_t V, begin, end;
-
-  __device__ __forceinline__ Row(const T* p, int64_t v) : z(p), V(v) {
-    const int64_t per = (v + kRowWaves * 64 * E - 1) / (kRowWaves * 64 * E) * (64 * E);
-    begin = (int64_t)(threadIdx.x >> 6) * per;
-    end = begin + per < v ? begin + per : v;
-  }
-
-  // f(index, value) over this thread's elements of its wave's part, four
-  // loads under way.
-  template <typename F> __device__ __forceinline__ void each(F f) const {
-    constexpr int kUnroll = 4;
-    for (int64_t c = begin + (threadIdx.x & 63) * E; c < end; c += 64 * E * kUnroll) {
-      typename RowVec<T>::type v[kUnroll];
-#pragma unroll
-      for (int j = 0; j < kUnroll; ++j)
-        if (c + j * 64 * E < end) v[j] = load_row(z, c + j * 64 * E, V);
-#pragma unroll
-      for (int j = 0; j < kUnroll; ++j)
-        if (c + j * 64 * E < end) {
-#pragma unroll
-          for (int e = 0; e < E; ++e)
-            if (c + j * 64 * E + e < V) f(c + j * 64 * E + e, clean(to_f32(v[j][e])));
-        }
-    }
-  }
-
-  // The first index at which the running sum of f (u64, in index order)
-  // exceeds the target that `target_of` makes of the whole sum; `sum` gets
-  // that.  -1 if there is none.
-  template <typename F, typename G> __device__ __forceinline__ int64_t locate(F f, G target_of, u64& sum, RowShared& sh) const {
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    u64 s = 0;
-    each([&](int64_t i, float x) { s += f(i, x); });
-    s = wave_sum_u64(s);
-    __syncthreads();
-    if (lane == 0) sh.scratch.wsum[w] = s;
-    if (threadIdx.x == 0) sh.idx = -1;
-    __syncthreads();
-    u64 before = 0;
-    sum = 0;
-    for (int i = 0; i < kRowWaves; ++i) {
-      if (i < w) before += sh.scratch.wsum[i];
-      sum += sh.scratch.wsum[i];
-    }
-    const u64 target = target_of(sum);
-    if (before <= target && target < before + s) {   // one wave
-      for (int64_t b = begin; b < end; b += 64 * E) {
-        const int64_t c = b + lane * E;
-        u64 own[E], part = 0;
-        const typename RowVec<T>::type v = load_row(z, c, V);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          own[e] = c + e < V ? f(c + e, clean(to_f32(v[e]))) : 0;
-          part += own[e];
-        }
-        u64 all;
-        const u64 inc = wave_scan_u64(part, all);
-        if (target < before + all) {
-          u64 run = before + inc - part;
-          if (run <= target && target < run + part) {   // one lane
-            int64_t at = c;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-              run += own[e];
-              if (run <= target) at = c + e + 1;
-            }
-            sh.idx = at;
-          }
-          break;
-        }
-        before += all;
-      }
-    }
-    __syncthreads();
-    return sh.idx;
-  }
-
-  // The key K at which the sum of f over keys above K is below `need` and
-  // the sum with K reaches it; `above` receives the former.  `need_of` maps
-  // the sum over everything to `need` (1 <= need <= that sum).  One pass of
-  // 11 key bits after another, the passes after the first over the keys that
-  // share K's leading bits.
-  template <typename F, typename G> __device__ __forceinline__ uint32_t search(F f, G need_of, u64& above, RowShared& sh) const {
-    constexpr int low = sizeof(T) == 2 ? 16 : 0;   // a bf16 key's last 16 bits follow from its first
-    uint32_t prefix = 0;
-    u64 need = 0;
-    above = 0;
-    int hi = 32;
-    while (hi > low) {
-      const int bits = hi - low < 11 ? hi - low : 11, lo = hi - bits;
-      clear_bins(sh);
-      each([&](int64_t i, float x) {
-        const uint32_t k = key_of(x);
-        if (hi == 32 || (k >> hi) == prefix) {
-          const u64 w = f(i, x);
-          if (w) atomicAdd(&sh.hist[(k >> lo) & ((1u << bits) - 1)], w);
-        }
-      });
-      __syncthreads();
-      const uint32_t d = find_bin([&](u64 all) { return hi == 32 ? need = need_of(all) : need; }, above, sh);
-      prefix = (hi == 32 ? 0u : prefix << bits) | d;
-      hi = lo;
-    }
-    if (low == 0) return prefix;
-    return prefix << 16 | ((prefix & 0x8000u) ? 0u : 0xFFFFu);
-  }
-};
-
 // Kept by a filter: keys above `key`, and `key` itself up to index `idx`.
 struct Cut {
   uint32_t key;
@@ -759,7 +591,8 @@ template <> struct Interval<bf16> {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const i16x2 s = __builtin_bit_cast(i16x2, (uint32_t)w[q]);
-        const u16x2 key = __builtin_bit_cast(u16x2, s) ^ (__builtin_bit_cast(u16x2, (i16x2)(s >> 15)) | (uint16_t)0x8000);
+        const u16x2 sign = __builtin_bit_cast(u16x2, (i16x2)(s >> 15));
+        const u16x2 key = __builtin_bit_cast(u16x2, s) ^ (sign | (uint16_t)0x8000);
         const u16x2 d = key - least;
         uint32_t in;   // (spelled out: the compiler would make two compares and selects of it)
         asm("v_pk_sub_u16 %0, %1, %2 clamp\n\tv_pk_min_u16 %0, %0, 1 op_sel_hi:[1,0]" : "=v"(in) : "v"(width), "v"(d));
@@ -772,6 +605,190 @@ template <> struct Interval<bf16> {
   // vectors is pair p
   static __device__ __forceinline__ int bit(int b, int n) { return 2 * (4 * n - 1 - (b & 15)) + (b >> 4); }
   static __device__ __forceinline__ uint32_t bits_of_vector(int j) { return 0x000F000Fu << (12 - 4 * j); }
+};
+
+// A row's work-group of TH threads: its shared memory, and what it does.  1024
+// threads have the shortest way through one row; 512, with half the list,
+// leave room for two rows on a compute unit.
+template <int TH>
+struct Picker {
+static constexpr int kRowThreads = TH, kRowWaves = TH / 64;
+static constexpr int kBinBits = TH == 1024 ? 11 : 10, kBins = 1 << kBinBits;   // bits of a key per search pass
+static constexpr int kList = 8 * TH;                              // candidates (8 bytes each)
+static constexpr int kMaxPieces = TH == 1024 ? (1 << 24) / kPiece : 256;
+static constexpr int kGroupBatch = 4 * TH;                        // groups looked through at a time
+static_assert(kBins == 2 * TH, "find_bin gives every thread two bins");
+
+struct RowShared {
+  u64 hist[kBins];
+  GroupScratch<kRowThreads> scratch;
+  u64 above;
+  uint32_t digit;
+  uint32_t kmax[kRowWaves];
+  int64_t idx;
+};
+
+struct PickShared {
+  RowShared row;
+  u64 list[kList];                    // composites
+  u64 cmass[kMaxPieces];              // kept weight per piece
+  double factor[kMaxPieces];          // weight of each piece's maximum
+  u64 slot[kSlots];
+  u64 sum;
+  uint16_t glist[kGroupBatch];        // accepted groups of a batch
+  int groups;
+  int count;
+  int found;
+};
+
+static __device__ __forceinline__ u64 group_sum(u64 x, RowShared& sh) {
+  u64 all;
+  group_scan<kRowThreads>(x, all, sh.scratch);
+  return all;
+}
+
+// The bin, from the highest down, at which the running sum reaches `need`
+// (1 <= need <= the sum); `above` gets the sum of the bins over it, plus what
+// it held.  `need_of` maps the whole sum to `need`.
+template <typename G>
+static __device__ __forceinline__ uint32_t find_bin(G need_of, u64& above, RowShared& sh) {
+  const int top = kBins - 1 - 2 * threadIdx.x;
+  const u64 a = sh.hist[top], b = sh.hist[top - 1];
+  u64 all;
+  const u64 exc = group_scan<kRowThreads>(a + b, all, sh.scratch) + above, inc = exc + a + b;
+  const u64 need = need_of(all);
+  if (exc < need && need <= inc) {   // one thread
+    const bool first = need <= exc + a;
+    sh.digit = (uint32_t)(first ? top : top - 1);
+    sh.above = first ? exc : exc + a;
+  }
+  __syncthreads();
+  above = sh.above;
+  return sh.digit;
+}
+
+static __device__ __forceinline__ void clear_bins(RowShared& sh) {
+  __syncthreads();
+  sh.hist[threadIdx.x] = 0;
+  sh.hist[threadIdx.x + kRowThreads] = 0;
+  __syncthreads();
+}
+
+// A row of V logits: every wave of the work-group owns a consecutive part of
+// it, so sums over waves are sums in index order.
+template <typename T>
+struct Row {
+  static constexpr int E = RowVec<T>::E;
+  const T* z;
+  int64_t V, begin, end;
+
+  __device__ __forceinline__ Row(const T* p, int64_t v) : z(p), V(v) {
+    const int64_t per = (v + kRowWaves * 64 * E - 1) / (kRowWaves * 64 * E) * (64 * E);
+    begin = (int64_t)(threadIdx.x >> 6) * per;
+    end = begin + per < v ? begin + per : v;
+  }
+
+  // f(index, value) over this thread's elements of its wave's part, four
+  // loads under way.
+  template <typename F> __device__ __forceinline__ void each(F f) const {
+    constexpr int kUnroll = 4;
+    for (int64_t c = begin + (threadIdx.x & 63) * E; c < end; c += 64 * E * kUnroll) {
+      typename RowVec<T>::type v[kUnroll];
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j)
+        if (c + j * 64 * E < end) v[j] = load_row(z, c + j * 64 * E, V);
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j)
+        if (c + j * 64 * E < end) {
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if (c + j * 64 * E + e < V) f(c + j * 64 * E + e, clean(to_f32(v[j][e])));
+        }
+    }
+  }
+
+  // The first index at which the running sum of f (u64, in index order)
+  // exceeds the target that `target_of` makes of the whole sum; `sum` gets
+  // that.  -1 if there is none.
+  template <typename F, typename G>
+  __device__ __forceinline__ int64_t locate(F f, G target_of, u64& sum, RowShared& sh) const {
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    u64 s = 0;
+    each([&](int64_t i, float x) { s += f(i, x); });
+    s = wave_sum_u64(s);
+    __syncthreads();
+    if (lane == 0) sh.scratch.wsum[w] = s;
+    if (threadIdx.x == 0) sh.idx = -1;
+    __syncthreads();
+    u64 before = 0;
+    sum = 0;
+    for (int i = 0; i < kRowWaves; ++i) {
+      if (i < w) before += sh.scratch.wsum[i];
+      sum += sh.scratch.wsum[i];
+    }
+    const u64 target = target_of(sum);
+    if (before <= target && target < before + s) {   // one wave
+      for (int64_t b = begin; b < end; b += 64 * E) {
+        const int64_t c = b + lane * E;
+        u64 own[E], part = 0;
+        const typename RowVec<T>::type v = load_row(z, c, V);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          own[e] = c + e < V ? f(c + e, clean(to_f32(v[e]))) : 0;
+          part += own[e];
+        }
+        u64 all;
+        const u64 inc = wave_scan_u64(part, all);
+        if (target < before + all) {
+          u64 run = before + inc - part;
+          if (run <= target && target < run + part) {   // one lane
+            int64_t at = c;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+              run += own[e];
+              if (run <= target) at = c + e + 1;
+            }
+            sh.idx = at;
+          }
+          break;
+        }
+        before += all;
+      }
+    }
+    __syncthreads();
+    return sh.idx;
+  }
+
+  // The key K at which the sum of f over keys above K is below `need` and
+  // the sum with K reaches it; `above` receives the former.  `need_of` maps
+  // the sum over everything to `need` (1 <= need <= that sum).  One pass of
+  // kBinBits key bits after another, the passes after the first over the keys that
+  // share K's leading bits.
+  template <typename F, typename G>
+  __device__ __forceinline__ uint32_t search(F f, G need_of, u64& above, RowShared& sh) const {
+    constexpr int low = sizeof(T) == 2 ? 16 : 0;   // a bf16 key's last 16 bits follow from its first
+    uint32_t prefix = 0;
+    u64 need = 0;
+    above = 0;
+    int hi = 32;
+    while (hi > low) {
+      const int bits = hi - low < kBinBits ? hi - low : kBinBits, lo = hi - bits;
+      clear_bins(sh);
+      each([&](int64_t i, float x) {
+        const uint32_t k = key_of(x);
+        if (hi == 32 || (k >> hi) == prefix) {
+          const u64 w = f(i, x);
+          if (w) atomicAdd(&sh.hist[(k >> lo) & ((1u << bits) - 1)], w);
+        }
+      });
+      __syncthreads();
+      const uint32_t d = find_bin([&](u64 all) { return hi == 32 ? need = need_of(all) : need; }, above, sh);
+      prefix = (hi == 32 ? 0u : prefix << bits) | d;
+      hi = lo;
+    }
+    if (low == 0) return prefix;
+    return prefix << 16 | ((prefix & 0x8000u) ? 0u : 0xFFFFu);
+  }
 };
 
 // The candidates of a row in LDS.
@@ -822,12 +839,12 @@ struct Candidates {
 
   // The value X of `part` (`width` bits) at which the sum of f over
   // candidates with a larger part is below `need` and the sum with X reaches
-  // it; 11 bits per pass.
+  // it; kBinBits bits per pass.
   template <typename P, typename F> __device__ __forceinline__ u64 search(P part, int width, F f, u64 need) const {
     RowShared& r = sh.row;
     u64 prefix = 0, above = 0;
     for (int hi = width; hi > 0;) {
-      const int b = hi < 11 ? hi : 11, lo = hi - b;
+      const int b = hi < kBinBits ? hi : kBinBits, lo = hi - b;
       clear_bins(r);
       each([&](u64 c) {
         const u64 x = part(c);
@@ -956,7 +973,8 @@ struct Candidates {
 // (in index order) exceeds `target`; a target at or past the piece's sum is
 // taken as its last counted element.  -1 if the piece counts nothing.
 template <typename T, typename F>
-__device__ __forceinline__ int64_t locate_in_piece(const T* z, int64_t V, int64_t base, F f, u64 target, RowShared& sh) {
+static __device__ __forceinline__ int64_t locate_in_piece(const T* z, int64_t V, int64_t base, F f, u64 target,
+                                                          RowShared& sh) {
   constexpr int E = RowVec<T>::E, kVec = kPiece / (kRowThreads * E);
   const int64_t c = base + (int64_t)threadIdx.x * E * kVec;
   u64 own[kVec * E], part = 0;
@@ -987,7 +1005,8 @@ __device__ __forceinline__ int64_t locate_in_piece(const T* z, int64_t V, int64_
 }
 
 // sh.factor[i] = weight of piece i's maximum (0 where the piece is masked).
-__device__ __forceinline__ void piece_factors(const SampleArgs& a, int64_t row_i, const RowParams& r, PickShared& sh) {
+static __device__ __forceinline__ void piece_factors(const SampleArgs& a, int64_t row_i, const RowParams& r,
+                                                     PickShared& sh) {
   __syncthreads();
   for (int i = threadIdx.x; i < a.pieces; i += kRowThreads) {
     const uint32_t k = a.pmax[row_i * a.pieces + i];
@@ -997,17 +1016,17 @@ __device__ __forceinline__ void piece_factors(const SampleArgs& a, int64_t row_i
 }
 
 // An integer weight relative to a piece's maximum, relative to the row's.
-__device__ __forceinline__ u64 rescale(u64 h, double factor) {
+static __device__ __forceinline__ u64 rescale(u64 h, double factor) {
   return factor == 1.0 ? h : (u64)((double)h * factor + 0.5);
 }
-__device__ __forceinline__ u64 piece_weight(double psum, double factor, double scale) {
+static __device__ __forceinline__ u64 piece_weight(double psum, double factor, double scale) {
   return (u64)(psum * factor * scale + 0.5);
 }
 
 // The listed candidates (which hold every token at least as likely as the
 // least of them): by one wave, or searched where they are more.
 template <typename T>
-__device__ __forceinline__ void pick_from_list(const SampleArgs& a, int64_t row_i, Candidates<T>& list,
+static __device__ __forceinline__ void pick_from_list(const SampleArgs& a, int64_t row_i, Candidates<T>& list,
                                                const RowParams& r, bool top_k, u64 row_sum, PickShared& sh) {
   top_k = top_k && r.k < list.n;
   if (list.n <= 64) {
@@ -1050,8 +1069,8 @@ __device__ __forceinline__ void pick_from_list(const SampleArgs& a, int64_t row_
 
 // Top-k or min-p: false if the candidates overflow the list.
 template <typename T>
-__device__ __forceinline__ bool pick_bounded(const SampleArgs& a, const T* z, int64_t row_i, const RowParams& r, uint32_t km, Mode mode,
-                             PickShared& sh) {
+static __device__ __forceinline__ bool pick_bounded(const SampleArgs& a, const T* z, int64_t row_i, const RowParams& r,
+                                                    uint32_t km, Mode mode, PickShared& sh) {
   const uint32_t* gmax = a.gmax + row_i * a.pieces * kPieceGroups;
   uint32_t bound = kKeyNegInf + 1;   // candidates' keys from here on
   u64 row_sum = 0;
@@ -1060,11 +1079,11 @@ __device__ __forceinline__ bool pick_bounded(const SampleArgs& a, const T* z, in
     // too few groups or a short row's bound would be loose (with k above a
     // quarter of the groups, more than 1.15 k logits reach it), by its key's
     // distance from the row's maximum: in steps of 2^13 (a thousandth of a
-    // binade) over two binades, or to the first 11 bits
+    // binade; 2^14 with fewer bins) over two binades, or to the first bits
     const int groups = (int)((a.V + kGroup - 1) / kGroup);
     const bool by_group = r.k <= (a.V <= 4 * kPiece ? groups / 4 : groups);
     uint32_t* bins = reinterpret_cast<uint32_t*>(sh.row.hist);
-    for (int step = 13; step <= 21; step += 8) {
+    for (int step = 24 - kBinBits; step < 32; step += 8) {
       auto count = [&](uint32_t key) {
         const uint32_t d = (km - key) >> step;
         if (d < kBins - 1) atomicAdd(&bins[d], 1u);
@@ -1114,8 +1133,8 @@ __device__ __forceinline__ bool pick_bounded(const SampleArgs& a, const T* z, in
 // piece that holds the answer; a short list where the kept set is small.
 // False if the cut lies below the bins or its bin overflows the list.
 template <typename T>
-__device__ __forceinline__ bool pick_by_pieces(const SampleArgs& a, const T* z, int64_t row_i, const RowParams& r, uint32_t km,
-                               Mode mode, PickShared& sh) {
+static __device__ __forceinline__ bool pick_by_pieces(const SampleArgs& a, const T* z, int64_t row_i, const RowParams& r,
+                                                      uint32_t km, Mode mode, PickShared& sh) {
   const double scale = scale_of(a);
   const uint32_t* pmax = a.pmax + row_i * a.pieces;
   Cut cut{0u, a.V};
@@ -1217,7 +1236,7 @@ __device__ __forceinline__ bool pick_by_pieces(const SampleArgs& a, const T* z, 
 // its arguments by value: inlined or by reference it would put what the
 // common paths hold in registers on the stack.
 template <typename T>
-__device__ __attribute__((noinline)) void pick_whole_row(SampleArgs a, const T* z, int64_t row_i, RowParams r,
+static __device__ __attribute__((noinline)) void pick_whole_row(SampleArgs a, const T* z, int64_t row_i, RowParams r,
                                                          RowShared& sh) {
   const Row<T> row(z, a.V);
   const double scale = scale_of(a);
@@ -1257,10 +1276,8 @@ __device__ __attribute__((noinline)) void pick_whole_row(SampleArgs a, const T* 
   if (threadIdx.x == 0) emit(a, row_i, tok, clean(to_f32(z[tok])), r, (double)sum / scale);
 }
 
-// One row per work-group.
 template <typename T>
-__global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleArgs a) {
-  __shared__ PickShared sh;
+static __device__ __forceinline__ void run(const SampleArgs& a, PickShared& sh) {
   const int64_t row_i = blockIdx.x;
   RowParams r = row_params(a, row_i);
   const T* z = static_cast<const T*>(a.z) + row_i * a.ld;
@@ -1295,6 +1312,27 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleArgs a) 
     done = pick_by_pieces(a, z, row_i, r, km, mode, sh);
   }
   if (!done) pick_whole_row(a, z, row_i, r, sh.row);
+}
+};
+
+// One row per work-group; at most 128 registers, so that 512 threads fit twice.
+template <typename T, int TH>
+__global__ __launch_bounds__(TH) __attribute__((amdgpu_waves_per_eu(4))) void sample_pick_kernel(SampleArgs a) {
+  __shared__ typename Picker<TH>::PickShared sh;
+  Picker<TH>::template run<T>(a, sh);
+}
+
+// Two rows at a time on a compute unit where there are more rows than compute
+// units and a flat row's border bin still fits the shorter list.  1024 rows of
+// 4000 bf16 logits, 512 against 1024 threads: k = 50 and p = 0.95 on peaked
+// rows 31 against 53 us, p = 0.9 on flat ones 45 against 76 us, no filter 22
+// against 30 us.
+template <typename T>
+void launch_pick(const SampleArgs& a, hipStream_t st) {
+  if (a.N > 256 && a.V <= 65536)
+    sample_pick_kernel<T, 512><<<(unsigned)a.N, 512, 0, st>>>(a);
+  else
+    sample_pick_kernel<T, 1024><<<(unsigned)a.N, 1024, 0, st>>>(a);
 }
 
 template <typename T>
@@ -1399,9 +1437,9 @@ extern "C" int flce_sample(const void* logits, int64_t ld_logits, const float* u
   {
     ProfileScope ps(FLCE_KERNEL_SAMPLE_PICK, stream);
     if (dtype == FLCE_DTYPE_BF16)
-      sample_pick_kernel<bf16><<<(unsigned)N, kRowThreads, 0, stream>>>(a);
+      launch_pick<bf16>(a, stream);
     else
-      sample_pick_kernel<float><<<(unsigned)N, kRowThreads, 0, stream>>>(a);
+      launch_pick<float>(a, stream);
   }
   return hipGetLastError() == hipSuccess ? FLCE_OK : FLCE_EDEVICE;
 }

@@ -182,6 +182,27 @@ def test_sample_masked_pieces_and_extreme_temperatures(dtype):
         _compare(z, u, L.sample(z, u, **prm, logprobs=True), **_kw(prm))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["flat", "peaked", "masked", "ties"])
+@pytest.mark.parametrize("V", [2049, 9001, 40000])
+def test_sample_more_rows_than_compute_units(V, dtype, kind):
+    """A batch of 300 equals its rows in smaller batches, all of them, and the
+    definition on every 37th."""
+    import torch
+    import linear_cross_entropy_gemm_amd as L
+    N = 300
+    z, u = _logits(N, V, dtype, kind, V), _u(N, V)
+    pick = slice(0, N, 37)
+    for name in ("plain", "greedy", "k5", "k300", "k5000", "p50", "p90", "q5", "all"):
+        prm = PARAMS[name]
+        log(f"[sample] N={N} V={V} {dtype} {kind} {name}")
+        o = L.sample(z, u, **prm, logprobs=True)
+        parts = [L.sample(z[i:i + 100], u[i:i + 100], **prm, logprobs=True) for i in range(0, N, 100)]
+        assert torch.equal(o.tokens, torch.cat([q.tokens for q in parts]))
+        assert torch.allclose(o.logprobs, torch.cat([q.logprobs for q in parts]), rtol=2.0 ** -23, atol=1e-9)
+        _compare(z[pick], u[pick], L.SampleOutputs(o.tokens[pick], o.logprobs[pick]), **_kw(prm))
+
+
 def test_sample_many_short_rows():
     import linear_cross_entropy_gemm_amd as L
     z, u = _logits(70001, 5, "f32", "flat", 33), _u(70001, 34)
