@@ -16,7 +16,7 @@
 // pieces of 8192 logits spread over the work-groups of sample_scan_kernel,
 // which leaves behind what decides where the answer lies:
 //   * the maximum of each 64 logits and of the piece;
-//   * with top-p alone: the piece's weight by bins of z, 1/8 of min(t, 1) wide,
+//   * with top-p alone: the piece's weight by bins of z, 1/8 of min(t, 3/2) wide,
 //     counted down from the piece's maximum (bins are aligned in z, so bins
 //     of different pieces add up);
 //   * without any filter, or with min-p: the piece's weight.
@@ -29,7 +29,7 @@
 //     row's: the candidates are the logits from that bin up where those are
 //     few, and the bin's own logits where the kept set is most of a flat row;
 //   * then one wave compares up to 64 candidates with each other, or a search
-//     in LDS finds the cuts among up to 8192, or, in a flat row, the weights
+//     in LDS finds the cuts among up to 12288, or, in a flat row, the weights
 //     of one piece are summed in index order.
 // What bounds them: the scan the memory where no weights are needed (256 rows
 // of 202048 bf16 logits, 103 MB, in 19 us: 5.4 TB/s, a plain copy's rate) and
@@ -148,11 +148,12 @@ __device__ __forceinline__ Mode mode_of(const RowParams& r, int64_t V) {
   return r.p < 1.0 ? kTopP : kAll;
 }
 
-// Bins of z, 1/8 of min(t, 1) wide, by whole-number floats ascending with z.
+// Bins of z, 1/8 of min(t, 3/2) wide, by whole-number floats ascending with z.
 // Differences of two are exact below kBinLimit.
 constexpr float kBinLimit = 8388608.0f;   // 2^23
 __device__ __forceinline__ float bin_scale(const RowParams& r) {
-  return r.t < 1.0 ? (float)(8.0 / r.t < 1e30 ? 8.0 / r.t : 1e30) : 8.0f;
+  const double a = 8.0 / (r.t < 1.5 ? r.t : 1.5);
+  return (float)(a < 1e30 ? a : 1e30);
 }
 __device__ __forceinline__ float bin_of(float x, float alpha) { return __builtin_floorf(x * alpha); }
 // The least float in bin b or above: within a few steps of b / alpha.
@@ -614,7 +615,7 @@ template <int TH>
 struct Picker {
 static constexpr int kRowThreads = TH, kRowWaves = TH / 64;
 static constexpr int kBinBits = TH == 1024 ? 11 : 10, kBins = 1 << kBinBits;   // bits of a key per search pass
-static constexpr int kList = 8 * TH;                              // candidates (8 bytes each)
+static constexpr int kList = 12 * TH;                             // candidates (8 bytes each)
 static constexpr int kMaxPieces = TH == 1024 ? (1 << 24) / kPiece : 256;
 static constexpr int kGroupBatch = 4 * TH;                        // groups looked through at a time
 static_assert(kBins == 2 * TH, "find_bin gives every thread two bins");
