@@ -446,8 +446,18 @@ __global__ __launch_bounds__(1024) void ln_reduce_kernel(const float* partial, i
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const int c = blockIdx.x * 64 + lane;
   float s = 0.0f;
-  if (c < 2 * H)
-    for (int g = wv; g < groups; g += 16) s += partial[(int64_t)g * 2 * H + c];
+  if (c < 2 * H) {
+    // eight loads under way, added in order
+    int g = wv;
+    for (; g + 7 * 16 < groups; g += 8 * 16) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = partial[(int64_t)(g + i * 16) * 2 * H + c];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += v[i];
+    }
+    for (; g < groups; g += 16) s += partial[(int64_t)g * 2 * H + c];
+  }
   lds[wv][lane] = s;
   __syncthreads();
   if (wv == 0 && c < 2 * H) {

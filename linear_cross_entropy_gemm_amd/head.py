@@ -201,20 +201,23 @@ def _dropout(x, p, seed, offset, residual) -> torch.Tensor:
 class _Dropout(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, p, seed, offset):
-        tensor = torch.is_tensor(offset)
-        # kept as autograd state: changing it in place before the backward
-        # pass raises there instead of drawing another mask
-        ctx.save_for_backward(offset if tensor else None)
-        ctx.args = (p, seed, None if tensor else offset)
+        if torch.is_tensor(offset):
+            # kept as autograd state: changing it in place before the backward
+            # pass raises there instead of drawing another mask
+            ctx.save_for_backward(offset)
+            ctx.args = (p, seed, None)
+        else:
+            ctx.args = (p, seed, offset)
         return _dropout(x, p, seed, offset, residual)
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, grad_y):
-        need_x, need_r = ctx.needs_input_grad[:2]
+        # the same map on the upstream gradient, itself differentiable
         p, seed, offset = ctx.args
-        gx = _dropout(grad_y, p, seed, ctx.saved_tensors[0] if offset is None else offset, None) if need_x else None
-        return gx, grad_y if need_r else None, None, None, None
+        gx = None
+        if ctx.needs_input_grad[0]:
+            gx = dropout(grad_y, p, seed, ctx.saved_tensors[0] if offset is None else offset)
+        return gx, grad_y if ctx.needs_input_grad[1] else None, None, None, None
 
 
 def dropout(x: torch.Tensor, p: float, seed: int, offset: Union[int, torch.Tensor] = 0,

@@ -266,6 +266,18 @@ def test_dropout_gradients_and_shapes():
             L.dropout(x, **{"p": 0.4, "seed": 9, **bad})
 
 
+def test_dropout_second_derivative():
+    """The map is linear, so the gradient of its gradient with respect to the
+    upstream gradient is the map again."""
+    import torch
+    import linear_cross_entropy_gemm_amd as L
+    x, v = _rand((3, 70), "f32", 26).requires_grad_(), _rand((3, 70), "f32", 27)
+    g = _rand((3, 70), "f32", 28).requires_grad_()
+    gx, = torch.autograd.grad(L.dropout(x, 0.3, 5), x, g, create_graph=True)
+    gg, = torch.autograd.grad(gx, g, v)
+    assert torch.equal(gg, L.dropout(v, 0.3, 5))
+
+
 def test_dropout_offset_changed_before_the_backward_pass_raises():
     import torch
     import linear_cross_entropy_gemm_amd as L
