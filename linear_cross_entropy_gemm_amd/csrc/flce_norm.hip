@@ -15,8 +15,8 @@
 //   ln_reduce_kernel sum of the groups' dw and db in a fixed order
 //
 // Bound by memory, at 70 to 95% of what a plain copy moves (launch_fwd lists
-// the shapes): forward 8192 x 6656 bf16 in 50 us (4.4 TB/s), backward in 80 us
-// (4.1 TB/s, 6 us of it the reduction).  A persistent work-group keeps the
+// the shapes): forward 8192 x 6656 bf16 in 50 us (4.4 TB/s), backward in 75 us
+// (4.4 TB/s, 5 us of it the reduction).  A persistent work-group keeps the
 // parameters and the next row in registers; the loads of the next row must
 // not wait on a branch, so a vector past the row's end is read from inside the
 // row and put right when it is used (a branch per vector cost a tenth).
