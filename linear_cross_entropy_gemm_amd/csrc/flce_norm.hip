@@ -152,9 +152,9 @@ __global__ __launch_bounds__(kRow* kRows) __attribute__((amdgpu_waves_per_eu(kEu
     for (int i = 0; i < kVec; ++i) {
       row_tail<T>(cur[i], (t + i * kRow) * E, p.H);
 #pragma unroll
-      for (int e = 0; e < E; ++e) s += to_f32(cur[i][e]);
+      for (int e = 0; e < E; ++e) s = __builtin_fmaf(to_f32(cur[i][e]), inv_mine, s);   // a sum could overflow
     }
-    const float m0 = wave_sum(s) * inv_mine;
+    const float m0 = wave_sum(s);
     // squares of the deviations, and the deviations' own sum: what the
     // rounding of m0 left over is taken out of both results
     float d1 = 0.0f, d2 = 0.0f;
@@ -241,10 +241,10 @@ __global__ __launch_bounds__(kWide) void ln_fwd_wide_kernel(LnFwdArgs p) {
     for (int c = threadIdx.x * E; c < p.H; c += kWide * E) {
       const vec_t v = load_row(xr, c, p.H);
 #pragma unroll
-      for (int e = 0; e < E; ++e) s[0] += to_f32(v[e]);
+      for (int e = 0; e < E; ++e) s[0] = __builtin_fmaf(to_f32(v[e]), inv, s[0]);
     }
     row_sums<kWide>(s, lds1, buf);
-    const float mean0 = s[0] * inv;
+    const float mean0 = s[0];
     float dev[2] = {0.0f, 0.0f};
     for (int c = threadIdx.x * E; c < p.H; c += kWide * E) {
       const vec_t v = load_row(xr, c, p.H);

@@ -1,8 +1,11 @@
 """The operators around the vocabulary projection, on torch tensors: dropout
 with its residual add and the final layer norm in front of it, with their
-backward passes, and drawing tokens from the logits behind it.  Every step of the computation runs in the library's HIP
-kernels on torch's current stream of the tensors' device; nothing
-synchronises."""
+backward passes, and drawing tokens from the logits behind it.  Every step
+of the computation runs in the library's HIP kernels on torch's current
+stream of the tensors' device; nothing synchronises, and every function can
+be captured in a graph.  (A captured ``backward()`` needs leaves of which no
+eagerly built graph is alive: torch runs the accumulation into a leaf on the
+stream on which its node was made.)"""
 from __future__ import annotations
 
 import dataclasses
@@ -113,14 +116,19 @@ def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias:
 
 def layer_norm_bwd(grad_y: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor], mean: torch.Tensor,
                    rstd: torch.Tensor, workspace: Optional[torch.Tensor] = None, *, need_x: bool = True,
-                   need_params: bool = True) -> LayerNormGrads:
+                   need_params: bool = True, param_dtype: Optional[torch.dtype] = None) -> LayerNormGrads:
     """One call of ``flce_layer_norm_bwd``: the gradients of ``x``, of the
-    weight and of the bias (in the weight's dtype; in that of ``x`` without a
-    weight).  ``mean`` and ``rstd`` are those of ``layer_norm_fwd``.  A
+    weight and of the bias (in the weight's dtype; without a weight in
+    ``param_dtype``, that of ``x`` by default).  ``mean`` and ``rstd`` are those of ``layer_norm_fwd``.  A
     caller-owned ``workspace`` (uint8, ``flce_layer_norm_bwd_workspace_size``)
     may be reused by ordered calls."""
     _check_rows("x", x)
     w, _, w_dtype = _check_params(x, weight, None)
+    if param_dtype is not None and param_dtype != w_dtype:
+        if w is not None or param_dtype not in _DTYPES:
+            raise TypeError(f"param_dtype must be the weight's dtype, or bfloat16 or float32 without one (got "
+                            f"{param_dtype})")
+        w_dtype = param_dtype
     if grad_y.shape != x.shape or grad_y.dtype != x.dtype or grad_y.device != x.device:
         raise ValueError(f"grad_y must match x: {tuple(x.shape)} {x.dtype} on {x.device} (got "
                          f"{tuple(grad_y.shape)} {grad_y.dtype} on {grad_y.device})")
@@ -167,11 +175,9 @@ class _LayerNorm(torch.autograd.Function):
     def backward(ctx, grad_y):
         x, weight, mean, rstd = ctx.saved_tensors
         need_x, need_w, need_b, _ = ctx.needs_input_grad
-        g = layer_norm_bwd(grad_y, x, weight, mean, rstd, need_x=need_x, need_params=need_w or need_b)
-        gb = g.grad_bias if need_b else None
-        if gb is not None and gb.dtype != ctx.b_dtype:   # a bias without a weight
-            gb = gb.to(ctx.b_dtype)
-        return g.grad_x, g.grad_weight if need_w else None, gb, None
+        g = layer_norm_bwd(grad_y, x, weight, mean, rstd, need_x=need_x, need_params=need_w or need_b,
+                           param_dtype=ctx.b_dtype)
+        return g.grad_x, g.grad_weight if need_w else None, g.grad_bias if need_b else None, None
 
 
 def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,

@@ -289,6 +289,40 @@ def test_dropout_offset_changed_before_the_backward_pass_raises():
         y.sum().backward()
 
 
+@pytest.mark.parametrize("H", [5, 700, 6656, 20001])
+@pytest.mark.parametrize("c", [-3e38, 1e38, 1e30])
+def test_layer_norm_of_a_huge_constant_row(H, c):
+    """The row's sum overflows fp32, its mean does not: y is the bias.  (Exactly:
+    the rounding of the mean leaves deviations of 0, or of at least one step of
+    c, whose squares overflow and make rstd 0.)"""
+    import torch
+    import linear_cross_entropy_gemm_amd as L
+    x = torch.full((3, H), c, dtype=torch.float32, device="cuda")
+    b = _rand((1, H), "f32", 60)[0].clone()
+    o = L.layer_norm_fwd(x, None, b)
+    assert torch.all((o.mean.double() - x[0, 0].double()).abs() <= 2.0 ** -18 * abs(c))
+    assert torch.equal(o.y, b.expand(3, H))
+
+
+def test_layer_norm_bias_gradient_without_a_weight():
+    """A float32 bias beside bfloat16 rows: its gradient is not rounded to
+    bfloat16 on the way."""
+    import torch
+    import linear_cross_entropy_gemm_amd as L
+    M, H = 200, 300
+    x, dy = _rand((M, H), "bf16", 61), _rand((M, H), "bf16", 62)
+    b = torch.zeros(H, device="cuda", requires_grad=True)
+    gb, = torch.autograd.grad(L.layer_norm(x, None, b), b, dy)
+    assert gb.dtype == torch.float32
+    _check("db", gb, _np(dy).sum(0), (M + 4) * U * np.abs(_np(dy)).sum(0))
+    o = L.layer_norm_fwd(x)
+    g = L.layer_norm_bwd(dy, x, None, o.mean, o.rstd, param_dtype=torch.float32)
+    assert torch.equal(g.grad_bias, gb) and g.grad_weight.dtype == torch.float32
+    for weight, d in ((b.detach(), torch.bfloat16), (None, torch.float16)):
+        with pytest.raises(TypeError):
+            L.layer_norm_bwd(dy, x, weight, o.mean, o.rstd, param_dtype=d)
+
+
 def test_step_replays_from_a_captured_graph():
     """Dropout, layer norm and their gradients in one captured graph, four
     replays with eager work in between; the dropout offset advances on the
