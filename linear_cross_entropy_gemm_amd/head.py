@@ -57,6 +57,12 @@ def _rows(x: torch.Tensor) -> torch.Tensor:
     return x2 if x2.stride(1) == 1 or x2.shape[1] == 1 else x2.contiguous()
 
 
+def _like(x: torch.Tensor) -> torch.Tensor:
+    """A new contiguous tensor of x's shape and dtype (a shape read from
+    Python and passed back takes twice as long)."""
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
+
+
 def _check_tensor(name: str, x: torch.Tensor) -> None:
     if x.dtype not in _DTYPES:
         raise TypeError(f"{name} must be bfloat16 or float32 (got {x.dtype})")
@@ -93,25 +99,32 @@ def _check_params(x: torch.Tensor, weight: Optional[torch.Tensor], bias: Optiona
     return weight, bias, w_dtype
 
 
-def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
-                   eps: float = 1e-5) -> LayerNormForward:
-    """One call of ``flce_layer_norm_fwd`` over the last dimension of ``x``:
-    y and the row statistics that ``layer_norm_bwd`` takes.  ``weight`` and
-    ``bias`` [H] may be absent and may be float32 next to a bfloat16 ``x``."""
+def _layer_norm_fwd(x, weight, bias, eps, stats: bool):
     _check_rows("x", x)
     w, b, w_dtype = _check_params(x, weight, bias)
     eps = float(eps)
     x2 = _rows(x)
     M, H = x2.shape
     dev = x.device
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    mean, rstd = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=dev).unbind(0)
+    y = _like(x)
+    mean = rstd = None
+    if stats:
+        mean = torch.empty(M if x.dim() == 2 else x.shape[:-1], dtype=torch.float32, device=dev)
+        rstd = torch.empty_like(mean)
     rc = _enqueue(dev, lambda stream: _lib.flce_layer_norm_fwd(
-        x2.data_ptr(), x2.stride(0), _ptr(w), _ptr(b), M, H, eps, y.data_ptr(), H, mean.data_ptr(), rstd.data_ptr(),
-        stream, _DTYPES[x.dtype], _DTYPES[w_dtype]))
+        x2.data_ptr(), x2.stride(0), _ptr(w), _ptr(b), M, H, eps, y.data_ptr(), H, _ptr(mean), _ptr(rstd), stream,
+        _DTYPES[x.dtype], _DTYPES[w_dtype]))
     if rc != _lib.FLCE_OK:
         raise _lib.FlceError(rc, "flce_layer_norm_fwd")
-    return LayerNormForward(y, mean, rstd)
+    return y, mean, rstd
+
+
+def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                   eps: float = 1e-5) -> LayerNormForward:
+    """One call of ``flce_layer_norm_fwd`` over the last dimension of ``x``:
+    y and the row statistics that ``layer_norm_bwd`` takes.  ``weight`` and
+    ``bias`` [H] may be absent and may be float32 next to a bfloat16 ``x``."""
+    return LayerNormForward(*_layer_norm_fwd(x, weight, bias, eps, True))
 
 
 def layer_norm_bwd(grad_y: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor], mean: torch.Tensor,
@@ -138,12 +151,12 @@ def layer_norm_bwd(grad_y: torch.Tensor, x: torch.Tensor, weight: Optional[torch
     for name, t in (("mean", mean), ("rstd", rstd)):
         if t.dtype != torch.float32 or t.numel() != M or t.device != dev or not t.is_contiguous():
             raise ValueError(f"{name} must hold one contiguous float32 value per row of x on its device")
-    gx = torch.empty(x.shape, dtype=x.dtype, device=dev) if need_x else None
+    gx = _like(x) if need_x else None
     gw = gb = None
     ws_bytes = 0
     if need_params:
         gw = torch.empty(H, dtype=w_dtype, device=dev)
-        gb = torch.empty(H, dtype=w_dtype, device=dev)
+        gb = torch.empty_like(gw)
         ws_bytes = _lib.flce_layer_norm_bwd_workspace_size(M, H, _DTYPES[x.dtype])
         if ws_bytes == 0:
             raise _lib.FlceError(_lib.FLCE_EUNSUPPORTED, "flce_layer_norm_bwd_workspace_size")
@@ -186,7 +199,7 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     statistics are kept for the backward pass, the normalised values are not:
     they are formed again from ``x``."""
     if not _needs_grad(x, weight, bias):
-        return layer_norm_fwd(x, weight, bias, eps).y
+        return _layer_norm_fwd(x, weight, bias, eps, False)[0]
     return _LayerNorm.apply(x, weight, bias, eps)
 
 
@@ -194,7 +207,7 @@ def _dropout(x, p, seed, offset, residual) -> torch.Tensor:
     xc = x.contiguous()
     res = None if residual is None else residual.contiguous()
     dev = x.device
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    y = _like(x)
     tensor = torch.is_tensor(offset)
     rc = _enqueue(dev, lambda stream: _lib.flce_dropout(
         xc.data_ptr(), _ptr(res), y.data_ptr(), xc.numel(), p, seed, 0 if tensor else offset,
@@ -302,7 +315,6 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature: Union[float, torc
     z = _rows(logits)
     N, V = z.shape
     dev = logits.device
-    shape = logits.shape[:-1]
     if u.dtype != torch.float32 or u.device != dev or u.numel() != N:
         raise ValueError(f"u must hold one float32 per row of logits on {dev}")
     u = u.contiguous()
@@ -315,6 +327,7 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature: Union[float, torc
     if ws_bytes == 0:
         raise _lib.FlceError(_lib.FLCE_EUNSUPPORTED, "flce_sample_workspace_size")
     workspace = _workspace(workspace, ws_bytes, dev)
+    shape = N if logits.dim() == 2 else logits.shape[:-1]
     res = SampleOutputs(torch.empty(shape, dtype=torch.int64, device=dev),
                         torch.empty(shape, dtype=torch.float32, device=dev) if logprobs else None)
     rc = _enqueue(dev, lambda stream: _lib.flce_sample(
@@ -334,7 +347,7 @@ def lm_head_sample(x: torch.Tensor, W: torch.Tensor, u: torch.Tensor, norm_weigh
     """The whole head of a decoding step: the final layer norm of the hidden
     states ``x`` [..., H], the materialised logits (``logits``), and one token
     per row (``sample``)."""
-    y = layer_norm_fwd(x, norm_weight, norm_bias, eps).y
+    y = _layer_norm_fwd(x, norm_weight, norm_bias, eps, False)[0]
     H = x.shape[-1]
     z = _logits(y.reshape(-1, H), W, softcap, multiplier)
     o = sample(z, u, temperature, top_k, top_p, min_p, logprobs=logprobs)
