@@ -3,9 +3,9 @@ with its residual add and the final layer norm in front of it, with their
 backward passes, and drawing tokens from the logits behind it.  Every step
 of the computation runs in the library's HIP kernels on torch's current
 stream of the tensors' device; nothing synchronises, and every function can
-be captured in a graph.  (A captured ``backward()`` needs leaves of which no
-eagerly built graph is alive: torch runs the accumulation into a leaf on the
-stream on which its node was made.)"""
+be captured in a graph.  (A captured backward pass needs leaves of which no
+graph built on another stream is alive; where one of these functions built
+it, the pass is refused.)"""
 from __future__ import annotations
 
 import dataclasses
@@ -15,7 +15,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib
-from .torch_api import _DTYPES, _ptr, _workspace, linear_cross_entropy, logits as _logits
+from .torch_api import _DTYPES, _ptr, _workspace, check_leaves, linear_cross_entropy, logits as _logits, note_leaves
 
 _U64 = (1 << 64) - 1
 
@@ -186,6 +186,7 @@ class _LayerNorm(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, grad_y):
+        check_leaves(ctx, grad_y)
         x, weight, mean, rstd = ctx.saved_tensors
         need_x, need_w, need_b, _ = ctx.needs_input_grad
         g = layer_norm_bwd(grad_y, x, weight, mean, rstd, need_x=need_x, need_params=need_w or need_b,
@@ -200,7 +201,9 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     they are formed again from ``x``."""
     if not _needs_grad(x, weight, bias):
         return _layer_norm_fwd(x, weight, bias, eps, False)[0]
-    return _LayerNorm.apply(x, weight, bias, eps)
+    y = _LayerNorm.apply(x, weight, bias, eps)
+    note_leaves(y)
+    return y
 
 
 def _dropout(x, p, seed, offset, residual) -> torch.Tensor:
@@ -231,6 +234,7 @@ class _Dropout(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad_y):
+        check_leaves(ctx, grad_y)
         # the same map on the upstream gradient, itself differentiable
         p, seed, offset = ctx.args
         gx = None
@@ -267,7 +271,9 @@ def dropout(x: torch.Tensor, p: float, seed: int, offset: Union[int, torch.Tenso
                          f"{tuple(residual.shape)} {residual.dtype} on {residual.device})")
     if not _needs_grad(x, residual):
         return _dropout(x, float(p), seed, offset, residual)
-    return _Dropout.apply(x, residual, float(p), seed, offset)
+    y = _Dropout.apply(x, residual, float(p), seed, offset)
+    note_leaves(y)
+    return y
 
 
 def lm_head_loss(x: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, norm_weight: Optional[torch.Tensor],

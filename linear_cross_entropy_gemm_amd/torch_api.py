@@ -356,6 +356,37 @@ def scale_grads(g: torch.Tensor, grad_h: Optional[torch.Tensor], grad_W: Optiona
     return gh_out, gW_out
 
 
+# torch accumulates the gradient of a leaf on the stream on which the leaf's
+# accumulation node was made, and the node lives as long as any graph built
+# from the leaf.  A captured backward pass that meets one made on another
+# stream would draw that stream into the capture, which ends the process where
+# it is the default stream.  So each node is marked with the stream on which
+# it was first seen, and such a pass is refused.
+_STREAM_MARK = "flce_stream"
+
+
+def note_leaves(out: torch.Tensor) -> None:
+    """After an apply(): marks the accumulation nodes of its leaves."""
+    if out.grad_fn is None:
+        return
+    stream = torch.cuda.current_stream(out.device).cuda_stream
+    for node, _ in out.grad_fn.next_functions:
+        if node is not None and node.name() == "torch::autograd::AccumulateGrad":
+            node.metadata.setdefault(_STREAM_MARK, stream)
+
+
+def check_leaves(ctx, grad: torch.Tensor) -> None:
+    """First in a backward(): refuses to be captured with a leaf whose
+    accumulation node belongs to another stream."""
+    if not torch.cuda.is_current_stream_capturing():
+        return
+    stream = torch.cuda.current_stream(grad.device).cuda_stream
+    for node, _ in ctx.next_functions:
+        if node is not None and node.metadata.get(_STREAM_MARK, stream) != stream:
+            raise RuntimeError("this backward pass cannot be captured: a graph built from the same leaf on another "
+                               "stream is still alive (drop its outputs before the capture)")
+
+
 class _LinearCrossEntropy(torch.autograd.Function):
     """mean / sum: the gradients come out of the fused forward call; backward
     scales them by the upstream scalar on the device (``flce_scale_grads``).
@@ -386,6 +417,7 @@ class _LinearCrossEntropy(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad_loss, _grad_n_correct):
+        check_leaves(ctx, grad_loss)
         need_h, need_W = ctx.needs_input_grad[:2]
         if ctx.reduction == "none":
             h, W, labels = ctx.saved_tensors
@@ -410,4 +442,7 @@ def linear_cross_entropy(h: torch.Tensor, W: torch.Tensor, labels: torch.Tensor,
     Nothing synchronises the host by default: out-of-range labels are
     reported by ``read_status(workspace)`` on a caller-owned ``workspace``
     (uint8, reused across steps), or at once with ``check=True``."""
-    return _LinearCrossEntropy.apply(h, W, labels, ignore_index, softcap, multiplier, reduction, workspace, check)
+    loss, n_correct = _LinearCrossEntropy.apply(h, W, labels, ignore_index, softcap, multiplier, reduction, workspace,
+                                                check)
+    note_leaves(loss)
+    return loss, n_correct

@@ -365,6 +365,40 @@ def test_step_replays_from_a_captured_graph():
     assert not torch.equal(seen[0], seen[1])
 
 
+def test_autograd_step_replays_from_a_captured_graph():
+    """The differentiable functions and their backward pass in one captured
+    graph; eager steps of the same leaves run before it and between replays."""
+    import torch
+    import linear_cross_entropy_gemm_amd as L
+    x, r = (_rand((70, 900), "bf16", 63 + i).requires_grad_() for i in range(2))
+    w, b = (_rand((1, 900), "f32", 65 + i, 0.2, 1.0)[0].clone().requires_grad_() for i in range(2))
+    dy = _rand((70, 900), "bf16", 67)
+    off = torch.zeros(1, dtype=torch.int64, device="cuda")
+
+    def step(offset):
+        y = L.layer_norm(L.dropout(x, 0.2, 78, offset, residual=r), w, b)
+        return (y.detach(), *torch.autograd.grad(y, (x, r, w, b), dy))
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step(off)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step(off)
+    torch.cuda.synchronize()
+    for rep in range(4):
+        off.fill_(rep)
+        for t in outs:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in outs]
+        want = step(rep)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, c) for a, c in zip(got, want)), rep
+
+
 def test_two_streams_match_separate_calls():
     import torch
     import linear_cross_entropy_gemm_amd as L

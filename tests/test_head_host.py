@@ -128,3 +128,56 @@ def test_sample_workspace_size():
         assert b >= 256 and b % 256 == 0
     assert L.flce_sample_workspace_size(-1, 8, 0) == 0 and L.flce_sample_workspace_size(1, 0, 0) == 0
     assert L.flce_sample_workspace_size(1, 8, 2) == 0 and L.flce_sample_workspace_size(1, (1 << 24) + 1, 0) == 0
+
+
+def _identity():
+    """A differentiable identity with the package's notes and checks, on the CPU."""
+    from linear_cross_entropy_gemm_amd import torch_api
+
+    class F(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, a, b, n):
+            return a * 1
+
+        @staticmethod
+        def backward(ctx, g):
+            torch_api.check_leaves(ctx, g)
+            return g, None, None
+
+    def call(x):
+        y = F.apply(x, None, 3)
+        torch_api.note_leaves(y)
+        return y
+    return call
+
+
+def test_captured_backward_is_refused_beside_a_live_graph_of_another_stream(monkeypatch):
+    """The streams and the capture are played by stand-ins: a leaf whose graph
+    from stream 1 is alive refuses a backward pass captured on stream 2, and
+    is accepted uncaptured, on stream 1, and once that graph is gone."""
+    import gc
+    import types
+    state = {"stream": 1, "capturing": False}
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: state["capturing"])
+    monkeypatch.setattr(torch.cuda, "current_stream",
+                        lambda dev=None: types.SimpleNamespace(cuda_stream=state["stream"]))
+    f = _identity()
+    x, one = torch.ones(3, requires_grad=True), torch.ones(3)
+
+    def grad():
+        return torch.autograd.grad(f(x), x, one)[0]
+
+    alive = f(x)
+    assert torch.equal(grad(), one)
+    state.update(stream=2)
+    assert torch.equal(grad(), one)
+    state.update(capturing=True)
+    with pytest.raises(RuntimeError, match="cannot be captured"):
+        grad()
+    state.update(stream=1)
+    assert torch.equal(grad(), one)
+    state.update(stream=2)
+    del alive
+    gc.collect()
+    assert torch.equal(grad(), one)
+    assert torch.equal(torch.autograd.grad(f(f(x)), x, one)[0], one)   # a node in between has no mark
