@@ -38,7 +38,8 @@ EXPORTED = ("flce_plan", "flce_workspace_size", "flce_fwd_bwd", "flce_fwd_bwd_ex
             "flce_fwd_workspace_size",
             "flce_fwd", "flce_logits", "flce_cross_entropy_workspace_size", "flce_cross_entropy",
             "flce_scale_grads", "flce_layer_norm_fwd", "flce_layer_norm_bwd_workspace_size",
-            "flce_layer_norm_bwd", "flce_dropout", "flce_sample_workspace_size", "flce_sample", "flce_read_status", "flce_strerror", "flce_profile_enable", "flce_profile_read")
+            "flce_layer_norm_bwd", "flce_dropout", "flce_sample_workspace_size", "flce_sample",
+            "flce_read_status", "flce_strerror", "flce_profile_enable", "flce_profile_read")
 
 # Kernel kinds of the per-kernel timing facility (index order of the arrays).
 KERNEL_KINDS = ("label_scan", "fwd_logits", "row_merge", "grad_logits", "grad_h", "grad_h_reduce",
