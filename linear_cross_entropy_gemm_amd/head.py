@@ -9,6 +9,7 @@ it, the pass is refused.)"""
 from __future__ import annotations
 
 import dataclasses
+import operator
 from typing import Optional, Union
 
 import torch
@@ -255,14 +256,14 @@ def dropout(x: torch.Tensor, p: float, seed: int, offset: Union[int, torch.Tenso
     _check_tensor("x", x)
     if not 0.0 <= p <= 1.0:
         raise ValueError(f"p must lie in [0, 1] (got {p})")
-    seed = int(seed)
+    seed = operator.index(seed)
     if not 0 <= seed <= _U64:
         raise ValueError("seed must be an unsigned 64-bit integer")
     if torch.is_tensor(offset):
         if offset.dtype != torch.int64 or offset.numel() != 1 or offset.device != x.device:
             raise ValueError("a tensor offset must be one int64 on the device of x")
     else:
-        offset = int(offset)
+        offset = operator.index(offset)
         if not 0 <= offset <= _U64:
             raise ValueError("offset must be an unsigned 64-bit integer")
     if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype
@@ -296,7 +297,13 @@ def _sample_param(name: str, v, dtype, N: int, dev, prm) -> Optional[torch.Tenso
     """A scalar goes into the parameter block, a tensor's address into its
     per-row field; the tensor is returned to be kept alive for the call."""
     if not torch.is_tensor(v):
-        setattr(prm, name, int(v) if dtype == torch.int64 else float(v))
+        if dtype == torch.int64:
+            v = operator.index(v)
+            if not -1 << 63 <= v < 1 << 63:   # the C field would take it modulo 2^64
+                raise ValueError(f"{name} must fit 64 bits (got {v})")
+            setattr(prm, name, v)
+        else:
+            setattr(prm, name, float(v))
         return None
     if v.dtype != dtype or v.device != dev or v.numel() != N:
         raise ValueError(f"{name} must be a number or one {dtype} per row on {dev}")

@@ -181,3 +181,15 @@ def test_captured_backward_is_refused_beside_a_live_graph_of_another_stream(monk
     gc.collect()
     assert torch.equal(grad(), one)
     assert torch.equal(torch.autograd.grad(f(f(x)), x, one)[0], one)   # a node in between has no mark
+
+
+@pytest.mark.parametrize("k", [-(1 << 63) - 1, 1 << 63, (1 << 64) + 5])
+def test_top_k_outside_the_parameter_block_is_refused(k):
+    from linear_cross_entropy_gemm_amd import head
+    prm = L.flce_sample_params_t()
+    with pytest.raises(ValueError):
+        head._sample_param("top_k", k, torch.int64, 1, torch.device("cpu"), prm)
+    with pytest.raises(TypeError):
+        head._sample_param("top_k", 2.5, torch.int64, 1, torch.device("cpu"), prm)
+    head._sample_param("top_k", (1 << 63) - 1, torch.int64, 1, torch.device("cpu"), prm)
+    assert prm.top_k == (1 << 63) - 1
