@@ -105,7 +105,10 @@ __device__ __forceinline__ void row_sums(float (&v)[N], SumLds<N>& lds, int& buf
 // Mean and 1 / standard deviation of a row from its waves' own: a wave's mean
 // and sum of squared deviations from it need no barrier, and
 //   mean = sum n_w mean_w / H,  sum of squares = sum (q_w + n_w (mean_w - mean)^2)
-// joins them behind one.  Neither a far mean nor an outlier costs accuracy.
+// joins them behind one.  A mean is kept in two parts throughout, the rounded
+// one that the deviations were taken from and what its rounding left over: one
+// fp32 number for a wave's mean would move every y of a row at 1e5 standard
+// deviations from zero by 3e-3, the two parts leave 4e-7.
 // kRow threads hold a row in kVec vectors each; a work-group holds kRows
 // rows (more than one only where a row is one wave) and walks over the rows
 // in steps of the grid, the next row's loads issued before the current row's
@@ -115,7 +118,7 @@ __global__ __launch_bounds__(kRow* kRows) __attribute__((amdgpu_waves_per_eu(kEu
   static_assert(kRow == 64 || kRows == 1, "a work-group barrier must see one row");
   constexpr int E = RowVec<T>::E, kWaves = kRow / 64;
   typedef typename RowVec<T>::type vec_t;
-  __shared__ float lds[2][2][kWaves];
+  __shared__ float lds[2][3][kWaves];
   int buf = 0;
   const int t = threadIdx.x % kRow, wave = t >> 6;
   const int64_t step = (int64_t)gridDim.x * kRows;
@@ -184,20 +187,22 @@ __global__ __launch_bounds__(kRow* kRows) __attribute__((amdgpu_waves_per_eu(kEu
     float m = m0, rest = rest0, q = q0;
     if (kRow > 64) {
       if ((threadIdx.x & 63) == 0) {
-        lds[buf][0][wave] = m0 + rest0;
-        lds[buf][1][wave] = q0;
+        lds[buf][0][wave] = m0;
+        lds[buf][1][wave] = rest0;
+        lds[buf][2][wave] = q0;
       }
       __syncthreads();
-      m = lds[buf][0][0];   // deviations of the waves' means from the first
+      m = lds[buf][0][0];   // deviations of the waves' means from the first's rounded one
+      auto from_first = [&](int i) { return (lds[buf][0][i] - m) + lds[buf][1][i]; };
       rest = 0.0f;
 #pragma unroll
-      for (int i = 1; i < kWaves; ++i) rest = __builtin_fmaf(count(i), lds[buf][0][i] - m, rest);
+      for (int i = 0; i < kWaves; ++i) rest = __builtin_fmaf(count(i), from_first(i), rest);
       rest *= inv;
       q = 0.0f;
 #pragma unroll
       for (int i = 0; i < kWaves; ++i) {
-        const float d = (lds[buf][0][i] - m) - rest, n = count(i);
-        q += n > 0.0f ? __builtin_fmaf(n * d, d, lds[buf][1][i]) : 0.0f;
+        const float d = from_first(i) - rest, n = count(i);
+        q += n > 0.0f ? __builtin_fmaf(n * d, d, lds[buf][2][i]) : 0.0f;
       }
       buf ^= 1;
     }
