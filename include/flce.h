@@ -321,11 +321,13 @@ int flce_scale_grads(const float* grad_scale, const void* grad_h_in, void* grad_
  * (NULL: not written) and are what flce_layer_norm_bwd takes.  Pointers need
  * the alignment of one element only.  eps > 0, finite.  y may be x itself
  * (then ld_y == ld_x) and must not overlap it otherwise.  Statistics and
- * arithmetic are fp32, y is rounded once.  (Deviations from the mean beyond
- * 2^63 overflow in their squares: rstd is 0 there and y carries nothing of
- * x.)  Any H from 1 to 2^21, M < 2^31 (else FLCE_EUNSUPPORTED); M = 0 does nothing.  Enqueued on
- * `stream`; nothing is allocated, nothing synchronises.  Returns FLCE_OK,
- * FLCE_EINVAL, FLCE_EUNSUPPORTED or FLCE_EDEVICE.
+ * arithmetic are fp32, y is rounded once.  A row whose sum of squared
+ * deviations passes fp32's range (a standard deviation beyond 2^64 / sqrt(H))
+ * has rstd 0 and the bias for y; one with two values more than the largest
+ * float apart may be NaN.  Any H from 1 to 2^21, M < 2^31 (else
+ * FLCE_EUNSUPPORTED); M = 0 does nothing.  Enqueued on `stream`; nothing is
+ * allocated, nothing synchronises.  Returns FLCE_OK, FLCE_EINVAL,
+ * FLCE_EUNSUPPORTED or FLCE_EDEVICE.
  */
 int flce_layer_norm_fwd(const void* x, int64_t ld_x, const void* weight, const void* bias, int64_t M, int64_t H,
                         float eps, void* y, int64_t ld_y, float* mean, float* rstd,

@@ -158,8 +158,9 @@ __global__ __launch_bounds__(kRow* kRows) __attribute__((amdgpu_waves_per_eu(kEu
       for (int e = 0; e < E; ++e) s = __builtin_fmaf(to_f32(cur[i][e]), inv_mine, s);   // a sum could overflow
     }
     const float m0 = wave_sum(s);
-    // squares of the deviations, and the deviations' own sum: what the
-    // rounding of m0 left over is taken out of both results
+    // squares of the deviations, and the deviations' own average: what the
+    // rounding of m0 left over is taken out of both results (as a sum, the
+    // half of a row's deviations that has one sign could overflow)
     float d1 = 0.0f, d2 = 0.0f;
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
@@ -168,21 +169,19 @@ __global__ __launch_bounds__(kRow* kRows) __attribute__((amdgpu_waves_per_eu(kEu
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           const float x = e < left ? to_f32(cur[i][e]) - m0 : 0.0f;
-          d1 += x;
+          d1 = __builtin_fmaf(x, inv_mine, d1);
           d2 = __builtin_fmaf(x, x, d2);
         }
       } else {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           const float x = to_f32(cur[i][e]) - m0;
-          d1 += x;
+          d1 = __builtin_fmaf(x, inv_mine, d1);
           d2 = __builtin_fmaf(x, x, d2);
         }
       }
     }
-    d1 = wave_sum(d1);
-    d2 = wave_sum(d2);
-    const float rest0 = d1 * inv_mine, q0 = __builtin_fmaf(-rest0, d1, d2);
+    const float rest0 = wave_sum(d1), q0 = __builtin_fmaf(-(rest0 * mine), rest0, wave_sum(d2));
     // the row's mean is m + rest
     float m = m0, rest = rest0, q = q0;
     if (kRow > 64) {
@@ -196,8 +195,7 @@ __global__ __launch_bounds__(kRow* kRows) __attribute__((amdgpu_waves_per_eu(kEu
       auto from_first = [&](int i) { return (lds[buf][0][i] - m) + lds[buf][1][i]; };
       rest = 0.0f;
 #pragma unroll
-      for (int i = 0; i < kWaves; ++i) rest = __builtin_fmaf(count(i), from_first(i), rest);
-      rest *= inv;
+      for (int i = 0; i < kWaves; ++i) rest = __builtin_fmaf(count(i) * inv, from_first(i), rest);
       q = 0.0f;
 #pragma unroll
       for (int i = 0; i < kWaves; ++i) {
@@ -256,12 +254,12 @@ __global__ __launch_bounds__(kWide) void ln_fwd_wide_kernel(LnFwdArgs p) {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const float d = c + e < p.H ? to_f32(v[e]) - mean0 : 0.0f;
-        dev[0] += d;
+        dev[0] = __builtin_fmaf(d, inv, dev[0]);
         dev[1] = __builtin_fmaf(d, d, dev[1]);
       }
     }
     row_sums<kWide>(dev, lds2, buf2);
-    const float rest = dev[0] * inv;
+    const float rest = dev[0];
     const float var = __builtin_fmaf(-rest, rest, dev[1] * inv);
     const float rstd = 1.0f / sqrtf((var > 0.0f ? var : var == var ? 0.0f : var) + p.eps);
     T* yr = static_cast<T*>(p.y) + row * p.ldy;

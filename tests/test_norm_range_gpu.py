@@ -35,3 +35,24 @@ def test_layer_norm_far_from_zero(M, H, shift):
     _check("y", o.y, y, grow * U * (60 + k + (44 + k) * xh) + 4 * U * np.abs(y))
     _check("mean", o.mean, mean, U * (np.abs(mean) + grow * (60 + k) / rstd))
     _check("rstd", o.rstd, rstd, grow * U * (40 + k) * rstd)
+
+
+@pytest.mark.parametrize("H", [5, 700, 2000, 5003, 8192, 20001])
+@pytest.mark.parametrize("c", [1e21, 1e35, 1e37, 1.6e38])
+def test_layer_norm_of_values_far_apart(H, c):
+    """Squares of the deviations overflow (1e21^2 does), the mean does not:
+    rstd is 0 and y is the bias, however the two signs lie in the row.  The
+    mean's sums round at most 54 + 20 times a number of at most c: 2^-17 c."""
+    import torch
+    import linear_cross_entropy_gemm_amd as L
+    x = torch.full((4, H), c, device="cuda")
+    x[0, :H // 2] = -c
+    x[1, ::2] = -c
+    x[2, 1:] = -c
+    x[3] *= torch.rand(H, generator=torch.Generator().manual_seed(H)).cuda() * 2 - 1
+    b = _rand((1, H), "f32", 102)[0].clone()
+    o = L.layer_norm_fwd(x, None, b, EPS)
+    log(f"[ln] values far apart H={H} c={c}")
+    ref = _np(x).mean(1)
+    assert np.all(np.abs(_np(o.mean) - ref) <= 2.0 ** -17 * c)
+    assert not o.rstd.any() and torch.equal(o.y, b.expand(4, H))
