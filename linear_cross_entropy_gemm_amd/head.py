@@ -3,7 +3,8 @@ with its residual add and the final layer norm in front of it, with their
 backward passes, and drawing tokens from the logits behind it.  Every step
 of the computation runs in the library's HIP kernels on torch's current
 stream of the tensors' device; nothing synchronises, and every function can
-be captured in a graph.  (A captured backward pass needs leaves of which no
+be captured in a graph.  The differentiable ones have a backward pass;
+forward-mode derivatives are refused (NotImplementedError).  (A captured backward pass needs leaves of which no
 graph built on another stream is alive; where one of these functions built
 it, the pass is refused.)"""
 from __future__ import annotations
@@ -16,7 +17,8 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib
-from .torch_api import _DTYPES, _ptr, _workspace, check_leaves, linear_cross_entropy, logits as _logits, note_leaves
+from .torch_api import (_DTYPES, _ptr, _workspace, check_backward, has_tangent, linear_cross_entropy,
+                        logits as _logits, note_leaves)
 
 _U64 = (1 << 64) - 1
 
@@ -173,7 +175,12 @@ def layer_norm_bwd(grad_y: torch.Tensor, x: torch.Tensor, weight: Optional[torch
 
 
 def _needs_grad(*tensors) -> bool:
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+    """Whether the call has to go through its autograd function: for a backward
+    pass, or because an input carries a forward-mode tangent (in grad mode or
+    not), which the function refuses and a plain call would drop."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        return True
+    return has_tangent(*tensors)
 
 
 class _LayerNorm(torch.autograd.Function):
@@ -187,7 +194,7 @@ class _LayerNorm(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, grad_y):
-        check_leaves(ctx, grad_y)
+        check_backward(ctx, grad_y)
         x, weight, mean, rstd = ctx.saved_tensors
         need_x, need_w, need_b, _ = ctx.needs_input_grad
         g = layer_norm_bwd(grad_y, x, weight, mean, rstd, need_x=need_x, need_params=need_w or need_b,
@@ -235,7 +242,7 @@ class _Dropout(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad_y):
-        check_leaves(ctx, grad_y)
+        check_backward(ctx, grad_y)
         # the same map on the upstream gradient, itself differentiable
         p, seed, offset = ctx.args
         gx = None

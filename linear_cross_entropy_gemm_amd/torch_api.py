@@ -7,6 +7,7 @@ import dataclasses
 from typing import Optional
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _lib
 
@@ -387,6 +388,19 @@ def check_leaves(ctx, grad: torch.Tensor) -> None:
                                "stream is still alive (drop its outputs before the capture)")
 
 
+def has_tangent(*tensors) -> bool:
+    """Whether one of the tensors (None: none) carries a forward-mode derivative."""
+    return forward_ad._current_level >= 0 and any(
+        t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
+
+
+def check_backward(ctx, grad: torch.Tensor) -> None:
+    """First in a backward(): refuses what its kernels would pass over."""
+    check_leaves(ctx, grad)
+    if has_tangent(grad):
+        raise NotImplementedError("forward-mode derivatives of a backward pass (jvp) are not implemented")
+
+
 class _LinearCrossEntropy(torch.autograd.Function):
     """mean / sum: the gradients come out of the fused forward call; backward
     scales them by the upstream scalar on the device (``flce_scale_grads``).
@@ -417,7 +431,7 @@ class _LinearCrossEntropy(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad_loss, _grad_n_correct):
-        check_leaves(ctx, grad_loss)
+        check_backward(ctx, grad_loss)
         need_h, need_W = ctx.needs_input_grad[:2]
         if ctx.reduction == "none":
             h, W, labels = ctx.saved_tensors
