@@ -4,9 +4,10 @@ backward passes, and drawing tokens from the logits behind it.  Every step
 of the computation runs in the library's HIP kernels on torch's current
 stream of the tensors' device; nothing synchronises, and every function can
 be captured in a graph.  The differentiable ones have a backward pass;
-forward-mode derivatives are refused (NotImplementedError).  (A captured backward pass needs leaves of which no
-graph built on another stream is alive; where one of these functions built
-it, the pass is refused.)"""
+forward-mode derivatives are refused (NotImplementedError).  (A captured
+backward pass may meet leaves of which a graph built on another side stream is
+alive, but none built on the default stream; where one of these functions
+built it, the pass is refused.)"""
 from __future__ import annotations
 
 import dataclasses

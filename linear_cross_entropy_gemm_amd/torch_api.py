@@ -360,32 +360,47 @@ def scale_grads(g: torch.Tensor, grad_h: Optional[torch.Tensor], grad_W: Optiona
 # torch accumulates the gradient of a leaf on the stream on which the leaf's
 # accumulation node was made, and the node lives as long as any graph built
 # from the leaf.  A captured backward pass that meets one made on another
-# stream would draw that stream into the capture, which ends the process where
-# it is the default stream.  So each node is marked with the stream on which
-# it was first seen, and such a pass is refused.
+# stream draws that stream into the capture.  A stream of torch's own pool
+# joins it and is joined back at the end of the pass; the default stream cannot
+# be captured, and the attempt ends the process.  So each node is marked with
+# the stream on which one of these functions first met it (that is where it was
+# made, unless another torch operation used the leaf before, elsewhere: torch
+# does not tell), and a pass that would capture the default stream, or one that
+# torch does not own, is refused.
 _STREAM_MARK = "flce_stream"
+
+
+def _stream_mark(dev):
+    """(handle, whether it is of torch's own pool: ids of those are odd, the
+    default stream's is 0 and a foreign one's its address)."""
+    stream = torch.cuda.current_stream(dev)
+    return stream.cuda_stream, getattr(stream, "stream_id", 0) % 2 == 1
 
 
 def note_leaves(out: torch.Tensor) -> None:
     """After an apply(): marks the accumulation nodes of its leaves."""
     if out.grad_fn is None:
         return
-    stream = torch.cuda.current_stream(out.device).cuda_stream
+    mark = _stream_mark(out.device)
     for node, _ in out.grad_fn.next_functions:
         if node is not None and node.name() == "torch::autograd::AccumulateGrad":
-            node.metadata.setdefault(_STREAM_MARK, stream)
+            node.metadata.setdefault(_STREAM_MARK, mark)
 
 
 def check_leaves(ctx, grad: torch.Tensor) -> None:
     """First in a backward(): refuses to be captured with a leaf whose
-    accumulation node belongs to another stream."""
+    accumulation node belongs to a stream that cannot join the capture."""
     if not torch.cuda.is_current_stream_capturing():
         return
-    stream = torch.cuda.current_stream(grad.device).cuda_stream
+    mine = _stream_mark(grad.device)
     for node, _ in ctx.next_functions:
-        if node is not None and node.metadata.get(_STREAM_MARK, stream) != stream:
-            raise RuntimeError("this backward pass cannot be captured: a graph built from the same leaf on another "
-                               "stream is still alive (drop its outputs before the capture)")
+        if node is None:
+            continue
+        stream, joins = node.metadata.get(_STREAM_MARK, mine)
+        if stream != mine[0] and not joins:
+            raise RuntimeError("this backward pass cannot be captured: a graph built from the same leaf on the default "
+                               "stream, or on one that torch does not own, is still alive (drop its outputs before "
+                               "the capture, or build it under torch.cuda.stream(torch.cuda.Stream()))")
 
 
 def has_tangent(*tensors) -> bool:
@@ -455,7 +470,12 @@ def linear_cross_entropy(h: torch.Tensor, W: torch.Tensor, labels: torch.Tensor,
 
     Nothing synchronises the host by default: out-of-range labels are
     reported by ``read_status(workspace)`` on a caller-owned ``workspace``
-    (uint8, reused across steps), or at once with ``check=True``."""
+    (uint8, reused across steps), or at once with ``check=True``.
+
+    A backward pass can be captured in a graph beside live graphs of the same
+    leaves that were built on side streams (a warm-up's ``loss``), not beside
+    one built on the default stream: that raises, where this function met the
+    leaves first."""
     loss, n_correct = _LinearCrossEntropy.apply(h, W, labels, ignore_index, softcap, multiplier, reduction, workspace,
                                                 check)
     note_leaves(loss)

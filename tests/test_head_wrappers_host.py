@@ -64,3 +64,29 @@ def test_a_tangent_of_the_upstream_gradient_is_refused(monkeypatch):
             with pytest.raises(NotImplementedError, match="jvp"):
                 torch.autograd.grad(y, x, fw.make_dual(one, one), retain_graph=True)
             torch.autograd.grad(y, x, one)
+
+
+def test_captured_backward_beside_live_graphs_of_each_kind_of_stream(monkeypatch):
+    """A warm-up's graph from a side stream of torch's own pool (odd ids) may be
+    alive when a backward pass is captured on another; one from the default
+    stream (id 0) or a foreign stream (its address, even) may not."""
+    import types
+    from test_head_host import _identity
+    now = {}
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: now["capturing"])
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: types.SimpleNamespace(
+        cuda_stream=now["handle"], stream_id=now["id"]))
+    f, one = _identity(), torch.ones(3)
+    for warm, ident, refused in ((0x1000, 33, False), (0, 0, True), (0x2000, 0x2000, True)):
+        x = torch.ones(3, requires_grad=True)
+        now.update(handle=warm, id=ident, capturing=False)
+        alive = f(x)
+        alive.backward(one, retain_graph=True)
+        now.update(handle=0x3000, id=65, capturing=True)
+        y = f(x)
+        if refused:
+            with pytest.raises(RuntimeError, match="cannot be captured"):
+                torch.autograd.grad(y, x, one)
+        else:
+            assert torch.equal(torch.autograd.grad(y, x, one)[0], one)
+        del alive
