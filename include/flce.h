@@ -488,10 +488,19 @@ int flce_profile_enable(int on);
 
 /*
  * Synchronise `stream`, fold all pending event pairs into the running totals
- * and copy them out: total_ms[k] and launches[k] for k < FLCE_KERNEL_KINDS
- * (caller-owned host arrays).  reset != 0 clears the totals afterwards.
- * Returns FLCE_OK, FLCE_EINVAL (null array) or FLCE_EDEVICE.
+ * and copy them out: total_ms[k] and launches[k] for k < n (caller-owned host
+ * arrays of n entries; those past FLCE_KERNEL_KINDS are set to 0).
+ * reset != 0 clears the totals of all kinds afterwards.  Returns FLCE_OK,
+ * FLCE_EINVAL (null array, n < 0) or FLCE_EDEVICE.
  */
+int flce_profile_read_n(hipStream_t stream, double* total_ms, int64_t* launches, int n, int reset);
+
+/*
+ * flce_profile_read_n with n = FLCE_PROFILE_READ_KINDS, the kinds of the head
+ * itself: a program built when there were no others passes arrays of that
+ * length, so this call never writes more.
+ */
+enum { FLCE_PROFILE_READ_KINDS = 12 };
 int flce_profile_read(hipStream_t stream, double* total_ms, int64_t* launches, int reset);
 
 #ifdef __cplusplus

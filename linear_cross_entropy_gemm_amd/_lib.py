@@ -39,7 +39,8 @@ EXPORTED = ("flce_plan", "flce_workspace_size", "flce_fwd_bwd", "flce_fwd_bwd_ex
             "flce_fwd", "flce_logits", "flce_cross_entropy_workspace_size", "flce_cross_entropy",
             "flce_scale_grads", "flce_layer_norm_fwd", "flce_layer_norm_bwd_workspace_size",
             "flce_layer_norm_bwd", "flce_dropout", "flce_sample_workspace_size", "flce_sample",
-            "flce_read_status", "flce_strerror", "flce_profile_enable", "flce_profile_read")
+            "flce_read_status", "flce_strerror", "flce_profile_enable", "flce_profile_read",
+            "flce_profile_read_n")
 
 # Kernel kinds of the per-kernel timing facility (index order of the arrays).
 KERNEL_KINDS = ("label_scan", "fwd_logits", "row_merge", "grad_logits", "grad_h", "grad_h_reduce",
@@ -160,6 +161,8 @@ def _load() -> ctypes.CDLL:
     lib.flce_profile_enable.restype = i32
     lib.flce_profile_read.argtypes = [vp, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(i64), i32]
     lib.flce_profile_read.restype = i32
+    lib.flce_profile_read_n.argtypes = [vp, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(i64), i32, i32]
+    lib.flce_profile_read_n.restype = i32
     return lib
 
 
@@ -302,9 +305,9 @@ def flce_profile_read(stream: int, reset: bool = True) -> dict:
     n = len(KERNEL_KINDS)
     ms = (ctypes.c_double * n)()
     cnt = (ctypes.c_int64 * n)()
-    rc = _lib.flce_profile_read(stream, ms, cnt, 1 if reset else 0)
+    rc = _lib.flce_profile_read_n(stream, ms, cnt, n, 1 if reset else 0)
     if rc != FLCE_OK:
-        raise FlceError(rc, "flce_profile_read")
+        raise FlceError(rc, "flce_profile_read_n")
     return {k: (ms[i], cnt[i]) for i, k in enumerate(KERNEL_KINDS)}
 
 

@@ -1,7 +1,7 @@
 // Per-kernel timing with HIP events on the caller's stream (measurement only).
 //
 // When enabled, run_call brackets every kernel launch with a pair of events
-// recorded on the launch stream.  flce_profile_read synchronises the stream,
+// recorded on the launch stream.  flce_profile_read_n synchronises the stream,
 // folds the elapsed times into per-kind totals and recycles the events.
 #include <mutex>
 #include <vector>
@@ -81,8 +81,8 @@ extern "C" int flce_profile_enable(int on) {
   return FLCE_OK;
 }
 
-extern "C" int flce_profile_read(hipStream_t stream, double* total_ms, int64_t* launches, int reset) {
-  if (!total_ms || !launches) return FLCE_EINVAL;
+extern "C" int flce_profile_read_n(hipStream_t stream, double* total_ms, int64_t* launches, int n, int reset) {
+  if (!total_ms || !launches || n < 0) return FLCE_EINVAL;
   flce::State& s = flce::state();
   if (hipStreamSynchronize(stream) != hipSuccess) return FLCE_EDEVICE;
   std::lock_guard<std::mutex> g(s.mu);
@@ -99,13 +99,18 @@ extern "C" int flce_profile_read(hipStream_t stream, double* total_ms, int64_t* 
     s.pool.push_back(p.b);
   }
   s.pending.clear();
-  for (int k = 0; k < FLCE_KERNEL_KINDS; ++k) {
-    total_ms[k] = s.total_ms[k];
-    launches[k] = s.launches[k];
-    if (reset) {
-      s.total_ms[k] = 0.0;
-      s.launches[k] = 0;
-    }
+  for (int k = 0; k < n; ++k) {
+    const bool known = k < FLCE_KERNEL_KINDS;
+    total_ms[k] = known ? s.total_ms[k] : 0.0;
+    launches[k] = known ? s.launches[k] : 0;
+  }
+  for (int k = 0; reset && k < FLCE_KERNEL_KINDS; ++k) {
+    s.total_ms[k] = 0.0;
+    s.launches[k] = 0;
   }
   return rc;
+}
+
+extern "C" int flce_profile_read(hipStream_t stream, double* total_ms, int64_t* launches, int reset) {
+  return flce_profile_read_n(stream, total_ms, launches, FLCE_PROFILE_READ_KINDS, reset);
 }
