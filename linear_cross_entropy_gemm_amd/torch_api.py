@@ -59,11 +59,22 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+def _check_projection(h: torch.Tensor, W: torch.Tensor) -> None:
+    """The kernels read H columns of every row of W from their own GPU."""
+    if h.dim() < 1 or W.dim() != 2 or W.shape[1] != h.shape[-1]:
+        raise ValueError(f"W must be [V, H] next to h [..., H] (got {tuple(W.shape)}, {tuple(h.shape)})")
+    if W.device != h.device:
+        raise ValueError(f"W is on {W.device}, h is on {h.device}")
+
+
 def _prepare(h, W, labels, reduction):
     if h.dtype not in _DTYPES or W.dtype != h.dtype:
         raise TypeError(f"h and W must both be bfloat16 or float32 (got {h.dtype}, {W.dtype})")
     if not h.is_cuda or not W.is_cuda or not labels.is_cuda:
         raise ValueError("h, W and labels must be on the GPU")
+    _check_projection(h, W)
+    if labels.device != h.device:
+        raise ValueError(f"labels are on {labels.device}, h is on {h.device}")
     if reduction not in _REDUCTIONS:
         raise ValueError(f"unknown reduction {reduction!r}")
     H = h.shape[-1]
@@ -265,6 +276,9 @@ def logits(h: torch.Tensor, W: torch.Tensor, softcap: Optional[float] = None, mu
     or 4 (fp32)."""
     if h.dtype not in _DTYPES or W.dtype != h.dtype:
         raise TypeError(f"h and W must both be bfloat16 or float32 (got {h.dtype}, {W.dtype})")
+    if not h.is_cuda or not W.is_cuda:
+        raise ValueError("h and W must be on the GPU")
+    _check_projection(h, W)
     H = h.shape[-1]
     h2 = h.reshape(-1, H).contiguous()
     Wc = W.contiguous()
@@ -272,8 +286,10 @@ def logits(h: torch.Tensor, W: torch.Tensor, softcap: Optional[float] = None, mu
     ld = _padded_cols(V, h.dtype)
     if out is None:
         out = torch.empty((N, ld), dtype=h.dtype, device=h.device)
-    if out.shape[0] != N or out.stride(1) != 1 or out.stride(0) < V:
+    if out.dim() != 2 or out.shape[0] != N or out.shape[1] < V or out.stride(1) != 1 or out.stride(0) < V:
         raise ValueError("out must be [N, ld >= V] with unit column stride")
+    if out.dtype != h.dtype or out.device != h.device:
+        raise ValueError(f"out is {out.dtype} on {out.device}, h is {h.dtype} on {h.device}")
     stream = torch.cuda.current_stream(h.device).cuda_stream
     rc = _lib.flce_logits(_ptr(h2), _ptr(Wc), N, H, V, float(softcap) if softcap else 0.0, float(multiplier),
                           _ptr(out), out.stride(0), stream, _DTYPES[h.dtype])

@@ -90,3 +90,43 @@ def test_captured_backward_beside_live_graphs_of_each_kind_of_stream(monkeypatch
         else:
             assert torch.equal(torch.autograd.grad(y, x, one)[0], one)
         del alive
+
+
+class _OnGpu(torch.Tensor):
+    """A CPU tensor that says it is on the GPU."""
+    is_cuda = property(lambda self: True)
+
+
+def _on_gpu(*shape, dtype=torch.float32):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(_OnGpu)
+
+
+@pytest.mark.parametrize("kind", ["logits", "lm_head_sample", "linear_cross_entropy", "lm_head_loss", "fwd_bwd", "forward"])
+def test_a_projection_of_another_width_never_reaches_the_kernels(kind, monkeypatch):
+    """The kernels read H columns of each row of W: one with fewer, or one that
+    is not on the GPU of the hidden states, would be read past its end."""
+    import types
+    from linear_cross_entropy_gemm_amd import torch_api
+    calls = []
+    _stand_ins(monkeypatch)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: types.SimpleNamespace(cuda_stream=0))
+    for name in ("flce_logits", "flce_fwd", "flce_fwd_bwd_ex", "flce_sample"):
+        monkeypatch.setattr(torch_api._lib, name, lambda *a, _n=name: calls.append(_n) or 0)
+    monkeypatch.setattr(head, "_layer_norm_fwd", lambda x, w, b, eps, stats: (x, None, None))
+    x, u, lab = _on_gpu(3, 8), _on_gpu(3), _on_gpu(3, dtype=torch.int64)
+    call = {"logits": lambda W: L.logits(x, W), "lm_head_sample": lambda W: L.lm_head_sample(x, W, u, None),
+            "linear_cross_entropy": lambda W: L.linear_cross_entropy(x, W, lab),
+            "lm_head_loss": lambda W: L.lm_head_loss(x, W, lab, None),
+            "fwd_bwd": lambda W: L.fwd_bwd(x, W, lab), "forward": lambda W: L.forward(x, W, lab)}[kind]
+    for W in (_on_gpu(20, 7), _on_gpu(20, 9), _on_gpu(20), _on_gpu(2, 20, 8), torch.zeros(20, 8)):
+        with pytest.raises(ValueError):
+            call(W)
+    if kind == "logits":
+        for out in (_on_gpu(3, 20, dtype=torch.bfloat16), _on_gpu(3, 16), _on_gpu(2, 20), _on_gpu(60)):
+            with pytest.raises(ValueError):
+                L.logits(x, _on_gpu(20, 8), out=out)
+        assert not calls
+        L.logits(x, _on_gpu(20, 8), out=_on_gpu(3, 24))
+        assert calls == ["flce_logits"]
+    else:
+        assert not calls
