@@ -18,7 +18,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib
-from .torch_api import (_DTYPES, _ptr, _workspace, check_backward, has_tangent, linear_cross_entropy,
+from .torch_api import (_DTYPES, _enqueue, _ptr, _workspace, check_backward, has_tangent, linear_cross_entropy,
                         logits as _logits, note_leaves)
 
 _U64 = (1 << 64) - 1
@@ -42,16 +42,6 @@ class LayerNormGrads:
 class SampleOutputs:
     tokens: torch.Tensor                     # [...] int64; -1: nothing to draw
     logprobs: Optional[torch.Tensor] = None  # [...] fp32, of the filtered distribution
-
-
-def _enqueue(dev, call) -> int:
-    """call(stream) with the tensors' device current, on torch's current
-    stream there (the raw handle: a stream object costs as much as a launch)."""
-    index = dev.index
-    if index == torch.cuda.current_device():
-        return call(torch._C._cuda_getCurrentRawStream(index))
-    with torch.cuda.device(dev):
-        return call(torch._C._cuda_getCurrentRawStream(index))
 
 
 def _rows(x: torch.Tensor) -> torch.Tensor:

@@ -59,6 +59,18 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+def _enqueue(dev, call) -> int:
+    """call(stream) with the tensors' device current, on torch's current
+    stream there (the raw handle: a stream object costs as much as a launch).
+    The default stream's handle is 0 on every device, so a launch on it goes
+    to whichever device is current."""
+    index = dev.index
+    if index == torch.cuda.current_device():
+        return call(torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.device(dev):
+        return call(torch._C._cuda_getCurrentRawStream(index))
+
+
 def _check_projection(h: torch.Tensor, W: torch.Tensor) -> None:
     """The kernels read H columns of every row of W from their own GPU."""
     if h.dim() < 1 or W.dim() != 2 or W.shape[1] != h.shape[-1]:
@@ -198,15 +210,14 @@ def fwd_bwd(h: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, ignore_index
         pred_rows=_ptr(out.pred_rows) if row_outputs else None,
         grad_rows=_ptr(gr), grad_scale=float(grad_scale) if grad_scale is not None else 0.0,
         accumulate_grad_W=1 if accumulate_grad_W else 0, use_grad_scale=0 if grad_scale is None else 1)
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    rc = _lib.flce_fwd_bwd_ex(_ptr(h2), _ptr(Wc), _ptr(lab), N, H, V, int(ignore_index),
-                              float(softcap) if softcap else 0.0, float(multiplier), red,
-                              _ptr(out.loss), _ptr(out.grad_h), _ptr(out.grad_W), _ptr(out.n_correct),
-                              stream, dtype, _ptr(workspace), int(workspace.numel()), opts)
+    rc = _enqueue(dev, lambda stream: _lib.flce_fwd_bwd_ex(
+        _ptr(h2), _ptr(Wc), _ptr(lab), N, H, V, int(ignore_index), float(softcap) if softcap else 0.0,
+        float(multiplier), red, _ptr(out.loss), _ptr(out.grad_h), _ptr(out.grad_W), _ptr(out.n_correct),
+        stream, dtype, _ptr(workspace), int(workspace.numel()), opts))
     if rc != _lib.FLCE_OK:
         raise _lib.FlceError(rc, "flce_fwd_bwd_ex")
     if check:
-        st = _lib.flce_read_status(_ptr(workspace), stream)
+        st = _status(workspace)
         if st != _lib.FLCE_OK:
             raise _lib.FlceError(st, "flce_fwd_bwd_ex (device status)")
     out.grad_h = out.grad_h.reshape(shape)
@@ -217,11 +228,14 @@ def fwd_bwd(h: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, ignore_index
     return out
 
 
+def _status(workspace: torch.Tensor) -> int:
+    return _enqueue(workspace.device, lambda stream: _lib.flce_read_status(_ptr(workspace), stream))
+
+
 def read_status(workspace: torch.Tensor) -> None:
     """Synchronise torch's current stream and raise if the last call that used
     ``workspace`` found a label outside [0, V) that is not ignore_index."""
-    stream = torch.cuda.current_stream(workspace.device).cuda_stream
-    st = _lib.flce_read_status(_ptr(workspace), stream)
+    st = _status(workspace)
     if st != _lib.FLCE_OK:
         raise _lib.FlceError(st, "device status")
 
@@ -246,15 +260,14 @@ def forward(h: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, ignore_index
                       n_correct=torch.empty((), dtype=torch.int64, device=dev), workspace=workspace,
                       loss_rows=loss_rows, lse_rows=lse_rows, pred_rows=pred_rows)
     opts = _lib.flce_options_t(loss_rows=_ptr(loss_rows), lse_rows=_ptr(lse_rows), pred_rows=_ptr(pred_rows))
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    rc = _lib.flce_fwd(_ptr(h2), _ptr(Wc), _ptr(lab), N, H, V, int(ignore_index),
-                       float(softcap) if softcap else 0.0, float(multiplier), _REDUCTIONS[reduction],
-                       _ptr(res.loss), _ptr(res.n_correct), stream, dtype, _ptr(workspace),
-                       int(workspace.numel()), opts)
+    rc = _enqueue(dev, lambda stream: _lib.flce_fwd(
+        _ptr(h2), _ptr(Wc), _ptr(lab), N, H, V, int(ignore_index), float(softcap) if softcap else 0.0,
+        float(multiplier), _REDUCTIONS[reduction], _ptr(res.loss), _ptr(res.n_correct), stream, dtype,
+        _ptr(workspace), int(workspace.numel()), opts))
     if rc != _lib.FLCE_OK:
         raise _lib.FlceError(rc, "flce_fwd")
     if check:
-        st = _lib.flce_read_status(_ptr(workspace), stream)
+        st = _status(workspace)
         if st != _lib.FLCE_OK:
             raise _lib.FlceError(st, "flce_fwd (device status)")
     if reduction == "none":
@@ -290,9 +303,9 @@ def logits(h: torch.Tensor, W: torch.Tensor, softcap: Optional[float] = None, mu
         raise ValueError("out must be [N, ld >= V] with unit column stride")
     if out.dtype != h.dtype or out.device != h.device:
         raise ValueError(f"out is {out.dtype} on {out.device}, h is {h.dtype} on {h.device}")
-    stream = torch.cuda.current_stream(h.device).cuda_stream
-    rc = _lib.flce_logits(_ptr(h2), _ptr(Wc), N, H, V, float(softcap) if softcap else 0.0, float(multiplier),
-                          _ptr(out), out.stride(0), stream, _DTYPES[h.dtype])
+    rc = _enqueue(h.device, lambda stream: _lib.flce_logits(
+        _ptr(h2), _ptr(Wc), N, H, V, float(softcap) if softcap else 0.0, float(multiplier), _ptr(out), out.stride(0),
+        stream, _DTYPES[h.dtype]))
     if rc != _lib.FLCE_OK:
         raise _lib.FlceError(rc, "flce_logits")
     return out[:, :V].reshape(*h.shape[:-1], V)
@@ -340,14 +353,14 @@ def cross_entropy(z: torch.Tensor, labels: torch.Tensor, ignore_index: int = -10
                                pred_rows=_ptr(res.pred_rows), grad_rows=_ptr(gr),
                                grad_scale=float(grad_scale) if grad_scale is not None else 0.0,
                                use_grad_scale=0 if grad_scale is None else 1)
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    rc = _lib.flce_cross_entropy(_ptr(z), z.stride(0), _ptr(lab), N, V, int(ignore_index), _REDUCTIONS[reduction],
-                                 _ptr(res.loss), _ptr(res.n_correct), _ptr(g), g.stride(0) if g is not None else 0,
-                                 stream, _DTYPES[z.dtype], _ptr(ws), ws_bytes, opts)
+    rc = _enqueue(dev, lambda stream: _lib.flce_cross_entropy(
+        _ptr(z), z.stride(0), _ptr(lab), N, V, int(ignore_index), _REDUCTIONS[reduction], _ptr(res.loss),
+        _ptr(res.n_correct), _ptr(g), g.stride(0) if g is not None else 0, stream, _DTYPES[z.dtype], _ptr(ws),
+        ws_bytes, opts))
     if rc != _lib.FLCE_OK:
         raise _lib.FlceError(rc, "flce_cross_entropy")
     if check:
-        st = _lib.flce_read_status(_ptr(ws), stream)
+        st = _status(ws)
         if st != _lib.FLCE_OK:
             raise _lib.FlceError(st, "flce_cross_entropy (device status)")
     return res
@@ -364,10 +377,10 @@ def scale_grads(g: torch.Tensor, grad_h: Optional[torch.Tensor], grad_W: Optiona
     gW_out = torch.empty(grad_W.shape, dtype=w_dtype, device=dev) if grad_W is not None else None
     n_h = grad_h.numel() if grad_h is not None else 0
     n_W = grad_W.numel() if grad_W is not None else 0
-    rc = _lib.flce_scale_grads(_ptr(g32), _ptr(grad_h) if n_h else None, _ptr(gh_out) if n_h else None, n_h,
-                               _DTYPES[grad_h.dtype] if grad_h is not None else _lib.FLCE_DTYPE_F32,
-                               _ptr(grad_W) if n_W else None, _ptr(gW_out) if n_W else None, n_W,
-                               _DTYPES[w_dtype], torch.cuda.current_stream(dev).cuda_stream)
+    rc = _enqueue(dev, lambda stream: _lib.flce_scale_grads(
+        _ptr(g32), _ptr(grad_h) if n_h else None, _ptr(gh_out) if n_h else None, n_h,
+        _DTYPES[grad_h.dtype] if grad_h is not None else _lib.FLCE_DTYPE_F32, _ptr(grad_W) if n_W else None,
+        _ptr(gW_out) if n_W else None, n_W, _DTYPES[w_dtype], stream))
     if rc != _lib.FLCE_OK:
         raise _lib.FlceError(rc, "flce_scale_grads")
     return gh_out, gW_out

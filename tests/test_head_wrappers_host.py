@@ -105,11 +105,10 @@ def _on_gpu(*shape, dtype=torch.float32):
 def test_a_projection_of_another_width_never_reaches_the_kernels(kind, monkeypatch):
     """The kernels read H columns of each row of W: one with fewer, or one that
     is not on the GPU of the hidden states, would be read past its end."""
-    import types
     from linear_cross_entropy_gemm_amd import torch_api
     calls = []
     _stand_ins(monkeypatch)
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: types.SimpleNamespace(cuda_stream=0))
+    monkeypatch.setattr(torch_api, "_enqueue", lambda dev, call: call(0))
     for name in ("flce_logits", "flce_fwd", "flce_fwd_bwd_ex", "flce_sample"):
         monkeypatch.setattr(torch_api._lib, name, lambda *a, _n=name: calls.append(_n) or 0)
     monkeypatch.setattr(head, "_layer_norm_fwd", lambda x, w, b, eps, stats: (x, None, None))
@@ -130,3 +129,50 @@ def test_a_projection_of_another_width_never_reaches_the_kernels(kind, monkeypat
         assert calls == ["flce_logits"]
     else:
         assert not calls
+
+
+def test_launches_go_to_the_tensors_device(monkeypatch):
+    """The default stream's handle is 0 on every device: a launch on it runs on
+    the current one, so that has to be the tensors' own."""
+    from linear_cross_entropy_gemm_amd import torch_api
+    now = [0]
+
+    class Device:
+        def __init__(self, dev):
+            self.dev = dev
+
+        def __enter__(self):
+            now.append(self.dev.index)
+
+        def __exit__(self, *a):
+            now.pop()
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[-1])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 100 + i, raising=False)
+    for i in (0, 1):
+        assert torch_api._enqueue(torch.device("cuda", i), lambda s: (s, now[-1])) == (100 + i, i)
+    assert now == [0]
+
+
+@pytest.mark.parametrize("kind", ["fwd_bwd", "forward", "logits", "cross_entropy", "scale_grads", "read_status"])
+def test_every_launch_of_the_projection_goes_to_the_tensors_device(kind, monkeypatch):
+    from linear_cross_entropy_gemm_amd import torch_api
+    inside, seen = [], []
+
+    def enqueue(dev, call):
+        inside.append(dev)
+        rc = call(7)
+        inside.pop()
+        return rc
+
+    monkeypatch.setattr(torch_api, "_enqueue", enqueue)
+    names = ("flce_logits", "flce_fwd", "flce_fwd_bwd_ex", "flce_cross_entropy", "flce_scale_grads", "flce_read_status")
+    for name in names:
+        monkeypatch.setattr(torch_api._lib, name, lambda *a, _n=name: seen.append((_n, bool(inside))) or 0)
+    x, W, lab = _on_gpu(3, 8), _on_gpu(20, 8), _on_gpu(3, dtype=torch.int64)
+    {"fwd_bwd": lambda: L.fwd_bwd(x, W, lab), "forward": lambda: L.forward(x, W, lab),
+     "logits": lambda: L.logits(x, W), "cross_entropy": lambda: L.cross_entropy(_on_gpu(3, 20), lab, grad=True),
+     "scale_grads": lambda: torch_api.scale_grads(torch.ones(()), x, W, torch.float32),
+     "read_status": lambda: L.read_status(torch.zeros(8, dtype=torch.uint8))}[kind]()
+    assert seen and all(ok for _, ok in seen), seen
