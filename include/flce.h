@@ -340,7 +340,9 @@ int flce_layer_norm_fwd(const void* x, int64_t ld_x, const void* weight, const v
 size_t flce_layer_norm_bwd_workspace_size(int64_t M, int64_t H, int dtype);
 
 /*
- * Backward pass of layer norm.  With xh = (x - mean) rstd and g = grad_y w:
+ * Backward pass of layer norm.  With xh = (x - mean) rstd and g = grad_y w, on
+ * the statistics as given (a mean in one fp32 number leaves xh off by up to
+ * 2^-24 |mean| rstd: the gradients of rows far from zero are less exact than y):
  *   grad_x      = rstd (g - avg g - xh avg(g xh))      [M, H] dtype
  *   grad_weight = sum over rows of grad_y xh           [H] w_dtype
  *   grad_bias   = sum over rows of grad_y              [H] w_dtype
@@ -348,7 +350,8 @@ size_t flce_layer_norm_bwd_workspace_size(int64_t M, int64_t H, int dtype);
  * outputs may be NULL (not computed); with M = 0 the two parameter gradients
  * are set to 0.  grad_x must not overlap grad_y or x.  `workspace` (needed
  * when a parameter gradient is asked for): 256-byte aligned, at least
- * flce_layer_norm_bwd_workspace_size(M, H, dtype) bytes.  Sums over rows are
+ * flce_layer_norm_bwd_workspace_size(M, H, dtype) bytes, of one call at a time
+ * (calls in stream order may share it).  Sums over rows are
  * fp32 in an order that depends on M, H and dtype alone: the same call gives
  * the same bits.  Strides, alignment, limits and errors as
  * flce_layer_norm_fwd, and FLCE_EWORKSPACE.
@@ -421,9 +424,13 @@ size_t flce_sample_workspace_size(int64_t N, int64_t V, int dtype);
  *   u          [N] fp32 in [0, 1)
  *   tokens     [N] int64 out
  *   logprobs   [N] fp32 out, or NULL
- *   workspace  256-byte aligned, flce_sample_workspace_size bytes
- * Decisions are taken on 64-bit exponentials rounded to integers, so they do
- * not depend on the order of any sum: the same call gives the same tokens.
+ *   workspace  256-byte aligned, flce_sample_workspace_size bytes; of one call
+ *              at a time (calls in stream order may share it)
+ * Decisions are taken on sums of 64-bit exponentials rounded to integers, in
+ * any order the same: a call repeated gives the same bits.  A row in another
+ * batch may take another way, whose sums agree to about 2^-38 of the row's
+ * weight: a u closer than that to the border of two tokens may give the other,
+ * and a logprob may differ in its last bit.
  * N <= 2^21, V <= 2^24 and N ceil(V / 8192) <= 2^23 (else
  * FLCE_EUNSUPPORTED).  Enqueued on `stream`;
  * nothing is allocated, nothing synchronises.  Returns FLCE_OK, FLCE_EINVAL

@@ -14,9 +14,13 @@
 //   ln_param_grad_kernel  dw and db of wide rows, by columns
 //   ln_reduce_kernel sum of the groups' dw and db in a fixed order
 //
-// Bound by memory, at 70 to 95% of what a plain copy moves (launch_fwd lists
-// the shapes): forward 8192 x 6656 bf16 in 50 us (4.4 TB/s), backward in 75 us
-// (4.4 TB/s, 5 us of it the reduction).  A persistent work-group keeps the
+// Bound by memory, at 75 to 100% of the rate of torch's plain copy (launch_fwd
+// lists the shapes): forward 8192 x 6656 bf16 in 50 us (4.4 TB/s), backward in
+// 75 us (4.4 TB/s, 5 us of it the reduction).  The wide rows read x three
+// times forward and x and dy three times backward, partly out of the caches:
+// 4096 x 16384 fp32 in 145 us (3.7 TB/s of one read and one write) and 292 us
+// (2.8 TB/s), so a row one vector beyond the registers takes 65 and 164 us
+// where 4096 x 8192 fp32 takes 55 and 83.  A persistent work-group keeps the
 // parameters and the next row in registers; the loads of the next row must
 // not wait on a branch, so a vector past the row's end is read from inside the
 // row and put right when it is used (a branch per vector cost a tenth).
@@ -511,8 +515,11 @@ int64_t bwd_groups(int64_t M, int64_t H, int dtype) {
 //   bwd    5.2       5.4       5.1       4.9       4.5       4.6       4.1
 //          [4.8]     [4.8]     [4.9]     [4.9]     [4.3]     [4.1]     [3.0]
 // What they lose to the copy is the wait between a row's last load and its
-// first store, which the registers for more rows in flight would hide; asking
-// the compiler for more resident waves spills and costs more (fwd 4.3 to 2.4).
+// first store, which the registers for more rows in flight would hide.  As it
+// is, the bf16 forward shapes of three and four vectors spill 104 to 152 scalar
+// registers (into vector ones) and <bf16, bf16, 256, 4> two vector registers
+// to memory; asking the compiler for more resident waves spills more of those
+// and costs more (fwd 4.3 to 2.4).
 template <typename T, typename WT>
 void launch_fwd(const LnFwdArgs& p, int dtype, hipStream_t st) {
   const int64_t v = row_vecs(p.H, dtype);

@@ -197,7 +197,8 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
                eps: float = 1e-5) -> torch.Tensor:
     """Differentiable layer norm over the last dimension of ``x``.  A row's
     statistics are kept for the backward pass, the normalised values are not:
-    they are formed again from ``x``."""
+    they are formed again from ``x``, in the gradients with the mean as one
+    fp32 number (off by up to 2^-24 |mean| / std there, not in the output)."""
     if not _needs_grad(x, weight, bias):
         return _layer_norm_fwd(x, weight, bias, eps, False)[0]
     y = _LayerNorm.apply(x, weight, bias, eps)
@@ -321,7 +322,8 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature: Union[float, torc
     or tensors with one value per row (float32; int64 for ``top_k``) on the
     device of ``logits``; they apply in that order, min-p relative to the
     largest probability.  A row without a logit above -inf, or with a per-row
-    value out of range, gets token -1."""
+    value out of range, gets token -1.  A caller-owned ``workspace`` (uint8,
+    ``flce_sample_workspace_size``) may be reused by ordered calls."""
     _check_rows("logits", logits)
     z = _rows(logits)
     N, V = z.shape
