@@ -101,7 +101,8 @@ def _on_gpu(*shape, dtype=torch.float32):
     return torch.zeros(*shape, dtype=dtype).as_subclass(_OnGpu)
 
 
-@pytest.mark.parametrize("kind", ["logits", "lm_head_sample", "linear_cross_entropy", "lm_head_loss", "fwd_bwd", "forward"])
+@pytest.mark.parametrize("kind", ["logits", "lm_head_sample", "linear_cross_entropy", "lm_head_loss", "fwd_bwd",
+                                  "forward"])
 def test_a_projection_of_another_width_never_reaches_the_kernels(kind, monkeypatch):
     """The kernels read H columns of each row of W: one with fewer, or one that
     is not on the GPU of the hidden states, would be read past its end."""
