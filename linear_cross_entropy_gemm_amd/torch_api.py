@@ -331,10 +331,14 @@ def cross_entropy(z: torch.Tensor, labels: torch.Tensor, ignore_index: int = -10
     z may be a row-padded view (row stride a multiple of 16 bytes)."""
     if z.dim() != 2 or z.stride(1) != 1 or z.dtype not in _DTYPES:
         raise ValueError("z must be a [N, V] bfloat16 / float32 tensor with unit column stride")
+    if not z.is_cuda or not labels.is_cuda or labels.device != z.device:
+        raise ValueError("z and labels must be on one GPU")
     if reduction not in _REDUCTIONS:
         raise ValueError(f"unknown reduction {reduction!r}")
     N, V = z.shape
     lab = labels.reshape(-1).to(torch.int64).contiguous()
+    if lab.numel() != N:
+        raise ValueError("labels must have one entry per row of z")
     dev = z.device
     ws_bytes = _lib.flce_cross_entropy_workspace_size(N)
     ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
@@ -349,6 +353,8 @@ def cross_entropy(z: torch.Tensor, labels: torch.Tensor, ignore_index: int = -10
     gr = None
     if grad_rows is not None:
         gr = grad_rows.reshape(-1).to(device=dev, dtype=torch.float32).contiguous()
+        if gr.numel() != N:
+            raise ValueError("grad_rows must have one entry per row")
     opts = _lib.flce_options_t(loss_rows=_ptr(res.loss_rows), lse_rows=_ptr(res.lse_rows),
                                pred_rows=_ptr(res.pred_rows), grad_rows=_ptr(gr),
                                grad_scale=float(grad_scale) if grad_scale is not None else 0.0,

@@ -177,3 +177,21 @@ def test_every_launch_of_the_projection_goes_to_the_tensors_device(kind, monkeyp
      "scale_grads": lambda: torch_api.scale_grads(torch.ones(()), x, W, torch.float32),
      "read_status": lambda: L.read_status(torch.zeros(8, dtype=torch.uint8))}[kind]()
     assert seen and all(ok for _, ok in seen), seen
+
+
+def test_cross_entropy_of_too_few_labels_never_reaches_the_kernels(monkeypatch):
+    """One label (and one upstream gradient) is read per row of the logits."""
+    from linear_cross_entropy_gemm_amd import torch_api
+    calls = []
+    monkeypatch.setattr(torch_api, "_enqueue", lambda dev, call: call(0))
+    monkeypatch.setattr(torch_api._lib, "flce_cross_entropy", lambda *a: calls.append(a) or 0)
+    monkeypatch.setattr(torch_api._lib, "flce_read_status", lambda *a: 0)
+    z, lab = _on_gpu(3, 20), _on_gpu(3, dtype=torch.int64)
+    for kw in (dict(labels=lab[:2]), dict(labels=_on_gpu(4, dtype=torch.int64)),
+               dict(labels=torch.zeros(3, dtype=torch.int64)), dict(z=torch.zeros(3, 20)),
+               dict(grad=True, reduction="none", grad_rows=_on_gpu(2))):
+        with pytest.raises(ValueError):
+            L.cross_entropy(**{"z": z, "labels": lab, **kw})
+    assert not calls
+    L.cross_entropy(z, lab, grad=True, reduction="none", grad_rows=_on_gpu(3))
+    assert len(calls) == 1
