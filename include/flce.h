@@ -362,6 +362,69 @@ int flce_layer_norm_bwd(const void* grad_y, int64_t ld_gy, const void* x, int64_
                         hipStream_t stream, int dtype, int w_dtype, void* workspace, size_t workspace_bytes);
 
 /*
+ * RMS norm over the last dimension with the residual's addition.  For each of
+ * M rows x of H values, with residual r (NULL: none) and weight w (NULL: the
+ * factor is 1, the offset is not used):
+ *   s = x + r, rounded to dtype (without a residual s = x and is not written)
+ *   rstd = 1 / sqrt(avg s^2 + eps),  y = s rstd (w + offset)
+ * x, residual, y and sum (s; needed exactly when there is a residual) have
+ * `dtype` and row strides of ld_* elements (outputs: >= H when M > 1; inputs:
+ * >= 0, so a broadcast row is read with 0); the weight has H values of
+ * `w_dtype`; offset (0, or 1 for weights kept around zero) is added to it in
+ * fp32.  rstd receives M fp32 values (NULL: not written), which
+ * flce_rms_norm_bwd takes.  Pointers need the alignment of one element only.
+ * eps > 0, finite.  y and sum may each be x or residual itself (with its
+ * stride) and must not overlap an input or each other otherwise.  Sums and
+ * products are fp32, s and y are rounded once.  A finite row whose sum of
+ * squares passes fp32's range (a root mean square beyond 2^64 / sqrt(H)) has
+ * rstd 0 and y 0.  Any H from 1 to 2^21, M < 2^31 (else FLCE_EUNSUPPORTED);
+ * M = 0 does nothing.  Enqueued on `stream`; nothing is allocated, nothing
+ * synchronises.  Returns FLCE_OK, FLCE_EINVAL, FLCE_EUNSUPPORTED or
+ * FLCE_EDEVICE.
+ */
+int flce_rms_norm_fwd(const void* x, int64_t ld_x, const void* residual, int64_t ld_r, const void* weight,
+                      float offset, int64_t M, int64_t H, float eps, void* y, int64_t ld_y, void* sum, int64_t ld_s,
+                      float* rstd, hipStream_t stream, int dtype, int w_dtype);
+
+/*
+ * The same with y in 8 bits, the E4M3 block format of the OCP Microscaling
+ * specification (MXFP8): block j of a row holds its elements [32 j, 32 j + 32)
+ * (the last one what is left) and has the scale 2^(code - 127),
+ *   y      [M, H] E4M3 bytes, row stride ld_y >= H when M > 1
+ *   scales [M, ceil(H / 32)] E8M0 codes, row stride ld_scales (bytes)
+ * The scale is the least power of two (at least 2^-127) with max|y| / scale
+ * <= 448; y is rounded from fp32 once, to nearest even.  A block that holds an
+ * infinity or a NaN has code 255 (NaN) and elements 0x7F (NaN).  y must not
+ * overlap an input.
+ */
+int flce_rms_norm_mx(const void* x, int64_t ld_x, const void* residual, int64_t ld_r, const void* weight,
+                     float offset, int64_t M, int64_t H, float eps, void* y, int64_t ld_y, void* scales,
+                     int64_t ld_scales, void* sum, int64_t ld_s, float* rstd, hipStream_t stream, int dtype,
+                     int w_dtype);
+
+/* Workspace bytes of flce_rms_norm_bwd; 0 for sizes it does not take. */
+size_t flce_rms_norm_bwd_workspace_size(int64_t M, int64_t H, int dtype);
+
+/*
+ * Backward pass of RMS norm.  With s and rstd of the forward call (s is x
+ * itself without a residual), xh = s rstd and g = grad_y (w + offset):
+ *   grad_x      = rstd (g - xh avg(g xh)) [+ grad_s]   [M, H] dtype
+ *   grad_weight = sum over rows of grad_y xh           [H] w_dtype
+ * grad_x is the gradient of x and of the residual alike; grad_s (NULL: none)
+ * is the gradient that reaches s from elsewhere.  Either output may be NULL
+ * (not computed); with M = 0 grad_weight is set to 0.  grad_x must not overlap
+ * an input.  `workspace` (needed with grad_weight): 256-byte aligned, at least
+ * flce_rms_norm_bwd_workspace_size(M, H, dtype) bytes, of one call at a time.
+ * Sums over rows are fp32 in an order that depends on M, H and dtype alone:
+ * the same call gives the same bits.  Strides, alignment, limits and errors as
+ * flce_rms_norm_fwd, and FLCE_EWORKSPACE.
+ */
+int flce_rms_norm_bwd(const void* grad_y, int64_t ld_gy, const void* s, int64_t ld_s, const void* grad_s,
+                      int64_t ld_gs, const void* weight, float offset, const float* rstd, int64_t M, int64_t H,
+                      void* grad_x, int64_t ld_gx, void* grad_weight, hipStream_t stream, int dtype, int w_dtype,
+                      void* workspace, size_t workspace_bytes);
+
+/*
  * Dropout without a stored mask, on n contiguous elements:
  *   y_i = [residual_i +] (word_i >= floor(p 2^32) ? x_i / (1 - p) : 0)
  * word_i is word i % 4 of Philox4x32-10 (Salmon et al., SC 2011) on the
@@ -487,7 +550,10 @@ enum {
   FLCE_KERNEL_DROPOUT = 15,     /* flce_dropout */
   FLCE_KERNEL_SAMPLE_SCAN = 16, /* flce_sample: maxima and weights of each row's pieces */
   FLCE_KERNEL_SAMPLE_PICK = 17, /* flce_sample: the filters' cut and the token */
-  FLCE_KERNEL_KINDS = 18
+  FLCE_KERNEL_RMS_NORM = 18,    /* flce_rms_norm_fwd, flce_rms_norm_mx */
+  FLCE_KERNEL_RMS_NORM_BWD = 19,/* flce_rms_norm_bwd: grad_x and per-group weight gradients */
+  FLCE_KERNEL_RMS_NORM_REDUCE = 20,/* flce_rms_norm_bwd: sum of the groups' weight gradients */
+  FLCE_KERNEL_KINDS = 21
 };
 
 /* Turn event timing on (on != 0) or off for subsequent calls.  Returns FLCE_OK. */

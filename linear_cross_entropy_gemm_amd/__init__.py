@@ -44,6 +44,10 @@ from ._lib import (  # noqa: F401
     flce_profile_read,
     flce_plan,
     flce_read_status,
+    flce_rms_norm_bwd,
+    flce_rms_norm_bwd_workspace_size,
+    flce_rms_norm_fwd,
+    flce_rms_norm_mx,
     flce_sample,
     flce_sample_params_t,
     flce_sample_workspace_size,
@@ -54,6 +58,9 @@ from ._lib import (  # noqa: F401
 from .head import (  # noqa: F401
     LayerNormForward,
     LayerNormGrads,
+    RmsNormForward,
+    RmsNormGrads,
+    RmsNormMx8,
     SampleOutputs,
     dropout,
     layer_norm,
@@ -61,8 +68,13 @@ from .head import (  # noqa: F401
     layer_norm_fwd,
     lm_head_loss,
     lm_head_sample,
+    rms_norm,
+    rms_norm_bwd,
+    rms_norm_fwd,
+    rms_norm_mx8,
     sample,
 )
+from .mx import Mx8Rows  # noqa: F401
 from .torch_api import (  # noqa: F401
     CrossEntropyOutputs,
     FlceForward,

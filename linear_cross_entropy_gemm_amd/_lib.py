@@ -38,14 +38,16 @@ EXPORTED = ("flce_plan", "flce_workspace_size", "flce_fwd_bwd", "flce_fwd_bwd_ex
             "flce_fwd_workspace_size",
             "flce_fwd", "flce_logits", "flce_cross_entropy_workspace_size", "flce_cross_entropy",
             "flce_scale_grads", "flce_layer_norm_fwd", "flce_layer_norm_bwd_workspace_size",
-            "flce_layer_norm_bwd", "flce_dropout", "flce_sample_workspace_size", "flce_sample",
+            "flce_layer_norm_bwd", "flce_rms_norm_fwd", "flce_rms_norm_mx", "flce_rms_norm_bwd_workspace_size",
+            "flce_rms_norm_bwd", "flce_dropout", "flce_sample_workspace_size", "flce_sample",
             "flce_read_status", "flce_strerror", "flce_profile_enable", "flce_profile_read",
             "flce_profile_read_n")
 
 # Kernel kinds of the per-kernel timing facility (index order of the arrays).
 KERNEL_KINDS = ("label_scan", "fwd_logits", "row_merge", "grad_logits", "grad_h", "grad_h_reduce",
                 "grad_W", "finalize", "zero", "logits", "cross_entropy", "scale", "layer_norm",
-                "layer_norm_bwd", "layer_norm_reduce", "dropout", "sample_scan", "sample_pick")
+                "layer_norm_bwd", "layer_norm_reduce", "dropout", "sample_scan", "sample_pick", "rms_norm",
+                "rms_norm_bwd", "rms_norm_reduce")
 
 
 class flce_plan_t(ctypes.Structure):
@@ -147,6 +149,16 @@ def _load() -> ctypes.CDLL:
     lib.flce_layer_norm_bwd_workspace_size.restype = sz
     lib.flce_layer_norm_bwd.argtypes = [vp, i64, vp, i64, vp, vp, vp, i64, i64, vp, i64, vp, vp, vp, i32, i32, vp, sz]
     lib.flce_layer_norm_bwd.restype = i32
+    lib.flce_rms_norm_fwd.argtypes = [vp, i64, vp, i64, vp, f32, i64, i64, f32, vp, i64, vp, i64, vp, vp, i32, i32]
+    lib.flce_rms_norm_fwd.restype = i32
+    lib.flce_rms_norm_mx.argtypes = [vp, i64, vp, i64, vp, f32, i64, i64, f32, vp, i64, vp, i64, vp, i64, vp, vp, i32,
+                                     i32]
+    lib.flce_rms_norm_mx.restype = i32
+    lib.flce_rms_norm_bwd_workspace_size.argtypes = [i64, i64, i32]
+    lib.flce_rms_norm_bwd_workspace_size.restype = sz
+    lib.flce_rms_norm_bwd.argtypes = [vp, i64, vp, i64, vp, i64, vp, f32, vp, i64, i64, vp, i64, vp, vp, i32, i32, vp,
+                                      sz]
+    lib.flce_rms_norm_bwd.restype = i32
     lib.flce_dropout.argtypes = [vp, vp, vp, i64, f64, u64, u64, vp, vp, i32]
     lib.flce_dropout.restype = i32
     lib.flce_sample_workspace_size.argtypes = [i64, i64, i32]
@@ -269,6 +281,33 @@ def flce_layer_norm_bwd(grad_y: int, ld_gy: int, x: int, ld_x: int, weight, mean
     """Raw call; returns the C return code."""
     return _lib.flce_layer_norm_bwd(grad_y, ld_gy, x, ld_x, weight, mean, rstd, M, H, grad_x, ld_gx, grad_weight,
                                     grad_bias, stream, dtype, w_dtype, workspace, workspace_bytes)
+
+
+def flce_rms_norm_fwd(x: int, ld_x: int, residual, ld_r: int, weight, offset: float, M: int, H: int, eps: float, y: int,
+                      ld_y: int, sum, ld_s: int, rstd, stream: int, dtype: int, w_dtype: int) -> int:
+    """Raw call; returns the C return code."""
+    return _lib.flce_rms_norm_fwd(x, ld_x, residual, ld_r, weight, offset, M, H, eps, y, ld_y, sum, ld_s, rstd, stream,
+                                  dtype, w_dtype)
+
+
+def flce_rms_norm_mx(x: int, ld_x: int, residual, ld_r: int, weight, offset: float, M: int, H: int, eps: float, y: int,
+                     ld_y: int, scales: int, ld_scales: int, sum, ld_s: int, rstd, stream: int, dtype: int,
+                     w_dtype: int) -> int:
+    """Raw call; returns the C return code."""
+    return _lib.flce_rms_norm_mx(x, ld_x, residual, ld_r, weight, offset, M, H, eps, y, ld_y, scales, ld_scales, sum,
+                                 ld_s, rstd, stream, dtype, w_dtype)
+
+
+def flce_rms_norm_bwd_workspace_size(M: int, H: int, dtype: int) -> int:
+    return int(_lib.flce_rms_norm_bwd_workspace_size(M, H, dtype))
+
+
+def flce_rms_norm_bwd(grad_y: int, ld_gy: int, s: int, ld_s: int, grad_s, ld_gs: int, weight, offset: float, rstd: int,
+                      M: int, H: int, grad_x, ld_gx: int, grad_weight, stream: int, dtype: int, w_dtype: int, workspace,
+                      workspace_bytes: int) -> int:
+    """Raw call; returns the C return code."""
+    return _lib.flce_rms_norm_bwd(grad_y, ld_gy, s, ld_s, grad_s, ld_gs, weight, offset, rstd, M, H, grad_x, ld_gx,
+                                  grad_weight, stream, dtype, w_dtype, workspace, workspace_bytes)
 
 
 def flce_dropout(x: int, residual, y: int, n: int, p: float, seed: int, offset: int, offset_dev, stream: int,

@@ -59,53 +59,6 @@ struct LnBwdArgs {
   int H;
 };
 
-// The parameter's vector of a thread; absent parameters read as `fill`.
-template <typename WT, int E>
-__device__ __forceinline__ void load_param(float (&out)[E], const void* p, int col, int H, float fill) {
-#pragma unroll
-  for (int e = 0; e < E; ++e) out[e] = fill;
-  if (!p) return;
-  constexpr int W = RowVec<WT>::E;
-  constexpr int step = W < E ? W : E;   // a narrower row vector takes part of a parameter vector
-#pragma unroll
-  for (int q = 0; q < E / step; ++q) {
-    const int c = col + q * step;
-    if (W <= E) {
-      const typename RowVec<WT>::type v = load_row(static_cast<const WT*>(p), c, H, fill);
-#pragma unroll
-      for (int e = 0; e < step; ++e) out[q * step + e] = to_f32(v[e]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < step; ++e)
-        if (c + e < H) out[e] = to_f32(static_cast<const WT*>(p)[c + e]);
-    }
-  }
-}
-
-// Sums of N values over the kRow threads of a row (every thread gets them).
-// Rows wider than a wave go through LDS; `buf` alternates between calls so
-// that one barrier per call is enough.
-template <int N> using SumLds = float[2][N][16];
-template <int kRow, int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], SumLds<N>& lds, int& buf) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
-  if (kRow == 64) return;
-  const int w = threadIdx.x >> 6;
-  if ((threadIdx.x & 63) == 0) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) lds[buf][i][w] = v[i];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    v[i] = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kRow / 64; ++k) v[i] += lds[buf][i][k];
-  }
-  buf ^= 1;
-}
-
 // Mean and 1 / standard deviation of a row from its waves' own: a wave's mean
 // and sum of squared deviations from it need no barrier, and
 //   mean = sum n_w mean_w / H,  sum of squares = sum (q_w + n_w (mean_w - mean)^2)
@@ -479,24 +432,10 @@ __global__ __launch_bounds__(1024) void ln_reduce_kernel(const float* partial, i
   }
 }
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// The longest rows kept in registers: 2048 vectors of 16 bytes.
-constexpr int64_t kMaxRegVecs = 2048;
-
-int64_t row_vecs(int64_t H, int dtype) { return ceil_div(H, dtype == FLCE_DTYPE_BF16 ? 8 : 4); }
-
-// Work-groups for `sets` of rows, at most `most`: as few as leave every one
-// the same number of steps.
-int64_t even_grid(int64_t sets, int64_t most) {
-  if (sets <= most) return sets;
-  return ceil_div(sets, ceil_div(sets, most));
-}
-
 // Groups of rows that ln_bwd_kernel (or ln_param_grad_kernel) sums dw and db
 // over, one partial each.
 int64_t bwd_groups(int64_t M, int64_t H, int dtype) {
-  const int64_t v = row_vecs(H, dtype);
+  const int64_t v = row_vecs(H, dtype == FLCE_DTYPE_BF16 ? 2 : 4);
   if (v <= 64) return even_grid(ceil_div(M, 4), 1024);
   if (v <= 128) return even_grid(ceil_div(M, 4), 512);
   if (v <= 256) return even_grid(ceil_div(M, 4), 256);
@@ -522,7 +461,7 @@ int64_t bwd_groups(int64_t M, int64_t H, int dtype) {
 // and costs more (fwd 4.3 to 2.4).
 template <typename T, typename WT>
 void launch_fwd(const LnFwdArgs& p, int dtype, hipStream_t st) {
-  const int64_t v = row_vecs(p.H, dtype);
+  const int64_t v = row_vecs(p.H, sizeof(T));
   auto grid = [&](int rows, int64_t most) { return (unsigned)even_grid(ceil_div(p.M, rows), most); };
   if (v <= 64) ln_fwd_kernel<T, WT, 64, 1, 4, 1><<<grid(4, 4096), 256, 0, st>>>(p);
   else if (v <= 128) ln_fwd_kernel<T, WT, 64, 2, 4, 1><<<grid(4, 1024), 256, 0, st>>>(p);
@@ -536,7 +475,7 @@ void launch_fwd(const LnFwdArgs& p, int dtype, hipStream_t st) {
 
 template <typename T, typename WT>
 void launch_bwd(const LnBwdArgs& p, int dtype, hipStream_t st) {
-  const int64_t v = row_vecs(p.H, dtype);
+  const int64_t v = row_vecs(p.H, sizeof(T));
   const unsigned g = (unsigned)bwd_groups(p.M, p.H, dtype);
   if (v <= 64) ln_bwd_kernel<T, WT, 64, 1, 4, 1><<<g, 256, 0, st>>>(p);
   else if (v <= 128) ln_bwd_kernel<T, WT, 64, 2, 4, 1><<<g, 256, 0, st>>>(p);

@@ -1,6 +1,6 @@
-// Helpers of the row-wise operators around the vocabulary head (layer norm,
+// Helpers of the row-wise operators around the vocabulary head (norms,
 // dropout, sampling): vectors that need no alignment beyond their element's,
-// and sums over a 64-lane wave.
+// sums over a 64-lane wave and over a row's threads, and launch shapes.
 #pragma once
 
 #include "device_common.hpp"
@@ -183,6 +183,67 @@ __device__ __forceinline__ uint32_t wave_scan_u32(uint32_t x, uint32_t& all) {
   x += l < 16 ? 0 : l < 32 ? a : l < 48 ? b : c;
   all = lane(x, 63);
   return x;
+}
+
+// The parameter's vector of a thread; absent parameters read as `fill`.
+template <typename WT, int E>
+__device__ __forceinline__ void load_param(float (&out)[E], const void* p, int col, int H, float fill) {
+#pragma unroll
+  for (int e = 0; e < E; ++e) out[e] = fill;
+  if (!p) return;
+  constexpr int W = RowVec<WT>::E;
+  constexpr int step = W < E ? W : E;   // a narrower row vector takes part of a parameter vector
+#pragma unroll
+  for (int q = 0; q < E / step; ++q) {
+    const int c = col + q * step;
+    if (W <= E) {
+      const typename RowVec<WT>::type v = load_row(static_cast<const WT*>(p), c, H, fill);
+#pragma unroll
+      for (int e = 0; e < step; ++e) out[q * step + e] = to_f32(v[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < step; ++e)
+        if (c + e < H) out[e] = to_f32(static_cast<const WT*>(p)[c + e]);
+    }
+  }
+}
+
+// Sums of N values over the kRow threads of a row (every thread gets them).
+// Rows wider than a wave go through LDS; `buf` alternates between calls so
+// that one barrier per call is enough.
+template <int N> using SumLds = float[2][N][16];
+template <int kRow, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], SumLds<N>& lds, int& buf) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+  if (kRow == 64) return;
+  const int w = threadIdx.x >> 6;
+  if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) lds[buf][i][w] = v[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    v[i] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kRow / 64; ++k) v[i] += lds[buf][i][k];
+  }
+  buf ^= 1;
+}
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// The longest rows kept in registers: 2048 vectors of 16 bytes.
+constexpr int64_t kMaxRegVecs = 2048;
+
+inline int64_t row_vecs(int64_t H, int64_t elem_bytes) { return ceil_div(H, 16 / elem_bytes); }
+
+// Work-groups for `sets` of rows, at most `most`: as few as leave every one
+// the same number of steps.
+inline int64_t even_grid(int64_t sets, int64_t most) {
+  if (sets <= most) return sets;
+  return ceil_div(sets, ceil_div(sets, most));
 }
 
 }  // namespace flce

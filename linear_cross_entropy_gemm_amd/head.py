@@ -18,6 +18,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib
+from .mx import MX_BLOCK, Mx8Rows
 from .torch_api import (_DTYPES, _enqueue, _ptr, _workspace, check_backward, has_tangent, linear_cross_entropy,
                         logits as _logits, note_leaves)
 
@@ -36,6 +37,25 @@ class LayerNormGrads:
     grad_x: Optional[torch.Tensor]        # shape and dtype of x
     grad_weight: Optional[torch.Tensor]   # [H] dtype of the weight
     grad_bias: Optional[torch.Tensor]     # [H] dtype of the weight
+
+
+@dataclasses.dataclass
+class RmsNormForward:
+    y: torch.Tensor                   # shape and dtype of x
+    residual: Optional[torch.Tensor]  # x + residual, shape and dtype of x (None without a residual)
+    rstd: torch.Tensor                # [...] fp32, one per row
+
+
+@dataclasses.dataclass
+class RmsNormMx8:
+    rows: Mx8Rows                     # y in 8 bits
+    residual: Optional[torch.Tensor]  # x + residual, shape and dtype of x (None without a residual)
+
+
+@dataclasses.dataclass
+class RmsNormGrads:
+    grad_x: Optional[torch.Tensor]       # shape and dtype of x; also the gradient of the residual
+    grad_weight: Optional[torch.Tensor]  # [H] dtype of the weight
 
 
 @dataclasses.dataclass
@@ -206,6 +226,142 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     return y
 
 
+def _check_like(name: str, t: torch.Tensor, x: torch.Tensor, of: str = "x") -> None:
+    if t.shape != x.shape or t.dtype != x.dtype or t.device != x.device:
+        raise ValueError(f"{name} must match {of}: {tuple(x.shape)} {x.dtype} on {x.device} (got {tuple(t.shape)} "
+                         f"{t.dtype} on {t.device})")
+
+
+def _rms_norm_fwd(x, weight, eps, residual, offset, stats: bool, mx8: bool = False):
+    """(y or (data, scales), s, rstd): one call of the forward kernels."""
+    _check_rows("x", x)
+    w, _, w_dtype = _check_params(x, weight, None)
+    eps, offset = float(eps), float(offset)
+    x2 = _rows(x)
+    M, H = x2.shape
+    dev = x.device
+    s = r2 = None
+    if residual is not None:
+        _check_like("residual", residual, x)
+        r2 = _rows(residual)
+        s = _like(x)
+    rstd = torch.empty(M if x.dim() == 2 else x.shape[:-1], dtype=torch.float32, device=dev) if stats else None
+    ld_r = 0 if r2 is None else r2.stride(0)
+    if mx8:
+        nb = (H + MX_BLOCK - 1) // MX_BLOCK
+        y = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev)
+        scales = torch.empty((*x.shape[:-1], nb), dtype=torch.float8_e8m0fnu, device=dev)
+        rc = _enqueue(dev, lambda stream: _lib.flce_rms_norm_mx(
+            x2.data_ptr(), x2.stride(0), _ptr(r2), ld_r, _ptr(w), offset, M, H, eps, y.data_ptr(), H,
+            scales.data_ptr(), nb, _ptr(s), H, _ptr(rstd), stream, _DTYPES[x.dtype], _DTYPES[w_dtype]))
+        y = Mx8Rows(y, scales)
+    else:
+        y = _like(x)
+        rc = _enqueue(dev, lambda stream: _lib.flce_rms_norm_fwd(
+            x2.data_ptr(), x2.stride(0), _ptr(r2), ld_r, _ptr(w), offset, M, H, eps, y.data_ptr(), H, _ptr(s), H,
+            _ptr(rstd), stream, _DTYPES[x.dtype], _DTYPES[w_dtype]))
+    if rc != _lib.FLCE_OK:
+        raise _lib.FlceError(rc, "flce_rms_norm_mx" if mx8 else "flce_rms_norm_fwd")
+    return y, s, rstd
+
+
+def rms_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float = 1e-6, *,
+                 residual: Optional[torch.Tensor] = None, offset: float = 0.0) -> RmsNormForward:
+    """One call of ``flce_rms_norm_fwd`` over the last dimension of ``x`` (plus
+    ``residual``): y, the new residual stream (the sum rounded to its type,
+    which is what is normed) and the row statistic that ``rms_norm_bwd``
+    takes.  ``weight`` [H] may be absent and may be float32 next to a bfloat16
+    ``x``; ``offset`` is added to it (1 for weights kept around zero)."""
+    return RmsNormForward(*_rms_norm_fwd(x, weight, eps, residual, offset, True))
+
+
+def rms_norm_mx8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float = 1e-6, *,
+                 residual: Optional[torch.Tensor] = None, offset: float = 0.0) -> RmsNormMx8:
+    """``rms_norm_fwd`` with y in 8 bits, one scale for 32 elements
+    (``flce_rms_norm_mx``), as ``logits_mx4`` takes it."""
+    y, s, _ = _rms_norm_fwd(x, weight, eps, residual, offset, False, mx8=True)
+    return RmsNormMx8(y, s)
+
+
+def rms_norm_bwd(grad_y: torch.Tensor, s: torch.Tensor, weight: Optional[torch.Tensor], rstd: torch.Tensor,
+                 workspace: Optional[torch.Tensor] = None, *, offset: float = 0.0,
+                 grad_residual: Optional[torch.Tensor] = None, need_x: bool = True,
+                 need_weight: bool = True) -> RmsNormGrads:
+    """One call of ``flce_rms_norm_bwd``: the gradient of ``x`` (and alike of the
+    residual) and of the weight.  ``s`` and ``rstd`` are those of
+    ``rms_norm_fwd`` (``s``: its residual output, or ``x`` itself without one);
+    ``grad_residual`` is the gradient that reaches the residual stream from
+    elsewhere.  Without a weight there is no gradient of it.  A caller-owned
+    ``workspace`` (uint8, ``flce_rms_norm_bwd_workspace_size``) may be reused by
+    ordered calls."""
+    _check_rows("s", s)
+    w, _, w_dtype = _check_params(s, weight, None)
+    _check_like("grad_y", grad_y, s, "s")
+    s2, g2 = _rows(s), _rows(grad_y)
+    a2 = None
+    if grad_residual is not None:
+        _check_like("grad_residual", grad_residual, s, "s")
+        a2 = _rows(grad_residual)
+    M, H = s2.shape
+    dev = s.device
+    if rstd.dtype != torch.float32 or rstd.numel() != M or rstd.device != dev or not rstd.is_contiguous():
+        raise ValueError("rstd must hold one contiguous float32 value per row of s on its device")
+    gx = _like(s) if need_x else None
+    gw = None
+    ws_bytes = 0
+    if need_weight and w is not None:
+        gw = torch.empty(H, dtype=w_dtype, device=dev)
+        ws_bytes = _lib.flce_rms_norm_bwd_workspace_size(M, H, _DTYPES[s.dtype])
+        if ws_bytes == 0:
+            raise _lib.FlceError(_lib.FLCE_EUNSUPPORTED, "flce_rms_norm_bwd_workspace_size")
+        workspace = _workspace(workspace, ws_bytes, dev)
+        ws_bytes = workspace.numel()
+    rc = _enqueue(dev, lambda stream: _lib.flce_rms_norm_bwd(
+        g2.data_ptr(), g2.stride(0), s2.data_ptr(), s2.stride(0), _ptr(a2), 0 if a2 is None else a2.stride(0), _ptr(w),
+        float(offset), rstd.data_ptr(), M, H, _ptr(gx), H, _ptr(gw), stream, _DTYPES[s.dtype], _DTYPES[w_dtype],
+        _ptr(workspace) if gw is not None else None, ws_bytes))
+    if rc != _lib.FLCE_OK:
+        raise _lib.FlceError(rc, "flce_rms_norm_bwd")
+    return RmsNormGrads(gx, gw)
+
+
+class _RmsNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, weight, eps, offset):
+        o = rms_norm_fwd(x, weight, eps, residual=residual, offset=offset)
+        ctx.set_materialize_grads(False)
+        ctx.offset = offset
+        ctx.save_for_backward(x if residual is None else o.residual, weight, o.rstd)
+        return o.y if residual is None else (o.y, o.residual)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_y, grad_s=None):
+        need_x, need_r, need_w = ctx.needs_input_grad[:3]
+        for g in (grad_y, grad_s):
+            if g is not None:
+                check_backward(ctx, g)
+        if grad_y is None:   # only the residual stream goes on
+            return grad_s if need_x else None, grad_s if need_r else None, None, None, None
+        s, weight, rstd = ctx.saved_tensors
+        g = rms_norm_bwd(grad_y, s, weight, rstd, offset=ctx.offset, grad_residual=grad_s, need_x=need_x or need_r,
+                         need_weight=need_w)
+        return g.grad_x if need_x else None, g.grad_x if need_r else None, g.grad_weight, None, None
+
+
+def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float = 1e-6, *,
+             residual: Optional[torch.Tensor] = None, offset: float = 0.0):
+    """Differentiable RMS norm over the last dimension of ``x``: y, or with a
+    ``residual`` (y of x + residual, the new residual stream x + residual).
+    Kept for the backward pass are the stream and one number per row."""
+    if not _needs_grad(x, residual, weight):
+        y, s, _ = _rms_norm_fwd(x, weight, eps, residual, offset, False)
+        return y if residual is None else (y, s)
+    out = _RmsNorm.apply(x, residual, weight, float(eps), float(offset))
+    note_leaves(out if residual is None else out[0])
+    return out
+
+
 def _dropout(x, p, seed, offset, residual) -> torch.Tensor:
     xc = x.contiguous()
     res = None if residual is None else residual.contiguous()
@@ -276,19 +432,37 @@ def dropout(x: torch.Tensor, p: float, seed: int, offset: Union[int, torch.Tenso
     return y
 
 
+def _check_norm(norm: str, bias, offset: float) -> None:
+    if norm not in ("layer", "rms"):
+        raise ValueError(f"norm must be 'layer' or 'rms' (got {norm!r})")
+    if norm == "rms" and bias is not None:
+        raise ValueError("an RMS norm has no bias")
+    if norm == "layer" and offset != 0.0:
+        raise ValueError("norm_offset is that of an RMS norm")
+
+
 def lm_head_loss(x: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, norm_weight: Optional[torch.Tensor],
                  norm_bias: Optional[torch.Tensor] = None, eps: float = 1e-5, *,
                  residual: Optional[torch.Tensor] = None, dropout_p: float = 0.0, seed: int = 0,
                  offset: Union[int, torch.Tensor] = 0, ignore_index: int = -100, softcap: Optional[float] = None,
                  multiplier: float = 1.0, reduction: str = "mean", workspace: Optional[torch.Tensor] = None,
-                 check: bool = False):
+                 check: bool = False, norm: str = "layer", norm_offset: float = 0.0):
     """The whole head of a training step, differentiable: the last block's
     output ``x`` through dropout onto the ``residual`` stream (when either is
-    asked for), the final layer norm, and the fused linear cross-entropy.
-    Returns (loss, n_correct) as ``linear_cross_entropy`` does."""
-    if dropout_p != 0.0 or residual is not None:
-        x = dropout(x, dropout_p, seed, offset, residual)
-    y = layer_norm(x, norm_weight, norm_bias, eps)
+    asked for), the final norm (``norm``: "layer", or "rms" with
+    ``norm_offset`` added to its weight and no bias), and the fused linear
+    cross-entropy.  Returns (loss, n_correct) as ``linear_cross_entropy``
+    does."""
+    _check_norm(norm, norm_bias, norm_offset)
+    if norm == "rms" and residual is not None and dropout_p == 0.0:
+        y = rms_norm(x, norm_weight, eps, residual=residual, offset=norm_offset)[0]
+    else:
+        if dropout_p != 0.0 or residual is not None:
+            x = dropout(x, dropout_p, seed, offset, residual)
+        if norm == "rms":
+            y = rms_norm(x, norm_weight, eps, offset=norm_offset)
+        else:
+            y = layer_norm(x, norm_weight, norm_bias, eps)
     return linear_cross_entropy(y, W, labels, ignore_index, softcap, multiplier, reduction, workspace, check)
 
 

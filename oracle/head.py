@@ -97,3 +97,61 @@ def sample_row(z, u, t=1.0, k=0, p=1.0, q=0.0):
     lo, hi = (c[j - 1] if j else 0.0) / c[-1], c[j] / c[-1]
     border = min(u - lo if j else 1.0, hi - u if j + 1 < len(kept) else 1.0)
     return kept[j], float(np.log(w[kept[j]] / c[-1])), border
+
+
+def rms_norm(s, w, offset, eps):
+    """(y, rstd) of rows s [M, H]; w [H] or None."""
+    s = np.asarray(s, dtype=np.float64)
+    rstd = 1.0 / np.sqrt((s ** 2).mean(1) + eps)
+    y = s * rstd[:, None]
+    return (y if w is None else y * (np.asarray(w, dtype=np.float64) + offset)), rstd
+
+
+def rms_norm_grads(dy, s, w, offset, rstd, ds=None):
+    """(dx, dw) of sum(dy * y) + sum(ds * s) for given row statistics."""
+    dy, s = np.asarray(dy, dtype=np.float64), np.asarray(s, dtype=np.float64)
+    rstd = np.asarray(rstd, dtype=np.float64)[:, None]
+    xh = s * rstd
+    g = dy if w is None else dy * (np.asarray(w, dtype=np.float64) + offset)
+    dx = rstd * (g - xh * (g * xh).mean(1, keepdims=True))
+    if ds is not None:
+        dx = dx + np.asarray(ds, dtype=np.float64)
+    return dx, (dy * xh).sum(0)
+
+
+E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def e4m3_values():
+    """The 128 non-negative codes' values (code 127 is NaN): 4 exponent bits of
+    bias 7, 3 mantissa bits, subnormal steps of 2^-9."""
+    c = np.arange(128)
+    e, m = c >> 3, c & 7
+    v = np.where(e == 0, m * 2.0 ** -9, (8 + m) * 2.0 ** (e - 10.0))
+    v[127] = np.nan
+    return v
+
+
+def mx_quantize(y, values):
+    """Blocks of 32 along the rows of y [M, H]: (codes into `values` with the
+    sign in the bit above, scale exponents).  The scale is the least power of
+    two, at least 2^-127, under which the block's magnitudes fit the largest
+    value; elements go to the nearest one, ties to the even code."""
+    y = np.asarray(y, dtype=np.float64)
+    M, H = y.shape
+    nb = (H + 31) // 32
+    full = np.zeros((M, nb * 32))
+    full[:, :H] = y
+    blocks = full.reshape(M, nb, 32)
+    values = values[~np.isnan(values)]
+    top, amax = values[-1], np.abs(blocks).max(2)
+    e = np.full(amax.shape, -127, dtype=np.int64)
+    for x in range(-126, 128):
+        e = np.where(amax > top * 2.0 ** (x - 1), x, e)
+    v = np.abs(blocks) / 2.0 ** e[:, :, None].astype(np.float64)
+    hi = np.clip(np.searchsorted(values, v, side="left"), 0, values.size - 1)
+    lo = np.maximum(hi - 1, 0)
+    up, down = values[hi] - v, v - values[lo]
+    code = np.where((up < down) | ((up == down) & (hi % 2 == 0)), hi, lo)
+    code = np.where((blocks < 0) & (code > 0), code | 1 << int(np.log2(values.size + 1)), code)
+    return code.reshape(M, nb * 32)[:, :H], e
