@@ -48,6 +48,9 @@ extern "C" {
 /* Storage dtype of h, W and grad_h. */
 typedef enum { FLCE_DTYPE_BF16 = 0, FLCE_DTYPE_F32 = 1 } flce_dtype;
 
+/* Rows in 8 bits, as flce_rms_norm_mx writes them (flce_logits_mx only). */
+enum { FLCE_DTYPE_MX8 = 2 };
+
 /*
  * Reduction of the per-row losses.  FLCE_REDUCTION_NONE (flce_fwd_bwd_ex and
  * flce_fwd only) keeps the per-row losses (options.loss_rows, required): the
@@ -449,6 +452,49 @@ int flce_dropout(const void* x, const void* residual, void* y, int64_t n, double
                  const uint64_t* offset_dev, hipStream_t stream, int dtype);
 
 /*
+ * Pack a projection W [V, H] (row stride ld_w >= 0 elements, aligned to one
+ * element, `dtype`) into the E2M1 block format of the OCP Microscaling
+ * specification (MXFP4) for flce_logits_mx.  With Kp = H rounded up to a
+ * multiple of 128:
+ *   packed [V, Kp / 2]   two elements a byte, the first in the low half
+ *   scales [V, Kp / 32]  E8M0 codes: element k of a row has the scale
+ *                        2^(scales[k / 32] - 127)
+ * both contiguous; columns from H on are 0.  The scale is the least power of
+ * two (at least 2^-127) under which no element of its block passes 6, the
+ * largest E2M1 value; elements are rounded to nearest even (0, 0.5, 1, 1.5, 2,
+ * 3, 4, 6 and their negatives).  A block that holds an infinity or a NaN has
+ * code 255 (NaN).  packed is 16-byte aligned.  V <= 2^24, H <= 2^21 and
+ * V Kp <= 2^34 (else FLCE_EUNSUPPORTED).  Enqueued on `stream`; nothing is
+ * allocated, nothing synchronises.  Returns FLCE_OK, FLCE_EINVAL,
+ * FLCE_EUNSUPPORTED or FLCE_EDEVICE.
+ */
+int flce_pack_mx(const void* W, int64_t ld_w, int64_t V, int64_t H, void* packed, void* scales, hipStream_t stream,
+                 int dtype);
+
+/*
+ * Logits from weights in 4 bits, for decoding:
+ *   z = cap(m x W^T)   [N, V] of `dtype` (bf16 or fp32), row stride ld_logits
+ * with W as flce_pack_mx lays it out (or any source of that format: the scales
+ * may be any code; an element beyond the largest bf16 counts as infinite, and
+ * columns from H on must be 0 under a scale that is not NaN).
+ *   x         [N, H], row stride ld_x >= 0 elements, aligned to one element, of
+ *             x_dtype: bf16, fp32, or FLCE_DTYPE_MX8 with x_scales
+ *             [N, ceil(H / 32)], row stride ld_xs >= 0 (NULL for the others)
+ *   packed    16-byte aligned
+ *   logits    aligned to one element, ld_logits >= V when N > 1; columns from V
+ *             on are not written; must not overlap an input
+ * Softcap and multiplier as flce_logits.  Products are exact, sums fp32 (over
+ * the three 8-bit parts of an fp32 x too; an x below 2^-102 may lose its last
+ * bits), z is rounded once.  N <= 2^20, V <= 2^24, H <= 2^21 (else
+ * FLCE_EUNSUPPORTED); N = 0 does nothing.  Enqueued on `stream`; nothing is allocated, nothing
+ * synchronises.  Returns FLCE_OK, FLCE_EINVAL, FLCE_EUNSUPPORTED or
+ * FLCE_EDEVICE.
+ */
+int flce_logits_mx(const void* x, int64_t ld_x, const void* x_scales, int64_t ld_xs, const void* packed,
+                   const void* scales, int64_t N, int64_t H, int64_t V, float softcap_T, float multiplier,
+                   void* logits, int64_t ld_logits, hipStream_t stream, int x_dtype, int dtype);
+
+/*
  * Parameters of flce_sample: one value for every row, or (pointer not NULL)
  * a device array with one value per row.  Zero-initialise the struct and set
  * temperature, top_p and what else is needed.
@@ -553,7 +599,9 @@ enum {
   FLCE_KERNEL_RMS_NORM = 18,    /* flce_rms_norm_fwd, flce_rms_norm_mx */
   FLCE_KERNEL_RMS_NORM_BWD = 19,/* flce_rms_norm_bwd: grad_x and per-group weight gradients */
   FLCE_KERNEL_RMS_NORM_REDUCE = 20,/* flce_rms_norm_bwd: sum of the groups' weight gradients */
-  FLCE_KERNEL_KINDS = 21
+  FLCE_KERNEL_PACK_MX = 21,     /* flce_pack_mx */
+  FLCE_KERNEL_LOGITS_MX = 22,   /* flce_logits_mx */
+  FLCE_KERNEL_KINDS = 23
 };
 
 /* Turn event timing on (on != 0) or off for subsequent calls.  Returns FLCE_OK. */

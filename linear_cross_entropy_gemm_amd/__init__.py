@@ -13,6 +13,7 @@ from ._lib import (  # noqa: F401
     EXPORTED,
     FLCE_DTYPE_BF16,
     FLCE_DTYPE_F32,
+    FLCE_DTYPE_MX8,
     FLCE_EDEVICE,
     FLCE_EINVAL,
     FLCE_ELABEL,
@@ -39,7 +40,9 @@ from ._lib import (  # noqa: F401
     flce_layer_norm_bwd_workspace_size,
     flce_layer_norm_fwd,
     flce_logits,
+    flce_logits_mx,
     flce_options_t,
+    flce_pack_mx,
     flce_profile_enable,
     flce_profile_read,
     flce_plan,
@@ -74,7 +77,7 @@ from .head import (  # noqa: F401
     rms_norm_mx8,
     sample,
 )
-from .mx import Mx8Rows  # noqa: F401
+from .mx import Mx4Weight, Mx8Rows, logits_mx4, mx4_pack  # noqa: F401
 from .torch_api import (  # noqa: F401
     CrossEntropyOutputs,
     FlceForward,

@@ -15,6 +15,7 @@ LIB_PATH = os.path.join(_PKG, "libflce.so")
 
 FLCE_DTYPE_BF16 = 0
 FLCE_DTYPE_F32 = 1
+FLCE_DTYPE_MX8 = 2
 FLCE_REDUCTION_MEAN = 0
 FLCE_REDUCTION_SUM = 1
 FLCE_REDUCTION_NONE = 2
@@ -39,7 +40,7 @@ EXPORTED = ("flce_plan", "flce_workspace_size", "flce_fwd_bwd", "flce_fwd_bwd_ex
             "flce_fwd", "flce_logits", "flce_cross_entropy_workspace_size", "flce_cross_entropy",
             "flce_scale_grads", "flce_layer_norm_fwd", "flce_layer_norm_bwd_workspace_size",
             "flce_layer_norm_bwd", "flce_rms_norm_fwd", "flce_rms_norm_mx", "flce_rms_norm_bwd_workspace_size",
-            "flce_rms_norm_bwd", "flce_dropout", "flce_sample_workspace_size", "flce_sample",
+            "flce_rms_norm_bwd", "flce_pack_mx", "flce_logits_mx", "flce_dropout", "flce_sample_workspace_size", "flce_sample",
             "flce_read_status", "flce_strerror", "flce_profile_enable", "flce_profile_read",
             "flce_profile_read_n")
 
@@ -47,7 +48,7 @@ EXPORTED = ("flce_plan", "flce_workspace_size", "flce_fwd_bwd", "flce_fwd_bwd_ex
 KERNEL_KINDS = ("label_scan", "fwd_logits", "row_merge", "grad_logits", "grad_h", "grad_h_reduce",
                 "grad_W", "finalize", "zero", "logits", "cross_entropy", "scale", "layer_norm",
                 "layer_norm_bwd", "layer_norm_reduce", "dropout", "sample_scan", "sample_pick", "rms_norm",
-                "rms_norm_bwd", "rms_norm_reduce")
+                "rms_norm_bwd", "rms_norm_reduce", "pack_mx", "logits_mx")
 
 
 class flce_plan_t(ctypes.Structure):
@@ -159,6 +160,10 @@ def _load() -> ctypes.CDLL:
     lib.flce_rms_norm_bwd.argtypes = [vp, i64, vp, i64, vp, i64, vp, f32, vp, i64, i64, vp, i64, vp, vp, i32, i32, vp,
                                       sz]
     lib.flce_rms_norm_bwd.restype = i32
+    lib.flce_pack_mx.argtypes = [vp, i64, i64, i64, vp, vp, vp, i32]
+    lib.flce_pack_mx.restype = i32
+    lib.flce_logits_mx.argtypes = [vp, i64, vp, i64, vp, vp, i64, i64, i64, f32, f32, vp, i64, vp, i32, i32]
+    lib.flce_logits_mx.restype = i32
     lib.flce_dropout.argtypes = [vp, vp, vp, i64, f64, u64, u64, vp, vp, i32]
     lib.flce_dropout.restype = i32
     lib.flce_sample_workspace_size.argtypes = [i64, i64, i32]
@@ -308,6 +313,19 @@ def flce_rms_norm_bwd(grad_y: int, ld_gy: int, s: int, ld_s: int, grad_s, ld_gs:
     """Raw call; returns the C return code."""
     return _lib.flce_rms_norm_bwd(grad_y, ld_gy, s, ld_s, grad_s, ld_gs, weight, offset, rstd, M, H, grad_x, ld_gx,
                                   grad_weight, stream, dtype, w_dtype, workspace, workspace_bytes)
+
+
+def flce_pack_mx(W: int, ld_w: int, V: int, H: int, packed: int, scales: int, stream: int, dtype: int) -> int:
+    """Raw call; returns the C return code."""
+    return _lib.flce_pack_mx(W, ld_w, V, H, packed, scales, stream, dtype)
+
+
+def flce_logits_mx(x: int, ld_x: int, x_scales, ld_xs: int, packed: int, scales: int, N: int, H: int, V: int,
+                   softcap_T: float, multiplier: float, logits: int, ld_logits: int, stream: int, x_dtype: int,
+                   dtype: int) -> int:
+    """Raw call; returns the C return code."""
+    return _lib.flce_logits_mx(x, ld_x, x_scales, ld_xs, packed, scales, N, H, V, softcap_T, multiplier, logits,
+                               ld_logits, stream, x_dtype, dtype)
 
 
 def flce_dropout(x: int, residual, y: int, n: int, p: float, seed: int, offset: int, offset_dev, stream: int,

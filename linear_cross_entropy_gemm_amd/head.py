@@ -18,7 +18,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib
-from .mx import MX_BLOCK, Mx8Rows
+from .mx import MX_BLOCK, Mx4Weight, Mx8Rows, logits_mx4
 from .torch_api import (_DTYPES, _enqueue, _ptr, _workspace, check_backward, has_tangent, linear_cross_entropy,
                         logits as _logits, note_leaves)
 
@@ -526,17 +526,41 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature: Union[float, torc
     return res
 
 
-def lm_head_sample(x: torch.Tensor, W: torch.Tensor, u: torch.Tensor, norm_weight: Optional[torch.Tensor],
-                   norm_bias: Optional[torch.Tensor] = None, eps: float = 1e-5, *, softcap: Optional[float] = None,
-                   multiplier: float = 1.0, temperature: Union[float, torch.Tensor] = 1.0,
-                   top_k: Union[int, torch.Tensor] = 0, top_p: Union[float, torch.Tensor] = 1.0,
-                   min_p: Union[float, torch.Tensor] = 0.0, logprobs: bool = False) -> SampleOutputs:
-    """The whole head of a decoding step: the final layer norm of the hidden
-    states ``x`` [..., H], the materialised logits (``logits``), and one token
-    per row (``sample``)."""
-    y = _layer_norm_fwd(x, norm_weight, norm_bias, eps, False)[0]
+def _head_logits(x, W, norm_weight, norm_bias, eps, norm, norm_offset, residual, mx8, softcap, multiplier):
+    """([N, V] logits of x's rows, the new residual stream): the final norm and
+    the projection in bf16, fp32 or 4 bits."""
+    _check_norm(norm, norm_bias, norm_offset)
+    if residual is not None and norm != "rms":
+        raise ValueError("a residual is added by an RMS norm")
+    packed = isinstance(W, Mx4Weight)
+    if mx8 and not (packed and norm == "rms"):
+        raise ValueError("8-bit rows are those of an RMS norm in front of a projection in 4 bits")
     H = x.shape[-1]
-    z = _logits(y.reshape(-1, H), W, softcap, multiplier)
+    s = None
+    if norm == "rms":
+        y, s, _ = _rms_norm_fwd(x, norm_weight, eps, residual, norm_offset, False, mx8)
+    else:
+        y = _layer_norm_fwd(x, norm_weight, norm_bias, eps, False)[0]
+    if mx8:
+        y = Mx8Rows(y.data.reshape(-1, H), y.scales.reshape(-1, y.scales.shape[-1]))
+    else:
+        y = y.reshape(-1, H)
+    return (logits_mx4 if packed else _logits)(y, W, softcap, multiplier), s
+
+
+def lm_head_sample(x: torch.Tensor, W: Union[torch.Tensor, Mx4Weight], u: torch.Tensor,
+                   norm_weight: Optional[torch.Tensor], norm_bias: Optional[torch.Tensor] = None, eps: float = 1e-5, *,
+                   softcap: Optional[float] = None, multiplier: float = 1.0,
+                   temperature: Union[float, torch.Tensor] = 1.0, top_k: Union[int, torch.Tensor] = 0,
+                   top_p: Union[float, torch.Tensor] = 1.0, min_p: Union[float, torch.Tensor] = 0.0,
+                   logprobs: bool = False, norm: str = "layer", norm_offset: float = 0.0,
+                   residual: Optional[torch.Tensor] = None, mx8: bool = False) -> SampleOutputs:
+    """The whole head of a decoding step: the final norm of the hidden states
+    ``x`` [..., H] (``norm``: "layer", or "rms" of ``x`` plus ``residual`` with
+    ``norm_offset`` added to its weight), the materialised logits (``logits``,
+    or ``logits_mx4`` where ``W`` is in 4 bits, with ``mx8`` from 8-bit rows),
+    and one token per row (``sample``)."""
+    z, _ = _head_logits(x, W, norm_weight, norm_bias, eps, norm, norm_offset, residual, mx8, softcap, multiplier)
     o = sample(z, u, temperature, top_k, top_p, min_p, logprobs=logprobs)
     shape = x.shape[:-1]
     return SampleOutputs(o.tokens.reshape(shape), o.logprobs.reshape(shape) if logprobs else None)

@@ -1,0 +1,266 @@
+"""GPU parity of the 4-bit projection against its fp64 definition on exactly the
+values the GPU reads.
+
+Packing is exact arithmetic (a maximum's exponent, a division by a power of
+two, comparisons): codes and scales have to be equal.
+
+Logits: products of a bf16 (or each part of an fp32) with a 4-bit weight are
+exact.  A sum of K of them (3 K with fp32) adds at most Kp (3 Kp) times, each
+off by at most 2 u of the running sum, u = 2^-24 (nothing is assumed about how
+the matrix unit rounds inside an instruction): |dz| <= 2 u Kp parts sum|x w| m.
+The softcap adds 1e-6 of its value, the store half a step.
+"""
+import numpy as np
+import pytest
+
+from gpu_util import log
+from oracle import head as O
+
+pytestmark = [pytest.mark.gpu, pytest.mark.usefixtures("require_gpu")]
+
+U = 2.0 ** -24
+HALF = {"bf16": 2.0 ** -8, "f32": U}
+
+
+def _dt(name):
+    import torch
+    return torch.bfloat16 if name == "bf16" else torch.float32
+
+
+def _rand(shape, dtype, seed, scale=1.0, pad=0, off=0):
+    """A seeded tensor; its rows lie `pad` elements apart in a buffer that
+    starts `off` elements past an aligned address."""
+    import torch
+    g = torch.Generator().manual_seed(seed)
+    v = (torch.randn(shape, generator=g) * scale).to(_dt(dtype))
+    M, H = shape
+    buf = torch.zeros(M * (H + pad) + off + 8, dtype=_dt(dtype), device="cuda")
+    out = buf[off:off + M * (H + pad)].view(M, H + pad)[:, :H]
+    out.copy_(v)
+    return out
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _codes(w):
+    b = w.data.cpu().numpy()
+    return np.stack((b & 15, b >> 4), 2).reshape(b.shape[0], -1)
+
+
+def _weights(w):
+    """[V, hidden] in fp64."""
+    import torch
+    c = _codes(w)
+    v = O.E2M1[c & 7] * (1 - 2.0 * (c >> 3))
+    e = w.scales.view(torch.uint8).cpu().numpy().astype(np.float64) - 127
+    return (v * np.repeat(2.0 ** e, 32, 1))[:, :w.hidden]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V,H", [(1, 1), (3, 31), (7, 32), (5, 100), (40, 128), (33, 1001), (300, 513), (1000, 2048)])
+def test_pack_is_exact(V, H, dtype):
+    import torch
+    import linear_cross_entropy_gemm_amd as L
+    W = _rand((V, H), dtype, 1, 0.02, pad=H % 3, off=1) * (10.0 ** torch.linspace(-8, 8, V, device="cuda"))[:, None]
+    W = W.to(_dt(dtype))
+    W[V // 2, : H // 2] = 0
+    # ties and borders of the scale
+    W[0, : min(H, 8)] = torch.tensor([6.0, 5.0, -2.5, 0.25, 0.75, 1.25, 1.75, 3.5], device="cuda")[:min(H, 8)].to(W.dtype)
+    q = L.mx4_pack(W)
+    code, e = O.mx_quantize(_np(W), O.E2M1)
+    assert np.array_equal(_codes(q)[:, :H], code) and not _codes(q)[:, H:].any()
+    s = q.scales.view(torch.uint8).cpu().numpy()
+    assert np.array_equal(s[:, :e.shape[1]], e + 127) and not s[:, e.shape[1]:].any()
+
+
+def test_pack_special_blocks():
+    import torch
+    import linear_cross_entropy_gemm_amd as L
+    W = torch.ones(3, 96, device="cuda")
+    W[0, 40], W[1, 3], W[2, 95] = float("inf"), float("nan"), 3.4e38
+    s = L.mx4_pack(W).scales.view(torch.uint8).cpu()
+    assert s[:, :3].tolist() == [[125, 255, 125], [255, 125, 125], [125, 125, 253]]
+    e = L.mx4_pack(W[:0])
+    assert e.data.shape == (0, 64) and L.mx4_pack(W.t().contiguous().t()).scales.view(torch.uint8).cpu().equal(s)
+
+
+def _check_logits(z, x, w, cap, mult, out, parts):
+    z, ref = _np(z), x @ w.T * mult
+    tol = 2 * U * parts * ((w.shape[1] + 127) // 128 * 128) * (np.abs(x) @ np.abs(w).T) * abs(mult)
+    if cap:
+        ref = cap * np.tanh(ref / cap)
+        tol = tol + 1e-6 * np.abs(ref)
+    tol = tol + HALF[out] * (np.abs(ref) + tol) + 2 * U * np.abs(ref)
+    bad = np.abs(z - ref) - tol
+    log(f"  worst error minus bound {bad.max():.2e}, relative {np.linalg.norm(z - ref) / np.linalg.norm(ref):.1e}")
+    assert bad.max() <= 0.0, np.unravel_index(int(np.argmax(bad)), bad.shape)
+
+
+# one column, a block, a step and their neighbours, several chunks; one vocabulary
+# entry, a tile, ragged ones; tokens across every border between the kernels
+SHAPES = [(1, 1, 1), (2, 31, 15), (5, 32, 64), (1, 100, 129), (16, 128, 130), (17, 129, 1000), (3, 255, 70),
+          (33, 1001, 2001), (64, 512, 300), (65, 640, 77), (1, 6656, 4099), (130, 2049, 1003), (5, 7168, 515)]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32", "mx8"])
+@pytest.mark.parametrize("N,H,V", SHAPES)
+def test_logits(N, H, V, kind):
+    import torch
+    import linear_cross_entropy_gemm_amd as L
+    log(f"[mx4] N={N} H={H} V={V} {kind}")
+    q = L.mx4_pack(_rand((V, H), "f32", 1, 0.05))
+    w = _weights(q)
+    cap, mult = (3.0, 0.5) if H % 2 else (0.0, 1.0)
+    out = "f32" if kind == "f32" else "bf16"
+    if kind == "mx8":
+        x = L.rms_norm_mx8(_rand((N, H), "bf16", 2), None, 1e-6).rows
+        xn = _np(x.data) * np.repeat(_np(x.scales), 32, 1)[:, :H]
+    else:
+        x = _rand((N, H), kind, 2, pad=H % 3, off=1)
+        xn = _np(x)
+    z = L.logits_mx4(x, q, cap, mult)
+    assert z.shape == (N, V) and z.dtype == _dt(out)
+    _check_logits(z, xn, w, cap, mult, out, 3 if kind == "f32" else 1)
+    # the other output type, rows of a wider buffer, not a byte behind them
+    other = "bf16" if out == "f32" else "f32"
+    buf = torch.full((N, V + 3), 7.0, dtype=_dt(other), device="cuda")
+    z2 = L.logits_mx4(x, q, cap, mult, out=buf)
+    _check_logits(z2, xn, w, cap, mult, other, 3 if kind == "f32" else 1)
+    assert buf[:, V:].eq(7.0).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32", "mx8"])
+def test_special_values(kind):
+    """What is not finite stays in its row, and in its vocabulary entry."""
+    import torch
+    import linear_cross_entropy_gemm_amd as L
+    W = _rand((200, 300), "f32", 1, 0.05)
+    W[77, 100] = float("nan")
+    W[5] = 0.0
+    q = L.mx4_pack(W)
+    x = _rand((20, 300), "bf16" if kind == "mx8" else kind, 2)
+    x[3, 7], x[4, 9] = float("nan"), float("inf")
+    x[6] = 0.0
+    if kind == "mx8":
+        data = x.float().to(torch.float8_e4m3fn)
+        s = torch.full((20, 10), 127, dtype=torch.uint8, device="cuda")
+        s[4, 0] = 255
+        x = L.Mx8Rows(data, s.view(torch.float8_e8m0fnu))
+    z = L.logits_mx4(x, q).float().cpu()
+    fine = [i for i in range(20) if i not in (3, 4)]
+    cols = [i for i in range(200) if i not in (77,)]
+    assert z[3].isnan().all() and not z[4, cols].isfinite().any()
+    assert z[:, 77].isnan().all() and z[fine][:, cols].isfinite().all()
+    assert z[fine, 5].eq(0).all() and z[6, cols].eq(0).all()
+    # the far ends of the scale
+    c = q.scales.view(torch.uint8).clone()
+    c[:, 0], c[:, 1] = 0, 252
+    far = L.Mx4Weight(q.data, c.view(torch.float8_e8m0fnu), 300)
+    one = torch.zeros(1, 300, dtype=torch.bfloat16, device="cuda")
+    one[0, 2] = 2.0 ** 100
+    assert np.array_equal(_np(L.logits_mx4(one.float(), far))[0, cols], _weights(far)[cols, 2] * 2.0 ** 100)
+    one.zero_()
+    one[0, 33] = 2.0 ** -100
+    assert np.array_equal(_np(L.logits_mx4(one, far))[0, cols], _weights(far)[cols, 33] * 2.0 ** -100)
+
+
+def test_fp32_parts_are_exact():
+    """One nonzero column and a weight of 1 return x itself, over its range."""
+    import torch
+    import linear_cross_entropy_gemm_amd as L
+    W = torch.zeros(16, 128, device="cuda")
+    W[3, 17] = 1.0
+    q = L.mx4_pack(W)
+    v = torch.randn(1000, device="cuda") * 10.0 ** torch.linspace(-30, 37.9, 1000, device="cuda")
+    v[0], v[1], v[2] = 3.4028234663852886e38, -3.4028234663852886e38, 1.0 + 2.0 ** -23
+    v = torch.where(v.isfinite(), v, 1.5)
+    x = torch.zeros(1000, 128, device="cuda")
+    x[:, 17] = v
+    assert torch.equal(L.logits_mx4(x, q)[:, 3], v)
+
+
+def test_layouts_and_refusals():
+    import torch
+    import linear_cross_entropy_gemm_amd as L
+    q = L.mx4_pack(_rand((70, 96), "bf16", 1, 0.05))
+    x = _rand((6, 96), "bf16", 2)
+    ref = L.logits_mx4(x, q)
+    assert torch.equal(L.logits_mx4(x.view(2, 3, 96), q), ref.view(2, 3, 70))
+    assert torch.equal(L.logits_mx4(x.t().contiguous().t(), q), ref)
+    assert torch.equal(L.logits_mx4(x[2:3].expand(4, 96), q), ref[2:3].expand(4, 70))
+    assert L.logits_mx4(x[:0], q).shape == (0, 70)
+    r = L.rms_norm_mx8(x.view(2, 3, 96), None).rows
+    assert torch.equal(L.logits_mx4(r, q).view(6, 70), L.logits_mx4(L.rms_norm_mx8(x, None).rows, q))
+    for bad in (lambda: L.logits_mx4(x[:, :95], q), lambda: L.logits_mx4(x, q, out=ref[:, :69]),
+                lambda: L.logits_mx4(x, q, out=ref.half()), lambda: L.logits_mx4(L.Mx8Rows(r.data, r.scales[:1]), q),
+                lambda: L.logits_mx4(x, L.Mx4Weight(q.data.cpu(), q.scales.cpu(), 96))):
+        with pytest.raises(ValueError):
+            bad()
+
+
+def test_rows_far_apart():
+    """Rows of x and of the logits more than 2^31 elements from the first."""
+    import torch
+    import linear_cross_entropy_gemm_amd as L
+    q = L.mx4_pack(_rand((70, 96), "bf16", 1, 0.05))
+    ld = (1 << 30) + 12345
+    v = _rand((3, 96), "bf16", 2)
+    x = torch.zeros(2 * ld + 128, dtype=torch.bfloat16, device="cuda").as_strided((3, 96), (ld, 1))
+    out = torch.zeros(2 * ld + 128, dtype=torch.bfloat16, device="cuda").as_strided((3, 70), (ld, 1))
+    x.copy_(v)
+    L.logits_mx4(x, q, out=out)
+    assert torch.equal(out, L.logits_mx4(v, q))
+
+
+def test_captured_and_on_two_streams():
+    import torch
+    import linear_cross_entropy_gemm_amd as L
+    q = L.mx4_pack(_rand((3000, 640), "bf16", 1, 0.05))
+    x = [_rand((n, 640), "bf16", n) for n in (1, 40)]
+    ref = [L.logits_mx4(v, q) for v in x]
+    s = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    out = [None, None]
+    for k in range(2):
+        with torch.cuda.stream(s[k]):
+            out[k] = L.logits_mx4(x[k], q)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, ref))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r = L.rms_norm_mx8(x[1], None).rows
+        z = L.logits_mx4(r, q)
+    for k in range(3):
+        x[1].copy_(_rand((40, 640), "bf16", 50 + k))
+        ref = L.logits_mx4(L.rms_norm_mx8(x[1], None).rows, q)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(z, ref)
+
+
+@pytest.mark.parametrize("mx8", [False, True])
+def test_decoding_head(mx8):
+    """lm_head_sample over an RMS norm and a 4-bit projection is its operators
+    one by one."""
+    import torch
+    import linear_cross_entropy_gemm_amd as L
+    x, r = _rand((10, 192), "bf16", 1), _rand((10, 192), "bf16", 2)
+    w = _rand((1, 192), "f32", 3, 0.2)[0]
+    W = _rand((5000, 192), "bf16", 4, 0.1)
+    q = L.mx4_pack(W)
+    u = torch.rand(10, device="cuda")
+    o = L.lm_head_sample(x, q, u, w, eps=1e-6, temperature=0.8, top_p=0.9, logprobs=True, norm="rms", norm_offset=1.0,
+                         residual=r, mx8=mx8)
+    f = L.rms_norm_mx8 if mx8 else L.rms_norm_fwd
+    y = f(x, w, 1e-6, residual=r, offset=1.0)
+    t = L.sample(L.logits_mx4(y.rows if mx8 else y.y, q), u, temperature=0.8, top_p=0.9, logprobs=True)
+    assert torch.equal(o.tokens, t.tokens) and torch.equal(o.logprobs, t.logprobs)
+    # with bf16 weights, and behind a layer norm
+    o = L.lm_head_sample(x, W, u, w, eps=1e-6, norm="rms", residual=r)
+    y = L.rms_norm_fwd(x, w, 1e-6, residual=r).y
+    assert torch.equal(o.tokens, L.sample(L.logits(y, W), u).tokens)
+    o = L.lm_head_sample(x.view(2, 5, 192), q, u.view(2, 5), w)
+    t = L.sample(L.logits_mx4(L.layer_norm(x, w), q), u)
+    assert torch.equal(o.tokens.view(-1), t.tokens)
