@@ -550,6 +550,57 @@ int flce_sample(const void* logits, int64_t ld_logits, const float* u, int64_t N
                 const flce_sample_params_t* params, int64_t* tokens, float* logprobs,
                 hipStream_t stream, int dtype, void* workspace, size_t workspace_bytes);
 
+/* Workspace bytes of flce_verify; 0 for sizes it does not take. */
+size_t flce_verify_workspace_size(int64_t B, int64_t K, int64_t V, int dtype, int with_draft);
+
+/*
+ * Verify drafted tokens against the target's distribution (speculative
+ * decoding).  For each of B sequences, with K drafted tokens x_0 .. x_{K-1} of
+ * which the first len count, the distributions p_0 .. p_K that the target gives
+ * behind each prefix, and the q_0 .. q_{K-1} that the tokens were drawn from:
+ *   n      = the first i with i >= len or u_i q_i(x_i) >= p_i(x_i)
+ *   r      = max(p_n - q_n, 0), or p_n where n >= len or nothing is left of r
+ *   y      = the lowest j with sum_{k <= j} r_k > u_draw sum_k r_k
+ *   tokens = x_0 .. x_{n-1}, y, then -1;  accepted = n
+ *   logprobs_i = log p_i(tokens_i), -inf behind the last token
+ * A row's distribution is what flce_sample draws from under its parameters
+ * (temperature, top-k, top-p, min-p; masks and special logits as there), so
+ * tokens that flce_sample drew from the draft's logits come out distributed as
+ * if it had drawn them from the target's.
+ *   target        [B (K + 1), V] logits of dtype, row stride ld_target >= 0
+ *   draft         [B K, V] logits of dtype, row stride ld_draft >= 0; NULL: the
+ *                 draft was certain of its tokens (q_i(x_i) = 1)
+ *   draft_tokens  [B, K] int64; one outside [0, V) is not accepted
+ *   draft_lens    [B] int64 (values outside [0, K] count as the nearer end), or
+ *                 NULL: K
+ *   u             [B, K] fp32 in [0, 1) (one outside accepts nothing)
+ *   u_draw        [B] fp32 in [0, 1) (one outside gives y = -1)
+ *   params        of the target's rows; a per-row array holds one value per
+ *                 SEQUENCE.  draft_params: of the draft's, NULL for the same
+ *   tokens        [B, K + 1] int64 out
+ *   accepted      [B] int64 out
+ *   logprobs      [B, K + 1] fp32 out, or NULL
+ *   workspace     256-byte aligned, flce_verify_workspace_size bytes (with_draft:
+ *                 draft is not NULL); of one call at a time
+ * A target's row without a logit above -inf, or with a per-row parameter out of
+ * range, has p = 0: its token is not accepted, and y is -1; such a row of the
+ * draft has q = 0.  Decisions are taken in 64 bits: where u q is within about
+ * 2^-36 of p, relative to them, or u_draw within 2^-35 of a border in weight of
+ * r, either side is possible.  Weights of r go into sums in units of 2^-51: a
+ * token with less is not drawn.  The same call gives the same bits.
+ * K <= 1024, B <= 2^21, and with R = B (2 K + 1) rows (B (K + 1) without a
+ * draft) R <= 2^21, V <= 2^24 and R ceil(V / 8192) <= 2^23 (else
+ * FLCE_EUNSUPPORTED); K = 0 samples.  Enqueued on `stream`; nothing is
+ * allocated, nothing synchronises.  Returns FLCE_OK, FLCE_EINVAL (also for a
+ * scalar parameter out of its range), FLCE_EUNSUPPORTED, FLCE_EWORKSPACE or
+ * FLCE_EDEVICE.
+ */
+int flce_verify(const void* target, int64_t ld_target, const void* draft, int64_t ld_draft,
+                const int64_t* draft_tokens, const int64_t* draft_lens, const float* u, const float* u_draw, int64_t B,
+                int64_t K, int64_t V, const flce_sample_params_t* params, const flce_sample_params_t* draft_params,
+                int64_t* tokens, int64_t* accepted, float* logprobs, hipStream_t stream, int dtype, void* workspace,
+                size_t workspace_bytes);
+
 /*
  * Synchronise `stream` and return the device-side status of the last
  * flce_fwd_bwd, flce_fwd_bwd_ex, flce_fwd or flce_cross_entropy that used
@@ -601,7 +652,11 @@ enum {
   FLCE_KERNEL_RMS_NORM_REDUCE = 20,/* flce_rms_norm_bwd: sum of the groups' weight gradients */
   FLCE_KERNEL_PACK_MX = 21,     /* flce_pack_mx */
   FLCE_KERNEL_LOGITS_MX = 22,   /* flce_logits_mx */
-  FLCE_KERNEL_KINDS = 23
+  FLCE_KERNEL_VERIFY_SCAN = 23, /* flce_verify: maxima and weights of each row's pieces */
+  FLCE_KERNEL_VERIFY_ROWS = 24, /* flce_verify: each row's cut and sum of weights */
+  FLCE_KERNEL_VERIFY_RESIDUAL = 25,/* flce_verify: accepted tokens, weight left of the target by pieces */
+  FLCE_KERNEL_VERIFY_DRAW = 26, /* flce_verify: the token drawn from what is left, outputs */
+  FLCE_KERNEL_KINDS = 27
 };
 
 /* Turn event timing on (on != 0) or off for subsequent calls.  Returns FLCE_OK. */

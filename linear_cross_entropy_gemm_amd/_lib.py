@@ -41,6 +41,7 @@ EXPORTED = ("flce_plan", "flce_workspace_size", "flce_fwd_bwd", "flce_fwd_bwd_ex
             "flce_scale_grads", "flce_layer_norm_fwd", "flce_layer_norm_bwd_workspace_size",
             "flce_layer_norm_bwd", "flce_rms_norm_fwd", "flce_rms_norm_mx", "flce_rms_norm_bwd_workspace_size",
             "flce_rms_norm_bwd", "flce_pack_mx", "flce_logits_mx", "flce_dropout", "flce_sample_workspace_size", "flce_sample",
+            "flce_verify_workspace_size", "flce_verify",
             "flce_read_status", "flce_strerror", "flce_profile_enable", "flce_profile_read",
             "flce_profile_read_n")
 
@@ -48,7 +49,8 @@ EXPORTED = ("flce_plan", "flce_workspace_size", "flce_fwd_bwd", "flce_fwd_bwd_ex
 KERNEL_KINDS = ("label_scan", "fwd_logits", "row_merge", "grad_logits", "grad_h", "grad_h_reduce",
                 "grad_W", "finalize", "zero", "logits", "cross_entropy", "scale", "layer_norm",
                 "layer_norm_bwd", "layer_norm_reduce", "dropout", "sample_scan", "sample_pick", "rms_norm",
-                "rms_norm_bwd", "rms_norm_reduce", "pack_mx", "logits_mx")
+                "rms_norm_bwd", "rms_norm_reduce", "pack_mx", "logits_mx", "verify_scan", "verify_rows",
+                "verify_residual", "verify_draw")
 
 
 class flce_plan_t(ctypes.Structure):
@@ -170,6 +172,11 @@ def _load() -> ctypes.CDLL:
     lib.flce_sample_workspace_size.restype = sz
     lib.flce_sample.argtypes = [vp, i64, vp, i64, i64, ctypes.POINTER(flce_sample_params_t), vp, vp, vp, i32, vp, sz]
     lib.flce_sample.restype = i32
+    lib.flce_verify_workspace_size.argtypes = [i64, i64, i64, i32, i32]
+    lib.flce_verify_workspace_size.restype = sz
+    prm = ctypes.POINTER(flce_sample_params_t)
+    lib.flce_verify.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, i64, i64, i64, prm, prm, vp, vp, vp, vp, i32, vp, sz]
+    lib.flce_verify.restype = i32
     lib.flce_read_status.argtypes = [vp, vp]
     lib.flce_read_status.restype = i32
     lib.flce_strerror.argtypes = [i32]
@@ -343,6 +350,20 @@ def flce_sample(logits: int, ld_logits: int, u: int, N: int, V: int, params: flc
     """Raw call; returns the C return code."""
     return _lib.flce_sample(logits, ld_logits, u, N, V, None if params is None else ctypes.byref(params), tokens,
                             logprobs, stream, dtype, workspace, workspace_bytes)
+
+
+def flce_verify_workspace_size(B: int, K: int, V: int, dtype: int, with_draft: int) -> int:
+    return int(_lib.flce_verify_workspace_size(B, K, V, dtype, with_draft))
+
+
+def flce_verify(target: int, ld_target: int, draft, ld_draft: int, draft_tokens, draft_lens, u, u_draw: int, B: int,
+                K: int, V: int, params: flce_sample_params_t, draft_params, tokens: int, accepted: int, logprobs,
+                stream: int, dtype: int, workspace: int, workspace_bytes: int) -> int:
+    """Raw call (``draft_params`` None: as ``params``); returns the C return code."""
+    return _lib.flce_verify(target, ld_target, draft, ld_draft, draft_tokens, draft_lens, u, u_draw, B, K, V,
+                            None if params is None else ctypes.byref(params),
+                            None if draft_params is None else ctypes.byref(draft_params), tokens, accepted, logprobs,
+                            stream, dtype, workspace, workspace_bytes)
 
 
 def flce_read_status(workspace: int, stream: int) -> int:

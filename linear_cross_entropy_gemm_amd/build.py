@@ -16,9 +16,10 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libflce.so")
 
 SOURCES = ["flce_kernels.hip", "flce_logits.hip", "flce_scale.hip", "flce_noalloc.hip", "flce_norm.hip",
-           "flce_rms.hip", "flce_mx.hip", "flce_dropout.hip", "flce_sample.hip", "flce_plan.cpp", "flce_api.cpp",
-           "flce_profile.cpp"]
-HEADERS = ["device_common.hpp", "gemm_tile.hpp", "flce_internal.hpp", "kernel_args.hpp", "row_ops.hpp", "mx_ops.hpp"]
+           "flce_rms.hip", "flce_mx.hip", "flce_dropout.hip", "flce_sample.hip", "flce_verify.hip",
+           "flce_plan.cpp", "flce_api.cpp", "flce_profile.cpp"]
+HEADERS = ["device_common.hpp", "gemm_tile.hpp", "flce_internal.hpp", "kernel_args.hpp", "row_ops.hpp", "mx_ops.hpp",
+           "sample_ops.hpp"]
 
 ARCH = "gfx950"
 # Packed fp32 VALU forms are kept out of the generated code (the compiler would

@@ -56,234 +56,28 @@
 // is a search for (K, I).
 #include <cmath>
 
-#include "flce_internal.hpp"
-#include "row_ops.hpp"
+#include "sample_ops.hpp"
 
 namespace flce {
 
 namespace {
 
-constexpr uint32_t kKeyNegInf = 0x007FFFFFu;
-constexpr int kSmall = 2048;         // rows one wave holds
-constexpr int kPiece = 8192;         // logits per work-group of the scan
-constexpr int kGroup = 64;           // logits per stored maximum
-constexpr int kPieceGroups = kPiece / kGroup;
-constexpr int kSlots = 128;          // bins of z per piece; the last holds the rest
-constexpr int kScanThreads = 256;
-
-constexpr double kInfMax = 1e300;   // stands for an infinite maximum
-
-struct SampleArgs {
-  const void* z;
-  int64_t ld;      // elements
-  const float* u;
-  int64_t N, V;
-  flce_sample_params_t prm;
-  int s;           // weights are multiples of 2^-s
-  int64_t* tokens;
-  float* logprobs;
-  // left by the scan (rows longer than kSmall)
-  int pieces;
-  uint32_t* pmax;   // [N][pieces] key of the piece's maximum
-  double* psum;     // [N][pieces] its weight relative to that maximum
-  uint32_t* gmax;   // [N][pieces][kPieceGroups] keys
-  u64* hist;        // [N][pieces][kSlots]
-};
-
-__device__ __forceinline__ float clean(float x) { return x == x ? x + 0.0f : kNegInf; }   // NaN, -0
-
-__device__ __forceinline__ uint32_t key_of(float x) {
-  const uint32_t b = __builtin_bit_cast(uint32_t, x);
-  return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+// Leaves a row's statistics (one thread; kmax and live come from its start).
+__device__ __forceinline__ void emit_stat(const SampleArgs& a, int64_t row, u64 cut, u64 sum) {
+  a.stats[row].cut = cut;
+  a.stats[row].sum = sum;
 }
-__device__ __forceinline__ float value_of(uint32_t k) {
-  return __builtin_bit_cast(float, k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+__device__ __forceinline__ void begin_stat(const SampleArgs& a, int64_t row, uint32_t kmax, bool live) {
+  a.stats[row].kmax = kmax;
+  a.stats[row].live = live ? 1 : 0;
 }
-
-// Coefficients of P, held in scalar registers: they feed the multiply-adds
-// directly there, where literals take two moves each.  The empty asm keeps
-// the compiler from seeing their values.
-struct ExpCoef {
-  double c[8];
-  __device__ __forceinline__ void load() {
-    const double v[8] = {0x1.62e42fef9cc69p-1,  0x1.ebfbdff82a733p-3,  0x1.c6b08da70cce5p-5,  0x1.3b2ab70ad2596p-7,
-                         0x1.5d87759834f12p-10, 0x1.4308c7183804ap-13, 0x1.00c0e4e161930p-16, 0x1.63b2d79cc14d7p-20};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      c[i] = v[i];
-      asm("" : "+s"(c[i]));
-    }
-  }
-};
-
-// A row's parameters and the weights they define.
-struct RowParams {
-  double t, p, q, zmax, rate;   // rate = log2(e) / t
-  ExpCoef coef;
-  int64_t k;
-  float u, xmin;
-  bool ok;
-
-  __device__ __forceinline__ void set_max(float m) {
-    zmax = m < __builtin_inff() ? (double)m : kInfMax;
-    xmin = (float)((double)m - t * (0.69314718055994530942 * 0.8 * 0x1p30));
-  }
-};
-
-__device__ __forceinline__ RowParams row_params(const SampleArgs& a, int64_t row) {
-  RowParams r;
-  const float t = a.prm.temperature_rows ? a.prm.temperature_rows[row] : a.prm.temperature;
-  const float p = a.prm.top_p_rows ? a.prm.top_p_rows[row] : a.prm.top_p;
-  const float q = a.prm.min_p_rows ? a.prm.min_p_rows[row] : a.prm.min_p;
-  r.k = a.prm.top_k_rows ? a.prm.top_k_rows[row] : a.prm.top_k;
-  r.u = a.u[row];
-  r.ok = t >= 0.0f && t < __builtin_inff() && p > 0.0f && p <= 1.0f && q >= 0.0f && q <= 1.0f && r.k >= 0 &&
-         r.u >= 0.0f && r.u < 1.0f;
-  r.t = t;
-  r.p = p;
-  r.q = q;
-  r.set_max(0.0f);
-  r.rate = 1.4426950408889634074 / r.t;
-  r.coef.load();
-  return r;
-}
-
-// How a row's candidates are found.
-enum Mode { kGreedy, kTopK, kMinP, kTopP, kAll };
-__device__ __forceinline__ Mode mode_of(const RowParams& r, int64_t V) {
-  if (r.t == 0.0) return kGreedy;
-  if (r.k > 0 && r.k < V) return kTopK;
-  if (r.q > 0.0) return kMinP;
-  return r.p < 1.0 ? kTopP : kAll;
-}
-
-// Bins of z, 1/8 of min(t, 3/2) wide, by whole-number floats ascending with z.
-// Differences of two are exact below kBinLimit.
-constexpr float kBinLimit = 8388608.0f;   // 2^23
-__device__ __forceinline__ float bin_scale(const RowParams& r) {
-  const double a = 8.0 / (r.t < 1.5 ? r.t : 1.5);
-  return (float)(a < 1e30 ? a : 1e30);
-}
-__device__ __forceinline__ float bin_of(float x, float alpha) { return __builtin_floorf(x * alpha); }
-// The least float in bin b or above: within a few steps of b / alpha.
-__device__ __forceinline__ float bin_edge(float b, float alpha) {
-  uint32_t k = key_of(clean(b / alpha)) + 8;
-  for (int i = 0; i < 32 && bin_of(value_of(k - 1), alpha) >= b; ++i) --k;
-  return value_of(k);
-}
-
-// 2^(d rate) as 2^(n + f), |f| <= 1/2 and |d rate| < 2^31: adding 1.5 2^52
-// leaves n in the low bits, 2^f = 1 + f P(f) with P through the Chebyshev
-// nodes (relative error 2^-38.8; exactly 1 at d = 0), n put into the exponent.
-__device__ __forceinline__ double exp2_of(double d, double rate, const ExpCoef& k) {
-  const double big = __builtin_fma(d, rate, 0x1.8p52);
-  const double f = __builtin_fma(d, rate, -(big - 0x1.8p52));
-  double v = k.c[7];
-#pragma unroll
-  for (int i = 6; i >= 0; --i) v = __builtin_fma(v, f, k.c[i]);
-  return __builtin_amdgcn_ldexp(__builtin_fma(v, f, 1.0), (int)(uint32_t)__builtin_bit_cast(u64, big));
-}
-// exp((x - max) / t) in any row: the maximum may be infinite (zmax is 1e300
-// then), so the exponent is clamped.
-__device__ __forceinline__ double weight_any(float x, const RowParams& r) {
-  const double y = ((double)x - r.zmax) * r.rate;
-  return exp2_of(__builtin_fmin(__builtin_fmax(y, -1000.0), 0.0), 1.0, r.coef);
-}
-// In ordinary rows the clamp is one fp32 maximum: xmin lies 0.8 2^30 in the
-// exponent below the row's maximum, and takes NaN and -inf too.
-__device__ __forceinline__ bool ordinary(float m, const RowParams& r) {
-  return (double)__builtin_fabsf(m) < r.t * 0x1p48 && r.t < 1e20;
-}
-__device__ __forceinline__ double weight(float x, const RowParams& r) {
-  return exp2_of((double)__builtin_fmaxf(x, r.xmin) - r.zmax, r.rate, r.coef);
-}
-
-// round(w 2^s) for w <= 1, s <= 51: adding 2^52 leaves the integer in the
-// mantissa.
-__device__ __forceinline__ u64 fixed(double w, double scale) {
-  return __builtin_bit_cast(u64, __builtin_fma(w, scale, 0x1p52)) & 0xFFFFFFFFFFFFFull;
-}
-
-__device__ __forceinline__ double scale_of(const SampleArgs& a) {
-  return __builtin_bit_cast(double, (u64)(1023 + a.s) << 52);
-}
-
-// The least integer weight that min-p keeps (a weight of 0 is never drawn).
-__device__ __forceinline__ u64 floor_weight(const RowParams& r, double scale) {
-  const u64 f = (u64)ceil(r.q * scale);
-  return f < 1 ? 1 : f;
-}
-
-// The share of a sum that u (or p) asks for, as a running-sum target.
-__device__ __forceinline__ u64 draw_target(float u, u64 sum) {
-  const u64 t = (u64)((double)u * (double)sum);
-  return t < sum ? t : sum - 1;
-}
-__device__ __forceinline__ u64 share(double p, u64 sum) {
-  const u64 n = (u64)ceil(p * (double)sum);
-  return n < 1 ? 1 : n > sum ? sum : n;
-}
-
-// A row's result; `weight_sum` is the kept set's.  Its logarithm starts
-// from the hardware's fp32 one and takes one step of log s = log a + log(1 +
-// (s / a - 1)), where the rest is below 1e-6.
-__device__ __forceinline__ void emit(const SampleArgs& a, int64_t row, int64_t tok, float x, const RowParams& r,
-                                     double weight_sum) {
-  a.tokens[row] = tok;
-  if (!a.logprobs) return;
-  const double l2 = (double)__builtin_amdgcn_logf((float)weight_sum);
-  const double e = __builtin_fma(weight_sum, exp2_of(-l2, 1.0, r.coef), -1.0);
-  const double ls = __builtin_fma(l2, 0.69314718055994530942, e - 0.5 * e * e);
-  const double y = __builtin_fmin(((double)x - r.zmax) * r.rate, 0.0);
-  a.logprobs[row] = (float)(__builtin_fma(y, 0.69314718055994530942, -ls));
-}
-__device__ __forceinline__ void emit_none(const SampleArgs& a, int64_t row) {
-  a.tokens[row] = -1;
-  if (a.logprobs) a.logprobs[row] = kNegInf;
-}
-
-__device__ __forceinline__ int bits_of(u64 x) { return x ? 64 - __builtin_clzll(x) : 0; }
-
-// Sums over a work-group of TH threads.
-template <int TH>
-struct GroupScratch {
-  u64 wsum[TH / 64];
-};
-
-// Exclusive sum of x over the threads in order; `all` gets the whole sum.
-template <int TH>
-__device__ __forceinline__ u64 group_scan(u64 x, u64& all, GroupScratch<TH>& sh) {
-  u64 sum;
-  const u64 inc = wave_scan_u64(x, sum);
-  if (TH > 64) {
-    const int w = threadIdx.x >> 6;
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) sh.wsum[w] = sum;
-    __syncthreads();
-    // every wave scans the waves' sums
-    const int lane = threadIdx.x & 63;
-    const u64 inc_w = wave_scan_u64(lane < TH / 64 ? sh.wsum[lane] : 0, sum);
-    all = sum;
-    return (w ? lane_u64(inc_w, w - 1) : 0) + inc - x;
-  }
-  all = sum;
-  return inc - x;
-}
-
-// ---------------------------------------------------------------------------
-// Candidates as composites that order them by descending logit, then
-// ascending index.
-
-__device__ __forceinline__ u64 composite(uint32_t key, int64_t i) { return (u64)key << 32 | (uint32_t)~(uint32_t)i; }
-__device__ __forceinline__ uint32_t key_in(u64 c) { return (uint32_t)(c >> 32); }
-__device__ __forceinline__ int64_t index_in(u64 c) { return (int64_t)(uint32_t)~(uint32_t)c; }
-__device__ __forceinline__ float value_in(u64 c) { return value_of(key_in(c)); }
 
 // Draws from n <= 64 candidates, one per lane of a wave (c = 0 beyond them),
 // that hold every token at least as likely as the least of them.  top-p is a
 // share of the candidates' weight after top-k, or of `row_sum` where that is
 // not 0.  A candidate's rank and the weights before it come from comparing it
 // with every other one.
+template <bool kStats>
 __device__ __forceinline__ void pick_in_wave(const SampleArgs& a, int64_t row, u64 c, int n, const RowParams& r,
                                              bool top_k, u64 row_sum) {
   const double scale = scale_of(a);
@@ -296,12 +90,24 @@ __device__ __forceinline__ void pick_in_wave(const SampleArgs& a, int64_t row, u
     rank += more ? 1 : 0;
     above += more ? lane_u64(f, i) : 0;
   }
-  if (top_k && rank >= r.k) f = 0;
+  bool kept = c != 0;
+  if (top_k && rank >= r.k) {
+    f = 0;
+    kept = false;
+  }
   if (r.p < 1.0) {
     const u64 all = wave_sum_u64(f);
-    if (above >= share(r.p, row_sum ? row_sum : all)) f = 0;
+    if (above >= share(r.p, row_sum ? row_sum : all)) {
+      f = 0;
+      kept = false;
+    }
   }
   if (f < floor_weight(r, scale)) f = 0;
+  if constexpr (kStats) {
+    const u64 cut = wave_min_u64(kept ? c : ~(u64)0), all = wave_sum_u64(f);
+    if ((threadIdx.x & 63) == 0) emit_stat(a, row, cut, all);
+    return;
+  }
   u64 before = 0, sum = 0;   // in index order
 #pragma unroll 1
   for (u64 left = __builtin_amdgcn_ballot_w64(f != 0); left; left &= left - 1) {
@@ -320,14 +126,14 @@ __device__ __forceinline__ void pick_in_wave(const SampleArgs& a, int64_t row, u
 // of its key, from counts and sums over the wave, until one key is left.  1024
 // rows of 1000 bf16 logits: 8 us without filters, 14 with top-p, 18 with top-k
 // and top-p, bound by the searches' instructions.
-template <typename T, int kPer>
+template <typename T, int kPer, bool kStats>
 __global__ __launch_bounds__(256) void sample_small_kernel(SampleArgs a) {
   constexpr int low = sizeof(T) == 2 ? 16 : 0, E = RowVec<T>::E;
   const int lane = threadIdx.x & 63;
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (row >= a.N) return;
-  RowParams r = row_params(a, row);
-  const T* z = static_cast<const T*>(a.z) + row * a.ld;
+  RowParams r = row_params<kStats>(a, row);
+  const T* z = row_logits<T, kStats>(a, row);
   float x[kPer];
   if (kPer == 1) {
     x[0] = lane < a.V ? clean(to_f32(z[lane])) : kNegInf;
@@ -343,8 +149,9 @@ __global__ __launch_bounds__(256) void sample_small_kernel(SampleArgs a) {
 #pragma unroll
   for (int j = 1; j < kPer; ++j) m = __builtin_fmaxf(m, x[j]);
   m = wave_max(m);
+  if (kStats && lane == 0) begin_stat(a, row, key_of(m), r.ok && m > kNegInf);
   if (!r.ok || m == kNegInf) {
-    if (lane == 0) emit_none(a, row);
+    if (!kStats && lane == 0) emit_none(a, row);
     return;
   }
   r.set_max(m);
@@ -353,7 +160,10 @@ __global__ __launch_bounds__(256) void sample_small_kernel(SampleArgs a) {
 #pragma unroll
     for (int j = kPer - 1; j >= 0; --j) at = x[j] == m ? j : at;
     const int l = __builtin_ctzll(__builtin_amdgcn_ballot_w64(at < kPer));
-    if (lane == l) emit(a, row, lane * kPer + at, m, r, 1.0);
+    if (lane == l) {
+      if constexpr (kStats) emit_stat(a, row, composite(key_of(m), lane * kPer + at), 1);
+      else emit(a, row, lane * kPer + at, m, r, 1.0);
+    }
     return;
   }
   uint32_t key[kPer];   // 0: not kept
@@ -433,6 +243,18 @@ __global__ __launch_bounds__(256) void sample_small_kernel(SampleArgs a) {
     w[j] = key[j] && w[j] >= least ? w[j] : 0;
     own += w[j];
   }
+  if constexpr (kStats) {
+    u64 cut = ~(u64)0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const u64 c = composite(key[j], lane * kPer + j);
+      cut = key[j] && c < cut ? c : cut;
+    }
+    cut = wave_min_u64(cut);
+    const u64 all = wave_sum_u64(own);
+    if (lane == 0) emit_stat(a, row, cut, all);
+    return;
+  }
   u64 sum;
   u64 run = wave_scan_u64(own, sum) - own;
   const u64 target = draw_target(r.u, sum);
@@ -462,7 +284,7 @@ template <int kLanes> __device__ __forceinline__ float lanes_max(float x) {
 }
 
 // One piece of one row per work-group: the only pass over all logits.
-template <typename T>
+template <typename T, bool kStats>
 __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a) {
   constexpr int E = RowVec<T>::E, kVec = kPiece / (kScanThreads * E), kLanes = kGroup / E;
   constexpr int kWaves = kScanThreads / 64;
@@ -473,12 +295,12 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a)
   const int64_t row_i = blockIdx.x / a.pieces;
   const int piece = blockIdx.x % a.pieces;
   const int t = threadIdx.x, lane = t & 63, w = t >> 6;
-  const T* z = static_cast<const T*>(a.z) + row_i * a.ld;
+  const T* z = row_logits<T, kStats>(a, row_i);
   const int64_t base = (int64_t)piece * kPiece;
   typename RowVec<T>::type v[kVec];
 #pragma unroll
   for (int j = 0; j < kVec; ++j) v[j] = load_row(z, base + (j * kScanThreads + t) * E, a.V, kNegInf);
-  RowParams r = row_params(a, row_i);
+  RowParams r = row_params<kStats>(a, row_i);
   const int64_t out = row_i * a.pieces + piece;
   float m = kNegInf;
 #pragma unroll
@@ -621,7 +443,7 @@ template <> struct Interval<bf16> {
 // A row's work-group of TH threads: its shared memory, and what it does.  1024
 // threads have the shortest way through one row; 512, with half the list,
 // leave room for two rows on a compute unit.
-template <int TH>
+template <int TH, bool kStats>
 struct Picker {
 static constexpr int kRowThreads = TH, kRowWaves = TH / 64;
 static constexpr int kBinBits = TH == 1024 ? 11 : 10, kBins = 1 << kBinBits;   // bits of a key per search pass
@@ -1042,7 +864,7 @@ static __device__ __forceinline__ void pick_from_list(const SampleArgs& a, int64
   top_k = top_k && r.k < list.n;
   if (list.n <= 64) {
     if (threadIdx.x < 64)
-      pick_in_wave(a, row_i, (int)threadIdx.x < list.n ? sh.list[threadIdx.x] : 0, list.n, r, top_k, row_sum);
+      pick_in_wave<kStats>(a, row_i, (int)threadIdx.x < list.n ? sh.list[threadIdx.x] : 0, list.n, r, top_k, row_sum);
     return;
   }
   const double scale = scale_of(a);
@@ -1070,12 +892,16 @@ static __device__ __forceinline__ void pick_from_list(const SampleArgs& a, int64
   u64 s = 0;
   list.each([&](u64 c) { s += mass(c); });
   s = group_sum(s, sh.row);
+  if constexpr (kStats) {   // without a cut every listed key stays, and none below
+    if (threadIdx.x == 0) emit_stat(a, row_i, cut ? cut : list.unpack(0), s);
+    return;
+  }
   // in index order: the larger its complement, the earlier an index
   const u64 at = list.search([&](u64 c) { return list.mask() - (u64)index_in(c); }, list.ib, mass,
                              draw_target(r.u, s) + 1);
   const int64_t tok = (int64_t)(list.mask() - at);
   if (threadIdx.x == 0)
-    emit(a, row_i, tok, clean(to_f32(static_cast<const T*>(a.z)[row_i * a.ld + tok])), r, (double)s / scale);
+    emit(a, row_i, tok, clean(to_f32(row_logits<T, kStats>(a, row_i)[tok])), r, (double)s / scale);
 }
 
 // Top-k or min-p: false if the candidates overflow the list.
@@ -1225,6 +1051,10 @@ static __device__ __forceinline__ bool pick_by_pieces(const SampleArgs& a, const
   const u64 m0 = i2 < a.pieces ? sh.cmass[i2] : 0, m1 = i2 + 1 < a.pieces ? sh.cmass[i2 + 1] : 0;
   u64 sum;
   const u64 exc = group_scan<kRowThreads>(m0 + m1, sum, sh.row.scratch);
+  if constexpr (kStats) {
+    if (threadIdx.x == 0) emit_stat(a, row_i, composite(cut.key, cut.idx), sum);
+    return true;
+  }
   u64 target = draw_target(r.u, sum);
   if (exc <= target && target < exc + m0 + m1) {   // one thread
     const bool first = target < exc + m0;
@@ -1278,6 +1108,16 @@ static __device__ __attribute__((noinline)) void pick_whole_row(SampleArgs a, co
   }
   const u64 least = floor_weight(r, scale);
   u64 sum;
+  if constexpr (kStats) {
+    sum = 0;
+    row.each([&](int64_t i, float x) {
+      const u64 w = cut.keeps(i, key_of(x)) ? fixed(weight_any(x, r), scale) : 0;
+      sum += w >= least ? w : (u64)0;
+    });
+    sum = group_sum(sum, sh);
+    if (threadIdx.x == 0) emit_stat(a, row_i, composite(cut.key, cut.idx), sum);
+    return;
+  }
   const int64_t tok = row.locate(
       [&](int64_t i, float x) {
         const u64 w = cut.keeps(i, key_of(x)) ? fixed(weight_any(x, r), scale) : 0;
@@ -1290,8 +1130,8 @@ static __device__ __attribute__((noinline)) void pick_whole_row(SampleArgs a, co
 template <typename T>
 static __device__ __forceinline__ void run(const SampleArgs& a, PickShared& sh) {
   const int64_t row_i = blockIdx.x;
-  RowParams r = row_params(a, row_i);
-  const T* z = static_cast<const T*>(a.z) + row_i * a.ld;
+  RowParams r = row_params<kStats>(a, row_i);
+  const T* z = row_logits<T, kStats>(a, row_i);
   const uint32_t* pmax = a.pmax + row_i * a.pieces;
   uint32_t km = 0;
   for (int i = threadIdx.x; i < a.pieces; i += kRowThreads) km = pmax[i] > km ? pmax[i] : km;
@@ -1300,8 +1140,9 @@ static __device__ __forceinline__ void run(const SampleArgs& a, PickShared& sh) 
   if (threadIdx.x == 0) sh.found = a.pieces;
   __syncthreads();
   for (int i = 0; i < kRowWaves; ++i) km = sh.row.kmax[i] > km ? sh.row.kmax[i] : km;
+  if (kStats && threadIdx.x == 0) begin_stat(a, row_i, km, r.ok && km > kKeyNegInf);
   if (!r.ok || km <= kKeyNegInf) {
-    if (threadIdx.x == 0) emit_none(a, row_i);
+    if (!kStats && threadIdx.x == 0) emit_none(a, row_i);
     return;
   }
   r.set_max(value_of(km));
@@ -1314,7 +1155,10 @@ static __device__ __forceinline__ void run(const SampleArgs& a, PickShared& sh) 
     __syncthreads();
     const int64_t tok = locate_in_piece(z, a.V, (int64_t)sh.found * kPiece,
                                         [&](int64_t, float x) { return (u64)(key_of(x) == km); }, 0, sh.row);
-    if (threadIdx.x == 0) emit(a, row_i, tok, value_of(km), r, 1.0);
+    if (threadIdx.x == 0) {
+      if constexpr (kStats) emit_stat(a, row_i, composite(km, tok), 1);
+      else emit(a, row_i, tok, value_of(km), r, 1.0);
+    }
     done = true;
   } else if (!ordinary(value_of(km), r)) {
   } else if (mode == kTopK || mode == kMinP) {
@@ -1327,10 +1171,10 @@ static __device__ __forceinline__ void run(const SampleArgs& a, PickShared& sh) 
 };
 
 // One row per work-group; at most 128 registers, so that 512 threads fit twice.
-template <typename T, int TH>
+template <typename T, int TH, bool kStats>
 __global__ __launch_bounds__(TH) __attribute__((amdgpu_waves_per_eu(4))) void sample_pick_kernel(SampleArgs a) {
-  __shared__ typename Picker<TH>::PickShared sh;
-  Picker<TH>::template run<T>(a, sh);
+  __shared__ typename Picker<TH, kStats>::PickShared sh;
+  Picker<TH, kStats>::template run<T>(a, sh);
 }
 
 // Two rows at a time on a compute unit where there are more rows than compute
@@ -1338,29 +1182,49 @@ __global__ __launch_bounds__(TH) __attribute__((amdgpu_waves_per_eu(4))) void sa
 // 4000 bf16 logits, 512 against 1024 threads: k = 50 and p = 0.95 on peaked
 // rows 31 against 53 us, p = 0.9 on flat ones 45 against 76 us, no filter 22
 // against 30 us.
-template <typename T>
+template <typename T, bool kStats>
 void launch_pick(const SampleArgs& a, hipStream_t st) {
   if (a.N > 256 && a.V <= 65536)
-    sample_pick_kernel<T, 512><<<(unsigned)a.N, 512, 0, st>>>(a);
+    sample_pick_kernel<T, 512, kStats><<<(unsigned)a.N, 512, 0, st>>>(a);
   else
-    sample_pick_kernel<T, 1024><<<(unsigned)a.N, 1024, 0, st>>>(a);
+    sample_pick_kernel<T, 1024, kStats><<<(unsigned)a.N, 1024, 0, st>>>(a);
 }
 
-template <typename T>
+template <typename T, bool kStats>
 void launch_small(const SampleArgs& a, hipStream_t st) {
   const unsigned g = (unsigned)((a.N + 3) / 4);
-  if (a.V <= 64) sample_small_kernel<T, 1><<<g, 256, 0, st>>>(a);
-  else if (a.V <= 512) sample_small_kernel<T, 8><<<g, 256, 0, st>>>(a);
-  else if (a.V <= 1024) sample_small_kernel<T, 16><<<g, 256, 0, st>>>(a);
-  else sample_small_kernel<T, 32><<<g, 256, 0, st>>>(a);
+  if (a.V <= 64) sample_small_kernel<T, 1, kStats><<<g, 256, 0, st>>>(a);
+  else if (a.V <= 512) sample_small_kernel<T, 8, kStats><<<g, 256, 0, st>>>(a);
+  else if (a.V <= 1024) sample_small_kernel<T, 16, kStats><<<g, 256, 0, st>>>(a);
+  else sample_small_kernel<T, 32, kStats><<<g, 256, 0, st>>>(a);
 }
 
-// Workspace: what the scan leaves, for rows longer than kSmall.
-struct SampleLayout {
-  int64_t pieces;
-  size_t psum, hist, gmax, total;   // byte offsets (pmax at 0); total 0: not supported
-};
+bool on(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
+// The rows' kernels: tokens, or with kStats the rows' statistics.
+template <bool kStats>
+void launch_rows(const SampleArgs& a, hipStream_t stream, int dtype, int kind_scan, int kind_pick) {
+  const bool b = dtype == FLCE_DTYPE_BF16;
+  if (a.V <= kSmall) {
+    ProfileScope ps(kind_pick, stream);
+    b ? launch_small<bf16, kStats>(a, stream) : launch_small<float, kStats>(a, stream);
+    return;
+  }
+  {
+    ProfileScope ps(kind_scan, stream);
+    const unsigned g = (unsigned)(a.N * a.pieces);
+    if (b)
+      sample_scan_kernel<bf16, kStats><<<g, kScanThreads, 0, stream>>>(a);
+    else
+      sample_scan_kernel<float, kStats><<<g, kScanThreads, 0, stream>>>(a);
+  }
+  ProfileScope ps(kind_pick, stream);
+  b ? launch_pick<bf16, kStats>(a, stream) : launch_pick<float, kStats>(a, stream);
+}
+
+}  // namespace
+
+// Workspace: what the scan leaves, for rows longer than kSmall.
 SampleLayout sample_layout(int64_t N, int64_t V) {
   SampleLayout l{(V + kPiece - 1) / kPiece, 0, 0, 0, 0};
   // launches of fewer than 2^32 threads
@@ -1379,9 +1243,32 @@ SampleLayout sample_layout(int64_t N, int64_t V) {
   return l;
 }
 
-bool on(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+void sample_args(SampleArgs& a, int64_t N, int64_t V, const SampleLayout& l, void* workspace) {
+  a.N = N;
+  a.V = V;
+  int bits = 0;
+  while ((int64_t(1) << bits) < V) ++bits;
+  a.s = 62 - bits < 51 ? 62 - bits : 51;
+  char* ws = static_cast<char*>(workspace);
+  a.pieces = (int)l.pieces;
+  a.pmax = reinterpret_cast<uint32_t*>(ws);
+  a.psum = reinterpret_cast<double*>(ws + l.psum);
+  a.hist = reinterpret_cast<u64*>(ws + l.hist);
+  a.gmax = reinterpret_cast<uint32_t*>(ws + l.gmax);
+}
 
-}  // namespace
+// The scalar parameters' ranges and the per-row arrays' alignment.
+bool sample_params_ok(const flce_sample_params_t& q) {
+  if (!q.temperature_rows && !(q.temperature >= 0.0f && std::isfinite(q.temperature))) return false;
+  if (!q.top_k_rows && q.top_k < 0) return false;
+  if (!q.top_p_rows && !(q.top_p > 0.0f && q.top_p <= 1.0f)) return false;
+  if (!q.min_p_rows && !(q.min_p >= 0.0f && q.min_p <= 1.0f)) return false;
+  return on(q.temperature_rows, 4) && on(q.top_k_rows, 8) && on(q.top_p_rows, 4) && on(q.min_p_rows, 4);
+}
+
+void launch_row_stats(const SampleArgs& a, hipStream_t stream, int dtype) {
+  launch_rows<true>(a, stream, dtype, FLCE_KERNEL_VERIFY_SCAN, FLCE_KERNEL_VERIFY_ROWS);
+}
 
 }  // namespace flce
 
@@ -1397,13 +1284,7 @@ extern "C" int flce_sample(const void* logits, int64_t ld_logits, const float* u
   if (dtype != FLCE_DTYPE_BF16 && dtype != FLCE_DTYPE_F32) return FLCE_EINVAL;
   if (N < 0 || V < 1 || !params) return FLCE_EINVAL;
   const uintptr_t es = dtype == FLCE_DTYPE_BF16 ? 2 : 4;
-  const flce_sample_params_t& q = *params;
-  if (!q.temperature_rows && !(q.temperature >= 0.0f && std::isfinite(q.temperature))) return FLCE_EINVAL;
-  if (!q.top_k_rows && q.top_k < 0) return FLCE_EINVAL;
-  if (!q.top_p_rows && !(q.top_p > 0.0f && q.top_p <= 1.0f)) return FLCE_EINVAL;
-  if (!q.min_p_rows && !(q.min_p >= 0.0f && q.min_p <= 1.0f)) return FLCE_EINVAL;
-  if (!on(q.temperature_rows, 4) || !on(q.top_k_rows, 8) || !on(q.top_p_rows, 4) || !on(q.min_p_rows, 4))
-    return FLCE_EINVAL;
+  if (!sample_params_ok(*params)) return FLCE_EINVAL;
   if (!on(logprobs, 4) || !on(workspace, 256)) return FLCE_EINVAL;
   if (N > 0 && (!logits || !u || !tokens || !workspace)) return FLCE_EINVAL;
   if (!on(logits, es) || !on(u, 4) || !on(tokens, 8) || ld_logits < 0) return FLCE_EINVAL;
@@ -1411,46 +1292,14 @@ extern "C" int flce_sample(const void* logits, int64_t ld_logits, const float* u
   if (l.total == 0) return FLCE_EUNSUPPORTED;
   if (N == 0) return FLCE_OK;
   if (workspace_bytes < l.total) return FLCE_EWORKSPACE;
-  SampleArgs a;
+  SampleArgs a{};
   a.z = logits;
   a.ld = ld_logits;
   a.u = u;
-  a.N = N;
-  a.V = V;
-  a.prm = q;
-  int bits = 0;
-  while ((int64_t(1) << bits) < V) ++bits;
-  a.s = 62 - bits < 51 ? 62 - bits : 51;
+  a.prm = *params;
   a.tokens = tokens;
   a.logprobs = logprobs;
-  char* ws = static_cast<char*>(workspace);
-  a.pieces = (int)l.pieces;
-  a.pmax = reinterpret_cast<uint32_t*>(ws);
-  a.psum = reinterpret_cast<double*>(ws + l.psum);
-  a.hist = reinterpret_cast<u64*>(ws + l.hist);
-  a.gmax = reinterpret_cast<uint32_t*>(ws + l.gmax);
-  if (V <= kSmall) {
-    ProfileScope ps(FLCE_KERNEL_SAMPLE_PICK, stream);
-    if (dtype == FLCE_DTYPE_BF16)
-      launch_small<bf16>(a, stream);
-    else
-      launch_small<float>(a, stream);
-    return hipGetLastError() == hipSuccess ? FLCE_OK : FLCE_EDEVICE;
-  }
-  {
-    ProfileScope ps(FLCE_KERNEL_SAMPLE_SCAN, stream);
-    const unsigned g = (unsigned)(N * l.pieces);
-    if (dtype == FLCE_DTYPE_BF16)
-      sample_scan_kernel<bf16><<<g, kScanThreads, 0, stream>>>(a);
-    else
-      sample_scan_kernel<float><<<g, kScanThreads, 0, stream>>>(a);
-  }
-  {
-    ProfileScope ps(FLCE_KERNEL_SAMPLE_PICK, stream);
-    if (dtype == FLCE_DTYPE_BF16)
-      launch_pick<bf16>(a, stream);
-    else
-      launch_pick<float>(a, stream);
-  }
+  sample_args(a, N, V, l, workspace);
+  launch_rows<false>(a, stream, dtype, FLCE_KERNEL_SAMPLE_SCAN, FLCE_KERNEL_SAMPLE_PICK);
   return hipGetLastError() == hipSuccess ? FLCE_OK : FLCE_EDEVICE;
 }

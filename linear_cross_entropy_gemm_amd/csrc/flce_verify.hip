@@ -1,0 +1,384 @@
+// Verification of drafted tokens against the target's distribution from given
+// random numbers (flce_verify), with the sampler's temperature and filters.
+//
+// Sequence b has K drafted tokens x_i (the first len_b of them), the draft's
+// distributions q_i that they were drawn from and the target's p_0 .. p_K:
+//   n = the first i with i >= len_b or u_i q_i(x_i) >= p_i(x_i)
+//   tokens = x_0 .. x_{n-1} and one drawn from r = max(p_n - q_n, 0) (from p_n
+//   where the draft had ended)
+// which leaves every token distributed as if drawn from p.
+//
+//   1. the sampler's scan and pick leave each row's cut and sum of weights
+//      instead of a token (flce_sample.hip): all 2K + 1 rows of a sequence at
+//      once, since a row's turn is known only after the rows before it
+//   2. verify_residual_kernel: n from K pairs of logits (every work-group of a
+//      sequence finds it by itself), and the weight of r by pieces of 4096
+//   3. verify_draw_kernel: the piece in which the running sum passes u, and the
+//      token in it, in index order
+// A distribution's values are formed from the logits again where they are
+// needed: 64-bit exponentials over a row's sum; r goes into integers of 2^-51,
+// whose sums are exact in any order.
+#include <cmath>
+
+#include "sample_ops.hpp"
+
+namespace flce {
+
+namespace {
+
+constexpr int kVerThreads = 256;
+constexpr int kVerPiece = 4096;
+constexpr int kVerPer = kVerPiece / kVerThreads;   // logits per thread
+constexpr double kVerScale = 0x1p51;
+constexpr int64_t kMaxDrafted = 1024;
+
+struct VerifyArgs {
+  SampleArgs s;   // rows, parameters and what the sampler's kernels left
+  bool drafts;    // the draft's logits are given (else its tokens are certain)
+  const int64_t* x;
+  const int64_t* lens;   // null: K
+  const float* u;
+  const float* u_draw;
+  int64_t B;
+  int K, pieces;
+  int* n;        // [B]
+  u64* rsum;     // [B][pieces] of r
+  u64* psum;     // [B][pieces] of p
+  int64_t* tokens;
+  int64_t* accepted;
+  float* logprobs;
+};
+
+// A row's distribution.
+template <typename T>
+struct Dist {
+  RowParams r;
+  const T* z;
+  u64 cut, least;
+  double scale, inv;   // probability = weight * inv
+  bool live, plain;
+
+  __device__ __forceinline__ Dist(const SampleArgs& a, int64_t row) : r(row_params<true>(a, row)) {
+    const RowStat st = a.stats[row];
+    z = row_logits<T, true>(a, row);
+    live = st.live != 0;
+    cut = live ? st.cut : ~(u64)0;
+    scale = scale_of(a);
+    least = floor_weight(r, scale);
+    const float m = value_of(st.kmax);
+    r.set_max(m);
+    plain = ordinary(m, r);
+    inv = r.t == 0.0 ? 1.0 : scale / (double)st.sum;
+  }
+  __device__ __forceinline__ bool reaches(float x) const { return key_of(x) >= key_in(cut); }
+  // (weights that round to 0 in the sums' unit count here, where a token is
+  // judged, and have no part in what is drawn; 2^-1000 stands for 0)
+  __device__ __forceinline__ double prob(int64_t i, float x) const {
+    if (!live || composite(key_of(x), i) < cut || !(x > kNegInf)) return 0.0;
+    if (r.t == 0.0) return 1.0;
+    const double w = plain ? weight(x, r) : weight_any(x, r);
+    if (w < 0x1p-900 || (r.q > 0.0 && fixed(w, scale) < least)) return 0.0;
+    return w * inv;
+  }
+  __device__ __forceinline__ double prob(int64_t i) const { return prob(i, clean(to_f32(z[i]))); }
+  __device__ __forceinline__ float logprob(int64_t i) const {
+    if (r.t == 0.0) return 0.0f;
+    const double y = __builtin_fmin(((double)clean(to_f32(z[i])) - r.zmax) * r.rate, 0.0);
+    return (float)(y * 0.69314718055994530942 + log(inv));
+  }
+};
+
+__device__ __forceinline__ int64_t target_row(const VerifyArgs& v, int64_t b, int i) { return b * (v.K + 1) + i; }
+__device__ __forceinline__ int64_t draft_row(const VerifyArgs& v, int64_t b, int i) { return v.s.n1 + b * v.K + i; }
+
+__device__ __forceinline__ int drafted(const VerifyArgs& v, int64_t b) {
+  if (!v.lens) return v.K;
+  const int64_t n = v.lens[b];
+  return n < 0 ? 0 : n > v.K ? v.K : (int)n;
+}
+
+// How many drafted tokens of sequence b are accepted: one wave, a lane per
+// position.
+template <typename T>
+__device__ __forceinline__ int count_accepted(const VerifyArgs& v, int64_t b) {
+  const int len = drafted(v, b), lane = threadIdx.x & 63;
+  for (int i0 = 0; i0 < len; i0 += 64) {
+    const int i = i0 + lane;
+    bool ok = false;
+    if (i < len) {
+      const int64_t x = v.x[b * v.K + i];
+      const float u = v.u[b * v.K + i];
+      if (x >= 0 && x < v.s.V && u >= 0.0f && u < 1.0f) {
+        const double p = Dist<T>(v.s, target_row(v, b, i)).prob(x);
+        const double q = v.drafts ? Dist<T>(v.s, draft_row(v, b, i)).prob(x) : 1.0;
+        ok = (double)u * q < p;
+      }
+    }
+    const unsigned long long bad = ~__builtin_amdgcn_ballot_w64(ok);
+    if (bad) {
+      const int n = i0 + __builtin_ctzll(bad);
+      return n < len ? n : len;
+    }
+  }
+  return len;
+}
+
+// The weights that sequence b's last token is drawn from, behind n accepted
+// ones.
+template <typename T>
+struct Residual {
+  Dist<T> p, q;
+  bool with_q;      // the draft's distribution
+  int64_t certain;  // its certain token, -1: none
+
+  __device__ __forceinline__ Residual(const VerifyArgs& v, int64_t b, int n)
+      : p(v.s, target_row(v, b, n)),
+        q(v.s, v.drafts && n < drafted(v, b) ? draft_row(v, b, n) : target_row(v, b, n)) {
+    const bool on = n < drafted(v, b);
+    with_q = on && v.drafts;
+    certain = on && !v.drafts ? v.x[b * v.K + n] : -1;
+  }
+  // both integer weights of E logits from index i on
+  template <int E>
+  __device__ __forceinline__ void weights(int64_t i, const typename RowVec<T>::type& zp,
+                                          const typename RowVec<T>::type& zq, u64 (&rw)[E], u64 (&pw)[E]) const {
+    bool any = false;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      any |= p.reaches(clean(to_f32(zp[e])));
+      rw[e] = pw[e] = 0;
+    }
+    if (!__builtin_amdgcn_ballot_w64(any)) return;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const double a = p.prob(i + e, clean(to_f32(zp[e])));
+      double c = with_q ? q.prob(i + e, clean(to_f32(zq[e]))) : 0.0;
+      if (i + e == certain) c = 1.0;
+      pw[e] = fixed(a, kVerScale);
+      rw[e] = a > c ? fixed(a - c, kVerScale) : 0;
+    }
+  }
+};
+
+template <typename T>
+__global__ __launch_bounds__(kVerThreads) void verify_residual_kernel(VerifyArgs v) {
+  constexpr int E = RowVec<T>::E, kVec = kVerPer / E;
+  __shared__ int n_of;
+  __shared__ u64 part[2][kVerThreads / 64];
+  const int64_t b = blockIdx.x / v.pieces;
+  const int piece = blockIdx.x % v.pieces;
+  if (threadIdx.x < 64) {
+    const int n = count_accepted<T>(v, b);
+    if (threadIdx.x == 0) n_of = n;
+  }
+  __syncthreads();
+  const int n = n_of;
+  if (piece == 0 && threadIdx.x == 0) v.n[b] = n;
+  const Residual<T> res(v, b, n);
+  u64 rs = 0, ps = 0;
+  if (res.p.live) {
+    const int64_t base = (int64_t)piece * kVerPiece;
+    typename RowVec<T>::type zp[kVec], zq[kVec];
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      const int64_t c = base + (j * kVerThreads + threadIdx.x) * E;
+      zp[j] = load_row(res.p.z, c, v.s.V, kNegInf);
+      zq[j] = zp[j];
+      if (res.with_q) zq[j] = load_row(res.q.z, c, v.s.V, kNegInf);
+    }
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      u64 rw[E], pw[E];
+      res.weights(base + (j * kVerThreads + threadIdx.x) * E, zp[j], zq[j], rw, pw);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        rs += rw[e];
+        ps += pw[e];
+      }
+    }
+  }
+  rs = wave_sum_u64(rs);
+  ps = wave_sum_u64(ps);
+  if ((threadIdx.x & 63) == 0) {
+    part[0][threadIdx.x >> 6] = rs;
+    part[1][threadIdx.x >> 6] = ps;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    v.rsum[b * v.pieces + piece] = part[0][0] + part[0][1] + part[0][2] + part[0][3];
+    v.psum[b * v.pieces + piece] = part[1][0] + part[1][1] + part[1][2] + part[1][3];
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kVerThreads) void verify_draw_kernel(VerifyArgs v) {
+  constexpr int E = RowVec<T>::E, kVec = kVerPer / E;
+  __shared__ GroupScratch<kVerThreads> scratch;
+  __shared__ int found;
+  __shared__ u64 rest;
+  __shared__ int64_t tok;
+  const int64_t b = blockIdx.x;
+  const int t = threadIdx.x, n = v.n[b];
+  const float u = v.u_draw[b];
+  const Residual<T> res(v, b, n);
+  if (t == 0) tok = -1;
+  // consecutive pieces per thread; p itself where nothing is left of r
+  const int per = (v.pieces + kVerThreads - 1) / kVerThreads;
+  const u64* sums = v.rsum + b * v.pieces;
+  u64 own = 0, all = 0, before = 0;
+  for (int way = 0; way < 2; ++way) {
+    if (way) sums = v.psum + b * v.pieces;
+    own = 0;
+    for (int i = t * per; i < (t + 1) * per && i < v.pieces; ++i) own += sums[i];
+    before = group_scan<kVerThreads>(own, all, scratch);
+    if (all) break;
+  }
+  const bool from_p = sums != v.rsum + b * v.pieces;
+  if (all && u >= 0.0f && u < 1.0f) {
+    const u64 target = draw_target(u, all);
+    if (before <= target && target < before + own) {   // one thread
+      int i = t * per;
+      for (; target >= before + sums[i]; ++i) before += sums[i];
+      found = i;
+      rest = target - before;
+    }
+    __syncthreads();
+    const int64_t c = (int64_t)found * kVerPiece + t * kVerPer;
+    u64 w[kVec][E];
+    own = 0;
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      const typename RowVec<T>::type zp = load_row(res.p.z, c + j * E, v.s.V, kNegInf);
+      typename RowVec<T>::type zq = zp;
+      if (res.with_q) zq = load_row(res.q.z, c + j * E, v.s.V, kNegInf);
+      u64 rw[E], pw[E];
+      res.weights(c + j * E, zp, zq, rw, pw);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        w[j][e] = from_p ? pw[e] : rw[e];
+        own += w[j][e];
+      }
+    }
+    before = group_scan<kVerThreads>(own, all, scratch);
+    if (before <= rest && rest < before + own) {   // one thread
+      int64_t at = c;
+#pragma unroll
+      for (int j = 0; j < kVec; ++j)
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          before += w[j][e];
+          if (before <= rest) at = c + j * E + e + 1;
+        }
+      tok = at;
+    }
+  }
+  __syncthreads();
+  for (int i = t; i <= v.K; i += kVerThreads) {
+    const int64_t x = i < n ? v.x[b * v.K + i] : i == n ? tok : -1;
+    const int64_t at = b * (v.K + 1) + i;
+    v.tokens[at] = x;
+    if (v.logprobs) v.logprobs[at] = x < 0 ? kNegInf : Dist<T>(v.s, target_row(v, b, i)).logprob(x);
+  }
+  if (t == 0) v.accepted[b] = n;
+}
+
+template <typename T>
+void launch_verify(const VerifyArgs& v, hipStream_t stream) {
+  {
+    ProfileScope ps(FLCE_KERNEL_VERIFY_RESIDUAL, stream);
+    verify_residual_kernel<T><<<(unsigned)(v.B * v.pieces), kVerThreads, 0, stream>>>(v);
+  }
+  ProfileScope ps(FLCE_KERNEL_VERIFY_DRAW, stream);
+  verify_draw_kernel<T><<<(unsigned)v.B, kVerThreads, 0, stream>>>(v);
+}
+
+struct VerifyLayout {
+  SampleLayout rows;
+  int64_t pieces;
+  size_t stats, n, rsum, psum, total;   // total 0: not supported
+};
+
+VerifyLayout verify_layout(int64_t B, int64_t K, int64_t V, bool drafts) {
+  VerifyLayout l{};
+  if (B > (int64_t(1) << 21) || K > kMaxDrafted) return l;
+  const int64_t R = B * (drafts ? 2 * K + 1 : K + 1);
+  l.rows = sample_layout(R, V);
+  l.pieces = ceil_div(V, kVerPiece);
+  if (l.rows.total == 0) return l;
+  auto pad = [](size_t b) { return (b + 255) & ~size_t(255); };
+  l.stats = pad(l.rows.total);
+  l.n = l.stats + pad((size_t)R * sizeof(RowStat));
+  l.rsum = l.n + pad((size_t)B * 4);
+  l.psum = l.rsum + pad((size_t)(B * l.pieces) * 8);
+  l.total = l.psum + pad((size_t)(B * l.pieces) * 8);
+  return l;
+}
+
+bool on(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+}  // namespace
+
+}  // namespace flce
+
+extern "C" size_t flce_verify_workspace_size(int64_t B, int64_t K, int64_t V, int dtype, int with_draft) {
+  if ((dtype != FLCE_DTYPE_BF16 && dtype != FLCE_DTYPE_F32) || B < 0 || K < 0 || V < 1) return 0;
+  return flce::verify_layout(B, K, V, with_draft != 0).total;
+}
+
+extern "C" int flce_verify(const void* target, int64_t ld_target, const void* draft, int64_t ld_draft,
+                           const int64_t* draft_tokens, const int64_t* draft_lens, const float* u, const float* u_draw,
+                           int64_t B, int64_t K, int64_t V, const flce_sample_params_t* params,
+                           const flce_sample_params_t* draft_params, int64_t* tokens, int64_t* accepted,
+                           float* logprobs, hipStream_t stream, int dtype, void* workspace, size_t workspace_bytes) {
+  using namespace flce;
+  if (dtype != FLCE_DTYPE_BF16 && dtype != FLCE_DTYPE_F32) return FLCE_EINVAL;
+  if (B < 0 || K < 0 || V < 1 || !params) return FLCE_EINVAL;
+  const uintptr_t es = dtype == FLCE_DTYPE_BF16 ? 2 : 4;
+  if (!draft_params) draft_params = params;
+  if (!sample_params_ok(*params) || !sample_params_ok(*draft_params)) return FLCE_EINVAL;
+  if (!on(target, es) || !on(draft, es) || !on(draft_tokens, 8) || !on(draft_lens, 8) || !on(u, 4) ||
+      !on(u_draw, 4) || !on(tokens, 8) || !on(accepted, 8) || !on(logprobs, 4) || !on(workspace, 256))
+    return FLCE_EINVAL;
+  if (ld_target < 0 || (draft && ld_draft < 0)) return FLCE_EINVAL;
+  if (B > 0 && (!target || !u_draw || !tokens || !accepted || !workspace)) return FLCE_EINVAL;
+  if (B > 0 && K > 0 && (!draft_tokens || !u)) return FLCE_EINVAL;
+  const bool drafts = draft && K > 0;
+  const VerifyLayout l = verify_layout(B, K, V, drafts);
+  if (l.total == 0) return FLCE_EUNSUPPORTED;
+  if (B == 0) return FLCE_OK;
+  if (workspace_bytes < l.total) return FLCE_EWORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  VerifyArgs v{};
+  SampleArgs& a = v.s;
+  a.z = target;
+  a.ld = ld_target;
+  a.z2 = draft;
+  a.ld2 = ld_draft;
+  a.n1 = B * (K + 1);
+  a.per1 = (uint32_t)(K + 1);
+  a.per2 = (uint32_t)(K > 0 ? K : 1);
+  a.prm = *params;
+  a.prm2 = *draft_params;
+  a.stats = reinterpret_cast<RowStat*>(ws + l.stats);
+  sample_args(a, B * (drafts ? 2 * K + 1 : K + 1), V, l.rows, ws);
+  v.drafts = drafts;
+  v.x = draft_tokens;
+  v.lens = draft_lens;
+  v.u = u;
+  v.u_draw = u_draw;
+  v.B = B;
+  v.K = (int)K;
+  v.pieces = (int)l.pieces;
+  v.n = reinterpret_cast<int*>(ws + l.n);
+  v.rsum = reinterpret_cast<u64*>(ws + l.rsum);
+  v.psum = reinterpret_cast<u64*>(ws + l.psum);
+  v.tokens = tokens;
+  v.accepted = accepted;
+  v.logprobs = logprobs;
+  launch_row_stats(a, stream, dtype);
+  if (dtype == FLCE_DTYPE_BF16)
+    launch_verify<bf16>(v, stream);
+  else
+    launch_verify<float>(v, stream);
+  return hipGetLastError() == hipSuccess ? FLCE_OK : FLCE_EDEVICE;
+}

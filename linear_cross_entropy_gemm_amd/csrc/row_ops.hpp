@@ -149,6 +149,14 @@ __device__ __forceinline__ u64 wave_sum_u64(u64 x) {
   x += dpp_u64<0x140>(x);
   return (lane_u64(x, 0) + lane_u64(x, 16)) + (lane_u64(x, 32) + lane_u64(x, 48));
 }
+__device__ __forceinline__ u64 wave_min_u64(u64 x) {
+  auto less = [](u64 a, u64 b) { return a < b ? a : b; };
+  x = less(x, dpp_u64<0xB1>(x));
+  x = less(x, dpp_u64<0x4E>(x));
+  x = less(x, dpp_u64<0x141>(x));
+  x = less(x, dpp_u64<0x140>(x));
+  return less(less(lane_u64(x, 0), lane_u64(x, 16)), less(lane_u64(x, 32), lane_u64(x, 48)));
+}
 __device__ __forceinline__ double wave_sum_f64(double x) {
   auto bits = [](double v) { return __builtin_bit_cast(u64, v); };
   auto val = [](u64 v) { return __builtin_bit_cast(double, v); };

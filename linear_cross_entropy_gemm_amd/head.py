@@ -64,6 +64,13 @@ class SampleOutputs:
     logprobs: Optional[torch.Tensor] = None  # [...] fp32, of the filtered distribution
 
 
+@dataclasses.dataclass
+class VerifyOutputs:
+    tokens: torch.Tensor                     # [..., K + 1] int64: the accepted, one drawn, then -1
+    accepted: torch.Tensor                   # [...] int64: how many of the drafted tokens
+    logprobs: Optional[torch.Tensor] = None  # [..., K + 1] fp32 of the target's distributions
+
+
 def _rows(x: torch.Tensor) -> torch.Tensor:
     """x as [M, H] with unit column stride: a view where the strides allow
     one, so a slice of a wider buffer is read in place."""
@@ -505,10 +512,7 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature: Union[float, torc
     if u.dtype != torch.float32 or u.device != dev or u.numel() != N:
         raise ValueError(f"u must hold one float32 per row of logits on {dev}")
     u = u.contiguous()
-    prm = _lib.flce_sample_params_t()
-    keep = [_sample_param(n, v, d, N, dev, prm) for n, v, d in (
-        ("temperature", temperature, torch.float32), ("top_k", top_k, torch.int64),
-        ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32))]
+    prm, keep = _sample_params(temperature, top_k, top_p, min_p, N, dev)
     dtype = _DTYPES[logits.dtype]
     ws_bytes = _lib.flce_sample_workspace_size(N, V, dtype)
     if ws_bytes == 0:
@@ -523,6 +527,84 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature: Union[float, torc
     del keep
     if rc != _lib.FLCE_OK:
         raise _lib.FlceError(rc, "flce_sample")
+    return res
+
+
+def _sample_params(temperature, top_k, top_p, min_p, N, dev):
+    """The parameter block, and the tensors to be kept alive for the call."""
+    prm = _lib.flce_sample_params_t()
+    keep = [_sample_param(n, v, d, N, dev, prm) for n, v, d in (
+        ("temperature", temperature, torch.float32), ("top_k", top_k, torch.int64),
+        ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32))]
+    return prm, keep
+
+
+def verify(target_logits: torch.Tensor, draft_tokens: torch.Tensor, u: torch.Tensor, u_draw: torch.Tensor, *,
+           draft_logits: Optional[torch.Tensor] = None, draft_lens: Optional[torch.Tensor] = None,
+           temperature: Union[float, torch.Tensor] = 1.0, top_k: Union[int, torch.Tensor] = 0,
+           top_p: Union[float, torch.Tensor] = 1.0, min_p: Union[float, torch.Tensor] = 0.0,
+           draft_temperature: Union[None, float, torch.Tensor] = None,
+           draft_top_k: Union[None, int, torch.Tensor] = None, draft_top_p: Union[None, float, torch.Tensor] = None,
+           draft_min_p: Union[None, float, torch.Tensor] = None, logprobs: bool = False,
+           workspace: Optional[torch.Tensor] = None) -> VerifyOutputs:
+    """One call of ``flce_verify``: which of the ``draft_tokens`` [..., K] (int64)
+    stand, and one token more, distributed as if ``sample`` had drawn them all
+    from ``target_logits`` [..., K + 1, V].  ``draft_logits`` [..., K, V] are
+    what the tokens were drawn from (None: they were certain); ``u`` [..., K]
+    and ``u_draw`` [...] are float32 random numbers in [0, 1); ``draft_lens``
+    [...] (int64) says how many tokens of each sequence were drafted.  The
+    sampling parameters are numbers, or tensors with one value per sequence;
+    the draft's are those of the target where not given.  A caller-owned
+    ``workspace`` (uint8, ``flce_verify_workspace_size``) may be reused by
+    ordered calls."""
+    _check_rows("target_logits", target_logits)
+    if target_logits.dim() < 2 or target_logits.shape[-2] < 1:
+        raise ValueError(f"target_logits must be [..., K + 1, V] (got {tuple(target_logits.shape)})")
+    lead, K, V = target_logits.shape[:-2], target_logits.shape[-2] - 1, target_logits.shape[-1]
+    dev = target_logits.device
+    z = _rows(target_logits)
+    B = z.shape[0] // (K + 1)
+
+    def check(name, t, dtype, shape):
+        if t.dtype != dtype or t.device != dev or t.shape != shape:
+            raise ValueError(f"{name} must be {tuple(shape)} {dtype} on {dev} (got {tuple(t.shape)} {t.dtype} on "
+                             f"{t.device})")
+        return t.contiguous()
+
+    x = check("draft_tokens", draft_tokens, torch.int64, (*lead, K))
+    u = check("u", u, torch.float32, (*lead, K))
+    u_draw = check("u_draw", u_draw, torch.float32, lead)
+    lens = None if draft_lens is None else check("draft_lens", draft_lens, torch.int64, lead)
+    d = None
+    if draft_logits is not None:
+        if draft_logits.shape != (*lead, K, V) or draft_logits.dtype != z.dtype or draft_logits.device != dev:
+            raise ValueError(f"draft_logits must be {(*lead, K, V)} {z.dtype} on {dev} (got "
+                             f"{tuple(draft_logits.shape)} {draft_logits.dtype} on {draft_logits.device})")
+        d = _rows(draft_logits) if K > 0 else None
+    prm, keep = _sample_params(temperature, top_k, top_p, min_p, B, dev)
+    prm2 = None
+    if not (draft_temperature is None and draft_top_k is None and draft_top_p is None and draft_min_p is None):
+        prm2, keep2 = _sample_params(
+            temperature if draft_temperature is None else draft_temperature, top_k if draft_top_k is None else
+            draft_top_k, top_p if draft_top_p is None else draft_top_p, min_p if draft_min_p is None else draft_min_p,
+            B, dev)
+        keep += keep2
+    dtype = _DTYPES[z.dtype]
+    ws_bytes = _lib.flce_verify_workspace_size(B, K, V, dtype, 0 if d is None else 1)
+    if ws_bytes == 0:
+        raise _lib.FlceError(_lib.FLCE_EUNSUPPORTED, "flce_verify_workspace_size")
+    workspace = _workspace(workspace, ws_bytes, dev)
+    shape = (*lead, K + 1)
+    res = VerifyOutputs(torch.empty(shape, dtype=torch.int64, device=dev),
+                        torch.empty(lead, dtype=torch.int64, device=dev),
+                        torch.empty(shape, dtype=torch.float32, device=dev) if logprobs else None)
+    rc = _enqueue(dev, lambda stream: _lib.flce_verify(
+        z.data_ptr(), z.stride(0), _ptr(d), 0 if d is None else d.stride(0), x.data_ptr(), _ptr(lens), u.data_ptr(),
+        u_draw.data_ptr(), B, K, V, prm, prm2, res.tokens.data_ptr(), res.accepted.data_ptr(), _ptr(res.logprobs),
+        stream, dtype, workspace.data_ptr(), workspace.numel()))
+    del keep
+    if rc != _lib.FLCE_OK:
+        raise _lib.FlceError(rc, "flce_verify")
     return res
 
 
@@ -564,3 +646,15 @@ def lm_head_sample(x: torch.Tensor, W: Union[torch.Tensor, Mx4Weight], u: torch.
     o = sample(z, u, temperature, top_k, top_p, min_p, logprobs=logprobs)
     shape = x.shape[:-1]
     return SampleOutputs(o.tokens.reshape(shape), o.logprobs.reshape(shape) if logprobs else None)
+
+
+def lm_head_verify(x: torch.Tensor, W: Union[torch.Tensor, Mx4Weight], draft_tokens: torch.Tensor, u: torch.Tensor,
+                   u_draw: torch.Tensor, norm_weight: Optional[torch.Tensor],
+                   norm_bias: Optional[torch.Tensor] = None, eps: float = 1e-5, *, softcap: Optional[float] = None,
+                   multiplier: float = 1.0, norm: str = "layer", norm_offset: float = 0.0,
+                   residual: Optional[torch.Tensor] = None, mx8: bool = False, **kwargs) -> VerifyOutputs:
+    """The whole head of a step that verifies drafted tokens: the final norm of
+    the hidden states ``x`` [..., K + 1, H], the materialised logits (both as
+    in ``lm_head_sample``) and ``verify``, which takes the other arguments."""
+    z, _ = _head_logits(x, W, norm_weight, norm_bias, eps, norm, norm_offset, residual, mx8, softcap, multiplier)
+    return verify(z.reshape(*x.shape[:-1], z.shape[1]), draft_tokens, u, u_draw, **kwargs)

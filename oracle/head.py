@@ -99,6 +99,66 @@ def sample_row(z, u, t=1.0, k=0, p=1.0, q=0.0):
     return kept[j], float(np.log(w[kept[j]] / c[-1])), border
 
 
+def row_distribution(z, t=1.0, k=0, p=1.0, q=0.0):
+    """Probabilities [V] of a row of logits under the sampler's parameters (all
+    zero where nothing can be drawn), as sample_row draws from them."""
+    z = np.asarray(z, dtype=np.float64).copy()
+    z[np.isnan(z)] = -np.inf
+    out = np.zeros(z.size)
+    zm = z.max()
+    if zm == -np.inf:
+        return out
+    if t == 0.0:
+        out[np.flatnonzero(z == zm)[0]] = 1.0
+        return out
+    with np.errstate(invalid="ignore"):
+        w = np.where(z == zm, 1.0, np.exp((z - zm) / t))
+    order = np.lexsort((np.arange(z.size), -z))
+    if k > 0:
+        order = order[:k]
+    if p < 1.0:
+        run = np.cumsum(w[order])
+        order = order[:np.flatnonzero(run >= p * run[-1])[0] + 1]
+    kept = order[w[order] >= q]
+    out[kept] = w[kept]
+    return out / out.sum()
+
+
+def verify(target, draft, x, length, u, u_draw, params, draft_params=None):
+    """(tokens, accepted, logprobs, borders) of one sequence: target [K + 1, V]
+    logits, draft [K, V] logits or None, drafted tokens x [K].  `borders` are
+    the distances from where a decision turns, of u q from p relative to them
+    and of u_draw from the ends of its token's interval in weight of r, and the
+    whole weight of r."""
+    K, V = len(x), target.shape[1]
+    tokens, logs, border, turn = np.full(K + 1, -1), np.full(K + 1, -np.inf), 1.0, 1.0
+    length = min(max(int(length), 0), K)
+    for i in range(K + 1):
+        p, q = row_distribution(target[i], *params), np.zeros(V)
+        if i < length:
+            if draft is not None:
+                q = row_distribution(draft[i], *(params if draft_params is None else draft_params))
+            elif 0 <= x[i] < V:
+                q[x[i]] = 1.0
+            if 0 <= x[i] < V and 0.0 <= u[i] < 1.0:
+                if p[x[i]] > 0.0:
+                    border = min(border, abs(u[i] * q[x[i]] - p[x[i]]) / max(u[i] * q[x[i]], p[x[i]]))
+                if u[i] * q[x[i]] < p[x[i]]:
+                    tokens[i], logs[i] = x[i], np.log(p[x[i]])
+                    continue
+        r = np.maximum(p - q, 0.0)
+        r = r if r.sum() > 0.0 else p
+        c = np.cumsum(r)
+        if c[-1] > 0.0 and 0.0 <= u_draw < 1.0:
+            kept = np.flatnonzero(r)
+            j = min(int(np.searchsorted(c, u_draw * c[-1], side="right")), kept[-1])
+            lo = c[j] - r[j]
+            turn = min(u_draw * c[-1] - lo if j != kept[0] else 1.0,
+                       c[j] - u_draw * c[-1] if j != kept[-1] else 1.0)
+            tokens[i], logs[i] = j, np.log(p[j])
+        return tokens, i, logs, (border, turn, c[-1])
+
+
 def rms_norm(s, w, offset, eps):
     """(y, rstd) of rows s [M, H]; w [H] or None."""
     s = np.asarray(s, dtype=np.float64)
