@@ -463,7 +463,7 @@ int flce_dropout(const void* x, const void* residual, void* y, int64_t n, double
  * two (at least 2^-127) under which no element of its block passes 6, the
  * largest E2M1 value; elements are rounded to nearest even (0, 0.5, 1, 1.5, 2,
  * 3, 4, 6 and their negatives).  A block that holds an infinity or a NaN has
- * code 255 (NaN).  packed is 16-byte aligned.  V <= 2^24, H <= 2^21 and
+ * code 255 (NaN).  packed is 16-byte aligned, scales 4-byte.  V <= 2^24, H <= 2^21 and
  * V Kp <= 2^34 (else FLCE_EUNSUPPORTED).  Enqueued on `stream`; nothing is
  * allocated, nothing synchronises.  Returns FLCE_OK, FLCE_EINVAL,
  * FLCE_EUNSUPPORTED or FLCE_EDEVICE.
@@ -471,28 +471,36 @@ int flce_dropout(const void* x, const void* residual, void* y, int64_t n, double
 int flce_pack_mx(const void* W, int64_t ld_w, int64_t V, int64_t H, void* packed, void* scales, hipStream_t stream,
                  int dtype);
 
+/* Workspace bytes of flce_logits_mx; 0 for sizes it does not take. */
+size_t flce_logits_mx_workspace_size(int64_t N, int64_t H, int x_dtype);
+
 /*
  * Logits from weights in 4 bits, for decoding:
  *   z = cap(m x W^T)   [N, V] of `dtype` (bf16 or fp32), row stride ld_logits
  * with W as flce_pack_mx lays it out (or any source of that format: the scales
- * may be any code; an element beyond the largest bf16 counts as infinite, and
- * columns from H on must be 0 under a scale that is not NaN).
+ * may be any code, columns from H on must be 0 under a scale that is not NaN).
  *   x         [N, H], row stride ld_x >= 0 elements, aligned to one element, of
  *             x_dtype: bf16, fp32, or FLCE_DTYPE_MX8 with x_scales
  *             [N, ceil(H / 32)], row stride ld_xs >= 0 (NULL for the others)
- *   packed    16-byte aligned
+ *   packed    16-byte aligned; scales 4-byte aligned
+ *   workspace 256-byte aligned, flce_logits_mx_workspace_size bytes (the tokens
+ *             in the form that the products take); of one call at a time
  *   logits    aligned to one element, ld_logits >= V when N > 1; columns from V
  *             on are not written; must not overlap an input
- * Softcap and multiplier as flce_logits.  Products are exact, sums fp32 (over
- * the three 8-bit parts of an fp32 x too; an x below 2^-102 may lose its last
- * bits), z is rounded once.  N <= 2^20, V <= 2^24, H <= 2^21 (else
- * FLCE_EUNSUPPORTED); N = 0 does nothing.  Enqueued on `stream`; nothing is allocated, nothing
- * synchronises.  Returns FLCE_OK, FLCE_EINVAL, FLCE_EUNSUPPORTED or
+ * Softcap and multiplier as flce_logits.  A bf16 or fp32 x enters as sums of
+ * E4M3 values under one scale for 32 columns: exactly where it is at least
+ * 2^-14 of the largest of its 32 (and 2^-102), else rounded to 2^-22 (bf16) or
+ * 2^-38 (fp32) of that largest; where one of the 32 is not finite, all of them
+ * count as NaN.  Products are exact, sums fp32, z is rounded once.  N <= 2^20,
+ * V <= 2^24, H <= 2^21 and N Kp <= 2^34 (else FLCE_EUNSUPPORTED); N = 0 does
+ * nothing.  Enqueued on `stream`; nothing is allocated, nothing synchronises.
+ * Returns FLCE_OK, FLCE_EINVAL, FLCE_EUNSUPPORTED, FLCE_EWORKSPACE or
  * FLCE_EDEVICE.
  */
 int flce_logits_mx(const void* x, int64_t ld_x, const void* x_scales, int64_t ld_xs, const void* packed,
                    const void* scales, int64_t N, int64_t H, int64_t V, float softcap_T, float multiplier,
-                   void* logits, int64_t ld_logits, hipStream_t stream, int x_dtype, int dtype);
+                   void* logits, int64_t ld_logits, hipStream_t stream, int x_dtype, int dtype, void* workspace,
+                   size_t workspace_bytes);
 
 /*
  * Parameters of flce_sample: one value for every row, or (pointer not NULL)
@@ -656,7 +664,8 @@ enum {
   FLCE_KERNEL_VERIFY_ROWS = 24, /* flce_verify: each row's cut and sum of weights */
   FLCE_KERNEL_VERIFY_RESIDUAL = 25,/* flce_verify: accepted tokens, weight left of the target by pieces */
   FLCE_KERNEL_VERIFY_DRAW = 26, /* flce_verify: the token drawn from what is left, outputs */
-  FLCE_KERNEL_KINDS = 27
+  FLCE_KERNEL_SPLIT_MX = 27,    /* flce_logits_mx: the tokens brought to 8-bit parts */
+  FLCE_KERNEL_KINDS = 28
 };
 
 /* Turn event timing on (on != 0) or off for subsequent calls.  Returns FLCE_OK. */

@@ -40,7 +40,8 @@ EXPORTED = ("flce_plan", "flce_workspace_size", "flce_fwd_bwd", "flce_fwd_bwd_ex
             "flce_fwd", "flce_logits", "flce_cross_entropy_workspace_size", "flce_cross_entropy",
             "flce_scale_grads", "flce_layer_norm_fwd", "flce_layer_norm_bwd_workspace_size",
             "flce_layer_norm_bwd", "flce_rms_norm_fwd", "flce_rms_norm_mx", "flce_rms_norm_bwd_workspace_size",
-            "flce_rms_norm_bwd", "flce_pack_mx", "flce_logits_mx", "flce_dropout", "flce_sample_workspace_size", "flce_sample",
+            "flce_rms_norm_bwd", "flce_pack_mx", "flce_logits_mx_workspace_size",
+            "flce_logits_mx", "flce_dropout", "flce_sample_workspace_size", "flce_sample",
             "flce_verify_workspace_size", "flce_verify",
             "flce_read_status", "flce_strerror", "flce_profile_enable", "flce_profile_read",
             "flce_profile_read_n")
@@ -50,7 +51,7 @@ KERNEL_KINDS = ("label_scan", "fwd_logits", "row_merge", "grad_logits", "grad_h"
                 "grad_W", "finalize", "zero", "logits", "cross_entropy", "scale", "layer_norm",
                 "layer_norm_bwd", "layer_norm_reduce", "dropout", "sample_scan", "sample_pick", "rms_norm",
                 "rms_norm_bwd", "rms_norm_reduce", "pack_mx", "logits_mx", "verify_scan", "verify_rows",
-                "verify_residual", "verify_draw")
+                "verify_residual", "verify_draw", "split_mx")
 
 
 class flce_plan_t(ctypes.Structure):
@@ -164,7 +165,9 @@ def _load() -> ctypes.CDLL:
     lib.flce_rms_norm_bwd.restype = i32
     lib.flce_pack_mx.argtypes = [vp, i64, i64, i64, vp, vp, vp, i32]
     lib.flce_pack_mx.restype = i32
-    lib.flce_logits_mx.argtypes = [vp, i64, vp, i64, vp, vp, i64, i64, i64, f32, f32, vp, i64, vp, i32, i32]
+    lib.flce_logits_mx_workspace_size.argtypes = [i64, i64, i32]
+    lib.flce_logits_mx_workspace_size.restype = sz
+    lib.flce_logits_mx.argtypes = [vp, i64, vp, i64, vp, vp, i64, i64, i64, f32, f32, vp, i64, vp, i32, i32, vp, sz]
     lib.flce_logits_mx.restype = i32
     lib.flce_dropout.argtypes = [vp, vp, vp, i64, f64, u64, u64, vp, vp, i32]
     lib.flce_dropout.restype = i32
@@ -327,12 +330,16 @@ def flce_pack_mx(W: int, ld_w: int, V: int, H: int, packed: int, scales: int, st
     return _lib.flce_pack_mx(W, ld_w, V, H, packed, scales, stream, dtype)
 
 
+def flce_logits_mx_workspace_size(N: int, H: int, x_dtype: int) -> int:
+    return int(_lib.flce_logits_mx_workspace_size(N, H, x_dtype))
+
+
 def flce_logits_mx(x: int, ld_x: int, x_scales, ld_xs: int, packed: int, scales: int, N: int, H: int, V: int,
                    softcap_T: float, multiplier: float, logits: int, ld_logits: int, stream: int, x_dtype: int,
-                   dtype: int) -> int:
+                   dtype: int, workspace: int, workspace_bytes: int) -> int:
     """Raw call; returns the C return code."""
     return _lib.flce_logits_mx(x, ld_x, x_scales, ld_xs, packed, scales, N, H, V, softcap_T, multiplier, logits,
-                               ld_logits, stream, x_dtype, dtype)
+                               ld_logits, stream, x_dtype, dtype, workspace, workspace_bytes)
 
 
 def flce_dropout(x: int, residual, y: int, n: int, p: float, seed: int, offset: int, offset_dev, stream: int,

@@ -5,17 +5,18 @@
 //
 // A decoding step reads the whole projection for a few tokens: V Kp 17 / 32
 // bytes (Kp: H padded to 128) where bf16 weights take 2 V H.  The weights pass
-// through registers once, from memory straight into the form that the matrix
-// instructions take: a lane's 16-byte load is one block of 32 along a row, its
-// scale one byte, and the hardware's conversion makes pairs of bf16 of it
-// (exactly: 2 significant bits times a power of two).  The order along K is
-// free as long as both operands agree, so element j of lane group g in step k
-// stands for column 128 k + 32 g + j on both sides.
+// through registers once and are never converted: the scaled matrix
+// instruction takes E2M1 rows with a scale for every 32 elements as they lie in
+// memory, next to E4M3 rows with theirs.  So the tokens are brought to E4M3
+// parts, x = sum_p part_p 2^(code - 4 p - 127) with four more significant bits
+// in each: one part for rows that are in 8 bits already, two for bf16 (8
+// bits), six for fp32 (24 bits).  An element above 2^-14 of its block's
+// largest is represented exactly, a smaller one to 2^-22 (bf16) or 2^-38 (fp32)
+// of that largest.  Products of a part are exact and sums are fp32.
 //
-// The tokens' rows are brought to bf16 fragments in LDS: bf16 as they are,
-// E4M3 times its power of two (4 significant bits: exact), fp32 as three bf16
-// parts of 8 bits each (exact: 24 bits).  Products are exact in fp32 and sums
-// are fp32.
+// (Conversion of the weights to bf16 pairs and plain bf16 products took 114 us
+// of the vector and matrix units for 1 x 6656 x 202048, as long as the memory
+// takes for the weights, and 180 together.)
 #include <cmath>
 
 #include "flce_internal.hpp"
@@ -25,114 +26,171 @@ namespace flce {
 
 namespace {
 
-constexpr int kStep = 128;      // columns of one step: four lane groups of one block
-constexpr int kThreads = 256;   // four waves, each with rows of its own
+// Loads that go straight to LDS: lane l's 16 (or 4) bytes at offset `at` of the
+// buffer land at LDS address lds + 16 l (4 l); zeros past the buffer's end.
+// Written as assembly so that the compiler does not make every later LDS read
+// wait for them: the kernel waits by counts.
+typedef uint32_t u32x4s __attribute__((ext_vector_type(4)));
+constexpr uint32_t kPastBuffer = 0x80000000u;
+__device__ __forceinline__ u32x4s buffer_of(const uint8_t* base, int64_t bytes) {   // the same in every lane
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  return u32x4s{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)a),
+                (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(a >> 32)) & 0xFFFFu,
+                (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)bytes), 0x00020000u};
+}
+__device__ __forceinline__ void dma16(const u32x4s& from, uint32_t lds, uint32_t at) {
+  asm volatile("buffer_load_dwordx4 %0, %1, 0 offen lds" : : "v"(at), "s"(from), "{m0}"(lds) : "memory");
+}
+__device__ __forceinline__ void dma4(const u32x4s& from, uint32_t lds, uint32_t at) {
+  asm volatile("buffer_load_dword %0, %1, 0 offen lds" : : "v"(at), "s"(from), "{m0}"(lds) : "memory");
+}
+// Waits until at most n of the wave's memory accesses are under way, and until
+// none of its LDS accesses is; no access moves across either.
+template <int n>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(n) : "memory");
+}
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); }
+__device__ __forceinline__ uint32_t lds_address(const uint8_t* p) {
+  return (uint32_t)__builtin_amdgcn_readfirstlane(
+      (uint32_t)reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) uint8_t*)p));
+}
 
-enum XKind { kXBf16, kXF32, kXMx8 };
+constexpr int kStep = 128;      // columns of one matrix instruction: four lane groups of one block
+constexpr int kThreads = 256;
+
+typedef int i32x4v __attribute__((ext_vector_type(4)));
+typedef int i32x8v __attribute__((ext_vector_type(8)));
 
 struct MxArgs {
+  // the tokens: raw rows (inline split), or parts [P][N][ldx] and codes [N][ldxs]
   const void* x;
-  const uint8_t* xs;   // scales of 8-bit rows
+  const uint8_t* xs;
+  int64_t ldx, ldxs;   // elements, bytes
   const uint8_t* w;    // [V][Kp / 2]
   const uint8_t* ws;   // [V][Kp / 32]
   void* z;
-  int64_t ldx, ldxs, ldz;   // elements
+  int64_t ldz;         // elements
   int64_t N, V;
-  int H, steps;   // steps = Kp / 128
+  int H, steps;        // steps = Kp / 128
   float softcap, mult;
-  int out_bf16;   // z in bf16, else fp32
+  int out_bf16;        // z in bf16, else fp32
 };
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x8v __attribute__((ext_vector_type(8)));
-
-// 8 elements of a weight row (one dword of codes) as bf16.
-__device__ __forceinline__ bf16x8v weights8(uint32_t codes, float scale) {
-  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0);
-  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 1);
-  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 2);
-  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 3);
-  return bf16x8v{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+// acc += A B^T over 128 columns: A 16 rows of E2M1 (lane (r, g): row r, block g),
+// B 16 rows of E4M3 (lane (r, g): row r, columns 16 g to 16 g + 15 and 64 + 16 g
+// to 64 + 16 g + 15), byte kByte of sa and sb the scale of block g of the lane's
+// row.  The empty asm keeps the sums in accumulation registers and the operands
+// alive past the instruction: the compiler may give the result the registers of
+// its 4-bit operand otherwise, which the hardware still reads while it writes.
+template <int kByte>
+__device__ __forceinline__ void mx_mma(f32x4& acc, const u32x4& a, const i32x8v& b, uint32_t sa, uint32_t sb) {
+  const i32x8v wide = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+  acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide, b, acc, 4, 0, kByte, (int)sa, kByte, (int)sb);
+  asm("" : "+a"(acc) : "v"(a), "v"(b));
+}
+__device__ __forceinline__ void mx_mma(int byte, f32x4& acc, const u32x4& a, const i32x8v& b, uint32_t sa, uint32_t sb) {
+  if (byte == 0) mx_mma<0>(acc, a, b, sa, sb);   // (byte is a constant where this is used)
+  else if (byte == 1) mx_mma<1>(acc, a, b, sa, sb);
+  else if (byte == 2) mx_mma<2>(acc, a, b, sa, sb);
+  else mx_mma<3>(acc, a, b, sa, sb);
 }
 
-// 8 values as kParts bf16 parts each (one is enough for what has 8 bits).
-// Cut, not rounded: the rest is exact and no part passes the largest float.
+// Four steps' scales of a row (four bytes each) -> those of the lane's own
+// block, a byte per step.
+__device__ __forceinline__ uint32_t own_scales(const u32x4& x) {
+  const uint32_t g = (threadIdx.x & 63) >> 4;
+  const uint32_t lo = __builtin_amdgcn_perm(x[1], x[0], 0x0c0c0400u + g * 0x0101u);
+  const uint32_t hi = __builtin_amdgcn_perm(x[3], x[2], 0x04000c0cu + g * 0x01010000u);
+  return lo | hi;
+}
+
+// 8 values of a block, whose other values are with the other three lanes of an
+// aligned group of four, as E4M3 parts; returns the block's code.  Parts are
+// rounded, so a part may take more than its share and the rest be negative;
+// codes below 4 (kParts - 1) are raised to it, so that no part's is negative.
 template <int kParts>
-__device__ __forceinline__ void cut_parts(const float (&v)[8], u32x4 (&out)[kParts]) {
+__device__ __forceinline__ uint32_t split8(const float (&v)[8], u32x2 (&out)[kParts]) {
+  uint32_t code = mx8_code(block_max_bits<8>(v));
+  if (code < 4 * (kParts - 1)) code = 4 * (kParts - 1);
+  const float inv = code == 255 ? 1.0f : mx_inverse(code);
+  // next to the largest float no part may round the sum up to 2^128: 15 in
+  // every digit of base 16
+  const float top = code == 247 ? 240.0f : 448.0f;
+  float x[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t w[kParts] = {};
+  for (int e = 0; e < 8; ++e) x[e] = code == 255 ? 0.0f : v[e] * inv;   // a block without a scale is NaN by its code
+#pragma unroll
+  for (int p = 0; p < kParts; ++p) {
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = __builtin_amdgcn_fmed3f(x[e], -top, top);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      float x = v[2 * i + h];
-      const bool special = !(__builtin_fabsf(x) < __builtin_inff());
-      if (x != x) x = __builtin_nanf("");
-#pragma unroll
-      for (int q = 0; q < kParts; ++q) {
-        const uint32_t b = __builtin_bit_cast(uint32_t, x) & 0xFFFF0000u;
-        w[q] |= h ? b : b >> 16;
-        x = special ? 0.0f : x - __builtin_bit_cast(float, b);
+      int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * h], y[4 * h + 1], 0, false);
+      w = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * h + 2], y[4 * h + 3], w, true);
+      out[p][h] = (uint32_t)w;
+      if (p + 1 < kParts) {
+        x[4 * h] = (x[4 * h] - __builtin_amdgcn_cvt_f32_fp8(w, 0)) * 16.0f;
+        x[4 * h + 1] = (x[4 * h + 1] - __builtin_amdgcn_cvt_f32_fp8(w, 1)) * 16.0f;
+        x[4 * h + 2] = (x[4 * h + 2] - __builtin_amdgcn_cvt_f32_fp8(w, 2)) * 16.0f;
+        x[4 * h + 3] = (x[4 * h + 3] - __builtin_amdgcn_cvt_f32_fp8(w, 3)) * 16.0f;
       }
     }
+  }
+  return code;
+}
+
+template <typename T>
+__device__ __forceinline__ void load8(float (&v)[8], const T* row, int k, int H) {
+  constexpr int E = RowVec<T>::E;
 #pragma unroll
-    for (int q = 0; q < kParts; ++q) out[q][i] = w[q];
+  for (int q = 0; q < 8 / E; ++q) {
+    const typename RowVec<T>::type x = load_row(row, k + q * E, H);
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[q * E + e] = to_f32(x[e]);
   }
 }
 
-// 8 elements of a token's row from column k on, as they come from memory
-// (load: rows of at least 8, k anything: what lies past the row's end is read
-// from inside it and put right by parts(), so that no load waits on a branch),
-// and as bf16 parts.
-template <XKind kX> struct XVec;
-template <> struct XVec<kXBf16> {
-  typename RowVec<bf16>::type v;
-  __device__ __forceinline__ void load(const MxArgs& p, int64_t n, int k) {
-    v = load_clamped_vec(static_cast<const bf16*>(p.x) + n * p.ldx, k, p.H);
-  }
-  __device__ __forceinline__ void parts(u32x4 (&out)[1], int k, int H) {
-    row_tail<bf16>(v, k, H);
-    out[0] = __builtin_bit_cast(u32x4, v);
-  }
-};
-template <> struct XVec<kXF32> {
-  f32x4 v[2];
-  __device__ __forceinline__ void load(const MxArgs& p, int64_t n, int k) {
-    const float* r = static_cast<const float*>(p.x) + n * p.ldx;
-    v[0] = load_clamped_vec(r, k, p.H);
-    v[1] = load_clamped_vec(r, k + 4, p.H);
-  }
-  __device__ __forceinline__ void parts(u32x4 (&out)[3], int k, int H) {
-    row_tail<float>(v[0], k, H);
-    row_tail<float>(v[1], k + 4, H);
-    const float x[8] = {v[0][0], v[0][1], v[0][2], v[0][3], v[1][0], v[1][1], v[1][2], v[1][3]};
-    cut_parts(x, out);
-  }
-};
-template <> struct XVec<kXMx8> {
-  u32x2 v;
-  uint32_t code;
-  __device__ __forceinline__ void load(const MxArgs& p, int64_t n, int k) {
-    typedef uint32_t mem __attribute__((ext_vector_type(2), aligned(1)));
-    const int at = k + 8 <= p.H ? k : p.H - 8, block = k < p.H ? k / kMxBlock : 0;
-    const mem m = *reinterpret_cast<const mem*>(static_cast<const uint8_t*>(p.x) + n * p.ldx + at);
-    v = u32x2{m[0], m[1]};
-    code = p.xs[n * p.ldxs + block];
-  }
-  __device__ __forceinline__ void parts(u32x4 (&out)[1], int k, int H) {
-    const int over = k + 8 - H;
-    u64 x = (u64)v[1] << 32 | v[0];
-    if (over > 0) x = over >= 8 ? 0 : x >> 8 * over;
-    // (past the row's end the scale is 1: what is there must not turn into NaN)
-    const float s = __builtin_bit_cast(float, (k < H ? code : 127u) << 23);
+// Parts and codes of rows that the products read from a workspace: one vector
+// of 8 columns per thread, `vecs` (a multiple of 16) in a row.
+template <typename T, int kParts>
+__global__ __launch_bounds__(256) void mx_split_kernel(const T* x, int64_t ldx, int64_t N, int H, int vecs,
+                                                       uint8_t* parts, int64_t ldp, uint8_t* codes, int64_t ldc) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= N * vecs) return;   // whole groups of 16 lanes
+  const int64_t n = i / vecs;
+  const int kv = (int)(i % vecs);
+  float v[8];
+  u32x2 out[kParts];
+  load8(v, x + n * ldx, kv * 8, H);
+  const uint32_t code = split8<kParts>(v, out);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint32_t half = (uint32_t)(x >> 32 * (q / 2));
-      const bf16x2 b = q & 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(half, s, true)
-                             : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(half, s, false);
-      out[0][q] = __builtin_bit_cast(uint32_t, b);
-    }
+  for (int p = 0; p < kParts; ++p) *reinterpret_cast<u32x2*>(parts + (p * N + n) * ldp + kv * 8) = out[p];
+  if (kv % 4 == 0) codes[n * ldc + kv / 4] = (uint8_t)code;
+}
+
+// Rows in 8 bits, padded to whole steps.
+__global__ __launch_bounds__(256) void mx_copy_kernel(const uint8_t* x, int64_t ldx, const uint8_t* xs, int64_t ldxs,
+                                                      int64_t N, int H, int vecs, uint8_t* parts, int64_t ldp,
+                                                      uint8_t* codes, int64_t ldc) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= N * vecs) return;
+  const int64_t n = i / vecs;
+  const int k = (int)(i % vecs) * 8;
+  u32x2 v = {0, 0};
+  if (k + 8 <= H) {
+    typedef uint32_t mem __attribute__((ext_vector_type(2), aligned(1)));
+    const mem m = *reinterpret_cast<const mem*>(x + n * ldx + k);
+    v = u32x2{m[0], m[1]};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (k + e < H) v[e / 4] |= (uint32_t)x[n * ldx + k + e] << 8 * (e % 4);
   }
-};
+  *reinterpret_cast<u32x2*>(parts + n * ldp + k) = v;
+  if (k % kMxBlock == 0) codes[n * ldc + k / kMxBlock] = k < H ? xs[n * ldxs + k / kMxBlock] : 127;
+}
 
 template <typename T>
 __device__ __forceinline__ void store_logits(T* p, int64_t left, const float (&v)[4]) {
@@ -171,14 +229,16 @@ __device__ __forceinline__ void put_logits(const MxArgs& p, int64_t n0, int64_t 
 }
 
 // A wave's weights on their way through its registers: kRt tiles of 16 rows,
-// a chunk of four steps.  A row's scales come four steps (16 bytes) at a time:
-// byte by byte the loads take longer than those of the codes (153 against 110
-// us for 202048 rows of 6656).
-template <int kRt>
+// four steps of codes.  A row's scales come four steps (16 bytes) at a time:
+// byte by byte their loads take longer than those of the codes (153 against 110
+// us for 202048 rows of 6656; 125 like this).  No load stands behind a branch:
+// the wait for it would be one for all.  kShort: rows of less than four steps.
+template <int kRt, bool kShort>
 struct WeightStream {
   const uint8_t *wp[kRt], *sp[kRt];
-  u32x4 w[4][kRt], sc[kRt], sc_next[kRt];
-  int steps, shift;
+  u32x4 w[4][kRt], next[kRt];
+  uint32_t scale[kRt];   // a byte per step
+  int steps;
 
   __device__ __forceinline__ void start(const MxArgs& p, int64_t v0) {
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
@@ -189,257 +249,329 @@ struct WeightStream {
       wp[i] = p.w + at * p.steps * 64 + g * 16;
       sp[i] = p.ws + at * p.steps * 4;
     }
+    load_scales(0);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) load(s, s);
   }
   __device__ __forceinline__ void load(int s, int step) {
     const int at = step < steps ? step : steps - 1;
 #pragma unroll
     for (int i = 0; i < kRt; ++i) w[s][i] = *reinterpret_cast<const u32x4*>(wp[i] + at * 64);
   }
-  // the scales of steps c to c + 3; the last 16 bytes of the row where it ends
-  // before (rows of four steps or more)
+  // the scales of steps c to c + 3; the row's last 16 bytes where it ends before
   __device__ __forceinline__ void load_scales(int c) {
     typedef uint32_t mem __attribute__((ext_vector_type(4), aligned(4)));
     const int at = c + 4 <= steps ? c : steps - 4;
 #pragma unroll
     for (int i = 0; i < kRt; ++i) {
-      const mem m = *reinterpret_cast<const mem*>(sp[i] + at * 4);
-      sc_next[i] = u32x4{m[0], m[1], m[2], m[3]};
+      if constexpr (kShort) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          next[i][s] = *reinterpret_cast<const uint32_t*>(sp[i] + (s < steps ? s : steps - 1) * 4);
+      } else {
+        const mem m = *reinterpret_cast<const mem*>(sp[i] + at * 4);
+        next[i] = u32x4{m[0], m[1], m[2], m[3]};
+      }
     }
   }
   __device__ __forceinline__ void take_scales(int c) {
-    const int d = c + 4 <= steps ? 0 : c + 4 - steps;   // the same for every lane
+    const int d = kShort || c + 4 <= steps ? 0 : c + 4 - steps;   // the same for every lane
 #pragma unroll
     for (int i = 0; i < kRt; ++i) {
-      u32x4 x = sc_next[i];
+      u32x4 x = next[i];
       if (d & 2) x = u32x4{x[2], x[3], 0, 0};
       if (d & 1) x = u32x4{x[1], x[2], x[3], 0};
-      sc[i] = x;
+      scale[i] = own_scales(x);
     }
-  }
-  // eight columns of step s as bf16: dword j of the block
-  __device__ __forceinline__ float scale(int s, int i) const {
-    const int g = (threadIdx.x & 63) >> 4;
-    return __builtin_bit_cast(float, (sc[i][s] >> 8 * g & 255u) << 23);
   }
 };
 
-constexpr int kMaxResident = 80 * 1024;   // bytes of LDS for the tokens' rows: two work-groups on a compute unit
-
-// A token's row in LDS: its columns in order, padded by 16 bytes so that the
-// 16 rows a wave reads at a time start in different banks.
-__host__ __device__ constexpr int row_bytes(int columns) { return columns * 2 + 16; }
-
-// Up to 16 tokens whose rows stay in LDS as a whole: they are brought there
-// once, and then the weights stream through without a barrier.
-template <XKind kX, int kRt>
-__global__ __launch_bounds__(512) void mx_logits_resident_kernel(MxArgs p) {
-  constexpr int kParts = kX == kXF32 ? 3 : 1;
-  extern __shared__ __align__(16) uint8_t rows[];   // [parts][N][row]
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-  const int64_t v0 = ((int64_t)blockIdx.x * 8 + wave) * (16 * kRt);
-  WeightStream<kRt> ws;
-  ws.start(p, v0);
-#pragma unroll
-  for (int s = 0; s < 4; ++s) ws.load(s, s);
-  ws.load_scales(0);
-  const int stride = row_bytes(p.steps * kStep), vecs = p.steps * 16;
-  const int part = (int)p.N * stride;
-  for (int n = 0; n < p.N; ++n)
-    for (int kv = threadIdx.x; kv < vecs; kv += 512) {
-      XVec<kX> x;
-      u32x4 parts[kParts];
-      x.load(p, n, kv * 8);
-      x.parts(parts, kv * 8, p.H);
-#pragma unroll
-      for (int q = 0; q < kParts; ++q) *reinterpret_cast<u32x4*>(rows + q * part + n * stride + kv * 16) = parts[q];
-    }
-  __syncthreads();
-  ws.take_scales(0);
-  const uint8_t* mine = rows + (r < p.N ? r : p.N - 1) * stride + g * 64;
-  f32x4 acc[kRt][1];
-#pragma unroll
-  for (int i = 0; i < kRt; ++i) acc[i][0] = f32x4{0, 0, 0, 0};
-  for (int c = 0; c < p.steps; c += 4) {
-    ws.load_scales(c + 4);
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      if (c + s < p.steps) {
-        float sc[kRt];
-#pragma unroll
-        for (int i = 0; i < kRt; ++i) sc[i] = ws.scale(s, i);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          bf16x8v b[kParts];
-#pragma unroll
-          for (int q = 0; q < kParts; ++q)
-            b[q] = *reinterpret_cast<const bf16x8v*>(mine + q * part + (c + s) * 256 + j * 16);
-#pragma unroll
-          for (int i = 0; i < kRt; ++i) {
-            const bf16x8v a = weights8(ws.w[s][i][j], sc[i]);
-#pragma unroll
-            for (int q = 0; q < kParts; ++q)
-              acc[i][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[q], acc[i][0], 0, 0, 0);
-          }
-        }
-      }
-      ws.load(s, c + 4 + s);
-    }
-    ws.take_scales(c + 4);
-  }
-  put_logits<kRt, 1>(p, 0, v0, acc);
+__device__ __forceinline__ i32x8v token_columns(const uint8_t* p) {
+  const i32x4v a = *reinterpret_cast<const i32x4v*>(p), b = *reinterpret_cast<const i32x4v*>(p + 64);
+  return i32x8v{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
 
-// Any number of tokens, kNt tiles of 16 a work-group: their rows pass through
-// LDS in chunks of kSt steps, double buffered, one barrier a chunk.
-template <XKind kX, int kRt, int kNt, int kSt>
+// Bytes of a row of codes: whole groups of four steps.
+__host__ __device__ constexpr int code_bytes(int steps) { return (steps + 3) / 4 * 16; }
+
+// A token's part in LDS: its columns in order, padded by 16 bytes so that the
+// 16 rows that a wave reads at a time start in different banks.
+__host__ __device__ constexpr int part_bytes(int steps) { return steps * kStep + 16; }
+
+// A wave's ring of weights in LDS: kG groups of four steps (16 rows of 256
+// bytes), each with its scales (16 rows of 16 bytes).
+constexpr int kGroupBytes = 4096 + 256;
+__host__ __device__ constexpr int ring_bytes(int groups) { return groups * kGroupBytes; }
+
+constexpr int kLdsMost = 160 * 1024;
+
+// Up to 16 tokens that stay in LDS as a whole, brought there once; then the
+// weights stream through every wave's own ring without a barrier, tile after
+// tile of 16 rows (tile blockIdx.x + gridDim.x (wave + waves i)).
+//
+// The loads go straight to LDS, 16 lanes to 256 bytes of a row, four rows a
+// load: straight to the lanes that need them (a lane a row, 64 different lines
+// a load) the address units take as long as the memory.  Piece k (16 bytes) of
+// row r lands at k ^ r, so that the 16 rows that a wave reads at a time lie in
+// different banks.  Loads return in order: a group is there when no more than
+// the groups behind it are under way.
+template <int kParts, int kG, bool kInline>
+__global__ __launch_bounds__(1024) void mx_logits_stream_kernel(MxArgs p, int tiles) {
+  extern __shared__ __align__(16) uint8_t lds[];   // parts [kParts][N][part_bytes], codes [N][code_bytes], rings
+  const int threads = blockDim.x, lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = threads >> 6;
+  const int N = (int)p.N, row = part_bytes(p.steps), part = N * row, crow = code_bytes(p.steps);
+  uint8_t* codes = lds + kParts * part;
+  uint8_t* ring = codes + N * crow + wave * ring_bytes(kG);
+  const uint32_t ring_at = lds_address(ring);
+
+  // where the next group's loads come from
+  const int w_row = p.steps * 64, s_row = p.steps * 4;
+  const uint32_t s_off = (uint32_t)((lane >> 2) * s_row + (lane & 3) * 4);
+  int tile_in = blockIdx.x + gridDim.x * wave, c_in = 0, slot_in = 0;
+  const int tile_step = gridDim.x * waves;
+  u32x4s from_w, from_s;
+  auto set_tile = [&]() {
+    const int64_t v = (int64_t)tile_in * 16;
+    const int64_t rows = tile_in < tiles ? (p.V - v < 16 ? p.V - v : 16) : 0;
+    from_w = buffer_of(p.w + (rows ? v : 0) * w_row, rows * w_row);
+    from_s = buffer_of(p.ws + (rows ? v : 0) * s_row, rows * s_row);
+  };
+  auto load_group = [&]() {   // (of what lies past the row's end the scales are not used, the codes not read)
+    const uint32_t to = ring_at + slot_in * kGroupBytes;
+    dma4(from_s, to + 4096, s_off + c_in * 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 4 * i + (lane >> 4), piece = (lane & 15) ^ row;
+      dma16(from_w, to + i * 1024, c_in + (piece >> 2) < p.steps ? row * w_row + c_in * 64 + piece * 16 : kPastBuffer);
+    }
+    if (++slot_in == kG) slot_in = 0;
+    c_in += 4;
+    if (c_in >= p.steps) {
+      c_in = 0;
+      tile_in += tile_step;
+      set_tile();
+    }
+  };
+  set_tile();
+#pragma unroll
+  for (int i = 0; i < kG; ++i) load_group();
+
+  if constexpr (kInline) {
+    const int vecs = p.steps * 16;
+    for (int n = 0; n < N; ++n)
+      for (int kv = threadIdx.x; kv < vecs; kv += threads) {   // groups of four lanes leave together
+        float v[8];
+        u32x2 out[kParts];
+        load8(v, static_cast<const bf16*>(p.x) + n * p.ldx, kv * 8, p.H);
+        const uint32_t code = split8<kParts>(v, out);
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) *reinterpret_cast<u32x2*>(lds + q * part + n * row + kv * 8) = out[q];
+        if (kv % 4 == 0) codes[n * crow + kv / 4] = (uint8_t)code;
+      }
+  } else {
+    const uint8_t* x = static_cast<const uint8_t*>(p.x);
+    const int vecs = p.steps * 8;
+    for (int n = 0; n < kParts * N; ++n)
+      for (int kv = threadIdx.x; kv < vecs; kv += threads)
+        *reinterpret_cast<u32x4*>(lds + n * row + kv * 16) = *reinterpret_cast<const u32x4*>(x + n * p.ldx + kv * 16);
+    for (int i = threadIdx.x; i < N * p.steps; i += threads) {
+      const int n = i / p.steps, s = i % p.steps;
+      *reinterpret_cast<uint32_t*>(codes + n * crow + s * 4) = *reinterpret_cast<const uint32_t*>(p.xs + n * p.ldxs + s * 4);
+    }
+  }
+  __syncthreads();
+
+  const int n = r < N ? r : N - 1;
+  const uint8_t* mine = lds + n * row + g * 16;
+  const uint8_t* my_codes = codes + n * crow;
+  int slot = 0;
+  for (int tile = blockIdx.x + gridDim.x * wave; tile < tiles; tile += tile_step) {
+    f32x4 acc[1][1] = {{{0, 0, 0, 0}}};
+    for (int c = 0; c < p.steps; c += 4) {
+      wait_loads<5 * (kG - 1)>();
+      const uint8_t* from = ring + slot * kGroupBytes;
+      const uint32_t scale = own_scales(*reinterpret_cast<const u32x4*>(from + 4096 + r * 16));
+      const uint32_t xc = own_scales(*reinterpret_cast<const u32x4*>(my_codes + c * 4));
+      u32x4 a[4];
+#pragma unroll
+      for (int s = 0; s < 4; ++s) a[s] = *reinterpret_cast<const u32x4*>(from + r * 256 + (((s * 4 + g) ^ r) * 16));
+      wait_lds();   // what was read is in registers: its place may be loaded again
+      load_group();
+      if (++slot == kG) slot = 0;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        if (c + s < p.steps) {
+#pragma unroll
+          for (int q = 0; q < kParts; ++q)
+            mx_mma(s, acc[0][0], a[s], token_columns(mine + q * part + (c + s) * kStep), scale, xc - q * 0x04040404u);
+        }
+      }
+    }
+    put_logits<1, 1>(p, 0, (int64_t)tile * 16, acc);
+  }
+  wait_loads<0>();   // nothing may land in LDS that is no longer this work-group's
+}
+
+// Any number of tokens, kNt tiles of 16 a work-group of four waves: their parts
+// pass through LDS in chunks of kSt steps, double buffered, one barrier a chunk.
+template <int kParts, int kRt, int kNt, int kSt, bool kShort>
 __global__ __launch_bounds__(kThreads) void mx_logits_kernel(MxArgs p) {
-  constexpr int kParts = kX == kXF32 ? 3 : 1;
-  constexpr int kVecs = kSt * 16;                            // vectors of 8 columns in a chunk
-  constexpr int kItems = kNt * 16 * kVecs / kThreads;        // of them, per thread
-  constexpr int kStride = row_bytes(kSt * kStep);
-  __shared__ __align__(16) uint8_t rows[2][kParts][kNt * 16][kStride];
+  constexpr int kVecs = kSt * 8;                                    // vectors of 16 columns in a chunk
+  constexpr int kItems = kParts * kNt * 16 * kVecs / kThreads;      // of them, per thread
+  constexpr int kRow = part_bytes(kSt);
+  static_assert(kItems >= 1 && kItems * kThreads == kParts * kNt * 16 * kVecs, "the threads share the vectors evenly");
+  __shared__ __align__(16) uint8_t lds[2][kParts][kNt * 16][kRow];
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6, r = lane & 15, g = lane >> 4;
   const int64_t n0 = (int64_t)blockIdx.y * (16 * kNt);
   const int64_t v0 = ((int64_t)blockIdx.x * 4 + wave) * (16 * kRt);
-  WeightStream<kRt> ws;
-  ws.start(p, v0);
-  XVec<kX> xv[kItems];
-  auto load_x = [&](int step0) {
+  WeightStream<kRt, kShort> ws;
+  const uint8_t* from[kItems];
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    const int idx = t + i * kThreads, q = idx / (kVecs * kNt * 16);
+    const int64_t n = n0 + idx / kVecs % (kNt * 16), at = n < p.N ? n : p.N - 1;
+    from[i] = static_cast<const uint8_t*>(p.x) + (q * p.N + at) * p.ldx;
+  }
+  u32x4 xv[kItems];
+  auto load_x = [&](int step) {
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
-      const int idx = t + i * kThreads;
-      const int64_t n = n0 + idx / kVecs;
-      xv[i].load(p, n < p.N ? n : p.N - 1, step0 * kStep + idx % kVecs * 8);
+      const int kv = (t + i * kThreads) % kVecs;
+      const int at = step + kv / 8 < p.steps ? step + kv / 8 : p.steps - 1;   // (not used past the last step)
+      xv[i] = *reinterpret_cast<const u32x4*>(from[i] + at * kStep + kv % 8 * 16);
     }
   };
-  auto stage_x = [&](int buf, int step0) {
+  auto stage_x = [&](int buf) {
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
       const int idx = t + i * kThreads;
-      u32x4 parts[kParts];
-      xv[i].parts(parts, step0 * kStep + idx % kVecs * 8, p.H);
-#pragma unroll
-      for (int q = 0; q < kParts; ++q)
-        *reinterpret_cast<u32x4*>(&rows[buf][q][idx / kVecs][idx % kVecs * 16]) = parts[q];
+      *reinterpret_cast<u32x4*>(&lds[buf][idx / (kVecs * kNt * 16)][idx / kVecs % (kNt * 16)][idx % kVecs * 16]) = xv[i];
     }
+  };
+  const uint8_t* codes[kNt];
+#pragma unroll
+  for (int n = 0; n < kNt; ++n) {
+    const int64_t tok = n0 + n * 16 + r;
+    codes[n] = p.xs + (tok < p.N ? tok : p.N - 1) * p.ldxs;
+  }
+  u32x4 cnext[kNt];
+  auto load_codes = [&](int c) {
+    const int at = c < p.steps ? c : 0;
+#pragma unroll
+    for (int n = 0; n < kNt; ++n) cnext[n] = *reinterpret_cast<const u32x4*>(codes[n] + at * 4);
   };
   load_x(0);
-#pragma unroll
-  for (int s = 0; s < 4; ++s) ws.load(s, s);
-  ws.load_scales(0);
-  stage_x(0, 0);
+  load_codes(0);
+  ws.start(p, v0);
+  stage_x(0);
   f32x4 acc[kRt][kNt];
 #pragma unroll
   for (int i = 0; i < kRt; ++i)
 #pragma unroll
     for (int j = 0; j < kNt; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-  ws.take_scales(0);
   __syncthreads();
   int buf = 0;
   for (int c = 0; c < p.steps; c += 4) {
+    ws.take_scales(c);
     ws.load_scales(c + 4);
+    uint32_t xc[kNt];
+#pragma unroll
+    for (int n = 0; n < kNt; ++n) xc[n] = own_scales(cnext[n]);
+    load_codes(c + 4);
 #pragma unroll
     for (int h = 0; h < 4; h += kSt, buf ^= 1) {
       load_x(c + h + kSt);
 #pragma unroll
       for (int s = h; s < h + kSt; ++s) {
         if (c + s < p.steps) {
-          float sc[kRt];
 #pragma unroll
-          for (int i = 0; i < kRt; ++i) sc[i] = ws.scale(s, i);
+          for (int q = 0; q < kParts; ++q)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            bf16x8v a[kRt];
+            for (int n = 0; n < kNt; ++n) {
+              const i32x8v b = token_columns(&lds[buf][q][n * 16 + r][(s - h) * kStep + g * 16]);
 #pragma unroll
-            for (int i = 0; i < kRt; ++i) a[i] = weights8(ws.w[s][i][j], sc[i]);
-#pragma unroll
-            for (int q = 0; q < kParts; ++q)
-#pragma unroll
-              for (int n = 0; n < kNt; ++n) {
-                const bf16x8v b = *reinterpret_cast<const bf16x8v*>(&rows[buf][q][n * 16 + r][(s - h) * 256 + g * 64 + j * 16]);
-#pragma unroll
-                for (int i = 0; i < kRt; ++i)
-                  acc[i][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b, acc[i][n], 0, 0, 0);
-              }
-          }
+              for (int i = 0; i < kRt; ++i) mx_mma(s, acc[i][n], ws.w[s][i], b, ws.scale[i], xc[n] - q * 0x04040404u);
+            }
         }
         ws.load(s, c + 4 + s);
       }
-      stage_x(buf ^ 1, c + h + kSt);
+      stage_x(buf ^ 1);
       __syncthreads();
     }
-    ws.take_scales(c + 4);
   }
   put_logits<kRt, kNt>(p, n0, v0, acc);
 }
 
-// A row of fewer than 8 elements, as parts.
-template <XKind kX, int kParts>
-__device__ __forceinline__ void load_few(const MxArgs& p, int64_t n, int k, u32x4 (&out)[kParts]) {
-  float x[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    x[e] = 0.0f;
-    if (k + e >= p.H) continue;
-    const int64_t at = n * p.ldx + k + e;
-    if (kX == kXBf16) x[e] = to_f32(static_cast<const bf16*>(p.x)[at]);
-    else if (kX == kXF32) x[e] = static_cast<const float*>(p.x)[at];
-    else x[e] = __builtin_amdgcn_cvt_f32_fp8(static_cast<const uint8_t*>(p.x)[at], 0) * mx_scale(p.xs[n * p.ldxs]);
-  }
-  cut_parts(x, out);
+// LDS of the streaming kernel beside its rings.
+int64_t stream_tokens(int64_t N, int64_t steps, int parts) {
+  return N * (parts * part_bytes((int)steps) + code_bytes((int)steps));
 }
 
-// Rows of less than four steps: nothing to stream.  A wave has 16 vocabulary
-// entries and 16 tokens and reads both from memory.
-template <XKind kX>
-__global__ __launch_bounds__(kThreads) void mx_logits_short_kernel(MxArgs p) {
-  constexpr int kParts = kX == kXF32 ? 3 : 1;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-  const int64_t v0 = ((int64_t)blockIdx.x * 4 + wave) * 16, n0 = (int64_t)blockIdx.y * 16;
-  const int64_t v = v0 + r < p.V ? v0 + r : p.V - 1, n = n0 + r < p.N ? n0 + r : p.N - 1;
-  f32x4 acc[1][1] = {{{0, 0, 0, 0}}};
-  for (int s = 0; s < p.steps; ++s) {
-    const u32x4 w = *reinterpret_cast<const u32x4*>(p.w + (v * p.steps + s) * 64 + g * 16);
-    const float scale = __builtin_bit_cast(float, (uint32_t)p.ws[(v * p.steps + s) * 4 + g] << 23);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int k = s * kStep + g * 32 + j * 8;
-      XVec<kX> x;
-      u32x4 parts[kParts];
-      if (p.H >= 8) {
-        x.load(p, n, k);
-        x.parts(parts, k, p.H);
-      } else {
-        load_few<kX>(p, n, k, parts);
-      }
-      const bf16x8v a = weights8(w[j], scale);
-#pragma unroll
-      for (int q = 0; q < kParts; ++q)
-        acc[0][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8v, parts[q]), acc[0][0], 0, 0, 0);
-    }
-  }
-  put_logits<1, 1>(p, n0, v0, acc);
+// One work-group on each of the 256 compute units; waves so that every one has
+// about as many tiles as the others.
+template <int kParts, int kG, bool kInline>
+void launch_stream(const MxArgs& p, int most, hipStream_t st) {
+  const int64_t tiles = ceil_div(p.V, 16), rounds = ceil_div(tiles, 256 * most);
+  int waves = (int)ceil_div(tiles, 256 * rounds);
+  if (waves < 4) waves = 4;   // they also bring the tokens to LDS
+  const int64_t bytes = stream_tokens(p.N, p.steps, kParts) + waves * ring_bytes(kG);
+  mx_logits_stream_kernel<kParts, kG, kInline><<<(unsigned)(tiles < 256 ? tiles : 256), waves * 64, (size_t)bytes, st>>>(
+      p, (int)tiles);
 }
 
-template <XKind kX>
-void launch_logits(const MxArgs& p, hipStream_t st) {
-  constexpr int kParts = kX == kXF32 ? 3 : 1;
+template <int kParts>
+void launch_products(const MxArgs& p, bool raw, hipStream_t st) {
   auto grid = [&](int rows, int tokens) {
     return dim3((unsigned)ceil_div(p.V, rows), (unsigned)ceil_div(p.N, tokens));
   };
-  if (p.steps < 4) {
-    mx_logits_short_kernel<kX><<<grid(64, 16), kThreads, 0, st>>>(p);
-    return;
+  const int64_t left = kLdsMost - stream_tokens(p.N, p.steps, kParts);
+  if (p.N <= 16 && left >= 4 * ring_bytes(1)) {
+    int most = (int)(left / ring_bytes(1));
+    if (most > 12) most = 12;
+    if constexpr (kParts == 2) {
+      if (raw) {
+        launch_stream<2, 1, true>(p, most, st);
+        return;
+      }
+    }
+    launch_stream<kParts, 1, false>(p, most, st);
+  } else if (p.steps < 4) {
+    mx_logits_kernel<kParts, 2, 2, 1, true><<<grid(128, 32), kThreads, 0, st>>>(p);
+  } else if (p.N <= 16) {
+    mx_logits_kernel<kParts, 2, 1, 2, false><<<grid(128, 16), kThreads, 0, st>>>(p);
+  } else {
+    if constexpr (kParts <= 2) {
+      if (p.N > 32) {
+        mx_logits_kernel<kParts, 4, 4, 1, false><<<grid(256, 64), kThreads, 0, st>>>(p);
+        return;
+      }
+    }
+    mx_logits_kernel<kParts, 2, 2, 1, false><<<grid(128, 32), kThreads, 0, st>>>(p);
   }
-  const int64_t resident = p.N * kParts * row_bytes(p.steps * kStep);
-  if (p.N <= 16 && resident <= kMaxResident)
-    mx_logits_resident_kernel<kX, 2><<<grid(256, 16), 512, (size_t)resident, st>>>(p);
-  else if (p.N <= 16)
-    mx_logits_kernel<kX, 2, 1, 2><<<grid(128, 16), kThreads, 0, st>>>(p);
-  else if (p.N <= 32)
-    mx_logits_kernel<kX, 2, 2, 2><<<grid(128, 32), kThreads, 0, st>>>(p);
-  else
-    mx_logits_kernel<kX, 2, 4, 1><<<grid(128, 64), kThreads, 0, st>>>(p);
+}
+
+// Tokens in parts: how many, and how they lie in the workspace.
+struct MxTokens {
+  int parts;
+  size_t codes, total;   // byte offsets in the workspace (parts at 0)
+  int64_t ldp, ldc;
+};
+
+MxTokens mx_tokens(int64_t N, int64_t H, int x_dtype) {
+  MxTokens t{};
+  const int64_t steps = ceil_div(H, kStep);
+  t.parts = x_dtype == FLCE_DTYPE_MX8 ? 1 : x_dtype == FLCE_DTYPE_BF16 ? 2 : 6;
+  t.ldp = steps * kStep;
+  t.ldc = code_bytes((int)steps);
+  t.codes = (size_t)(t.parts * N * t.ldp);
+  t.total = (t.codes + (size_t)(N * t.ldc) + 255) & ~size_t(255);
+  if (t.total < 256) t.total = 256;
+  return t;
+}
+
+bool mx_sizes_ok(int64_t N, int64_t H, int x_dtype) {
+  return (x_dtype == FLCE_DTYPE_BF16 || x_dtype == FLCE_DTYPE_F32 || x_dtype == FLCE_DTYPE_MX8) && N >= 0 && H >= 1;
 }
 
 // Nearest E2M1 code, ties to the even one.
@@ -491,7 +623,9 @@ extern "C" int flce_pack_mx(const void* W, int64_t ld_w, int64_t V, int64_t H, v
   const int64_t vecs = ceil_div(H, kStep) * (kStep / 8), total = V * vecs;
   if (total > (int64_t(1) << 31)) return FLCE_EUNSUPPORTED;   // a launch holds fewer than 2^32 threads
   if (V == 0) return FLCE_OK;
-  if (!W || !packed || !scales || addr(W) % (dtype == FLCE_DTYPE_BF16 ? 2 : 4) || addr(packed) % 16) return FLCE_EINVAL;
+  if (!W || !packed || !scales || addr(W) % (dtype == FLCE_DTYPE_BF16 ? 2 : 4) || addr(packed) % 16 ||
+      addr(scales) % 4)
+    return FLCE_EINVAL;
   if (ld_w < 0) return FLCE_EINVAL;
   ProfileScope ps(FLCE_KERNEL_PACK_MX, stream);
   const unsigned g = (unsigned)ceil_div(total, 256);
@@ -504,28 +638,64 @@ extern "C" int flce_pack_mx(const void* W, int64_t ld_w, int64_t V, int64_t H, v
   return hipGetLastError() == hipSuccess ? FLCE_OK : FLCE_EDEVICE;
 }
 
+extern "C" size_t flce_logits_mx_workspace_size(int64_t N, int64_t H, int x_dtype) {
+  using namespace flce;
+  if (!mx_sizes_ok(N, H, x_dtype) || N > (int64_t(1) << 20) || H > (int64_t(1) << 21)) return 0;
+  return mx_tokens(N, H, x_dtype).total;
+}
+
 extern "C" int flce_logits_mx(const void* x, int64_t ld_x, const void* x_scales, int64_t ld_xs, const void* packed,
                               const void* scales, int64_t N, int64_t H, int64_t V, float softcap_T, float multiplier,
-                              void* logits, int64_t ld_logits, hipStream_t stream, int x_dtype, int dtype) {
+                              void* logits, int64_t ld_logits, hipStream_t stream, int x_dtype, int dtype,
+                              void* workspace, size_t workspace_bytes) {
   using namespace flce;
-  if (x_dtype != FLCE_DTYPE_BF16 && x_dtype != FLCE_DTYPE_F32 && x_dtype != FLCE_DTYPE_MX8) return FLCE_EINVAL;
-  if ((dtype != FLCE_DTYPE_BF16 && dtype != FLCE_DTYPE_F32) || N < 0 || H < 1 || V < 1) return FLCE_EINVAL;
+  if (!mx_sizes_ok(N, H, x_dtype) || (dtype != FLCE_DTYPE_BF16 && dtype != FLCE_DTYPE_F32) || V < 1) return FLCE_EINVAL;
   if (!std::isfinite(softcap_T) || !std::isfinite(multiplier)) return FLCE_EINVAL;
   if (softcap_T > 0.0f && (!std::isfinite(1.0f / softcap_T) || !std::isfinite(multiplier / softcap_T)))
     return FLCE_EINVAL;
   if (N > (int64_t(1) << 20) || V > (int64_t(1) << 24) || H > (int64_t(1) << 21)) return FLCE_EUNSUPPORTED;
+  const int64_t steps = ceil_div(H, kStep), vecs = steps * 16;
+  if (N * vecs > (int64_t(1) << 31)) return FLCE_EUNSUPPORTED;   // a launch holds fewer than 2^32 threads
   if (N == 0) return FLCE_OK;
   const bool mx8 = x_dtype == FLCE_DTYPE_MX8;
   const uintptr_t es = mx8 ? 1 : x_dtype == FLCE_DTYPE_BF16 ? 2 : 4, os = dtype == FLCE_DTYPE_BF16 ? 2 : 4;
-  if (!x || !packed || !scales || !logits || (mx8 != (x_scales != nullptr))) return FLCE_EINVAL;
-  if (addr(x) % es || addr(packed) % 16 || addr(logits) % os) return FLCE_EINVAL;
+  if (!x || !packed || !scales || !logits || !workspace || (mx8 != (x_scales != nullptr))) return FLCE_EINVAL;
+  if (addr(x) % es || addr(packed) % 16 || addr(scales) % 4 || addr(logits) % os || addr(workspace) % 256)
+    return FLCE_EINVAL;
   if (ld_x < 0 || (mx8 && ld_xs < 0) || (N > 1 && ld_logits < V)) return FLCE_EINVAL;
-  MxArgs p{x, static_cast<const uint8_t*>(x_scales), static_cast<const uint8_t*>(packed),
-           static_cast<const uint8_t*>(scales), logits, ld_x, ld_xs, ld_logits, N, V, (int)H,
-           (int)ceil_div(H, kStep), softcap_T > 0.0f ? softcap_T : 0.0f, multiplier, dtype == FLCE_DTYPE_BF16};
+  const MxTokens t = mx_tokens(N, H, x_dtype);
+  if (workspace_bytes < t.total) return FLCE_EWORKSPACE;
+  uint8_t* parts = static_cast<uint8_t*>(workspace);
+  uint8_t* codes = parts + t.codes;
+  // rows in 8 bits that are whole groups of four steps are read where they are;
+  // one or two bf16 rows are split by the work-groups (a launch less)
+  const bool ready = mx8 && H % (4 * kStep) == 0 && ld_x % 16 == 0 && addr(x) % 16 == 0 && ld_xs % 16 == 0 &&
+                     addr(x_scales) % 16 == 0;
+  const bool raw = x_dtype == FLCE_DTYPE_BF16 && N <= 2 && stream_tokens(N, steps, 2) <= kLdsMost - 4 * ring_bytes(1);
+  MxArgs p{parts, codes, t.ldp, t.ldc, static_cast<const uint8_t*>(packed), static_cast<const uint8_t*>(scales), logits,
+           ld_logits, N, V, (int)H, (int)steps, softcap_T > 0.0f ? softcap_T : 0.0f, multiplier,
+           dtype == FLCE_DTYPE_BF16};
+  if (ready || raw) {
+    p.x = x;
+    p.xs = static_cast<const uint8_t*>(x_scales);
+    p.ldx = ld_x;
+    p.ldxs = ld_xs;
+  } else {
+    ProfileScope ps(FLCE_KERNEL_SPLIT_MX, stream);
+    const unsigned g = (unsigned)ceil_div(N * vecs, 256);
+    if (mx8)
+      mx_copy_kernel<<<g, 256, 0, stream>>>(static_cast<const uint8_t*>(x), ld_x, static_cast<const uint8_t*>(x_scales),
+                                            ld_xs, N, (int)H, (int)vecs, parts, t.ldp, codes, t.ldc);
+    else if (x_dtype == FLCE_DTYPE_BF16)
+      mx_split_kernel<bf16, 2><<<g, 256, 0, stream>>>(static_cast<const bf16*>(x), ld_x, N, (int)H, (int)vecs, parts,
+                                                      t.ldp, codes, t.ldc);
+    else
+      mx_split_kernel<float, 6><<<g, 256, 0, stream>>>(static_cast<const float*>(x), ld_x, N, (int)H, (int)vecs, parts,
+                                                       t.ldp, codes, t.ldc);
+  }
   ProfileScope ps(FLCE_KERNEL_LOGITS_MX, stream);
-  if (mx8) launch_logits<kXMx8>(p, stream);
-  else if (x_dtype == FLCE_DTYPE_BF16) launch_logits<kXBf16>(p, stream);
-  else launch_logits<kXF32>(p, stream);
+  if (mx8) launch_products<1>(p, false, stream);
+  else if (x_dtype == FLCE_DTYPE_BF16) launch_products<2>(p, raw, stream);
+  else launch_products<6>(p, false, stream);
   return hipGetLastError() == hipSuccess ? FLCE_OK : FLCE_EDEVICE;
 }

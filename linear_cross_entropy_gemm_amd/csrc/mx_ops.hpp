@@ -41,11 +41,6 @@ __device__ __forceinline__ float mx_inverse(uint32_t code) {
   return __builtin_bit_cast(float, (254u - code) << 23);
 }
 
-// The scale of any code.
-__device__ __forceinline__ float mx_scale(uint32_t code) {
-  return __builtin_bit_cast(float, code == 255 ? 0x7FC00000u : code ? code << 23 : 0x00400000u);
-}
-
 // E elements as E4M3 at [col, col + E) of a row of n bytes (rounded to nearest
 // even; every element of a block without a scale is NaN).
 template <int E>

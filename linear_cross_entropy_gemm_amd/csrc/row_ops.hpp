@@ -45,16 +45,11 @@ __device__ __forceinline__ typename RowVec<T>::type load_row(const T* p, int64_t
 // whole vector at `col`, or the row's last whole one where that would cross or
 // lie past the row's end (rows of at least one vector); row_tail, at the
 // vector's use, moves the elements that belong to it down and clears the rest.
-// (load_clamped_vec: of rows of at least one vector, for it reads nothing else)
-template <typename T>
-__device__ __forceinline__ typename RowVec<T>::type load_clamped_vec(const T* p, int col, int n) {
-  constexpr int E = RowVec<T>::E;
-  return *reinterpret_cast<const typename RowVec<T>::mem*>(p + (col + E <= n ? col : n - E));
-}
 template <typename T>
 __device__ __forceinline__ typename RowVec<T>::type load_clamped(const T* p, int col, int n) {
-  if (n < RowVec<T>::E) return load_row(p, col, n);
-  return load_clamped_vec(p, col, n);
+  constexpr int E = RowVec<T>::E;
+  if (n < E) return load_row(p, col, n);
+  return *reinterpret_cast<const typename RowVec<T>::mem*>(p + (col + E <= n ? col : n - E));
 }
 template <typename T>
 __device__ __forceinline__ void row_tail(typename RowVec<T>::type& v, int col, int n) {

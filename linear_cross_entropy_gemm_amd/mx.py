@@ -10,7 +10,7 @@ from typing import Optional, Union
 import torch
 
 from . import _lib
-from .torch_api import _DTYPES, _enqueue, _ptr
+from .torch_api import _DTYPES, _enqueue, _ptr, _workspace
 
 MX_BLOCK = 32
 MX_STEP = 128   # packed rows are padded to whole steps
@@ -74,12 +74,15 @@ def _check_weight(w: Mx4Weight) -> None:
 
 
 def logits_mx4(x: Union[torch.Tensor, Mx8Rows], weight: Mx4Weight, softcap: Optional[float] = None,
-               multiplier: float = 1.0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+               multiplier: float = 1.0, out: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Materialised logits z = cap(m x W^T) from a projection in 4 bits
     (``flce_logits_mx``), [..., V]; ``x`` [..., H] is bfloat16 or float32 (so
     are the logits), or rows in 8 bits (bfloat16 logits).  ``out``, when given,
     is [N, ld >= V] with unit column stride, bfloat16 or float32.  As with
-    ``logits`` the returned rows may have a stride padded to 16 bytes."""
+    ``logits`` the returned rows may have a stride padded to 16 bytes.  A
+    caller-owned ``workspace`` (uint8, ``flce_logits_mx_workspace_size``) may be
+    reused by ordered calls."""
     mx8 = isinstance(x, Mx8Rows)
     data = x.data if mx8 else x
     if mx8:
@@ -118,10 +121,15 @@ def logits_mx4(x: Union[torch.Tensor, Mx8Rows], weight: Mx4Weight, softcap: Opti
         raise ValueError("out must be [N, ld >= V] with unit column stride")
     if out.dtype not in _DTYPES or out.device != dev:
         raise ValueError(f"out is {out.dtype} on {out.device}, must be bfloat16 or float32 on {dev}")
+    x_dtype = _lib.FLCE_DTYPE_MX8 if mx8 else _DTYPES[data.dtype]
+    ws_bytes = _lib.flce_logits_mx_workspace_size(N, H, x_dtype)
+    if ws_bytes == 0:
+        raise _lib.FlceError(_lib.FLCE_EUNSUPPORTED, "flce_logits_mx_workspace_size")
+    workspace = _workspace(workspace, ws_bytes, dev)
     rc = _enqueue(dev, lambda stream: _lib.flce_logits_mx(
         x2.data_ptr(), x2.stride(0), _ptr(s2), s2.stride(0) if mx8 else 0, weight.data.data_ptr(),
         weight.scales.data_ptr(), N, H, V, float(softcap) if softcap else 0.0, float(multiplier), out.data_ptr(),
-        out.stride(0), stream, _lib.FLCE_DTYPE_MX8 if mx8 else _DTYPES[data.dtype], _DTYPES[out.dtype]))
+        out.stride(0), stream, x_dtype, _DTYPES[out.dtype], workspace.data_ptr(), workspace.numel()))
     if rc != _lib.FLCE_OK:
         raise _lib.FlceError(rc, "flce_logits_mx")
     return out[:, :V].reshape(*data.shape[:-1], V)

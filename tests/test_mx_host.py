@@ -19,7 +19,7 @@ def _pack(**kw):
     (dict(V=(1 << 24) + 1), L.FLCE_EUNSUPPORTED), (dict(H=(1 << 21) + 1), L.FLCE_EUNSUPPORTED),
     (dict(V=1 << 20, H=1 << 16), L.FLCE_EUNSUPPORTED), (dict(W=None), L.FLCE_EINVAL),
     (dict(packed=None), L.FLCE_EINVAL), (dict(scales=None), L.FLCE_EINVAL), (dict(W=17), L.FLCE_EINVAL),
-    (dict(W=18, dtype=1), L.FLCE_EINVAL), (dict(packed=24), L.FLCE_EINVAL), (dict(), L.FLCE_EINVAL),
+    (dict(W=18, dtype=1), L.FLCE_EINVAL), (dict(packed=24), L.FLCE_EINVAL), (dict(scales=18), L.FLCE_EINVAL), (dict(), L.FLCE_EINVAL),
     (dict(V=0, W=None, packed=None, scales=None), L.FLCE_OK),
 ])
 def test_pack_rejects_before_launch(kw, code):
@@ -28,8 +28,8 @@ def test_pack_rejects_before_launch(kw, code):
 
 def _logits(**kw):
     a = dict(x=16, ld_x=8, x_scales=None, ld_xs=0, packed=16, scales=16, N=2, H=8, V=8, softcap_T=0.0, multiplier=1.0,
-             logits=16, ld_logits=7, stream=0, x_dtype=0, dtype=0)
-    a.update(kw)
+             logits=16, ld_logits=8, stream=0, x_dtype=0, dtype=0, workspace=256, workspace_bytes=0)
+    a.update(kw)   # no workspace bytes: refused last
     return L.flce_logits_mx(*a.values())
 
 
@@ -44,11 +44,21 @@ def _logits(**kw):
     (dict(logits=None), L.FLCE_EINVAL), (dict(x_scales=16), L.FLCE_EINVAL), (dict(x_dtype=2), L.FLCE_EINVAL),
     (dict(x=17), L.FLCE_EINVAL), (dict(x=18, x_dtype=1), L.FLCE_EINVAL), (dict(packed=24), L.FLCE_EINVAL),
     (dict(logits=17), L.FLCE_EINVAL), (dict(logits=18, dtype=1), L.FLCE_EINVAL), (dict(ld_x=-1), L.FLCE_EINVAL),
-    (dict(x_dtype=2, x_scales=16, ld_xs=-1), L.FLCE_EINVAL), (dict(), L.FLCE_EINVAL),
+    (dict(x_dtype=2, x_scales=16, ld_xs=-1), L.FLCE_EINVAL), (dict(ld_logits=7), L.FLCE_EINVAL),
+    (dict(scales=18), L.FLCE_EINVAL), (dict(workspace=None), L.FLCE_EINVAL), (dict(workspace=128), L.FLCE_EINVAL),
+    (dict(N=1 << 20, H=1 << 20), L.FLCE_EUNSUPPORTED), (dict(), L.FLCE_EWORKSPACE),
     (dict(N=0, x=None, logits=None), L.FLCE_OK),
 ])
 def test_logits_reject_before_launch(kw, code):
     assert _logits(**kw) == code
+
+
+def test_workspace_size():
+    for N, H, dt in [(1, 1, 0), (320, 4096, 0), (33, 1001, 1), (5, 7168, 2), (0, 8, 0), (1 << 20, 128, 0)]:
+        b = L.flce_logits_mx_workspace_size(N, H, dt)
+        assert b >= 256 and b % 256 == 0 and b >= N * H * (2, 6, 1)[dt]
+    for bad in [(-1, 8, 0), (1, 0, 0), (1, 8, 3), ((1 << 20) + 1, 8, 0), (1, (1 << 21) + 1, 0)]:
+        assert L.flce_logits_mx_workspace_size(*bad) == 0
 
 
 def test_wrappers_refuse_bad_tensors():
