@@ -50,6 +50,9 @@ template <int n>
 __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" : : "n"(n) : "memory");
 }
+// Work-group barrier behind which this wave's LDS accesses are done (its loads
+// to LDS only as far as it waited for them).
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory"); }
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); }
 __device__ __forceinline__ uint32_t lds_address(const uint8_t* p) {
   return (uint32_t)__builtin_amdgcn_readfirstlane(
@@ -57,7 +60,7 @@ __device__ __forceinline__ uint32_t lds_address(const uint8_t* p) {
 }
 
 constexpr int kStep = 128;      // columns of one matrix instruction: four lane groups of one block
-constexpr int kThreads = 256;
+constexpr int64_t kMostRow = int64_t(1) << 21;   // bytes between rows that are read through a buffer's 32-bit offsets
 
 typedef int i32x4v __attribute__((ext_vector_type(4)));
 typedef int i32x8v __attribute__((ext_vector_type(8)));
@@ -228,64 +231,6 @@ __device__ __forceinline__ void put_logits(const MxArgs& p, int64_t n0, int64_t 
   }
 }
 
-// A wave's weights on their way through its registers: kRt tiles of 16 rows,
-// four steps of codes.  A row's scales come four steps (16 bytes) at a time:
-// byte by byte their loads take longer than those of the codes (153 against 110
-// us for 202048 rows of 6656; 125 like this).  No load stands behind a branch:
-// the wait for it would be one for all.  kShort: rows of less than four steps.
-template <int kRt, bool kShort>
-struct WeightStream {
-  const uint8_t *wp[kRt], *sp[kRt];
-  u32x4 w[4][kRt], next[kRt];
-  uint32_t scale[kRt];   // a byte per step
-  int steps;
-
-  __device__ __forceinline__ void start(const MxArgs& p, int64_t v0) {
-    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-    steps = p.steps;
-#pragma unroll
-    for (int i = 0; i < kRt; ++i) {
-      const int64_t v = v0 + i * 16 + r, at = v < p.V ? v : p.V - 1;
-      wp[i] = p.w + at * p.steps * 64 + g * 16;
-      sp[i] = p.ws + at * p.steps * 4;
-    }
-    load_scales(0);
-#pragma unroll
-    for (int s = 0; s < 4; ++s) load(s, s);
-  }
-  __device__ __forceinline__ void load(int s, int step) {
-    const int at = step < steps ? step : steps - 1;
-#pragma unroll
-    for (int i = 0; i < kRt; ++i) w[s][i] = *reinterpret_cast<const u32x4*>(wp[i] + at * 64);
-  }
-  // the scales of steps c to c + 3; the row's last 16 bytes where it ends before
-  __device__ __forceinline__ void load_scales(int c) {
-    typedef uint32_t mem __attribute__((ext_vector_type(4), aligned(4)));
-    const int at = c + 4 <= steps ? c : steps - 4;
-#pragma unroll
-    for (int i = 0; i < kRt; ++i) {
-      if constexpr (kShort) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-          next[i][s] = *reinterpret_cast<const uint32_t*>(sp[i] + (s < steps ? s : steps - 1) * 4);
-      } else {
-        const mem m = *reinterpret_cast<const mem*>(sp[i] + at * 4);
-        next[i] = u32x4{m[0], m[1], m[2], m[3]};
-      }
-    }
-  }
-  __device__ __forceinline__ void take_scales(int c) {
-    const int d = kShort || c + 4 <= steps ? 0 : c + 4 - steps;   // the same for every lane
-#pragma unroll
-    for (int i = 0; i < kRt; ++i) {
-      u32x4 x = next[i];
-      if (d & 2) x = u32x4{x[2], x[3], 0, 0};
-      if (d & 1) x = u32x4{x[1], x[2], x[3], 0};
-      scale[i] = own_scales(x);
-    }
-  }
-};
-
 __device__ __forceinline__ i32x8v token_columns(const uint8_t* p) {
   const i32x4v a = *reinterpret_cast<const i32x4v*>(p), b = *reinterpret_cast<const i32x4v*>(p + 64);
   return i32x8v{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
@@ -413,94 +358,133 @@ __global__ __launch_bounds__(1024) void mx_logits_stream_kernel(MxArgs p, int ti
   wait_loads<0>();   // nothing may land in LDS that is no longer this work-group's
 }
 
-// Any number of tokens, kNt tiles of 16 a work-group of four waves: their parts
-// pass through LDS in chunks of kSt steps, double buffered, one barrier a chunk.
-template <int kParts, int kRt, int kNt, int kSt, bool kShort>
-__global__ __launch_bounds__(kThreads) void mx_logits_kernel(MxArgs p) {
-  constexpr int kVecs = kSt * 8;                                    // vectors of 16 columns in a chunk
-  constexpr int kItems = kParts * kNt * 16 * kVecs / kThreads;      // of them, per thread
-  constexpr int kRow = part_bytes(kSt);
-  static_assert(kItems >= 1 && kItems * kThreads == kParts * kNt * 16 * kVecs, "the threads share the vectors evenly");
-  __shared__ __align__(16) uint8_t lds[2][kParts][kNt * 16][kRow];
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6, r = lane & 15, g = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.y * (16 * kNt);
-  const int64_t v0 = ((int64_t)blockIdx.x * 4 + wave) * (16 * kRt);
-  WeightStream<kRt, kShort> ws;
-  const uint8_t* from[kItems];
+// More tokens: a work-group of kWv x kWt waves has kWv kRt tiles of 16
+// vocabulary entries by kWt kNt tiles of 16 tokens, kRt x kNt a wave.  A stage is
+// one step of both: its weights (rows of 64 bytes) and its tokens' parts (rows of
+// 128 bytes), in a ring of kStages in LDS; the scales of a group of four steps
+// are two groups ahead of each other.  One barrier a step: behind it everyone's
+// loads of the step are there, and the stage before it is free.  A piece of 16
+// bytes lies at its place exclusive-or (row / 4 mod 4) (weights) or (row / 2 mod
+// 8) (tokens): no bank serves two of the 16 rows that a wave reads at a time.
+// Loads that do not divide evenly among the waves are done twice, alike.
+template <int kParts, int kWv, int kWt, int kRt, int kNt, int kStages>
+struct TileShape {
+  static constexpr int waves = kWv * kWt, rows = kWv * kRt * 16, tokens = kWt * kNt * 16;
+  static constexpr int w_loads = rows / 16, x_loads = kParts * tokens / 8, s_loads = (rows + tokens) / 16;
+  static constexpr int w_each = (w_loads + waves - 1) / waves, x_each = (x_loads + waves - 1) / waves;
+  static constexpr int s_each = (s_loads + waves - 1) / waves, each = w_each + x_each;
+  static constexpr int w_bytes = rows * 64, x_bytes = tokens * kStep, stage = w_bytes + kParts * x_bytes;
+  static constexpr int s_bytes = (rows + tokens) * 16;
+  static constexpr int lds = kStages * stage + 2 * s_bytes;
+  static_assert(lds <= kLdsMost, "a work-group's stages fit a compute unit");
+};
+
+template <int kParts, int kWv, int kWt, int kRt, int kNt, int kStages>
+__global__ __launch_bounds__(64 * kWv * kWt) void mx_logits_tile_kernel(MxArgs p, int row_blocks, int token_blocks) {
+  typedef TileShape<kParts, kWv, kWt, kRt, kNt, kStages> S;
+  extern __shared__ __align__(16) uint8_t lds[];   // stages, then two groups' scales: rows', tokens'
+  // the token blocks of a row block follow each other on one XCD, which reads
+  // the weights once
+  const int local = blockIdx.x / 8, rb = local / token_blocks * 8 + blockIdx.x % 8, tb = local % token_blocks;
+  if (rb >= row_blocks) return;
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wv = wave / kWt, wt = wave % kWt;
+  const int64_t v0 = (int64_t)rb * S::rows, n0 = (int64_t)tb * S::tokens;
+  const int rows = (int)(p.V - v0 < S::rows ? p.V - v0 : S::rows);
+  const int tokens = (int)(p.N - n0 < S::tokens ? p.N - n0 : S::tokens);
+  const int w_row = p.steps * 64, s_row = p.steps * 4;
+  const u32x4s from_w = buffer_of(p.w + v0 * w_row, (int64_t)rows * w_row);
+  const u32x4s from_s = buffer_of(p.ws + v0 * s_row, (int64_t)rows * s_row);
+  const u32x4s from_c = buffer_of(p.xs + n0 * p.ldxs, tokens * p.ldxs);
+  u32x4s from_x[S::x_each];   // the part that the wave's m-th load is of
 #pragma unroll
-  for (int i = 0; i < kItems; ++i) {
-    const int idx = t + i * kThreads, q = idx / (kVecs * kNt * 16);
-    const int64_t n = n0 + idx / kVecs % (kNt * 16), at = n < p.N ? n : p.N - 1;
-    from[i] = static_cast<const uint8_t*>(p.x) + (q * p.N + at) * p.ldx;
+  for (int m = 0; m < S::x_each; ++m) {
+    const int q = (wave + m * S::waves) % S::x_loads / (S::tokens / 8);
+    from_x[m] = buffer_of(static_cast<const uint8_t*>(p.x) + (q * p.N + n0) * p.ldx, tokens * p.ldx);
   }
-  u32x4 xv[kItems];
-  auto load_x = [&](int step) {
+  const uint32_t at = lds_address(lds), at_s = at + kStages * S::stage;
+  const uint32_t w_off = (uint32_t)((lane >> 2) * w_row + ((lane & 3) ^ (lane >> 4)) * 16);
+  const uint32_t x_off = (uint32_t)((lane >> 3) * (int)p.ldx);
+
+  auto load_stage = [&](int step, uint32_t to) {
+    const bool in = step < p.steps;
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-      const int kv = (t + i * kThreads) % kVecs;
-      const int at = step + kv / 8 < p.steps ? step + kv / 8 : p.steps - 1;   // (not used past the last step)
-      xv[i] = *reinterpret_cast<const u32x4*>(from[i] + at * kStep + kv % 8 * 16);
+    for (int m = 0; m < S::w_each; ++m) {
+      const int i = (wave + m * S::waves) % S::w_loads;
+      dma16(from_w, to + i * 1024, in ? w_off + i * 16 * w_row + step * 64 : kPastBuffer);
+    }
+#pragma unroll
+    for (int m = 0; m < S::x_each; ++m) {
+      const int i = (wave + m * S::waves) % S::x_loads, q = i / (S::tokens / 8), j = i % (S::tokens / 8);
+      // rows 8 j + lane / 8, so row / 2 mod 8 is (4 j + lane / 16) mod 8
+      const uint32_t piece = (uint32_t)((lane & 7) ^ ((4 * j + (lane >> 4)) & 7));
+      const uint32_t off = in ? x_off + j * 8 * (uint32_t)p.ldx + step * kStep + piece * 16 : kPastBuffer;
+      dma16(from_x[m], to + S::w_bytes + q * S::x_bytes + j * 1024, off);
     }
   };
-  auto stage_x = [&](int buf) {
+  auto load_scales = [&](int c, uint32_t to) {   // (what lies past a row's end is not used)
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-      const int idx = t + i * kThreads;
-      *reinterpret_cast<u32x4*>(&lds[buf][idx / (kVecs * kNt * 16)][idx / kVecs % (kNt * 16)][idx % kVecs * 16]) = xv[i];
+    for (int m = 0; m < S::s_each; ++m) {
+      const int i = (wave + m * S::waves) % S::s_loads, j = i - S::rows / 16;
+      if (j < 0) dma4(from_s, to + i * 256, (uint32_t)((16 * i + (lane >> 2)) * s_row + c * 4 + (lane & 3) * 4));
+      else dma4(from_c, to + i * 256, (uint32_t)((16 * j + (lane >> 2)) * (int)p.ldxs + c * 4 + (lane & 3) * 4));
     }
   };
-  const uint8_t* codes[kNt];
+
+  load_scales(0, at_s);
 #pragma unroll
-  for (int n = 0; n < kNt; ++n) {
-    const int64_t tok = n0 + n * 16 + r;
-    codes[n] = p.xs + (tok < p.N ? tok : p.N - 1) * p.ldxs;
-  }
-  u32x4 cnext[kNt];
-  auto load_codes = [&](int c) {
-    const int at = c < p.steps ? c : 0;
-#pragma unroll
-    for (int n = 0; n < kNt; ++n) cnext[n] = *reinterpret_cast<const u32x4*>(codes[n] + at * 4);
-  };
-  load_x(0);
-  load_codes(0);
-  ws.start(p, v0);
-  stage_x(0);
+  for (int t = 0; t < kStages - 1; ++t) load_stage(t, at + t * S::stage);
+  const uint8_t* my_w = lds + wv * kRt * 1024 + r * 64 + ((g ^ (r >> 2)) * 16);
+  const uint8_t* my_x = lds + S::w_bytes + (wt * kNt * 16 + r) * kStep;
+  const int x_lo = (g ^ (r >> 1)) * 16, x_hi = ((g + 4) ^ (r >> 1)) * 16;
+  const uint8_t* my_s = lds + kStages * S::stage + (wv * kRt * 16 + r) * 16;
+  const uint8_t* my_c = lds + kStages * S::stage + S::rows * 16 + (wt * kNt * 16 + r) * 16;
   f32x4 acc[kRt][kNt];
 #pragma unroll
   for (int i = 0; i < kRt; ++i)
 #pragma unroll
     for (int j = 0; j < kNt; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-  __syncthreads();
-  int buf = 0;
-  for (int c = 0; c < p.steps; c += 4) {
-    ws.take_scales(c);
-    ws.load_scales(c + 4);
-    uint32_t xc[kNt];
+  int use = 0, fill = (kStages - 1) * S::stage, group = 0;   // byte offsets of the stage in use and the one to be filled
+  for (int c = 0; c < p.steps; c += 4, group ^= 1) {
+    uint32_t scale[kRt], code[kNt];
 #pragma unroll
-    for (int n = 0; n < kNt; ++n) xc[n] = own_scales(cnext[n]);
-    load_codes(c + 4);
+    for (int s = 0; s < 4; ++s) {
+      // issued after this step's loads: the stages behind it, and the scales
+      // that one of those steps began with
+      if (kStages == 3 ? s == 1 : s == 1 || s == 2) wait_loads<(kStages - 2) * S::each + S::s_each>();
+      else wait_loads<(kStages - 2) * S::each>();
+      lds_barrier();
+      if (s == 0) {
+        load_scales(c + 4, at_s + (group ^ 1) * S::s_bytes);
 #pragma unroll
-    for (int h = 0; h < 4; h += kSt, buf ^= 1) {
-      load_x(c + h + kSt);
+        for (int i = 0; i < kRt; ++i)
+          scale[i] = own_scales(*reinterpret_cast<const u32x4*>(my_s + group * S::s_bytes + i * 256));
 #pragma unroll
-      for (int s = h; s < h + kSt; ++s) {
-        if (c + s < p.steps) {
-#pragma unroll
-          for (int q = 0; q < kParts; ++q)
-#pragma unroll
-            for (int n = 0; n < kNt; ++n) {
-              const i32x8v b = token_columns(&lds[buf][q][n * 16 + r][(s - h) * kStep + g * 16]);
-#pragma unroll
-              for (int i = 0; i < kRt; ++i) mx_mma(s, acc[i][n], ws.w[s][i], b, ws.scale[i], xc[n] - q * 0x04040404u);
-            }
-        }
-        ws.load(s, c + 4 + s);
+        for (int n = 0; n < kNt; ++n)
+          code[n] = own_scales(*reinterpret_cast<const u32x4*>(my_c + group * S::s_bytes + n * 256));
       }
-      stage_x(buf ^ 1);
-      __syncthreads();
+      load_stage(c + s + kStages - 1, at + fill);
+      if (c + s < p.steps) {
+        u32x4 a[kRt];
+#pragma unroll
+        for (int i = 0; i < kRt; ++i) a[i] = *reinterpret_cast<const u32x4*>(my_w + use + i * 1024);
+#pragma unroll
+        for (int q = 0; q < kParts; ++q)
+#pragma unroll
+          for (int n = 0; n < kNt; ++n) {
+            const uint8_t* x = my_x + use + q * S::x_bytes + n * 16 * kStep;
+            const i32x4v lo = *reinterpret_cast<const i32x4v*>(x + x_lo), hi = *reinterpret_cast<const i32x4v*>(x + x_hi);
+            const i32x8v b = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+#pragma unroll
+            for (int i = 0; i < kRt; ++i) mx_mma(s, acc[i][n], a[i], b, scale[i], code[n] - q * 0x04040404u);
+          }
+      }
+      use = use + S::stage == kStages * S::stage ? 0 : use + S::stage;
+      fill = fill + S::stage == kStages * S::stage ? 0 : fill + S::stage;
     }
   }
-  put_logits<kRt, kNt>(p, n0, v0, acc);
+  wait_loads<0>();   // nothing may land in LDS that is no longer this work-group's
+  put_logits<kRt, kNt>(p, n0 + wt * kNt * 16, v0 + wv * kRt * 16, acc);
 }
 
 // LDS of the streaming kernel beside its rings.
@@ -520,11 +504,16 @@ void launch_stream(const MxArgs& p, int most, hipStream_t st) {
       p, (int)tiles);
 }
 
+template <int kParts, int kWv, int kWt, int kRt, int kNt, int kStages>
+void launch_tiles(const MxArgs& p, hipStream_t st) {
+  typedef TileShape<kParts, kWv, kWt, kRt, kNt, kStages> S;
+  const int64_t rb = ceil_div(p.V, S::rows), tb = ceil_div(p.N, S::tokens);
+  mx_logits_tile_kernel<kParts, kWv, kWt, kRt, kNt, kStages>
+      <<<(unsigned)(ceil_div(rb, 8) * 8 * tb), 64 * S::waves, S::lds, st>>>(p, (int)rb, (int)tb);
+}
+
 template <int kParts>
 void launch_products(const MxArgs& p, bool raw, hipStream_t st) {
-  auto grid = [&](int rows, int tokens) {
-    return dim3((unsigned)ceil_div(p.V, rows), (unsigned)ceil_div(p.N, tokens));
-  };
   const int64_t left = kLdsMost - stream_tokens(p.N, p.steps, kParts);
   if (p.N <= 16 && left >= 4 * ring_bytes(1)) {
     int most = (int)(left / ring_bytes(1));
@@ -536,18 +525,14 @@ void launch_products(const MxArgs& p, bool raw, hipStream_t st) {
       }
     }
     launch_stream<kParts, 1, false>(p, most, st);
-  } else if (p.steps < 4) {
-    mx_logits_kernel<kParts, 2, 2, 1, true><<<grid(128, 32), kThreads, 0, st>>>(p);
-  } else if (p.N <= 16) {
-    mx_logits_kernel<kParts, 2, 1, 2, false><<<grid(128, 16), kThreads, 0, st>>>(p);
+    return;
+  }
+  if constexpr (kParts == 6) {
+    launch_tiles<6, 4, 1, 2, 2, 4>(p, st);
   } else {
-    if constexpr (kParts <= 2) {
-      if (p.N > 32) {
-        mx_logits_kernel<kParts, 4, 4, 1, false><<<grid(256, 64), kThreads, 0, st>>>(p);
-        return;
-      }
-    }
-    mx_logits_kernel<kParts, 2, 2, 1, false><<<grid(128, 32), kThreads, 0, st>>>(p);
+    if (p.N <= 32) launch_tiles<kParts, 4, 1, 2, 2, 4>(p, st);
+    else if (p.N <= 64) launch_tiles<kParts, 4, 2, 4, 2, 4>(p, st);
+    else launch_tiles<kParts, 4, 2, 4, 4, kParts == 1 ? 4 : 3>(p, st);
   }
 }
 
@@ -669,7 +654,7 @@ extern "C" int flce_logits_mx(const void* x, int64_t ld_x, const void* x_scales,
   uint8_t* codes = parts + t.codes;
   // rows in 8 bits that are whole groups of four steps are read where they are;
   // one or two bf16 rows are split by the work-groups (a launch less)
-  const bool ready = mx8 && H % (4 * kStep) == 0 && ld_x % 16 == 0 && addr(x) % 16 == 0 && ld_xs % 16 == 0 &&
+  const bool ready = mx8 && H % (4 * kStep) == 0 && ld_x % 16 == 0 && ld_x <= kMostRow && ld_xs <= kMostRow && addr(x) % 16 == 0 && ld_xs % 16 == 0 &&
                      addr(x_scales) % 16 == 0;
   const bool raw = x_dtype == FLCE_DTYPE_BF16 && N <= 2 && stream_tokens(N, steps, 2) <= kLdsMost - 4 * ring_bytes(1);
   MxArgs p{parts, codes, t.ldp, t.ldc, static_cast<const uint8_t*>(packed), static_cast<const uint8_t*>(scales), logits,
