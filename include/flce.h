@@ -488,10 +488,13 @@ size_t flce_logits_mx_workspace_size(int64_t N, int64_t H, int x_dtype);
  *   logits    aligned to one element, ld_logits >= V when N > 1; columns from V
  *             on are not written; must not overlap an input
  * Softcap and multiplier as flce_logits.  A bf16 or fp32 x enters as sums of
- * E4M3 values under one scale for 32 columns: exactly where it is at least
- * 2^-14 of the largest of its 32 (and 2^-102), else rounded to 2^-22 (bf16) or
- * 2^-38 (fp32) of that largest; where one of the 32 is not finite, all of them
- * count as NaN.  Products are exact, sums fp32, z is rounded once.  N <= 2^20,
+ * E4M3 values under one scale for 32 columns.  bf16: exactly where it is at least
+ * 2^-14 of the largest of its 32, else rounded to 2^-22 of that largest; fp32:
+ * rounded to 2^-24 of that largest.  Where one of the 32 is not finite, all of
+ * them count as NaN.  Sums are fp32; with 8-bit and bf16 rows the matrix unit
+ * cuts products below 2^-13 of the largest of the 8 that it adds at a time (sums
+ * of random rows end within 4e-6 of themselves; fp32 rows, whose parts are whole
+ * numbers, within 3e-7).  z is rounded once.  N <= 2^20,
  * V <= 2^24, H <= 2^21 and N Kp <= 2^34 (else FLCE_EUNSUPPORTED); N = 0 does
  * nothing.  Enqueued on `stream`; nothing is allocated, nothing synchronises.
  * Returns FLCE_OK, FLCE_EINVAL, FLCE_EUNSUPPORTED, FLCE_EWORKSPACE or

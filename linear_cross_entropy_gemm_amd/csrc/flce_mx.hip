@@ -8,11 +8,20 @@
 // through registers once and are never converted: the scaled matrix
 // instruction takes E2M1 rows with a scale for every 32 elements as they lie in
 // memory, next to E4M3 rows with theirs.  So the tokens are brought to E4M3
-// parts, x = sum_p part_p 2^(code - 4 p - 127) with four more significant bits
-// in each: one part for rows that are in 8 bits already, two for bf16 (8
-// bits), six for fp32 (24 bits).  An element above 2^-14 of its block's
-// largest is represented exactly, a smaller one to 2^-22 (bf16) or 2^-38 (fp32)
-// of that largest.  Products of a part are exact and sums are fp32.
+// parts, x = sum_p part_p 2^(code - s p - 127): one for rows that are in 8 bits
+// already, two with s = 4 for bf16 (8 significant bits), five with s = 5 for fp32.
+//
+// What the instruction keeps (measured with single products): it adds the 8
+// products of columns 8 i to 8 i + 7 down to 2^-13 of the largest, the 16 sums
+// and the accumulator down to 2^-23 of the largest, and cuts off the rest.  Where
+// the tokens are 8-bit or bf16 a product's loss, at most 2^-13 of its group's
+// largest, is a sixteenth of what half a step of that bf16 element stands for
+// (2^-9).  An element above 2^-14 of its block's largest has exact bf16 parts, a
+// smaller one to 2^-22 of that largest; sums of random rows end within 4e-6 of
+// themselves.  For fp32 the parts are digits: whole numbers to 16 times the
+// largest's exponent less 3, then base 32.  Products of digits and E2M1 are whole
+// numbers of halves to 96, which the instruction adds exactly; elements are held
+// to 2^-24 of their block's largest, and sums of random rows end within 3e-7.
 //
 // (Conversion of the weights to bf16 pairs and plain bf16 products took 114 us
 // of the vector and matrix units for 1 x 6656 x 202048, as long as the memory
@@ -99,6 +108,25 @@ __device__ __forceinline__ void mx_mma(int byte, f32x4& acc, const u32x4& a, con
   else mx_mma<3>(acc, a, b, sa, sb);
 }
 
+// Parts of a token.  fp32 rows have five whose elements are whole numbers up to
+// 16, digits of base 32: see the top.
+constexpr int kDigits = 5;
+template <int kParts>
+__device__ __forceinline__ constexpr int part_shift() { return kParts == kDigits ? 5 : 4; }
+
+// Their steps are summed by themselves, smallest part first, and added to the
+// sums so far by the vector unit, which rounds to nearest.  (bf16 and 8-bit
+// tokens would gain nothing: 320 x 4096 x 128256 takes 283 and 276 that way where
+// it takes 262 and 190.)
+template <int kParts>
+__device__ __forceinline__ f32x4 step_sums(const f32x4& acc) {
+  return kParts == kDigits ? f32x4{0, 0, 0, 0} : acc;
+}
+template <int kParts>
+__device__ __forceinline__ void add_step(f32x4& acc, const f32x4& sum) {
+  acc = kParts == kDigits ? acc + sum : sum;
+}
+
 // Four steps' scales of a row (four bytes each) -> those of the lane's own
 // block, a byte per step.
 __device__ __forceinline__ uint32_t own_scales(const u32x4& x) {
@@ -109,17 +137,18 @@ __device__ __forceinline__ uint32_t own_scales(const u32x4& x) {
 }
 
 // 8 values of a block, whose other values are with the other three lanes of an
-// aligned group of four, as E4M3 parts; returns the block's code.  Parts are
-// rounded, so a part may take more than its share and the rest be negative;
-// codes below 4 (kParts - 1) are raised to it, so that no part's is negative.
+// aligned group of four, as E4M3 parts; returns the block's code.  Codes below
+// kShift (kParts - 1) are raised to it, so that no part's is negative.
 template <int kParts>
 __device__ __forceinline__ uint32_t split8(const float (&v)[8], u32x2 (&out)[kParts]) {
-  uint32_t code = mx8_code(block_max_bits<8>(v));
-  if (code < 4 * (kParts - 1)) code = 4 * (kParts - 1);
+  constexpr int kShift = part_shift<kParts>();
+  const uint32_t bits = block_max_bits<8>(v);
+  uint32_t code = kParts == kDigits ? bits >> 23 : mx8_code(bits);
+  if (kParts == kDigits) code = code == 255 ? 255 : code < 3 ? 0 : code - 3;   // the largest: 8 to 16 units
+  if (code < kShift * (kParts - 1)) code = kShift * (kParts - 1);
   const float inv = code == 255 ? 1.0f : mx_inverse(code);
-  // next to the largest float no part may round the sum up to 2^128: 15 in
-  // every digit of base 16
-  const float top = code == 247 ? 240.0f : 448.0f;
+  // next to the largest float no part may round the sum up to 2^128
+  const float top = code == 247 && kParts != kDigits ? 240.0f : 448.0f;
   float x[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] = code == 255 ? 0.0f : v[e] * inv;   // a block without a scale is NaN by its code
@@ -127,17 +156,18 @@ __device__ __forceinline__ uint32_t split8(const float (&v)[8], u32x2 (&out)[kPa
   for (int p = 0; p < kParts; ++p) {
     float y[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = __builtin_amdgcn_fmed3f(x[e], -top, top);
+    for (int e = 0; e < 8; ++e) y[e] = kParts == kDigits ? rintf(x[e]) : __builtin_amdgcn_fmed3f(x[e], -top, top);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * h], y[4 * h + 1], 0, false);
       w = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * h + 2], y[4 * h + 3], w, true);
       out[p][h] = (uint32_t)w;
       if (p + 1 < kParts) {
-        x[4 * h] = (x[4 * h] - __builtin_amdgcn_cvt_f32_fp8(w, 0)) * 16.0f;
-        x[4 * h + 1] = (x[4 * h + 1] - __builtin_amdgcn_cvt_f32_fp8(w, 1)) * 16.0f;
-        x[4 * h + 2] = (x[4 * h + 2] - __builtin_amdgcn_cvt_f32_fp8(w, 2)) * 16.0f;
-        x[4 * h + 3] = (x[4 * h + 3] - __builtin_amdgcn_cvt_f32_fp8(w, 3)) * 16.0f;
+        constexpr float up = 1 << kShift;
+        x[4 * h] = (x[4 * h] - __builtin_amdgcn_cvt_f32_fp8(w, 0)) * up;
+        x[4 * h + 1] = (x[4 * h + 1] - __builtin_amdgcn_cvt_f32_fp8(w, 1)) * up;
+        x[4 * h + 2] = (x[4 * h + 2] - __builtin_amdgcn_cvt_f32_fp8(w, 2)) * up;
+        x[4 * h + 3] = (x[4 * h + 3] - __builtin_amdgcn_cvt_f32_fp8(w, 3)) * up;
       }
     }
   }
@@ -347,9 +377,11 @@ __global__ __launch_bounds__(1024) void mx_logits_stream_kernel(MxArgs p, int ti
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         if (c + s < p.steps) {
+          f32x4 sum = step_sums<kParts>(acc[0][0]);
 #pragma unroll
-          for (int q = 0; q < kParts; ++q)
-            mx_mma(s, acc[0][0], a[s], token_columns(mine + q * part + (c + s) * kStep), scale, xc - q * 0x04040404u);
+          for (int q = kParts - 1; q >= 0; --q)
+            mx_mma(s, sum, a[s], token_columns(mine + q * part + (c + s) * kStep), scale, xc - q * part_shift<kParts>() * 0x01010101u);
+          add_step<kParts>(acc[0][0], sum);
         }
       }
     }
@@ -360,28 +392,49 @@ __global__ __launch_bounds__(1024) void mx_logits_stream_kernel(MxArgs p, int ti
 
 // More tokens: a work-group of kWv x kWt waves has kWv kRt tiles of 16
 // vocabulary entries by kWt kNt tiles of 16 tokens, kRt x kNt a wave.  A stage is
-// one step of both: its weights (rows of 64 bytes) and its tokens' parts (rows of
-// 128 bytes), in a ring of kStages in LDS; the scales of a group of four steps
-// are two groups ahead of each other.  One barrier a step: behind it everyone's
-// loads of the step are there, and the stage before it is free.  A piece of 16
-// bytes lies at its place exclusive-or (row / 4 mod 4) (weights) or (row / 2 mod
-// 8) (tokens): no bank serves two of the 16 rows that a wave reads at a time.
-// Loads that do not divide evenly among the waves are done twice, alike.
-template <int kParts, int kWv, int kWt, int kRt, int kNt, int kStages>
+// kU steps of both, its weights' rows (64 kU bytes) and its tokens' (128 kU bytes
+// of each part), in a ring of kStages in LDS; the scales of a group of four steps
+// come a group ahead.  One barrier a stage: behind it everyone's loads of the
+// stage are there, and the one before it is free.  Rows are swizzled by pieces of
+// 16 bytes, so that no bank serves two of the 16 rows that a wave reads at a
+// time.  Loads that do not divide evenly among the waves are done twice, alike.
+template <int kParts, int kWv, int kWt, int kRt, int kNt, int kU, int kStages>
 struct TileShape {
   static constexpr int waves = kWv * kWt, rows = kWv * kRt * 16, tokens = kWt * kNt * 16;
-  static constexpr int w_loads = rows / 16, x_loads = kParts * tokens / 8, s_loads = (rows + tokens) / 16;
+  static constexpr int w_pieces = 4 * kU, x_pieces = 8 * kU;          // of a row in a stage
+  static constexpr int w_at_once = 64 / w_pieces, x_at_once = 64 / x_pieces;   // rows a load
+  static constexpr int w_loads = rows / w_at_once, x_part = tokens / x_at_once, x_loads = kParts * x_part;
+  static constexpr int s_loads = (rows + tokens) / 16;
   static constexpr int w_each = (w_loads + waves - 1) / waves, x_each = (x_loads + waves - 1) / waves;
   static constexpr int s_each = (s_loads + waves - 1) / waves, each = w_each + x_each;
-  static constexpr int w_bytes = rows * 64, x_bytes = tokens * kStep, stage = w_bytes + kParts * x_bytes;
+  static constexpr int w_bytes = rows * 64 * kU, x_bytes = tokens * kStep * kU, stage = w_bytes + kParts * x_bytes;
   static constexpr int s_bytes = (rows + tokens) * 16;
   static constexpr int lds = kStages * stage + 2 * s_bytes;
+  static constexpr int group = 4 / kU;   // stages of a group
   static_assert(lds <= kLdsMost, "a work-group's stages fit a compute unit");
+  static_assert(group > kStages - 2, "a group's scales are there with its first stage");
+  __device__ static constexpr int w_swizzle(int row) { return row / (4 / kU) % w_pieces; }
+  __device__ static constexpr int x_swizzle(int row) { return kU == 1 ? row / 2 % 8 : row % 16; }
+  // loads of this wave that may be under way when stage `i` of a group is needed:
+  // the stages behind it, and the scales that one of those began with
+  static constexpr int behind(int i) {
+    int n = (kStages - 2) * each;
+    for (int d = 1; d <= kStages - 2; ++d) n += (i + group * 4 - d) % group == 0 ? s_each : 0;
+    return n;
+  }
 };
 
-template <int kParts, int kWv, int kWt, int kRt, int kNt, int kStages>
+template <typename S, int i = 0>
+__device__ __forceinline__ void wait_stage(int which) {
+  if constexpr (i < S::group) {
+    if (which == i) wait_loads<S::behind(i)>();   // (a constant where this is used)
+    else wait_stage<S, i + 1>(which);
+  }
+}
+
+template <int kParts, int kWv, int kWt, int kRt, int kNt, int kU, int kStages>
 __global__ __launch_bounds__(64 * kWv * kWt) void mx_logits_tile_kernel(MxArgs p, int row_blocks, int token_blocks) {
-  typedef TileShape<kParts, kWv, kWt, kRt, kNt, kStages> S;
+  typedef TileShape<kParts, kWv, kWt, kRt, kNt, kU, kStages> S;
   extern __shared__ __align__(16) uint8_t lds[];   // stages, then two groups' scales: rows', tokens'
   // the token blocks of a row block follow each other on one XCD, which reads
   // the weights once
@@ -392,34 +445,45 @@ __global__ __launch_bounds__(64 * kWv * kWt) void mx_logits_tile_kernel(MxArgs p
   const int64_t v0 = (int64_t)rb * S::rows, n0 = (int64_t)tb * S::tokens;
   const int rows = (int)(p.V - v0 < S::rows ? p.V - v0 : S::rows);
   const int tokens = (int)(p.N - n0 < S::tokens ? p.N - n0 : S::tokens);
-  const int w_row = p.steps * 64, s_row = p.steps * 4;
+  const int w_row = p.steps * 64, s_row = p.steps * 4, x_row = (int)p.ldx, c_row = (int)p.ldxs;
   const u32x4s from_w = buffer_of(p.w + v0 * w_row, (int64_t)rows * w_row);
   const u32x4s from_s = buffer_of(p.ws + v0 * s_row, (int64_t)rows * s_row);
   const u32x4s from_c = buffer_of(p.xs + n0 * p.ldxs, tokens * p.ldxs);
   u32x4s from_x[S::x_each];   // the part that the wave's m-th load is of
 #pragma unroll
   for (int m = 0; m < S::x_each; ++m) {
-    const int q = (wave + m * S::waves) % S::x_loads / (S::tokens / 8);
+    const int q = (wave + m * S::waves) % S::x_loads / S::x_part;
     from_x[m] = buffer_of(static_cast<const uint8_t*>(p.x) + (q * p.N + n0) * p.ldx, tokens * p.ldx);
   }
   const uint32_t at = lds_address(lds), at_s = at + kStages * S::stage;
-  const uint32_t w_off = (uint32_t)((lane >> 2) * w_row + ((lane & 3) ^ (lane >> 4)) * 16);
-  const uint32_t x_off = (uint32_t)((lane >> 3) * (int)p.ldx);
 
+  // offsets of the wave's loads in step 0, and the steps that their pieces are of
+  uint32_t w_off[S::w_each], x_off[S::x_each];
+  int w_step[S::w_each], x_step[S::x_each];
+#pragma unroll
+  for (int m = 0; m < S::w_each; ++m) {
+    const int row = (wave + m * S::waves) % S::w_loads * S::w_at_once + lane / S::w_pieces;
+    const int piece = lane % S::w_pieces ^ S::w_swizzle(row % 16);
+    w_off[m] = (uint32_t)(row * w_row + piece * 16);
+    w_step[m] = piece / 4;
+  }
+#pragma unroll
+  for (int m = 0; m < S::x_each; ++m) {
+    const int row = (wave + m * S::waves) % S::x_loads % S::x_part * S::x_at_once + lane / S::x_pieces;
+    const int piece = lane % S::x_pieces ^ S::x_swizzle(row % 16);
+    x_off[m] = (uint32_t)(row * x_row + piece * 16);
+    x_step[m] = piece / 8;
+  }
   auto load_stage = [&](int step, uint32_t to) {
-    const bool in = step < p.steps;
 #pragma unroll
     for (int m = 0; m < S::w_each; ++m) {
       const int i = (wave + m * S::waves) % S::w_loads;
-      dma16(from_w, to + i * 1024, in ? w_off + i * 16 * w_row + step * 64 : kPastBuffer);
+      dma16(from_w, to + i * 1024, step + w_step[m] < p.steps ? w_off[m] + step * 64 : kPastBuffer);
     }
 #pragma unroll
     for (int m = 0; m < S::x_each; ++m) {
-      const int i = (wave + m * S::waves) % S::x_loads, q = i / (S::tokens / 8), j = i % (S::tokens / 8);
-      // rows 8 j + lane / 8, so row / 2 mod 8 is (4 j + lane / 16) mod 8
-      const uint32_t piece = (uint32_t)((lane & 7) ^ ((4 * j + (lane >> 4)) & 7));
-      const uint32_t off = in ? x_off + j * 8 * (uint32_t)p.ldx + step * kStep + piece * 16 : kPastBuffer;
-      dma16(from_x[m], to + S::w_bytes + q * S::x_bytes + j * 1024, off);
+      const int i = (wave + m * S::waves) % S::x_loads;
+      dma16(from_x[m], to + S::w_bytes + i * 1024, step + x_step[m] < p.steps ? x_off[m] + step * kStep : kPastBuffer);
     }
   };
   auto load_scales = [&](int c, uint32_t to) {   // (what lies past a row's end is not used)
@@ -427,16 +491,16 @@ __global__ __launch_bounds__(64 * kWv * kWt) void mx_logits_tile_kernel(MxArgs p
     for (int m = 0; m < S::s_each; ++m) {
       const int i = (wave + m * S::waves) % S::s_loads, j = i - S::rows / 16;
       if (j < 0) dma4(from_s, to + i * 256, (uint32_t)((16 * i + (lane >> 2)) * s_row + c * 4 + (lane & 3) * 4));
-      else dma4(from_c, to + i * 256, (uint32_t)((16 * j + (lane >> 2)) * (int)p.ldxs + c * 4 + (lane & 3) * 4));
+      else dma4(from_c, to + i * 256, (uint32_t)((16 * j + (lane >> 2)) * c_row + c * 4 + (lane & 3) * 4));
     }
   };
 
   load_scales(0, at_s);
 #pragma unroll
-  for (int t = 0; t < kStages - 1; ++t) load_stage(t, at + t * S::stage);
-  const uint8_t* my_w = lds + wv * kRt * 1024 + r * 64 + ((g ^ (r >> 2)) * 16);
-  const uint8_t* my_x = lds + S::w_bytes + (wt * kNt * 16 + r) * kStep;
-  const int x_lo = (g ^ (r >> 1)) * 16, x_hi = ((g + 4) ^ (r >> 1)) * 16;
+  for (int t = 0; t < kStages - 1; ++t) load_stage(t * kU, at + t * S::stage);
+  const uint8_t* my_w = lds + (wv * kRt * 16 + r) * 64 * kU;
+  const uint8_t* my_x = lds + S::w_bytes + (wt * kNt * 16 + r) * kStep * kU;
+  const int w_sw = S::w_swizzle(r), x_sw = S::x_swizzle(r);
   const uint8_t* my_s = lds + kStages * S::stage + (wv * kRt * 16 + r) * 16;
   const uint8_t* my_c = lds + kStages * S::stage + S::rows * 16 + (wt * kNt * 16 + r) * 16;
   f32x4 acc[kRt][kNt];
@@ -448,13 +512,10 @@ __global__ __launch_bounds__(64 * kWv * kWt) void mx_logits_tile_kernel(MxArgs p
   for (int c = 0; c < p.steps; c += 4, group ^= 1) {
     uint32_t scale[kRt], code[kNt];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      // issued after this step's loads: the stages behind it, and the scales
-      // that one of those steps began with
-      if (kStages == 3 ? s == 1 : s == 1 || s == 2) wait_loads<(kStages - 2) * S::each + S::s_each>();
-      else wait_loads<(kStages - 2) * S::each>();
+    for (int h = 0; h < S::group; ++h) {
+      wait_stage<S>(h);
       lds_barrier();
-      if (s == 0) {
+      if (h == 0) {
         load_scales(c + 4, at_s + (group ^ 1) * S::s_bytes);
 #pragma unroll
         for (int i = 0; i < kRt; ++i)
@@ -463,21 +524,32 @@ __global__ __launch_bounds__(64 * kWv * kWt) void mx_logits_tile_kernel(MxArgs p
         for (int n = 0; n < kNt; ++n)
           code[n] = own_scales(*reinterpret_cast<const u32x4*>(my_c + group * S::s_bytes + n * 256));
       }
-      load_stage(c + s + kStages - 1, at + fill);
-      if (c + s < p.steps) {
+      load_stage(c + (h + kStages - 1) * kU, at + fill);
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int s = h * kU + u;
+        if (c + s >= p.steps) continue;
         u32x4 a[kRt];
 #pragma unroll
-        for (int i = 0; i < kRt; ++i) a[i] = *reinterpret_cast<const u32x4*>(my_w + use + i * 1024);
+        for (int i = 0; i < kRt; ++i)
+          a[i] = *reinterpret_cast<const u32x4*>(my_w + use + i * 16 * 64 * kU + ((u * 4 + g) ^ w_sw) * 16);
 #pragma unroll
-        for (int q = 0; q < kParts; ++q)
+        for (int n = 0; n < kNt; ++n) {
+          f32x4 sum[kRt];
 #pragma unroll
-          for (int n = 0; n < kNt; ++n) {
-            const uint8_t* x = my_x + use + q * S::x_bytes + n * 16 * kStep;
-            const i32x4v lo = *reinterpret_cast<const i32x4v*>(x + x_lo), hi = *reinterpret_cast<const i32x4v*>(x + x_hi);
+          for (int i = 0; i < kRt; ++i) sum[i] = step_sums<kParts>(acc[i][n]);
+#pragma unroll
+          for (int q = kParts - 1; q >= 0; --q) {
+            const uint8_t* x = my_x + use + q * S::x_bytes + n * 16 * kStep * kU;
+            const i32x4v lo = *reinterpret_cast<const i32x4v*>(x + ((u * 8 + g) ^ x_sw) * 16);
+            const i32x4v hi = *reinterpret_cast<const i32x4v*>(x + ((u * 8 + g + 4) ^ x_sw) * 16);
             const i32x8v b = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 #pragma unroll
-            for (int i = 0; i < kRt; ++i) mx_mma(s, acc[i][n], a[i], b, scale[i], code[n] - q * 0x04040404u);
+            for (int i = 0; i < kRt; ++i) mx_mma(s, sum[i], a[i], b, scale[i], code[n] - q * part_shift<kParts>() * 0x01010101u);
           }
+#pragma unroll
+          for (int i = 0; i < kRt; ++i) add_step<kParts>(acc[i][n], sum[i]);
+        }
       }
       use = use + S::stage == kStages * S::stage ? 0 : use + S::stage;
       fill = fill + S::stage == kStages * S::stage ? 0 : fill + S::stage;
@@ -495,44 +567,69 @@ int64_t stream_tokens(int64_t N, int64_t steps, int parts) {
 // One work-group on each of the 256 compute units; waves so that every one has
 // about as many tiles as the others.
 template <int kParts, int kG, bool kInline>
-void launch_stream(const MxArgs& p, int most, hipStream_t st) {
-  const int64_t tiles = ceil_div(p.V, 16), rounds = ceil_div(tiles, 256 * most);
-  int waves = (int)ceil_div(tiles, 256 * rounds);
-  if (waves < 4) waves = 4;   // they also bring the tokens to LDS
+void launch_stream(const MxArgs& p, int waves, hipStream_t st) {
+  const int64_t tiles = ceil_div(p.V, 16);
   const int64_t bytes = stream_tokens(p.N, p.steps, kParts) + waves * ring_bytes(kG);
   mx_logits_stream_kernel<kParts, kG, kInline><<<(unsigned)(tiles < 256 ? tiles : 256), waves * 64, (size_t)bytes, st>>>(
       p, (int)tiles);
 }
 
-template <int kParts, int kWv, int kWt, int kRt, int kNt, int kStages>
+template <int kParts, int kWv, int kWt, int kRt, int kNt, int kU, int kStages>
 void launch_tiles(const MxArgs& p, hipStream_t st) {
-  typedef TileShape<kParts, kWv, kWt, kRt, kNt, kStages> S;
+  typedef TileShape<kParts, kWv, kWt, kRt, kNt, kU, kStages> S;
   const int64_t rb = ceil_div(p.V, S::rows), tb = ceil_div(p.N, S::tokens);
-  mx_logits_tile_kernel<kParts, kWv, kWt, kRt, kNt, kStages>
+  mx_logits_tile_kernel<kParts, kWv, kWt, kRt, kNt, kU, kStages>
       <<<(unsigned)(ceil_div(rb, 8) * 8 * tb), 64 * S::waves, S::lds, st>>>(p, (int)rb, (int)tb);
 }
 
+// Kernels by size, as measured (us; floor: the weights' bytes at 6.1 TB/s).
+// Streaming, 1 x 6656 x 202048 bf16: 124 with one group of four steps under way
+// in each of 12 waves (floor 117), 125 with two, 130 with three; by pieces of 64
+// bytes 137; with few tiles and four waves 1 x 8192 x 1000 takes 13 with one
+// group and 14 with three or more: its time is the way from launch to sum.
+// Tiles (waves along V x along N, tiles of 16 a wave, steps x stages), in order
+// (2 parts at the first four, 1 at the others):
+//                        16 x 6656  24 x 6656  320 x 4096  64 x 8192  320 x 4096  24 x 7168
+//                        x 202048   x 202048   x 128256    x 1000     x 128256    x 129280
+//   8x1 2x1 2x3          158        221        560         30         502         131
+//   4x1 2x2 2x3          162        171        506         29         287         96
+//   4x2 4x2 1x2          200        205        260         58         194         115
+//   4x2 2x4 1x2          317        317        372         57         186         116
+//   floor                117        117        46          1          46          81
+// The large ones are bound by the matrix units: 2.57 PFLOP/s of 8-bit products at
+// 320 bf16 tokens, two for each.  A second work-group on the compute unit is
+// worth more than deeper rings (two stages 260, four stages and one work-group
+// 334).
 template <int kParts>
 void launch_products(const MxArgs& p, bool raw, hipStream_t st) {
   const int64_t left = kLdsMost - stream_tokens(p.N, p.steps, kParts);
   if (p.N <= 16 && left >= 4 * ring_bytes(1)) {
-    int most = (int)(left / ring_bytes(1));
+    int64_t most = left / ring_bytes(1);
     if (most > 12) most = 12;
+    const int64_t tiles = ceil_div(p.V, 16);
+    int waves = (int)ceil_div(tiles, 256 * ceil_div(tiles, 256 * most));
+    if (waves < 4) waves = 4;   // they also bring the tokens to LDS
     if constexpr (kParts == 2) {
       if (raw) {
-        launch_stream<2, 1, true>(p, most, st);
+        launch_stream<2, 1, true>(p, waves, st);
         return;
       }
     }
-    launch_stream<kParts, 1, false>(p, most, st);
+    launch_stream<kParts, 1, false>(p, waves, st);
     return;
   }
-  if constexpr (kParts == 6) {
-    launch_tiles<6, 4, 1, 2, 2, 4>(p, st);
+  if constexpr (kParts == kDigits) {
+    // 8 x 4096 x 128256: 58, 77 by 32 tokens; 33 x 1001 x 50001: 23 by 48, 28 by 32
+    if (p.N <= 16) launch_tiles<kDigits, 4, 1, 2, 1, 2, 2>(p, st);
+    else if (p.N > 32 && p.N <= 48) launch_tiles<kDigits, 8, 1, 2, 3, 1, 2>(p, st);
+    else launch_tiles<kDigits, 4, 1, 2, 2, 1, 2>(p, st);
   } else {
-    if (p.N <= 32) launch_tiles<kParts, 4, 1, 2, 2, 4>(p, st);
-    else if (p.N <= 64) launch_tiles<kParts, 4, 2, 4, 2, 4>(p, st);
-    else launch_tiles<kParts, 4, 2, 4, 4, kParts == 1 ? 4 : 3>(p, st);
+    // (few tiles: rather more of them, for the other compute units)
+    const bool few = ceil_div(p.V, 256) * ceil_div(p.N, 64) < 256;
+    if (p.N <= 16) launch_tiles<kParts, 8, 1, 2, 1, 2, 3>(p, st);
+    else if (p.N <= 32 || few) launch_tiles<kParts, 4, 1, 2, 2, 2, 3>(p, st);
+    else if (kParts == 1 && p.N > 64) launch_tiles<1, 4, 2, 2, 4, 1, 2>(p, st);
+    else launch_tiles<kParts, 4, 2, 4, 2, 1, 2>(p, st);
   }
 }
 
@@ -546,7 +643,7 @@ struct MxTokens {
 MxTokens mx_tokens(int64_t N, int64_t H, int x_dtype) {
   MxTokens t{};
   const int64_t steps = ceil_div(H, kStep);
-  t.parts = x_dtype == FLCE_DTYPE_MX8 ? 1 : x_dtype == FLCE_DTYPE_BF16 ? 2 : 6;
+  t.parts = x_dtype == FLCE_DTYPE_MX8 ? 1 : x_dtype == FLCE_DTYPE_BF16 ? 2 : kDigits;
   t.ldp = steps * kStep;
   t.ldc = code_bytes((int)steps);
   t.codes = (size_t)(t.parts * N * t.ldp);
@@ -675,12 +772,12 @@ extern "C" int flce_logits_mx(const void* x, int64_t ld_x, const void* x_scales,
       mx_split_kernel<bf16, 2><<<g, 256, 0, stream>>>(static_cast<const bf16*>(x), ld_x, N, (int)H, (int)vecs, parts,
                                                       t.ldp, codes, t.ldc);
     else
-      mx_split_kernel<float, 6><<<g, 256, 0, stream>>>(static_cast<const float*>(x), ld_x, N, (int)H, (int)vecs, parts,
+      mx_split_kernel<float, kDigits><<<g, 256, 0, stream>>>(static_cast<const float*>(x), ld_x, N, (int)H, (int)vecs, parts,
                                                        t.ldp, codes, t.ldc);
   }
   ProfileScope ps(FLCE_KERNEL_LOGITS_MX, stream);
   if (mx8) launch_products<1>(p, false, stream);
   else if (x_dtype == FLCE_DTYPE_BF16) launch_products<2>(p, raw, stream);
-  else launch_products<6>(p, false, stream);
+  else launch_products<kDigits>(p, false, stream);
   return hipGetLastError() == hipSuccess ? FLCE_OK : FLCE_EDEVICE;
 }

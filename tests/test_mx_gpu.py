@@ -4,10 +4,14 @@ values the GPU reads.
 Packing is exact arithmetic (a maximum's exponent, a division by a power of
 two, comparisons): codes and scales have to be equal.
 
-Logits: products of a bf16 (or each part of an fp32) with a 4-bit weight are
-exact.  A sum of K of them (3 K with fp32) adds at most Kp (3 Kp) times, each
-off by at most 2 u of the running sum, u = 2^-24 (nothing is assumed about how
-the matrix unit rounds inside an instruction): |dz| <= 2 u Kp parts sum|x w| m.
+Logits: with u = 2^-24, a sum of Kp products (3 Kp with fp32) that adds them one
+by one is off by at most 2 u of the running sum each time:
+|dz| <= 2 u Kp parts sum|x w| m.  What the matrix unit cuts comes on top for bf16
+and 8-bit rows: of the 8 products that it adds at a time each may lose 2^-13 of
+the largest, and a bf16 element below 2^-14 of its block's largest is off by
+2^-22 of that largest.  fp32 rows' digits are whole numbers of 2^-24 of their
+block's largest, off by half of one, and their sums lose nothing but the fp32
+roundings.
 The softcap adds 1e-6 of its value, the store half a step.
 """
 import numpy as np
@@ -86,9 +90,26 @@ def test_pack_special_blocks():
     assert e.data.shape == (0, 64) and L.mx4_pack(W.t().contiguous().t()).scales.view(torch.uint8).cpu().equal(s)
 
 
+def _groups(a, n):
+    """[rows, K] padded to whole groups of n: [rows, K / n, n]."""
+    pad = -a.shape[1] % n
+    return np.pad(a, ((0, 0), (0, pad))).reshape(a.shape[0], -1, n)
+
+
+def _cut(x, w, fp32):
+    """What the rounding of the rows' parts and the matrix unit's sums of 8 may
+    cost, [N, V]; of the latter a bound: the largest product of 8 is at most the
+    largest |x| times the largest |w|, and the products beside it are 7."""
+    bx, bw = np.abs(_groups(x, 32)).max(2), np.abs(_groups(w, 32)).sum(2)
+    if fp32:
+        return U * bx @ bw.T
+    return 2.0 ** -22 * bx @ bw.T + 7 * 2.0 ** -13 * np.abs(_groups(x, 8)).max(2) @ np.abs(_groups(w, 8)).max(2).T
+
+
 def _check_logits(z, x, w, cap, mult, out, parts):
     z, ref = _np(z), x @ w.T * mult
     tol = 2 * U * parts * ((w.shape[1] + 127) // 128 * 128) * (np.abs(x) @ np.abs(w).T) * abs(mult)
+    tol = tol + _cut(x, w, parts == 3) * abs(mult)
     if cap:
         ref = cap * np.tanh(ref / cap)
         tol = tol + 1e-6 * np.abs(ref)
@@ -129,6 +150,76 @@ def test_logits(N, H, V, kind):
     z2 = L.logits_mx4(x, q, cap, mult, out=buf)
     _check_logits(z2, xn, w, cap, mult, other, 3 if kind == "f32" else 1)
     assert buf[:, V:].eq(7.0).all()
+
+
+@pytest.mark.parametrize("N,H,V", [(1, 1024, 2000), (1, 8192, 500), (5, 4096, 500), (20, 2049, 400), (40, 1001, 3001),
+                                   (100, 4096, 300), (300, 7168, 200)])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_logits_accuracy(N, H, V, kind):
+    """Over random rows the errors are independent, so they are held to their
+    root mean square.  fp32: Kp / 128 sums rounded to nearest (u / sqrt 3 of a
+    running sum that reaches the rms z only at the end: below u sqrt(64) / 2),
+    2 u for the last instruction of each, u / sqrt 3 x 2.5 for the digits (the
+    largest of 32 is 2.5 of their rms): below 8 u in all, 16 u allowed.  bf16:
+    7 of 8 products lose up to 2^-13 of the group's largest (2.2 rms of a
+    product), on average half, of which an rms of 2^-13 2.2 / sqrt 3 x 2^-3 at
+    most is behind the value's own last bit (a product of 8 by 2 significant
+    bits lies below 2^-13 of the largest with 3 or fewer of its bits): 2^-15.6 of
+    a product, and both sums grow with sqrt Kp; 2^-15 allowed."""
+    import torch
+    import linear_cross_entropy_gemm_amd as L
+    q = L.mx4_pack(_rand((V, H), "f32", 3, 0.02))
+    x = _rand((N, H), kind, 4)
+    ref = _np(x) @ _weights(q).T
+    z = _np(L.logits_mx4(x, q, out=torch.empty(N, V, device="cuda")))
+    err = np.sqrt(np.mean((z - ref) ** 2) / np.mean(ref ** 2))
+    log(f"[mx4] N={N} H={H} V={V} {kind}: relative rms error {err:.2e}")
+    assert err <= (16 * U if kind == "f32" else 2.0 ** -15)
+
+
+def _outlier_rows(N, H, kind):
+    x = _rand((N, H), kind, 6)
+    x[:, 5::97] *= 1000.0
+    return x
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32", "mx8"])
+@pytest.mark.parametrize("N", [1, 3, 16, 20, 48, 64, 200])
+@pytest.mark.parametrize("H,V", [(130, 700), (385, 257), (1500, 4100), (2560, 16)])
+def test_logits_outliers_and_borders(N, H, V, kind):
+    """Few columns a thousand times the others; steps that are no multiple of
+    four, token counts of every kernel, vocabularies of few tiles and of more
+    than the work-groups have."""
+    import linear_cross_entropy_gemm_amd as L
+    q = L.mx4_pack(_rand((V, H), "f32", 5, 0.05))
+    x = _outlier_rows(N, H, "bf16" if kind == "mx8" else kind)
+    if kind == "mx8":
+        x = L.rms_norm_mx8(x, None, 1e-6).rows
+        xn = _np(x.data) * np.repeat(_np(x.scales), 32, 1)[:, :H]
+    else:
+        xn = _np(x)
+    z = L.logits_mx4(x, q)
+    assert z.equal(L.logits_mx4(x, q))
+    _check_logits(z, xn, _weights(q), 0.0, 1.0, "f32" if kind == "f32" else "bf16", 3 if kind == "f32" else 1)
+
+
+@pytest.mark.parametrize("H", [512, 1024, 1536])
+@pytest.mark.parametrize("N", [5, 40, 130])
+def test_mx8_rows_of_every_alignment(N, H):
+    """Rows that the products read in place and rows that are brought to a
+    workspace first: the same logits, bit for bit."""
+    import torch
+    import linear_cross_entropy_gemm_amd as L
+    q = L.mx4_pack(_rand((333, H), "f32", 7, 0.05))
+    rows = L.rms_norm_mx8(_rand((N, H), "bf16", 8), None, 1e-6).rows
+    z = L.logits_mx4(rows, q)
+    wide = torch.zeros(N, H + 48, dtype=torch.uint8, device="cuda")
+    codes = torch.zeros(N, H // 32 + 3, dtype=torch.uint8, device="cuda")
+    for off in (0, 1, 16):
+        d, s = wide[:, off:off + H].view(torch.float8_e4m3fn), codes[:, off % 3:off % 3 + H // 32].view(torch.float8_e8m0fnu)
+        d.copy_(rows.data)
+        s.copy_(rows.scales)
+        assert L.logits_mx4(L.Mx8Rows(d, s), q).equal(z)
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f32", "mx8"])
