@@ -41,6 +41,7 @@ struct RmsFwdArgs {
   int64_t M, ldx, ldr, lds, ldy, ldsc;   // strides in elements
   int H;
   float eps, offset;
+  int past;               // see past_caches
 };
 
 struct RmsBwdArgs {
@@ -54,7 +55,32 @@ struct RmsBwdArgs {
   int64_t M, ldy, lds, ldd, ldx;
   int H;
   float offset;
+  int past;
 };
+
+// Rows that pass through the caches before anything can read them again: of a
+// call that moves more than the last-level cache's 256 MB.  Stored as such
+// they leave it to the loads: 8192 x 6656 bf16 forward with a residual takes 67
+// us, 82 without (436 MB; a loop that only copies two arrays to two others 82);
+// below the border there is no difference (268 MB: 44 and 45), and the next
+// kernel finds the rows in the cache.
+inline bool past_caches(int64_t bytes) { return bytes > int64_t(256) << 20; }
+template <typename T>
+__device__ __forceinline__ void put_vec(T* p, int64_t col, int64_t n, const typename RowVec<T>::type& v, bool past) {
+  if (past && col + RowVec<T>::E <= n)
+    __builtin_nontemporal_store(v, reinterpret_cast<typename RowVec<T>::mem*>(p + col));
+  else
+    store_row(p, col, n, v);
+}
+
+// A vector that is converted again at its next use: the compiler holds the
+// fp32 values, twice the registers, over a barrier otherwise.
+template <typename V>
+__device__ __forceinline__ void hold_packed(V& v) {
+  u32x4 x = __builtin_bit_cast(u32x4, v);
+  asm volatile("" : "+v"(x));
+  v = __builtin_bit_cast(V, x);
+}
 
 template <typename WT, int E>
 __device__ __forceinline__ void load_weight(float (&out)[E], const void* p, int col, int H, float offset) {
@@ -79,7 +105,7 @@ __device__ __forceinline__ void put_row(const RmsFwdArgs& p, int64_t row, int co
     typename RowVec<T>::type o;
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = (T)y[e];
-    store_row(static_cast<T*>(p.y) + row * p.ldy, col, p.H, o);
+    put_vec(static_cast<T*>(p.y) + row * p.ldy, col, p.H, o, p.past);
   }
 }
 
@@ -129,7 +155,7 @@ __global__ __launch_bounds__(kRow* kRows) void rms_fwd_kernel(RmsFwdArgs p) {
       const int col = (t + i * kRow) * E;
       if constexpr (kRes) add_residual<T, kRes>(cur.x[i], cur.r[i]);
       row_tail<T>(cur.x[i], col, p.H);
-      if constexpr (kRes) store_row(static_cast<T*>(p.sum) + row * p.lds, col, p.H, cur.x[i]);
+      if constexpr (kRes) put_vec(static_cast<T*>(p.sum) + row * p.lds, col, p.H, cur.x[i], p.past);
 #pragma unroll
       for (int e = 0; e < E; ++e) q[0] = __builtin_fmaf(to_f32(cur.x[i][e]), to_f32(cur.x[i][e]), q[0]);
     }
@@ -191,6 +217,9 @@ __global__ __launch_bounds__(kRow* kRows) void rms_bwd_kernel(RmsBwdArgs p) {
   static_assert(kRow == 64 || kRows == 1, "a work-group barrier must see one row");
   constexpr int E = RowVec<T>::E;
   typedef typename RowVec<T>::type vec_t;
+  // two vectors of bf16 each and 1024 threads: the next row has no registers left
+  // (4096 x 16384: 107 us without it, 218 with it in scratch memory)
+  constexpr bool kAhead = !(E == 8 && kRow * kVec == kMaxRegVecs);
   __shared__ SumLds<1> lds;
   int buf = 0;
   const int t = threadIdx.x % kRow, sub = threadIdx.x / kRow;
@@ -219,7 +248,7 @@ __global__ __launch_bounds__(kRow* kRows) void rms_bwd_kernel(RmsBwdArgs p) {
   }
   const float inv = 1.0f / (float)p.H;
   for (; row < p.M; row += step) {
-    if (row + step < p.M) load(nxt, row + step);
+    if (kAhead && row + step < p.M) load(nxt, row + step);
     // columns past the row's end hold dy = 0 and add nothing to any sum
     float m[1] = {0.0f};
 #pragma unroll
@@ -240,6 +269,8 @@ __global__ __launch_bounds__(kRow* kRows) void rms_bwd_kernel(RmsBwdArgs p) {
 #pragma unroll
       for (int i = 0; i < kVec; ++i) {
         vec_t o;
+        hold_packed(cur.s[i]);
+        hold_packed(cur.d[i]);
         if constexpr (kDs) row_tail<T>(cur.a[i], (t + i * kRow) * E, p.H);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
@@ -247,10 +278,11 @@ __global__ __launch_bounds__(kRow* kRows) void rms_bwd_kernel(RmsBwdArgs p) {
           const float g = __builtin_fmaf(-xh, m2, to_f32(cur.d[i][e]) * w[i][e]);
           o[e] = (T)(kDs ? __builtin_fmaf(g, cur.rstd, to_f32(cur.a[i][e])) : g * cur.rstd);
         }
-        store_row(gr, (t + i * kRow) * E, p.H, o);
+        put_vec(gr, (t + i * kRow) * E, p.H, o, p.past);
       }
     }
-    cur = nxt;
+    if constexpr (kAhead) cur = nxt;
+    else if (row + step < p.M) load(cur, row + step);
   }
   if (!p.partial) return;
   float* out = p.partial + (int64_t)blockIdx.x * p.H;
@@ -367,12 +399,14 @@ int64_t bwd_groups(int64_t M, int64_t H, int dtype) {
   const int64_t v = row_vecs(H, dtype == FLCE_DTYPE_BF16 ? 2 : 4);
   if (v <= 64) return even_grid(ceil_div(M, 4), 1024);
   if (v <= 128) return even_grid(ceil_div(M, 4), 512);
-  if (v <= 256) return even_grid(ceil_div(M, 4), 256);
-  if (v <= 1024) return even_grid(M, 512);
+  if (v <= 512) return even_grid(M, 512);
   if (v <= kMaxRegVecs) return even_grid(M, 256);
   return M < 64 ? M : 64;
 }
 
+// Threads and vectors a row, as measured (us): 8192 x 6656 bf16 with a residual
+// 67 by 512 x 2, 69 by 256 x 4, 66 by 1024 x 1 (with an 8-bit output, 8192 x
+// 7168: 67, 72, 82); one row of 6656 3.3, 4.1, 3.2.
 template <typename T, typename WT, bool kRes, bool kMx8>
 void launch_fwd(const RmsFwdArgs& p, hipStream_t st) {
   const int64_t v = row_vecs(p.H, sizeof(T));
@@ -381,21 +415,25 @@ void launch_fwd(const RmsFwdArgs& p, hipStream_t st) {
   else if (v <= 128) rms_fwd_kernel<T, WT, 64, 2, 4, kRes, kMx8><<<grid(4, 1024), 256, 0, st>>>(p);
   else if (v <= 256) rms_fwd_kernel<T, WT, 64, 4, 4, kRes, kMx8><<<grid(4, 512), 256, 0, st>>>(p);
   else if (v <= 512) rms_fwd_kernel<T, WT, 128, 4, 1, kRes, kMx8><<<grid(1, 1536), 128, 0, st>>>(p);
-  else if (v <= 1024) rms_fwd_kernel<T, WT, 256, 4, 1, kRes, kMx8><<<grid(1, 768), 256, 0, st>>>(p);
-  else if (v <= kMaxRegVecs) rms_fwd_kernel<T, WT, 512, 4, 1, kRes, kMx8><<<grid(1, 512), 512, 0, st>>>(p);
+  else if (v <= 1024) rms_fwd_kernel<T, WT, 512, 2, 1, kRes, kMx8><<<grid(1, 512), 512, 0, st>>>(p);
+  else if (v <= kMaxRegVecs) rms_fwd_kernel<T, WT, 1024, 2, 1, kRes, kMx8><<<grid(1, 512), 1024, 0, st>>>(p);
   else rms_fwd_wide_kernel<T, WT, kRes, kMx8><<<grid(1, 65536), kWide, 0, st>>>(p);
 }
 
+// As measured (us, with rms_reduce_kernel): 8192 x 6656 bf16 with ds 85 by 1024 x
+// 1 and 256 groups, 93 by 512 x 2 and 512, 111 by 256 x 4 and 512; 16384 x 2048 46
+// by 256 x 1 and 512 groups, 56 by four rows of 64 x 4; 4099 x 5003 fp32 48 by 1024
+// x 2, 55 by 512 x 4.
 template <typename T, typename WT, bool kDs>
 void launch_bwd(const RmsBwdArgs& p, int dtype, hipStream_t st) {
   const int64_t v = row_vecs(p.H, sizeof(T));
   const unsigned g = (unsigned)bwd_groups(p.M, p.H, dtype);
   if (v <= 64) rms_bwd_kernel<T, WT, 64, 1, 4, kDs><<<g, 256, 0, st>>>(p);
   else if (v <= 128) rms_bwd_kernel<T, WT, 64, 2, 4, kDs><<<g, 256, 0, st>>>(p);
-  else if (v <= 256) rms_bwd_kernel<T, WT, 64, 4, 4, kDs><<<g, 256, 0, st>>>(p);
+  else if (v <= 256) rms_bwd_kernel<T, WT, 256, 1, 1, kDs><<<g, 256, 0, st>>>(p);
   else if (v <= 512) rms_bwd_kernel<T, WT, 256, 2, 1, kDs><<<g, 256, 0, st>>>(p);
-  else if (v <= 1024) rms_bwd_kernel<T, WT, 256, 4, 1, kDs><<<g, 256, 0, st>>>(p);
-  else if (v <= kMaxRegVecs) rms_bwd_kernel<T, WT, 512, 4, 1, kDs><<<g, 512, 0, st>>>(p);
+  else if (v <= 1024) rms_bwd_kernel<T, WT, 1024, 1, 1, kDs><<<g, 1024, 0, st>>>(p);
+  else if (v <= kMaxRegVecs) rms_bwd_kernel<T, WT, 1024, 2, 1, kDs><<<g, 1024, 0, st>>>(p);
   else {
     if (p.dx) rms_bwd_wide_kernel<T, WT><<<(unsigned)(p.M < 65536 ? p.M : 65536), kWide, 0, st>>>(p);
     if (p.partial) rms_param_grad_kernel<T><<<dim3((unsigned)ceil_div(p.H, 256), g), 256, 0, st>>>(p);
@@ -414,7 +452,7 @@ int check_sizes(int64_t M, int64_t H, int dtype, int w_dtype) {
 
 // What both forward entries check and launch.
 template <bool kMx8>
-int rms_fwd(const RmsFwdArgs& p, int64_t H, hipStream_t stream, int dtype, int w_dtype) {
+int rms_fwd(RmsFwdArgs p, int64_t H, hipStream_t stream, int dtype, int w_dtype) {
   const int rc = check_sizes(p.M, H, dtype, w_dtype);
   if (rc != FLCE_OK) return rc;
   if (!(p.eps > 0.0f) || !std::isfinite(p.eps) || !std::isfinite(p.offset)) return FLCE_EINVAL;
@@ -435,6 +473,7 @@ int rms_fwd(const RmsFwdArgs& p, int64_t H, hipStream_t stream, int dtype, int w
     if (kMx8 && i == 0 && (at_x || at_r)) return FLCE_EINVAL;
     if (p.M > 1 && ((at_x && ld[i] != p.ldx) || (at_r && ld[i] != p.ldr))) return FLCE_EINVAL;
   }
+  p.past = past_caches(p.M * H * (int64_t)((p.residual ? 3 : 1) * es + os));
   ProfileScope ps(FLCE_KERNEL_RMS_NORM, stream);
   const bool b = dtype == FLCE_DTYPE_BF16, wb = w_dtype == FLCE_DTYPE_BF16;
   if (p.residual) {
@@ -454,7 +493,7 @@ int rms_fwd(const RmsFwdArgs& p, int64_t H, hipStream_t stream, int dtype, int w
 extern "C" int flce_rms_norm_fwd(const void* x, int64_t ld_x, const void* residual, int64_t ld_r, const void* weight,
                                  float offset, int64_t M, int64_t H, float eps, void* y, int64_t ld_y, void* sum,
                                  int64_t ld_s, float* rstd, hipStream_t stream, int dtype, int w_dtype) {
-  flce::RmsFwdArgs p{x, residual, weight, sum, y, nullptr, rstd, M, ld_x, ld_r, ld_s, ld_y, 0, (int)H, eps, offset};
+  flce::RmsFwdArgs p{x, residual, weight, sum, y, nullptr, rstd, M, ld_x, ld_r, ld_s, ld_y, 0, (int)H, eps, offset, 0};
   return flce::rms_fwd<false>(p, H, stream, dtype, w_dtype);
 }
 
@@ -463,7 +502,7 @@ extern "C" int flce_rms_norm_mx(const void* x, int64_t ld_x, const void* residua
                                  int64_t ld_scales, void* sum, int64_t ld_s, float* rstd, hipStream_t stream,
                                  int dtype, int w_dtype) {
   flce::RmsFwdArgs p{x,    residual, weight, sum,  y,         static_cast<uint8_t*>(scales), rstd, M,
-                     ld_x, ld_r,     ld_s,   ld_y, ld_scales, (int)H,                        eps,  offset};
+                     ld_x, ld_r,     ld_s,   ld_y, ld_scales, (int)H,                        eps,  offset, 0};
   return flce::rms_fwd<true>(p, H, stream, dtype, w_dtype);
 }
 
@@ -498,7 +537,7 @@ extern "C" int flce_rms_norm_bwd(const void* grad_y, int64_t ld_gy, const void* 
   float* partial = grad_weight ? static_cast<float*>(workspace) : nullptr;
   if (M > 0 && (grad_x || grad_weight)) {
     RmsBwdArgs p{grad_y, s, grad_x ? grad_s : nullptr, weight, rstd, grad_x, partial, M, ld_gy, ld_s, ld_gs, ld_gx,
-                 (int)H, offset};
+                 (int)H, offset, past_caches(M * H * (int64_t)(es * (2 + (grad_x ? 1 : 0) + (grad_s ? 1 : 0))))};
     ProfileScope ps(FLCE_KERNEL_RMS_NORM_BWD, stream);
     const bool b = dtype == FLCE_DTYPE_BF16, wb = w_dtype == FLCE_DTYPE_BF16;
     if (p.ds) {
