@@ -665,10 +665,11 @@ enum {
   FLCE_KERNEL_LOGITS_MX = 22,   /* flce_logits_mx */
   FLCE_KERNEL_VERIFY_SCAN = 23, /* flce_verify: maxima and weights of each row's pieces */
   FLCE_KERNEL_VERIFY_ROWS = 24, /* flce_verify: each row's cut and sum of weights */
-  FLCE_KERNEL_VERIFY_RESIDUAL = 25,/* flce_verify: accepted tokens, weight left of the target by pieces */
-  FLCE_KERNEL_VERIFY_DRAW = 26, /* flce_verify: the token drawn from what is left, outputs */
+  FLCE_KERNEL_VERIFY_RESIDUAL = 25,/* flce_verify: weight left of the target by pieces */
+  FLCE_KERNEL_VERIFY_DRAW = 26, /* flce_verify: the token drawn from what is left */
   FLCE_KERNEL_SPLIT_MX = 27,    /* flce_logits_mx: the tokens brought to 8-bit parts */
-  FLCE_KERNEL_KINDS = 28
+  FLCE_KERNEL_VERIFY_COUNT = 28,/* flce_verify: accepted tokens */
+  FLCE_KERNEL_KINDS = 29
 };
 
 /* Turn event timing on (on != 0) or off for subsequent calls.  Returns FLCE_OK. */

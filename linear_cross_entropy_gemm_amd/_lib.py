@@ -51,7 +51,7 @@ KERNEL_KINDS = ("label_scan", "fwd_logits", "row_merge", "grad_logits", "grad_h"
                 "grad_W", "finalize", "zero", "logits", "cross_entropy", "scale", "layer_norm",
                 "layer_norm_bwd", "layer_norm_reduce", "dropout", "sample_scan", "sample_pick", "rms_norm",
                 "rms_norm_bwd", "rms_norm_reduce", "pack_mx", "logits_mx", "verify_scan", "verify_rows",
-                "verify_residual", "verify_draw", "split_mx")
+                "verify_residual", "verify_draw", "split_mx", "verify_count")
 
 
 class flce_plan_t(ctypes.Structure):

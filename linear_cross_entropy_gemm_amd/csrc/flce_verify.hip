@@ -11,9 +11,10 @@
 //   1. the sampler's scan and pick leave each row's cut and sum of weights
 //      instead of a token (flce_sample.hip): all 2K + 1 rows of a sequence at
 //      once, since a row's turn is known only after the rows before it
-//   2. verify_residual_kernel: n from K pairs of logits (every work-group of a
-//      sequence finds it by itself), and the weight of r by pieces of 4096
-//   3. verify_draw_kernel: the piece in which the running sum passes u, and the
+//   2. verify_count_kernel: n from K pairs of logits, a wave per sequence, and
+//      what is known with it: the accepted tokens
+//   3. verify_residual_kernel: the weight of r by pieces of 4096
+//   4. verify_draw_kernel: the piece in which the running sum passes u, and the
 //      token in it, in index order
 // A distribution's values are formed from the logits again where they are
 // needed: 64-bit exponentials over a row's sum; r goes into integers of 2^-51,
@@ -28,7 +29,6 @@ namespace {
 
 constexpr int kVerThreads = 256;
 constexpr int kVerPiece = 4096;
-constexpr int kVerPer = kVerPiece / kVerThreads;   // logits per thread
 constexpr double kVerScale = 0x1p51;
 constexpr int64_t kMaxDrafted = 1024;
 
@@ -80,6 +80,27 @@ struct Dist {
     if (w < 0x1p-900 || (r.q > 0.0 && fixed(w, scale) < least)) return 0.0;
     return w * inv;
   }
+  // of E consecutive ones
+  template <int E>
+  __device__ __forceinline__ void probs(double (&out)[E], int64_t i, const float (&x)[E]) const {
+    if (live && plain && r.t != 0.0) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const double w = weight(x[e], r);
+        const bool in = composite(key_of(x[e]), i + e) >= cut && w >= 0x1p-900;
+        out[e] = in ? w : 0.0;
+      }
+      if (r.q > 0.0) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) out[e] = fixed(out[e], scale) < least ? 0.0 : out[e];
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) out[e] *= inv;
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) out[e] = prob(i + e, x[e]);
+    }
+  }
   __device__ __forceinline__ double prob(int64_t i) const { return prob(i, clean(to_f32(z[i]))); }
   __device__ __forceinline__ float logprob(int64_t i) const {
     if (r.t == 0.0) return 0.0f;
@@ -98,29 +119,50 @@ __device__ __forceinline__ int drafted(const VerifyArgs& v, int64_t b) {
 }
 
 // How many drafted tokens of sequence b are accepted: one wave, a lane per
-// position.
+// position.  With `put` the outputs that are known then are written: all but
+// the token that is drawn.
 template <typename T>
-__device__ __forceinline__ int count_accepted(const VerifyArgs& v, int64_t b) {
+__device__ __forceinline__ int count_accepted(const VerifyArgs& v, int64_t b, bool put) {
   const int len = drafted(v, b), lane = threadIdx.x & 63;
-  for (int i0 = 0; i0 < len; i0 += 64) {
+  int n = len;
+#pragma unroll 1
+  for (int i0 = 0; i0 < len && n == len; i0 += 64) {
     const int i = i0 + lane;
     bool ok = false;
+    int64_t x = -1;
+    float lp = kNegInf;
     if (i < len) {
-      const int64_t x = v.x[b * v.K + i];
+      x = v.x[b * v.K + i];
       const float u = v.u[b * v.K + i];
       if (x >= 0 && x < v.s.V && u >= 0.0f && u < 1.0f) {
-        const double p = Dist<T>(v.s, target_row(v, b, i)).prob(x);
+        const Dist<T> at(v.s, target_row(v, b, i));
+        const double p = at.prob(x);
         const double q = v.drafts ? Dist<T>(v.s, draft_row(v, b, i)).prob(x) : 1.0;
         ok = (double)u * q < p;
+        if (put && v.logprobs) lp = at.logprob(x);
       }
     }
     const unsigned long long bad = ~__builtin_amdgcn_ballot_w64(ok);
     if (bad) {
-      const int n = i0 + __builtin_ctzll(bad);
-      return n < len ? n : len;
+      n = i0 + __builtin_ctzll(bad);
+      if (n > len) n = len;
+    }
+    if (put && i < n) {
+      v.tokens[target_row(v, b, i)] = x;
+      if (v.logprobs) v.logprobs[target_row(v, b, i)] = lp;
     }
   }
-  return len;
+  if (put) {
+    for (int i = n + 1 + lane; i <= v.K; i += 64) {
+      v.tokens[target_row(v, b, i)] = -1;
+      if (v.logprobs) v.logprobs[target_row(v, b, i)] = kNegInf;
+    }
+    if (lane == 0) {
+      v.n[b] = n;
+      v.accepted[b] = n;
+    }
+  }
+  return n;
 }
 
 // The weights that sequence b's last token is drawn from, behind n accepted
@@ -138,50 +180,68 @@ struct Residual {
     with_q = on && v.drafts;
     certain = on && !v.drafts ? v.x[b * v.K + n] : -1;
   }
-  // both integer weights of E logits from index i on
+  // both integer weights of E logits from index i on; no branches among them in
+  // ordinary rows
   template <int E>
   __device__ __forceinline__ void weights(int64_t i, const typename RowVec<T>::type& zp,
                                           const typename RowVec<T>::type& zq, u64 (&rw)[E], u64 (&pw)[E]) const {
+    float x[E], y[E];
     bool any = false;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      any |= p.reaches(clean(to_f32(zp[e])));
+      x[e] = clean(to_f32(zp[e]));
+      y[e] = clean(to_f32(zq[e]));
+      any |= p.reaches(x[e]);
       rw[e] = pw[e] = 0;
     }
     if (!__builtin_amdgcn_ballot_w64(any)) return;
+    double a[E], c[E];
+    p.probs(a, i, x);
+#pragma unroll
+    for (int e = 0; e < E; ++e) c[e] = 0.0;
+    if (with_q) q.probs(c, i, y);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const double a = p.prob(i + e, clean(to_f32(zp[e])));
-      double c = with_q ? q.prob(i + e, clean(to_f32(zq[e]))) : 0.0;
-      if (i + e == certain) c = 1.0;
-      pw[e] = fixed(a, kVerScale);
-      rw[e] = a > c ? fixed(a - c, kVerScale) : 0;
+      if (i + e == certain) c[e] = 1.0;
+      pw[e] = fixed(a[e], kVerScale);
+      rw[e] = fixed(__builtin_fmax(a[e] - c[e], 0.0), kVerScale);
     }
   }
 };
 
+// One wave per sequence.
 template <typename T>
+__global__ __launch_bounds__(64) void verify_count_kernel(VerifyArgs v) {
+  count_accepted<T>(v, blockIdx.x, true);
+}
+
+// With kCount every work-group finds n by itself.
+template <typename T, bool kCount>
 __global__ __launch_bounds__(kVerThreads) void verify_residual_kernel(VerifyArgs v) {
-  constexpr int E = RowVec<T>::E, kVec = kVerPer / E;
-  __shared__ int n_of;
+  constexpr int E = RowVec<T>::E, kVec = kVerPiece / (kVerThreads * E);
   __shared__ u64 part[2][kVerThreads / 64];
+  __shared__ int n_of;
   const int64_t b = blockIdx.x / v.pieces;
   const int piece = blockIdx.x % v.pieces;
-  if (threadIdx.x < 64) {
-    const int n = count_accepted<T>(v, b);
-    if (threadIdx.x == 0) n_of = n;
+  int n;
+  if (kCount) {
+    if (threadIdx.x < 64) {
+      n = count_accepted<T>(v, b, piece == 0);
+      if (threadIdx.x == 0) n_of = n;
+    }
+    __syncthreads();
+    n = n_of;
+  } else {
+    n = v.n[b];
   }
-  __syncthreads();
-  const int n = n_of;
-  if (piece == 0 && threadIdx.x == 0) v.n[b] = n;
   const Residual<T> res(v, b, n);
   u64 rs = 0, ps = 0;
   if (res.p.live) {
-    const int64_t base = (int64_t)piece * kVerPiece;
+    const int64_t base = (int64_t)piece * kVerPiece + threadIdx.x * E;
     typename RowVec<T>::type zp[kVec], zq[kVec];
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
-      const int64_t c = base + (j * kVerThreads + threadIdx.x) * E;
+      const int64_t c = base + j * kVerThreads * E;
       zp[j] = load_row(res.p.z, c, v.s.V, kNegInf);
       zq[j] = zp[j];
       if (res.with_q) zq[j] = load_row(res.q.z, c, v.s.V, kNegInf);
@@ -189,7 +249,7 @@ __global__ __launch_bounds__(kVerThreads) void verify_residual_kernel(VerifyArgs
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
       u64 rw[E], pw[E];
-      res.weights(base + (j * kVerThreads + threadIdx.x) * E, zp[j], zq[j], rw, pw);
+      res.weights(base + j * kVerThreads * E, zp[j], zq[j], rw, pw);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         rs += rw[e];
@@ -210,86 +270,86 @@ __global__ __launch_bounds__(kVerThreads) void verify_residual_kernel(VerifyArgs
   }
 }
 
+// One vector of the piece per thread.
 template <typename T>
-__global__ __launch_bounds__(kVerThreads) void verify_draw_kernel(VerifyArgs v) {
-  constexpr int E = RowVec<T>::E, kVec = kVerPer / E;
-  __shared__ GroupScratch<kVerThreads> scratch;
+__global__ __launch_bounds__(kVerPiece / RowVec<T>::E) void verify_draw_kernel(VerifyArgs v) {
+  constexpr int E = RowVec<T>::E, TH = kVerPiece / E;
+  __shared__ GroupScratch<TH> scratch;
   __shared__ int found;
   __shared__ u64 rest;
-  __shared__ int64_t tok;
   const int64_t b = blockIdx.x;
   const int t = threadIdx.x, n = v.n[b];
   const float u = v.u_draw[b];
   const Residual<T> res(v, b, n);
-  if (t == 0) tok = -1;
+  const int64_t at = target_row(v, b, n);
   // consecutive pieces per thread; p itself where nothing is left of r
-  const int per = (v.pieces + kVerThreads - 1) / kVerThreads;
+  const int per = (v.pieces + TH - 1) / TH;
   const u64* sums = v.rsum + b * v.pieces;
   u64 own = 0, all = 0, before = 0;
   for (int way = 0; way < 2; ++way) {
     if (way) sums = v.psum + b * v.pieces;
     own = 0;
     for (int i = t * per; i < (t + 1) * per && i < v.pieces; ++i) own += sums[i];
-    before = group_scan<kVerThreads>(own, all, scratch);
+    before = group_scan<TH>(own, all, scratch);
     if (all) break;
   }
   const bool from_p = sums != v.rsum + b * v.pieces;
-  if (all && u >= 0.0f && u < 1.0f) {
-    const u64 target = draw_target(u, all);
-    if (before <= target && target < before + own) {   // one thread
-      int i = t * per;
-      for (; target >= before + sums[i]; ++i) before += sums[i];
-      found = i;
-      rest = target - before;
+  if (!all || !(u >= 0.0f && u < 1.0f)) {
+    if (t == 0) {
+      v.tokens[at] = -1;
+      if (v.logprobs) v.logprobs[at] = kNegInf;
     }
-    __syncthreads();
-    const int64_t c = (int64_t)found * kVerPiece + t * kVerPer;
-    u64 w[kVec][E];
-    own = 0;
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      const typename RowVec<T>::type zp = load_row(res.p.z, c + j * E, v.s.V, kNegInf);
-      typename RowVec<T>::type zq = zp;
-      if (res.with_q) zq = load_row(res.q.z, c + j * E, v.s.V, kNegInf);
-      u64 rw[E], pw[E];
-      res.weights(c + j * E, zp, zq, rw, pw);
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        w[j][e] = from_p ? pw[e] : rw[e];
-        own += w[j][e];
-      }
-    }
-    before = group_scan<kVerThreads>(own, all, scratch);
-    if (before <= rest && rest < before + own) {   // one thread
-      int64_t at = c;
-#pragma unroll
-      for (int j = 0; j < kVec; ++j)
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          before += w[j][e];
-          if (before <= rest) at = c + j * E + e + 1;
-        }
-      tok = at;
-    }
+    return;
+  }
+  const u64 target = draw_target(u, all);
+  if (before <= target && target < before + own) {   // one thread
+    int i = t * per;
+    for (; target >= before + sums[i]; ++i) before += sums[i];
+    found = i;
+    rest = target - before;
   }
   __syncthreads();
-  for (int i = t; i <= v.K; i += kVerThreads) {
-    const int64_t x = i < n ? v.x[b * v.K + i] : i == n ? tok : -1;
-    const int64_t at = b * (v.K + 1) + i;
+  const int64_t c = (int64_t)found * kVerPiece + t * E;
+  const typename RowVec<T>::type zp = load_row(res.p.z, c, v.s.V, kNegInf);
+  typename RowVec<T>::type zq = zp;
+  if (res.with_q) zq = load_row(res.q.z, c, v.s.V, kNegInf);
+  u64 rw[E], pw[E];
+  res.weights(c, zp, zq, rw, pw);
+  own = 0;
+#pragma unroll
+  for (int e = 0; e < E; ++e) own += from_p ? pw[e] : rw[e];
+  before = group_scan<TH>(own, all, scratch);
+  if (before <= rest && rest < before + own) {   // one thread
+    int64_t x = c;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      before += from_p ? pw[e] : rw[e];
+      if (before <= rest) x = c + e + 1;
+    }
     v.tokens[at] = x;
-    if (v.logprobs) v.logprobs[at] = x < 0 ? kNegInf : Dist<T>(v.s, target_row(v, b, i)).logprob(x);
+    if (v.logprobs) v.logprobs[at] = res.p.logprob(x);
   }
-  if (t == 0) v.accepted[b] = n;
 }
 
 template <typename T>
 void launch_verify(const VerifyArgs& v, hipStream_t stream) {
-  {
+  // The sequences' accepted counts by themselves, or again in every work-group
+  // where all of those are on the chip at once: 7 us against 5 + 6 with one
+  // sequence of 4 tokens, 37 against 6 + 32 with 32 of 7 (202048 logits).
+  const unsigned g = (unsigned)(v.B * v.pieces);
+  if (g <= 1024) {
     ProfileScope ps(FLCE_KERNEL_VERIFY_RESIDUAL, stream);
-    verify_residual_kernel<T><<<(unsigned)(v.B * v.pieces), kVerThreads, 0, stream>>>(v);
+    verify_residual_kernel<T, true><<<g, kVerThreads, 0, stream>>>(v);
+  } else {
+    {
+      ProfileScope ps(FLCE_KERNEL_VERIFY_COUNT, stream);
+      verify_count_kernel<T><<<(unsigned)v.B, 64, 0, stream>>>(v);
+    }
+    ProfileScope ps(FLCE_KERNEL_VERIFY_RESIDUAL, stream);
+    verify_residual_kernel<T, false><<<g, kVerThreads, 0, stream>>>(v);
   }
   ProfileScope ps(FLCE_KERNEL_VERIFY_DRAW, stream);
-  verify_draw_kernel<T><<<(unsigned)v.B, kVerThreads, 0, stream>>>(v);
+  verify_draw_kernel<T><<<(unsigned)v.B, kVerPiece / RowVec<T>::E, 0, stream>>>(v);
 }
 
 struct VerifyLayout {
