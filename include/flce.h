@@ -490,13 +490,13 @@ size_t flce_logits_mx_workspace_size(int64_t N, int64_t H, int x_dtype);
  * Softcap and multiplier as flce_logits.  A bf16 or fp32 x enters as sums of
  * E4M3 values under one scale for 32 columns.  bf16: exactly where it is at least
  * 2^-14 of the largest of its 32, else rounded to 2^-22 of that largest; fp32:
- * rounded to 2^-24 of that largest.  Where one of the 32 is not finite, all of
- * them count as NaN.  Sums are fp32; with 8-bit and bf16 rows the matrix unit
- * cuts products below 2^-13 of the largest of the 8 that it adds at a time (sums
- * of random rows end within 4e-6 of themselves; fp32 rows, whose parts are whole
- * numbers, within 3e-7).  z is rounded once.  N <= 2^20,
- * V <= 2^24, H <= 2^21 and N Kp <= 2^34 (else FLCE_EUNSUPPORTED); N = 0 does
- * nothing.  Enqueued on `stream`; nothing is allocated, nothing synchronises.
+ * rounded to 2^-24 of that largest (and 2^-137).  Where one of the 32 is not
+ * finite, all of them count as NaN.  Sums are fp32; with 8-bit and bf16 rows the
+ * matrix unit cuts products below 2^-13 of the largest of the 8 that it adds at
+ * a time (sums of random rows end within 4e-6 of themselves; fp32 rows, whose
+ * parts are whole numbers, within 3e-7).  z is rounded once.  N <= 2^20, V <=
+ * 2^24, H <= 2^21, N Kp <= 2^34 and N V <= 2^35 (else FLCE_EUNSUPPORTED); N = 0
+ * does nothing.  Enqueued on `stream`; nothing is allocated, nothing synchronises.
  * Returns FLCE_OK, FLCE_EINVAL, FLCE_EUNSUPPORTED, FLCE_EWORKSPACE or
  * FLCE_EDEVICE.
  */
@@ -600,8 +600,8 @@ size_t flce_verify_workspace_size(int64_t B, int64_t K, int64_t V, int dtype, in
  * r, either side is possible.  Weights of r go into sums in units of 2^-51: a
  * token with less is not drawn.  The same call gives the same bits.
  * K <= 1024, B <= 2^21, and with R = B (2 K + 1) rows (B (K + 1) without a
- * draft) R <= 2^21, V <= 2^24 and R ceil(V / 8192) <= 2^23 (else
- * FLCE_EUNSUPPORTED); K = 0 samples.  Enqueued on `stream`; nothing is
+ * draft) R <= 2^21, V <= 2^24, R ceil(V / 8192) <= 2^23 and B ceil(V / 4096) <
+ * 2^24 (else FLCE_EUNSUPPORTED); K = 0 samples.  Enqueued on `stream`; nothing is
  * allocated, nothing synchronises.  Returns FLCE_OK, FLCE_EINVAL (also for a
  * scalar parameter out of its range), FLCE_EUNSUPPORTED, FLCE_EWORKSPACE or
  * FLCE_EDEVICE.

@@ -8,8 +8,8 @@
 // through registers once and are never converted: the scaled matrix
 // instruction takes E2M1 rows with a scale for every 32 elements as they lie in
 // memory, next to E4M3 rows with theirs.  So the tokens are brought to E4M3
-// parts, x = sum_p part_p 2^(code - s p - 127): one for rows that are in 8 bits
-// already, two with s = 4 for bf16 (8 significant bits), five with s = 5 for fp32.
+// parts, each under the block's scale times a power of two: one for rows that are
+// in 8 bits already, two for bf16 (8 significant bits), five for fp32.
 //
 // What the instruction keeps (measured with single products): it adds the 8
 // products of columns 8 i to 8 i + 7 down to 2^-13 of the largest, the 16 sums
@@ -108,11 +108,15 @@ __device__ __forceinline__ void mx_mma(int byte, f32x4& acc, const u32x4& a, con
   else mx_mma<3>(acc, a, b, sa, sb);
 }
 
-// Parts of a token.  fp32 rows have five whose elements are whole numbers up to
-// 16, digits of base 32: see the top.
+// Parts of a token, and how far part q's code lies below the block's.  fp32 rows
+// have five whose elements are whole numbers up to 16, digits of base 32 (see the
+// top), kept in units down to 2^-9, E4M3's last: part q's unit is 2^-min(5 q, 9),
+// and its code has only the rest to go.
 constexpr int kDigits = 5;
 template <int kParts>
-__device__ __forceinline__ constexpr int part_shift() { return kParts == kDigits ? 5 : 4; }
+__device__ __forceinline__ constexpr uint32_t part_down(int q) {
+  return kParts == kDigits ? (5 * q > 9 ? 5 * q - 9 : 0) : 4 * q;
+}
 
 // Their steps are summed by themselves, smallest part first, and added to the
 // sums so far by the vector unit, which rounds to nearest.  (bf16 and 8-bit
@@ -138,36 +142,44 @@ __device__ __forceinline__ uint32_t own_scales(const u32x4& x) {
 
 // 8 values of a block, whose other values are with the other three lanes of an
 // aligned group of four, as E4M3 parts; returns the block's code.  Codes below
-// kShift (kParts - 1) are raised to it, so that no part's is negative.
+// the last part's part_down are raised to it, so that no part's is negative.
 template <int kParts>
 __device__ __forceinline__ uint32_t split8(const float (&v)[8], u32x2 (&out)[kParts]) {
-  constexpr int kShift = part_shift<kParts>();
   const uint32_t bits = block_max_bits<8>(v);
   uint32_t code = kParts == kDigits ? bits >> 23 : mx8_code(bits);
   if (kParts == kDigits) code = code == 255 ? 255 : code < 3 ? 0 : code - 3;   // the largest: 8 to 16 units
-  if (code < kShift * (kParts - 1)) code = kShift * (kParts - 1);
+  if (code < part_down<kParts>(kParts - 1)) code = part_down<kParts>(kParts - 1);
   const float inv = code == 255 ? 1.0f : mx_inverse(code);
-  // next to the largest float no part may round the sum up to 2^128
-  const float top = code == 247 && kParts != kDigits ? 240.0f : 448.0f;
   float x[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] = code == 255 ? 0.0f : v[e] * inv;   // a block without a scale is NaN by its code
+  // next to the largest float no part may round the sum up to 2^128
+  const float top = code == 247 ? 240.0f : 448.0f;
 #pragma unroll
   for (int p = 0; p < kParts; ++p) {
     float y[8];
+    if constexpr (kParts == kDigits) {
+      const float unit = 1.0f / (float)(1 << (5 * p < 9 ? 5 * p : 9));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = kParts == kDigits ? rintf(x[e]) : __builtin_amdgcn_fmed3f(x[e], -top, top);
+      for (int e = 0; e < 8; ++e) {
+        const float d = rintf(x[e]);
+        y[e] = d * unit;
+        x[e] = (x[e] - d) * 32.0f;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = __builtin_amdgcn_fmed3f(x[e], -top, top);
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * h], y[4 * h + 1], 0, false);
       w = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * h + 2], y[4 * h + 3], w, true);
       out[p][h] = (uint32_t)w;
-      if (p + 1 < kParts) {
-        constexpr float up = 1 << kShift;
-        x[4 * h] = (x[4 * h] - __builtin_amdgcn_cvt_f32_fp8(w, 0)) * up;
-        x[4 * h + 1] = (x[4 * h + 1] - __builtin_amdgcn_cvt_f32_fp8(w, 1)) * up;
-        x[4 * h + 2] = (x[4 * h + 2] - __builtin_amdgcn_cvt_f32_fp8(w, 2)) * up;
-        x[4 * h + 3] = (x[4 * h + 3] - __builtin_amdgcn_cvt_f32_fp8(w, 3)) * up;
+      if (kParts != kDigits && p + 1 < kParts) {
+        x[4 * h] = (x[4 * h] - __builtin_amdgcn_cvt_f32_fp8(w, 0)) * 16.0f;
+        x[4 * h + 1] = (x[4 * h + 1] - __builtin_amdgcn_cvt_f32_fp8(w, 1)) * 16.0f;
+        x[4 * h + 2] = (x[4 * h + 2] - __builtin_amdgcn_cvt_f32_fp8(w, 2)) * 16.0f;
+        x[4 * h + 3] = (x[4 * h + 3] - __builtin_amdgcn_cvt_f32_fp8(w, 3)) * 16.0f;
       }
     }
   }
@@ -380,7 +392,7 @@ __global__ __launch_bounds__(1024) void mx_logits_stream_kernel(MxArgs p, int ti
           f32x4 sum = step_sums<kParts>(acc[0][0]);
 #pragma unroll
           for (int q = kParts - 1; q >= 0; --q)
-            mx_mma(s, sum, a[s], token_columns(mine + q * part + (c + s) * kStep), scale, xc - q * part_shift<kParts>() * 0x01010101u);
+            mx_mma(s, sum, a[s], token_columns(mine + q * part + (c + s) * kStep), scale, xc - part_down<kParts>(q) * 0x01010101u);
           add_step<kParts>(acc[0][0], sum);
         }
       }
@@ -448,12 +460,14 @@ __global__ __launch_bounds__(64 * kWv * kWt) void mx_logits_tile_kernel(MxArgs p
   const int w_row = p.steps * 64, s_row = p.steps * 4, x_row = (int)p.ldx, c_row = (int)p.ldxs;
   const u32x4s from_w = buffer_of(p.w + v0 * w_row, (int64_t)rows * w_row);
   const u32x4s from_s = buffer_of(p.ws + v0 * s_row, (int64_t)rows * s_row);
-  const u32x4s from_c = buffer_of(p.xs + n0 * p.ldxs, tokens * p.ldxs);
+  // (the tokens' rows may lie closer than their length, or all be one)
+  const int64_t x_bytes = (tokens - 1) * p.ldx + (int64_t)p.steps * kStep;
+  const u32x4s from_c = buffer_of(p.xs + n0 * p.ldxs, (tokens - 1) * p.ldxs + p.steps * 4);
   u32x4s from_x[S::x_each];   // the part that the wave's m-th load is of
 #pragma unroll
   for (int m = 0; m < S::x_each; ++m) {
     const int q = (wave + m * S::waves) % S::x_loads / S::x_part;
-    from_x[m] = buffer_of(static_cast<const uint8_t*>(p.x) + (q * p.N + n0) * p.ldx, tokens * p.ldx);
+    from_x[m] = buffer_of(static_cast<const uint8_t*>(p.x) + (q * p.N + n0) * p.ldx, x_bytes);
   }
   const uint32_t at = lds_address(lds), at_s = at + kStages * S::stage;
 
@@ -545,7 +559,7 @@ __global__ __launch_bounds__(64 * kWv * kWt) void mx_logits_tile_kernel(MxArgs p
             const i32x4v hi = *reinterpret_cast<const i32x4v*>(x + ((u * 8 + g + 4) ^ x_sw) * 16);
             const i32x8v b = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 #pragma unroll
-            for (int i = 0; i < kRt; ++i) mx_mma(s, sum[i], a[i], b, scale[i], code[n] - q * part_shift<kParts>() * 0x01010101u);
+            for (int i = 0; i < kRt; ++i) mx_mma(s, sum[i], a[i], b, scale[i], code[n] - part_down<kParts>(q) * 0x01010101u);
           }
 #pragma unroll
           for (int i = 0; i < kRt; ++i) add_step<kParts>(acc[i][n], sum[i]);
@@ -737,7 +751,8 @@ extern "C" int flce_logits_mx(const void* x, int64_t ld_x, const void* x_scales,
     return FLCE_EINVAL;
   if (N > (int64_t(1) << 20) || V > (int64_t(1) << 24) || H > (int64_t(1) << 21)) return FLCE_EUNSUPPORTED;
   const int64_t steps = ceil_div(H, kStep), vecs = steps * 16;
-  if (N * vecs > (int64_t(1) << 31)) return FLCE_EUNSUPPORTED;   // a launch holds fewer than 2^32 threads
+  // a launch holds fewer than 2^32 threads (16 logits a thread of the products)
+  if (N * vecs > (int64_t(1) << 31) || N * V > (int64_t(1) << 35)) return FLCE_EUNSUPPORTED;
   if (N == 0) return FLCE_OK;
   const bool mx8 = x_dtype == FLCE_DTYPE_MX8;
   const uintptr_t es = mx8 ? 1 : x_dtype == FLCE_DTYPE_BF16 ? 2 : 4, os = dtype == FLCE_DTYPE_BF16 ? 2 : 4;

@@ -364,7 +364,7 @@ VerifyLayout verify_layout(int64_t B, int64_t K, int64_t V, bool drafts) {
   const int64_t R = B * (drafts ? 2 * K + 1 : K + 1);
   l.rows = sample_layout(R, V);
   l.pieces = ceil_div(V, kVerPiece);
-  if (l.rows.total == 0) return l;
+  if (l.rows.total == 0 || B * l.pieces >= (int64_t(1) << 24)) return l;   // launches of fewer than 2^32 threads
   auto pad = [](size_t b) { return (b + 255) & ~size_t(255); };
   l.stats = pad(l.rows.total);
   l.n = l.stats + pad((size_t)R * sizeof(RowStat));

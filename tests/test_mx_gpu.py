@@ -223,6 +223,44 @@ def test_mx8_rows_of_every_alignment(N, H):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f32", "mx8"])
+@pytest.mark.parametrize("N", [2, 7, 40, 130])
+def test_rows_that_overlap(N, kind):
+    """One row for all tokens, and windows that lie closer than their length:
+    the logits of the same rows apart, bit for bit."""
+    import torch
+    import linear_cross_entropy_gemm_amd as L
+    H = 1024
+    q = L.mx4_pack(_rand((333, H), "f32", 9, 0.05))
+    for step in (0, 16, 512):
+        x = _rand((1, step * (N - 1) + H), "bf16" if kind == "mx8" else kind, 10)[0]
+        if kind == "mx8":
+            s = torch.randint(120, 130, (step // 32 * (N - 1) + H // 32 + 512,), dtype=torch.uint8, device="cuda")
+            x = x.clamp(-400, 400).to(torch.float8_e4m3fn)
+            data = torch.as_strided(x, (N, H), (step, 1))
+            scales = torch.as_strided(s.view(torch.float8_e8m0fnu), (N, H // 32), (step // 32, 1))
+            rows = L.Mx8Rows(data, scales)
+            apart = L.Mx8Rows(data.view(torch.uint8).clone().view(data.dtype).contiguous(),
+                              scales.view(torch.uint8).clone().view(scales.dtype).contiguous())
+        else:
+            rows = torch.as_strided(x, (N, H), (step, 1))
+            apart = rows.clone().contiguous()
+        z = L.logits_mx4(rows, q)
+        assert z.equal(L.logits_mx4(apart, q))
+        assert step or (z == z[:1]).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_far_scales(kind):
+    """Tokens and weights near both ends of the exponent's range, whose products
+    are ordinary numbers."""
+    import linear_cross_entropy_gemm_amd as L
+    for up in (100, -90):
+        q = L.mx4_pack(_rand((200, 300), "f32", 11, 2.0 ** up))
+        x = _rand((20, 300), kind, 12, 2.0 ** -up)
+        _check_logits(L.logits_mx4(x, q), _np(x), _weights(q), 0.0, 1.0, kind, 3 if kind == "f32" else 1)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32", "mx8"])
 def test_special_values(kind):
     """What is not finite stays in its row, and in its vocabulary entry."""
     import torch
@@ -258,7 +296,8 @@ def test_special_values(kind):
 
 
 def test_fp32_parts_are_exact():
-    """One nonzero column and a weight of 1 return x itself, over its range."""
+    """One nonzero column and a weight of 1 return x itself, over its range: the
+    last digit's unit is 2^-136 at least, a 24th bit of 2^-113."""
     import torch
     import linear_cross_entropy_gemm_amd as L
     W = torch.zeros(16, 128, device="cuda")
@@ -266,7 +305,7 @@ def test_fp32_parts_are_exact():
     q = L.mx4_pack(W)
     v = torch.randn(1000, device="cuda") * 10.0 ** torch.linspace(-30, 37.9, 1000, device="cuda")
     v[0], v[1], v[2] = 3.4028234663852886e38, -3.4028234663852886e38, 1.0 + 2.0 ** -23
-    v = torch.where(v.isfinite(), v, 1.5)
+    v = torch.where(v.isfinite() & (v.abs() >= 2.0 ** -113), v, 1.5)
     x = torch.zeros(1000, 128, device="cuda")
     x[:, 17] = v
     assert torch.equal(L.logits_mx4(x, q)[:, 3], v)

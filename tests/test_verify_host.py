@@ -58,7 +58,8 @@ def test_verify_workspace_size():
         b = L.flce_verify_workspace_size(B, K, V, dt, d)
         assert b >= 256 and b % 256 == 0
         assert b >= L.flce_sample_workspace_size(B * (2 * K + 1 if d else K + 1), V, dt)
-    for bad in [(-1, 4, 8, 0, 1), (1, -1, 8, 0, 1), (1, 1, 0, 0, 1), (1, 1, 8, 2, 1), (1, 1025, 8, 0, 1)]:
+    for bad in [(-1, 4, 8, 0, 1), (1, -1, 8, 0, 1), (1, 1, 0, 0, 1), (1, 1, 8, 2, 1), (1, 1025, 8, 0, 1),
+                (1 << 20, 0, 1 << 16, 0, 0)]:
         assert L.flce_verify_workspace_size(*bad) == 0
 
 
