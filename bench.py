@@ -59,7 +59,8 @@ def kernel_source_hash() -> str:
     traffic figure measured on other kernels or launch plans is stale."""
     m = hashlib.sha256()
     # the operators before and after the head share no kernel with its GEMMs
-    others = ("flce_norm.hip", "flce_dropout.hip", "flce_sample.hip", "row_ops.hpp")
+    others = ("flce_norm.hip", "flce_rms.hip", "flce_mx.hip", "flce_dropout.hip", "flce_sample.hip", "flce_verify.hip",
+              "row_ops.hpp", "mx_ops.hpp", "sample_ops.hpp", "sample_rows.hpp")
     files = [f for f in glob.glob(os.path.join(CSRC, "*"))
              if (f.endswith((".hip", ".hpp")) or os.path.basename(f) == "flce_plan.cpp")
              and os.path.basename(f) not in others]

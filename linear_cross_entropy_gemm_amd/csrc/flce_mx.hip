@@ -101,7 +101,8 @@ __device__ __forceinline__ void mx_mma(f32x4& acc, const u32x4& a, const i32x8v&
   acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide, b, acc, 4, 0, kByte, (int)sa, kByte, (int)sb);
   asm("" : "+a"(acc) : "v"(a), "v"(b));
 }
-__device__ __forceinline__ void mx_mma(int byte, f32x4& acc, const u32x4& a, const i32x8v& b, uint32_t sa, uint32_t sb) {
+__device__ __forceinline__ void mx_mma(int byte, f32x4& acc, const u32x4& a, const i32x8v& b, uint32_t sa,
+                                       uint32_t sb) {
   if (byte == 0) mx_mma<0>(acc, a, b, sa, sb);   // (byte is a constant where this is used)
   else if (byte == 1) mx_mma<1>(acc, a, b, sa, sb);
   else if (byte == 2) mx_mma<2>(acc, a, b, sa, sb);
@@ -364,7 +365,8 @@ __global__ __launch_bounds__(1024) void mx_logits_stream_kernel(MxArgs p, int ti
         *reinterpret_cast<u32x4*>(lds + n * row + kv * 16) = *reinterpret_cast<const u32x4*>(x + n * p.ldx + kv * 16);
     for (int i = threadIdx.x; i < N * p.steps; i += threads) {
       const int n = i / p.steps, s = i % p.steps;
-      *reinterpret_cast<uint32_t*>(codes + n * crow + s * 4) = *reinterpret_cast<const uint32_t*>(p.xs + n * p.ldxs + s * 4);
+      const uint8_t* from = p.xs + n * p.ldxs + s * 4;
+      *reinterpret_cast<uint32_t*>(codes + n * crow + s * 4) = *reinterpret_cast<const uint32_t*>(from);
     }
   }
   __syncthreads();
@@ -392,7 +394,8 @@ __global__ __launch_bounds__(1024) void mx_logits_stream_kernel(MxArgs p, int ti
           f32x4 sum = step_sums<kParts>(acc[0][0]);
 #pragma unroll
           for (int q = kParts - 1; q >= 0; --q)
-            mx_mma(s, sum, a[s], token_columns(mine + q * part + (c + s) * kStep), scale, xc - part_down<kParts>(q) * 0x01010101u);
+            mx_mma(s, sum, a[s], token_columns(mine + q * part + (c + s) * kStep), scale,
+                   xc - part_down<kParts>(q) * 0x01010101u);
           add_step<kParts>(acc[0][0], sum);
         }
       }
@@ -522,7 +525,7 @@ __global__ __launch_bounds__(64 * kWv * kWt) void mx_logits_tile_kernel(MxArgs p
   for (int i = 0; i < kRt; ++i)
 #pragma unroll
     for (int j = 0; j < kNt; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-  int use = 0, fill = (kStages - 1) * S::stage, group = 0;   // byte offsets of the stage in use and the one to be filled
+  int use = 0, fill = (kStages - 1) * S::stage, group = 0;   // offsets of the stage in use and the one to be filled
   for (int c = 0; c < p.steps; c += 4, group ^= 1) {
     uint32_t scale[kRt], code[kNt];
 #pragma unroll
@@ -559,7 +562,8 @@ __global__ __launch_bounds__(64 * kWv * kWt) void mx_logits_tile_kernel(MxArgs p
             const i32x4v hi = *reinterpret_cast<const i32x4v*>(x + ((u * 8 + g + 4) ^ x_sw) * 16);
             const i32x8v b = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 #pragma unroll
-            for (int i = 0; i < kRt; ++i) mx_mma(s, sum[i], a[i], b, scale[i], code[n] - part_down<kParts>(q) * 0x01010101u);
+            for (int i = 0; i < kRt; ++i)
+              mx_mma(s, sum[i], a[i], b, scale[i], code[n] - part_down<kParts>(q) * 0x01010101u);
           }
 #pragma unroll
           for (int i = 0; i < kRt; ++i) add_step<kParts>(acc[i][n], sum[i]);
@@ -584,8 +588,8 @@ template <int kParts, int kG, bool kInline>
 void launch_stream(const MxArgs& p, int waves, hipStream_t st) {
   const int64_t tiles = ceil_div(p.V, 16);
   const int64_t bytes = stream_tokens(p.N, p.steps, kParts) + waves * ring_bytes(kG);
-  mx_logits_stream_kernel<kParts, kG, kInline><<<(unsigned)(tiles < 256 ? tiles : 256), waves * 64, (size_t)bytes, st>>>(
-      p, (int)tiles);
+  const unsigned g = (unsigned)(tiles < 256 ? tiles : 256);
+  mx_logits_stream_kernel<kParts, kG, kInline><<<g, waves * 64, (size_t)bytes, st>>>(p, (int)tiles);
 }
 
 template <int kParts, int kWv, int kWt, int kRt, int kNt, int kU, int kStages>
@@ -766,8 +770,8 @@ extern "C" int flce_logits_mx(const void* x, int64_t ld_x, const void* x_scales,
   uint8_t* codes = parts + t.codes;
   // rows in 8 bits that are whole groups of four steps are read where they are;
   // one or two bf16 rows are split by the work-groups (a launch less)
-  const bool ready = mx8 && H % (4 * kStep) == 0 && ld_x % 16 == 0 && ld_x <= kMostRow && ld_xs <= kMostRow && addr(x) % 16 == 0 && ld_xs % 16 == 0 &&
-                     addr(x_scales) % 16 == 0;
+  const bool ready = mx8 && H % (4 * kStep) == 0 && ld_x <= kMostRow && ld_xs <= kMostRow && ld_x % 16 == 0 &&
+                     ld_xs % 16 == 0 && addr(x) % 16 == 0 && addr(x_scales) % 16 == 0;
   const bool raw = x_dtype == FLCE_DTYPE_BF16 && N <= 2 && stream_tokens(N, steps, 2) <= kLdsMost - 4 * ring_bytes(1);
   MxArgs p{parts, codes, t.ldp, t.ldc, static_cast<const uint8_t*>(packed), static_cast<const uint8_t*>(scales), logits,
            ld_logits, N, V, (int)H, (int)steps, softcap_T > 0.0f ? softcap_T : 0.0f, multiplier,
@@ -787,8 +791,8 @@ extern "C" int flce_logits_mx(const void* x, int64_t ld_x, const void* x_scales,
       mx_split_kernel<bf16, 2><<<g, 256, 0, stream>>>(static_cast<const bf16*>(x), ld_x, N, (int)H, (int)vecs, parts,
                                                       t.ldp, codes, t.ldc);
     else
-      mx_split_kernel<float, kDigits><<<g, 256, 0, stream>>>(static_cast<const float*>(x), ld_x, N, (int)H, (int)vecs, parts,
-                                                       t.ldp, codes, t.ldc);
+      mx_split_kernel<float, kDigits><<<g, 256, 0, stream>>>(static_cast<const float*>(x), ld_x, N, (int)H, (int)vecs,
+                                                             parts, t.ldp, codes, t.ldc);
   }
   ProfileScope ps(FLCE_KERNEL_LOGITS_MX, stream);
   if (mx8) launch_products<1>(p, false, stream);

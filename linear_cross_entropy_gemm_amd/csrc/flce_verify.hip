@@ -9,7 +9,7 @@
 // which leaves every token distributed as if drawn from p.
 //
 //   1. the sampler's scan and pick leave each row's cut and sum of weights
-//      instead of a token (flce_sample.hip): all 2K + 1 rows of a sequence at
+//      instead of a token (sample_rows.hpp): all 2K + 1 rows of a sequence at
 //      once, since a row's turn is known only after the rows before it
 //   2. verify_count_kernel: n from K pairs of logits, a wave per sequence, and
 //      what is known with it: the accepted tokens
@@ -21,7 +21,7 @@
 // whose sums are exact in any order.
 #include <cmath>
 
-#include "sample_ops.hpp"
+#include "sample_rows.hpp"
 
 namespace flce {
 
@@ -33,7 +33,7 @@ constexpr double kVerScale = 0x1p51;
 constexpr int64_t kMaxDrafted = 1024;
 
 struct VerifyArgs {
-  SampleArgs s;   // rows, parameters and what the sampler's kernels left
+  StatsArgs s;   // rows, parameters and what the sampler's kernels left
   bool drafts;    // the draft's logits are given (else its tokens are certain)
   const int64_t* x;
   const int64_t* lens;   // null: K
@@ -58,7 +58,7 @@ struct Dist {
   double scale, inv;   // probability = weight * inv
   bool live, plain;
 
-  __device__ __forceinline__ Dist(const SampleArgs& a, int64_t row) : r(row_params<true>(a, row)) {
+  __device__ __forceinline__ Dist(const StatsArgs& a, int64_t row) : r(row_params<true>(a, row)) {
     const RowStat st = a.stats[row];
     z = row_logits<T, true>(a, row);
     live = st.live != 0;
@@ -409,7 +409,7 @@ extern "C" int flce_verify(const void* target, int64_t ld_target, const void* dr
   if (workspace_bytes < l.total) return FLCE_EWORKSPACE;
   char* ws = static_cast<char*>(workspace);
   VerifyArgs v{};
-  SampleArgs& a = v.s;
+  StatsArgs& a = v.s;
   a.z = target;
   a.ld = ld_target;
   a.z2 = draft;
@@ -435,7 +435,7 @@ extern "C" int flce_verify(const void* target, int64_t ld_target, const void* dr
   v.tokens = tokens;
   v.accepted = accepted;
   v.logprobs = logprobs;
-  launch_row_stats(a, stream, dtype);
+  launch_rows<true>(a, stream, dtype, FLCE_KERNEL_VERIFY_SCAN, FLCE_KERNEL_VERIFY_ROWS);
   if (dtype == FLCE_DTYPE_BF16)
     launch_verify<bf16>(v, stream);
   else

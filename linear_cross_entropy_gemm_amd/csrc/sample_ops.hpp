@@ -1,7 +1,9 @@
 // What the sampler (flce_sample.hip) and the verification of drafted tokens
 // (flce_verify.hip) share: keys, exact weights and parameters of a row of
-// logits, and sums over a work-group.  flce_sample.hip explains them.
+// logits, and sums over a work-group.  sample_rows.hpp explains them.
 #pragma once
+
+#include <type_traits>
 
 #include "flce_internal.hpp"
 #include "row_ops.hpp"
@@ -42,18 +44,27 @@ struct SampleArgs {
   double* psum;     // [N][pieces] its weight relative to that maximum
   uint32_t* gmax;   // [N][pieces][kPieceGroups] keys
   u64* hist;        // [N][pieces][kSlots]
-  // statistics of two sets of rows instead of tokens (kStats): the first n1
-  // rows are z's with a parameter for every per1 of them, the others z2's
+};
+
+// Statistics of two sets of rows instead of tokens (kStats): the first n1 rows
+// are z's with a parameter for every per1 of them, the others z2's.  (A type of
+// its own: a kernel's arguments are copied to every lane's scratch memory for the
+// functions that are not inlined, 1 us of a drawn token, 3 of 64.)
+struct StatsArgs : SampleArgs {
   RowStat* stats;
   const void* z2;
   int64_t ld2, n1;
   uint32_t per1, per2;
   flce_sample_params_t prm2;
 };
+template <bool kStats>
+using RowArgs = std::conditional_t<kStats, StatsArgs, SampleArgs>;
 
 template <typename T, bool kStats>
-__device__ __forceinline__ const T* row_logits(const SampleArgs& a, int64_t row) {
-  if (kStats && row >= a.n1) return static_cast<const T*>(a.z2) + (row - a.n1) * a.ld2;
+__device__ __forceinline__ const T* row_logits(const RowArgs<kStats>& a, int64_t row) {
+  if constexpr (kStats) {
+    if (row >= a.n1) return static_cast<const T*>(a.z2) + (row - a.n1) * a.ld2;
+  }
   return static_cast<const T*>(a.z) + row * a.ld;
 }
 
@@ -98,16 +109,21 @@ struct RowParams {
 };
 
 template <bool kStats>
-__device__ __forceinline__ RowParams row_params(const SampleArgs& a, int64_t row) {
+__device__ __forceinline__ RowParams row_params(const RowArgs<kStats>& a, int64_t row) {
   RowParams r;
-  const bool second = kStats && row >= a.n1;
-  const flce_sample_params_t& prm = second ? a.prm2 : a.prm;
-  r.u = kStats ? 0.0f : a.u[row];
-  if (kStats) row = second ? (uint32_t)(row - a.n1) / a.per2 : (uint32_t)row / a.per1;
+  const flce_sample_params_t* of = &a.prm;
+  if constexpr (kStats) {
+    const bool second = row >= a.n1;
+    if (second) of = &a.prm2;
+    row = second ? (uint32_t)(row - a.n1) / a.per2 : (uint32_t)row / a.per1;
+  }
+  const flce_sample_params_t& prm = *of;
   const float t = prm.temperature_rows ? prm.temperature_rows[row] : prm.temperature;
   const float p = prm.top_p_rows ? prm.top_p_rows[row] : prm.top_p;
   const float q = prm.min_p_rows ? prm.min_p_rows[row] : prm.min_p;
   r.k = prm.top_k_rows ? prm.top_k_rows[row] : prm.top_k;
+  r.u = 0.0f;
+  if constexpr (!kStats) r.u = a.u[row];
   r.ok = t >= 0.0f && t < __builtin_inff() && p > 0.0f && p <= 1.0f && q >= 0.0f && q <= 1.0f && r.k >= 0 &&
          r.u >= 0.0f && r.u < 1.0f;
   r.t = t;
@@ -251,8 +267,8 @@ __device__ __forceinline__ int64_t index_in(u64 c) { return (int64_t)(uint32_t)~
 __device__ __forceinline__ float value_in(u64 c) { return value_of(key_in(c)); }
 
 // What flce_sample.hip does for others: the workspace of N rows of V logits
-// (total 0: not supported), the arguments that follow from it, the checks of
-// parameters, and the statistics of rows (a.stats).
+// (total 0: not supported), the arguments that follow from it, and the checks of
+// parameters.
 struct SampleLayout {
   int64_t pieces;
   size_t psum, hist, gmax, total;   // byte offsets (pmax at 0)
@@ -260,6 +276,5 @@ struct SampleLayout {
 SampleLayout sample_layout(int64_t N, int64_t V);
 void sample_args(SampleArgs& a, int64_t N, int64_t V, const SampleLayout& l, void* workspace);
 bool sample_params_ok(const flce_sample_params_t& q);
-void launch_row_stats(const SampleArgs& a, hipStream_t stream, int dtype);
 
 }  // namespace flce
