@@ -15,6 +15,12 @@
 //   rms_param_grad_kernel  dw of wide rows, by columns
 //   rms_reduce_kernel sum of the groups' dw in a fixed order
 //
+// What bounds them is memory: 8192 x 6656 bf16 with a residual 66 us forward (436
+// MB, 6.5 TB/s), 82 backward with the stream's gradient (78 and 81 among calls on
+// other data, which find nothing in the caches); 8192 x 7168 to 8 bits 68 (413
+// MB); 4099 x 5003 fp32 backward, rows at odd addresses, 47 (246 MB).  One row of
+// 6656 takes 3.3, its call through the binding 12.
+//
 // 8 bits: a block of 32 elements of y shares a scale, the least power of two
 // s with max|y| / s <= 448 (the largest E4M3 value), from the bits of the
 // maximum; y goes from fp32 to E4M3 in one rounding.
@@ -217,9 +223,12 @@ __global__ __launch_bounds__(kRow* kRows) void rms_bwd_kernel(RmsBwdArgs p) {
   static_assert(kRow == 64 || kRows == 1, "a work-group barrier must see one row");
   constexpr int E = RowVec<T>::E;
   typedef typename RowVec<T>::type vec_t;
-  // two vectors of bf16 each and 1024 threads: the next row has no registers left
-  // (4096 x 16384: 107 us without it, 218 with it in scratch memory)
-  constexpr bool kAhead = !(E == 8 && kRow * kVec == kMaxRegVecs);
+  // The row in use and the next one, in turn (moving one to the other's place
+  // waits for its loads: 8192 x 6656 bf16 takes 87 us then, 81 so; a third row
+  // brings nothing).  Two vectors of bf16 each and 1024 threads: the next row has
+  // no registers left (4096 x 16384: 107 us without it, 218 with it in scratch
+  // memory).
+  constexpr int kRing = E == 8 && kRow * kVec == kMaxRegVecs ? 1 : 2;
   __shared__ SumLds<1> lds;
   int buf = 0;
   const int t = threadIdx.x % kRow, sub = threadIdx.x / kRow;
@@ -228,7 +237,7 @@ __global__ __launch_bounds__(kRow* kRows) void rms_bwd_kernel(RmsBwdArgs p) {
   struct Rows {
     vec_t s[kVec], d[kVec], a[kDs ? kVec : 1];
     float rstd;
-  } cur, nxt;
+  } ring[kRing];
   auto load = [&](Rows& to, int64_t from) {
     to.rstd = p.rstd[from];
 #pragma unroll
@@ -238,7 +247,7 @@ __global__ __launch_bounds__(kRow* kRows) void rms_bwd_kernel(RmsBwdArgs p) {
       if constexpr (kDs) to.a[i] = load_clamped(static_cast<const T*>(p.ds) + from * p.ldd, (t + i * kRow) * E, p.H);
     }
   };
-  if (row < p.M) load(cur, row);
+  if (row < p.M) load(ring[0], row);
   float w[kVec][E], dw[kVec][E];
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
@@ -247,8 +256,7 @@ __global__ __launch_bounds__(kRow* kRows) void rms_bwd_kernel(RmsBwdArgs p) {
     for (int e = 0; e < E; ++e) dw[i][e] = 0.0f;
   }
   const float inv = 1.0f / (float)p.H;
-  for (; row < p.M; row += step) {
-    if (kAhead && row + step < p.M) load(nxt, row + step);
+  auto use = [&](Rows& cur) {
     // columns past the row's end hold dy = 0 and add nothing to any sum
     float m[1] = {0.0f};
 #pragma unroll
@@ -281,8 +289,16 @@ __global__ __launch_bounds__(kRow* kRows) void rms_bwd_kernel(RmsBwdArgs p) {
         put_vec(gr, (t + i * kRow) * E, p.H, o, p.past);
       }
     }
-    if constexpr (kAhead) cur = nxt;
-    else if (row + step < p.M) load(cur, row + step);
+  };
+  while (row < p.M) {
+#pragma unroll
+    for (int j = 0; j < kRing; ++j) {
+      if (row >= p.M) break;
+      if (kRing == 2 && row + step < p.M) load(ring[(j + 1) % kRing], row + step);
+      use(ring[j]);
+      if (kRing == 1 && row + step < p.M) load(ring[0], row + step);
+      row += step;
+    }
   }
   if (!p.partial) return;
   float* out = p.partial + (int64_t)blockIdx.x * p.H;
@@ -420,10 +436,10 @@ void launch_fwd(const RmsFwdArgs& p, hipStream_t st) {
   else rms_fwd_wide_kernel<T, WT, kRes, kMx8><<<grid(1, 65536), kWide, 0, st>>>(p);
 }
 
-// As measured (us, with rms_reduce_kernel): 8192 x 6656 bf16 with ds 85 by 1024 x
-// 1 and 256 groups, 93 by 512 x 2 and 512, 111 by 256 x 4 and 512; 16384 x 2048 46
-// by 256 x 1 and 512 groups, 56 by four rows of 64 x 4; 4099 x 5003 fp32 48 by 1024
-// x 2, 55 by 512 x 4.
+// As measured (us, with rms_reduce_kernel, before a row's registers took turns):
+// 8192 x 6656 bf16 with ds 85 by 1024 x 1 and 256 groups, 93 by 512 x 2 and 512,
+// 111 by 256 x 4 and 512; 16384 x 2048 46 by 256 x 1 and 512 groups, 56 by four
+// rows of 64 x 4; 4099 x 5003 fp32 48 by 1024 x 2, 55 by 512 x 4.  Now 82, 48, 47.
 template <typename T, typename WT, bool kDs>
 void launch_bwd(const RmsBwdArgs& p, int dtype, hipStream_t st) {
   const int64_t v = row_vecs(p.H, sizeof(T));
