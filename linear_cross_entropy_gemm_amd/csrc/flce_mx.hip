@@ -614,10 +614,12 @@ void launch_tiles(const MxArgs& p, hipStream_t st) {
 //   4x2 4x2 1x2          200        205        260         58         194         115
 //   4x2 2x4 1x2          317        317        372         57         186         116
 //   floor                117        117        46          1          46          81
-// The large ones are bound by the matrix units: 2.57 PFLOP/s of 8-bit products at
-// 320 bf16 tokens, two for each.  A second work-group on the compute unit is
-// worth more than deeper rings (two stages 260, four stages and one work-group
-// 334).
+// The large ones are bound by the matrix units, which are busy 58% of 1.98 GHz:
+// 2.57 PFLOP/s of 8-bit products at 320 bf16 tokens, two for each.  A second
+// work-group on the compute unit is worth more than deeper rings (two stages 260,
+// four stages and one work-group 334) and than the next stage's operands read
+// into registers ahead of the products (two work-groups of four waves 311, one of
+// eight 326).
 template <int kParts>
 void launch_products(const MxArgs& p, bool raw, hipStream_t st) {
   const int64_t left = kLdsMost - stream_tokens(p.N, p.steps, kParts);

@@ -19,10 +19,10 @@
 // What bounds them (MI355X, us): 64 sequences of 4 on 129279 fp32 logits, each with
 // parameters of its own (298 MB): scan 50, its memory; rows 26, one work-group's
 // chain of steps each; count 6, residual 17, draw 9.  32 of 7 on 202048 bf16 logits
-// without filters (194 MB): scan 82, of 64-bit exponentials, 13 64-bit operations
-// a logit that take 8 cycles each; rows 5, count 6, residual 24, draw 9.  One
-// sequence of 4 with k = 50 and p = 0.95: 4, 14, 7 (residual and count), 6, each
-// kernel the latency of its steps.
+// without filters (194 MB): scan 82, where the vector units are busy 82% of the
+// time with 26 instructions a logit, half of them the 64-bit exponential's; rows
+// 5, count 6, residual 24, draw 9.  One sequence of 4 with k = 50 and p = 0.95: 4,
+// 14, 7 (residual and count), 6, each kernel the latency of its steps.
 // A distribution's values are formed from the logits again where they are
 // needed: 64-bit exponentials over a row's sum; r goes into integers of 2^-51,
 // whose sums are exact in any order.
