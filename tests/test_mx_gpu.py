@@ -344,6 +344,24 @@ def test_rows_far_apart():
     assert torch.equal(out, L.logits_mx4(v, q))
 
 
+@pytest.mark.parametrize("N,kind", [(3, "bf16"), (12, "mx8"), (40, "bf16"), (70, "mx8"), (20, "f32")])
+def test_weights_beyond_32_bits(N, kind):
+    """More than 2^32 bytes of weights: the last entries' logits as from those
+    entries alone, bit for bit (an entry's sums do not depend on its tile)."""
+    import torch
+    import linear_cross_entropy_gemm_amd as L
+    V, H, last = (1 << 20) + 5000, 8192, 4321
+    g = torch.Generator(device="cuda").manual_seed(13)
+    data = torch.randint(0, 256, (V, H // 2), dtype=torch.uint8, device="cuda", generator=g)
+    scales = torch.randint(115, 122, (V, H // 32), dtype=torch.uint8, device="cuda", generator=g)
+    x = _rand((N, H), "bf16" if kind == "mx8" else kind, 14)
+    if kind == "mx8":
+        x = L.rms_norm_mx8(x, None, 1e-6).rows
+    z = L.logits_mx4(x, L.Mx4Weight(data, scales.view(torch.float8_e8m0fnu), H))
+    few = L.Mx4Weight(data[-last:].clone(), scales[-last:].clone().view(torch.float8_e8m0fnu), H)
+    assert z.isfinite().all() and L.logits_mx4(x, few).equal(z[:, -last:])
+
+
 def test_captured_and_on_two_streams():
     import torch
     import linear_cross_entropy_gemm_amd as L

@@ -263,6 +263,39 @@ def test_rows_far_apart():
     assert torch.equal(L.rms_norm_fwd(x, None, EPS).y, L.rms_norm_fwd(v, None, EPS).y)
 
 
+@pytest.mark.parametrize("H,dtype", [(600, "bf16"), (5003, "f32"), (6656, "bf16"), (7173, "bf16"), (16384, "bf16")])
+def test_many_rows_as_few(H, dtype):
+    """Calls that move more than the caches hold, with many rows for each
+    work-group: every row comes out as from a call of 100 rows, bit for bit, and
+    the weight's gradient within its bound."""
+    import torch
+    import linear_cross_entropy_gemm_amd as L
+    M = max(2100, (300 << 20) // (H * 8))
+    g = torch.Generator(device="cuda").manual_seed(H)
+    x, r, dy, ds = (torch.randn(M * H + 1, device="cuda", generator=g).to(_dt(dtype))[1:].view(M, H) for _ in range(4))
+    w = torch.randn(H, device="cuda", generator=g).to(_dt(dtype))
+    o = L.rms_norm_fwd(x, w, EPS, residual=r, offset=1.0)
+    m = L.rms_norm_mx8(x, w, EPS, residual=r, offset=1.0)
+    b = L.rms_norm_bwd(dy, o.residual, w, o.rstd, offset=1.0, grad_residual=ds)
+    for i in list(range(0, M, max(100, M // 23 // 100 * 100))) + [M - 100]:
+        c = slice(i, min(i + 100, M))
+        few = L.rms_norm_fwd(x[c], w, EPS, residual=r[c], offset=1.0)
+        assert few.y.equal(o.y[c]) and few.residual.equal(o.residual[c]) and few.rstd.equal(o.rstd[c])
+        fm = L.rms_norm_mx8(x[c], w, EPS, residual=r[c], offset=1.0)
+        assert fm.rows.data.view(torch.uint8).equal(m.rows.data[c].view(torch.uint8))
+        assert fm.rows.scales.view(torch.uint8).equal(m.rows.scales[c].view(torch.uint8))
+        assert fm.residual.equal(m.residual[c])
+        fb = L.rms_norm_bwd(dy[c], o.residual[c], w, o.rstd[c], offset=1.0, grad_residual=ds[c])
+        assert fb.grad_x.equal(b.grad_x[c])
+    dw, mag = torch.zeros(H, dtype=torch.float64, device="cuda"), torch.zeros(H, dtype=torch.float64, device="cuda")
+    for i in range(0, M, 1000):
+        t = dy[i:i + 1000].double() * (o.residual[i:i + 1000].double() * o.rstd[i:i + 1000, None].double())
+        dw += t.sum(0)
+        mag += t.abs().sum(0)
+    tol = (M + 9) * U * mag
+    assert ((b.grad_weight.double() - dw).abs() <= tol + HALF[dtype] * (dw.abs() + tol)).all()
+
+
 @pytest.mark.parametrize("residual", [False, True])
 def test_autograd(residual):
     """Gradients through both outputs, against the formula's."""

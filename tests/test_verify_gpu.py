@@ -264,6 +264,29 @@ def test_tokens_follow_the_target(top_p):
     assert both.numel() == 0 or np.abs(freq(both) - second).max() < 5 * np.sqrt(0.25 / both.numel())
 
 
+@pytest.mark.parametrize("V", [1500, 9000])
+def test_rows_far_apart(V):
+    """Rows of both sets of logits more than 2^31 elements from the first."""
+    import torch
+    import linear_cross_entropy_gemm_amd as L
+    B, K, ld = 2, 1, (1 << 30) + 12345
+    g = torch.Generator(device="cuda").manual_seed(V)
+    z = torch.randn(B, K + 1, V, device="cuda", generator=g).bfloat16()
+    d = torch.randn(B, K, V, device="cuda", generator=g).bfloat16()
+    far = torch.zeros((B * (K + 1) - 1) * ld + V, dtype=torch.bfloat16, device="cuda")
+    fz = far.as_strided((B, K + 1, V), ((K + 1) * ld, ld, 1))
+    fz.copy_(z)
+    fard = torch.zeros(3 * ld + V, dtype=torch.bfloat16, device="cuda")
+    fd = fard.as_strided((B, K, V), (3 * ld, ld, 1))
+    fd.copy_(d)
+    x = torch.randint(0, V, (B, K), device="cuda", generator=g)
+    u, ud = torch.rand(B, K, device="cuda", generator=g), torch.rand(B, device="cuda", generator=g)
+    for prm in (dict(), dict(top_k=40, top_p=0.9), dict(top_p=0.8)):
+        a = L.verify(z, x, u, ud, draft_logits=d, logprobs=True, **prm)
+        b = L.verify(fz, x, u, ud, draft_logits=fd, logprobs=True, **prm)
+        assert a.tokens.equal(b.tokens) and a.accepted.equal(b.accepted) and a.logprobs.equal(b.logprobs)
+
+
 def test_layouts_workspaces_and_refusals():
     import torch
     import linear_cross_entropy_gemm_amd as L
