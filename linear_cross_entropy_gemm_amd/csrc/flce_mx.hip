@@ -121,8 +121,8 @@ __device__ __forceinline__ constexpr uint32_t part_down(int q) {
 
 // Their steps are summed by themselves, smallest part first, and added to the
 // sums so far by the vector unit, which rounds to nearest.  (bf16 and 8-bit
-// tokens would gain nothing: 320 x 4096 x 128256 takes 283 and 276 that way where
-// it takes 262 and 190.)
+// tokens would gain nothing: 320 x 4096 x 128256 takes 283 us and 212 that way
+// where it takes 262 and 190.)
 template <int kParts>
 __device__ __forceinline__ f32x4 step_sums(const f32x4& acc) {
   return kParts == kDigits ? f32x4{0, 0, 0, 0} : acc;

@@ -342,7 +342,8 @@ template <typename T>
 void launch_verify(const VerifyArgs& v, hipStream_t stream) {
   // The sequences' accepted counts by themselves, or again in every work-group
   // where all of those are on the chip at once: 7 us against 5 + 6 with one
-  // sequence of 4 tokens, 37 against 6 + 32 with 32 of 7 (202048 logits).
+  // sequence of 4 tokens (202048 logits); with 32 of 7 it was 37 against 6 + 32,
+  // of which the weights take less now (24).
   const unsigned g = (unsigned)(v.B * v.pieces);
   if (g <= 1024) {
     ProfileScope ps(FLCE_KERNEL_VERIFY_RESIDUAL, stream);
