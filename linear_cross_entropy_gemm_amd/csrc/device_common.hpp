@@ -13,6 +13,18 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
+// Wait states that inline assembly has to bring along, since the compiler counts
+// them for its own instructions and does not look inside: a load to LDS issues
+// one wait state after the scalar write of M0 (each such load's assembly starts
+// with s_nop 0), and a vector memory access reads a scalar register five wait
+// states after a vector instruction (v_readfirstlane) wrote it.  A descriptor
+// passes through here on its way to the loads.
+template <typename V>
+__device__ __forceinline__ V settled(V x) {
+  asm("s_nop 4" : "+s"(x));
+  return x;
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegInf = -__builtin_inff();
 

@@ -43,15 +43,17 @@ typedef uint32_t u32x4s __attribute__((ext_vector_type(4)));
 constexpr uint32_t kPastBuffer = 0x80000000u;
 __device__ __forceinline__ u32x4s buffer_of(const uint8_t* base, int64_t bytes) {   // the same in every lane
   const uint64_t a = reinterpret_cast<uint64_t>(base);
-  return u32x4s{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)a),
-                (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(a >> 32)) & 0xFFFFu,
-                (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)bytes), 0x00020000u};
+  return settled(u32x4s{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)a),
+                        (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(a >> 32)) & 0xFFFFu,
+                        (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)bytes), 0x00020000u});
 }
 __device__ __forceinline__ void dma16(const u32x4s& from, uint32_t lds, uint32_t at) {
-  asm volatile("buffer_load_dwordx4 %0, %1, 0 offen lds" : : "v"(at), "s"(from), "{m0}"(lds) : "memory");
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+               : : "v"(at), "s"(from), "{m0}"(lds) : "memory");
 }
 __device__ __forceinline__ void dma4(const u32x4s& from, uint32_t lds, uint32_t at) {
-  asm volatile("buffer_load_dword %0, %1, 0 offen lds" : : "v"(at), "s"(from), "{m0}"(lds) : "memory");
+  asm volatile("s_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
+               : : "v"(at), "s"(from), "{m0}"(lds) : "memory");
 }
 // Waits until at most n of the wave's memory accesses are under way, and until
 // none of its LDS accesses is; no access moves across either.

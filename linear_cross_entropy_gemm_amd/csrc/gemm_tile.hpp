@@ -483,16 +483,19 @@ __device__ __forceinline__ u32x4s make_rsrc_words(const char* base, int64_t byte
 // One direct-to-LDS load: lane l's 16 bytes at byte offset soff + voff of the
 // buffer land at LDS byte address lds + 16 l (zeros when the offset is out of
 // range).  `lds` is wave-uniform and goes to M0 through the register
-// constraint, so the compiler forms it there with one scalar add.  Written as
+// constraint, so the compiler forms it there with one scalar add, of which the
+// load sees the result one wait state later (s_nop 0).  Written as
 // inline assembly so that the compiler does not treat it as an LDS write that
 // every later LDS read must wait for: the K loop orders these loads itself with
 // explicit vmcnt waits and barriers, and waits for all of them (vmcnt(0))
 // before the LDS is reused.
 __device__ __forceinline__ void lds_dma16(const u32x4s& r, uint32_t lds, uint32_t voff, uint32_t soff) {
-  asm volatile("buffer_load_dwordx4 %0, %1, %2 offen lds" : : "v"(voff), "s"(r), "s"(soff), "{m0}"(lds) : "memory");
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+               : : "v"(voff), "s"(r), "s"(soff), "{m0}"(lds) : "memory");
 }
 __device__ __forceinline__ void lds_dma16(const u32x4s& r, uint32_t lds, uint32_t voff) {
-  asm volatile("buffer_load_dwordx4 %0, %1, 0 offen lds" : : "v"(voff), "s"(r), "{m0}"(lds) : "memory");
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+               : : "v"(voff), "s"(r), "{m0}"(lds) : "memory");
 }
 
 // LDS byte address of a __shared__ buffer, and this wave's scalar offset of
@@ -559,7 +562,7 @@ struct KMajorDirect {
     lds_dma16(rs, slot + lds_wave + j * 1024, off, (uint32_t)kpos);
   }
   __device__ __forceinline__ void set_records() {
-    rs[2] = __builtin_amdgcn_readfirstlane(kpos < k_bytes ? range0 : 0u);
+    rs[2] = settled((uint32_t)__builtin_amdgcn_readfirstlane(kpos < k_bytes ? range0 : 0u));
   }
   __device__ __forceinline__ void advance() {
     kpos += kDKBytes;
@@ -610,7 +613,7 @@ struct MNMajorDirect {
     const int rows = krem < kDKBytes / 2 ? (krem < 0 ? 0 : krem) : kDKBytes / 2;
     const uint64_t a = reinterpret_cast<uint64_t>(kbase);
     rs = u32x4s{(uint32_t)a, (uint32_t)(a >> 32) & 0xFFFFu,
-                (uint32_t)__builtin_amdgcn_readfirstlane(rows * ldb), 0x00020000u};
+                settled((uint32_t)__builtin_amdgcn_readfirstlane(rows * ldb)), 0x00020000u};
   }
   __device__ __forceinline__ void issue_part(uint32_t slot, int j) {
     lds_dma16(rs, slot + lds_wave + j * 1024, voff[j]);
