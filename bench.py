@@ -60,7 +60,7 @@ def kernel_source_hash() -> str:
     m = hashlib.sha256()
     # the operators before and after the head share no kernel with its GEMMs
     others = ("flce_norm.hip", "flce_rms.hip", "flce_mx.hip", "flce_dropout.hip", "flce_sample.hip", "flce_verify.hip",
-              "row_ops.hpp", "mx_ops.hpp", "sample_ops.hpp", "sample_rows.hpp")
+              "row_ops.hpp", "mx_ops.hpp", "sample_ops.hpp", "sample_rows.hpp", "sample_rule.hpp")
     files = [f for f in glob.glob(os.path.join(CSRC, "*"))
              if (f.endswith((".hip", ".hpp")) or os.path.basename(f) == "flce_plan.cpp")
              and os.path.basename(f) not in others]

@@ -19,7 +19,7 @@ SOURCES = ["flce_kernels.hip", "flce_logits.hip", "flce_scale.hip", "flce_noallo
            "flce_rms.hip", "flce_mx.hip", "flce_dropout.hip", "flce_sample.hip", "flce_verify.hip",
            "flce_plan.cpp", "flce_api.cpp", "flce_profile.cpp"]
 HEADERS = ["device_common.hpp", "gemm_tile.hpp", "flce_internal.hpp", "kernel_args.hpp", "row_ops.hpp", "mx_ops.hpp",
-           "sample_ops.hpp", "sample_rows.hpp"]
+           "sample_ops.hpp", "sample_rows.hpp", "sample_rule.hpp"]
 
 ARCH = "gfx950"
 # Packed fp32 VALU forms are kept out of the generated code (the compiler would

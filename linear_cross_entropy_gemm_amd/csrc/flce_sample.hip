@@ -19,7 +19,7 @@ bool on(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a 
 SampleLayout sample_layout(int64_t N, int64_t V) {
   SampleLayout l{(V + kPiece - 1) / kPiece, 0, 0, 0, 0};
   // launches of fewer than 2^32 threads
-  if (N > (int64_t(1) << 21) || V > (int64_t(1) << 24) || N * l.pieces > (int64_t(1) << 23)) return l;
+  if (N > (int64_t(1) << 21) || V > kMaxVocab || N * l.pieces > (int64_t(1) << 23)) return l;
   if (V <= kSmall) {
     l.total = 256;
     return l;

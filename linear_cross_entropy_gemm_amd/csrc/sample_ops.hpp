@@ -7,12 +7,12 @@
 
 #include "flce_internal.hpp"
 #include "row_ops.hpp"
+#include "sample_rule.hpp"
 
 namespace flce {
 
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;
 constexpr int kSmall = 2048;         // rows one wave holds
-constexpr int kPiece = 8192;         // logits per work-group of the scan
 constexpr int kGroup = 64;           // logits per stored maximum
 constexpr int kPieceGroups = kPiece / kGroup;
 constexpr int kSlots = 128;          // bins of z per piece; the last holds the rest

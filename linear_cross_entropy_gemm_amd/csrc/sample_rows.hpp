@@ -449,9 +449,10 @@ struct Picker {
 static constexpr int kRowThreads = TH, kRowWaves = TH / 64;
 static constexpr int kBinBits = TH == 1024 ? 11 : 10, kBins = 1 << kBinBits;   // bits of a key per search pass
 static constexpr int kList = 12 * TH;                             // candidates (8 bytes each)
-static constexpr int kMaxPieces = TH == 1024 ? (1 << 24) / kPiece : 256;
+static constexpr int kMaxPieces = picker_pieces(TH);              // of a row
 static constexpr int kGroupBatch = 4 * TH;                        // groups looked through at a time
 static_assert(kBins == 2 * TH, "find_bin gives every thread two bins");
+static_assert(kMaxPieces <= 2 * TH, "pick_by_pieces gives every thread two pieces");
 
 struct RowShared {
   u64 hist[kBins];
@@ -1180,11 +1181,7 @@ __global__ __launch_bounds__(TH) __attribute__((amdgpu_waves_per_eu(4))) void sa
   Picker<TH, kStats>::template run<T>(a, sh);
 }
 
-// Two rows at a time on a compute unit where there are more rows than compute
-// units and a flat row's border bin still fits the shorter list.  1024 rows of
-// 4000 bf16 logits, 512 against 1024 threads: k = 50 and p = 0.95 on peaked
-// rows 31 against 53 us, p = 0.9 on flat ones 45 against 76 us, no filter 22
-// against 30 us.
+// Two rows at a time on a compute unit (picker_threads), of shorter rows.
 // Statistics of longer rows too, 480 of 202048 bf16 logits, whole call: k = 50 and
 // p = 0.95 77 against 84 us, no filter 114 against 119, 576 of 129279 fp32 ones
 // with a request's parameters each 130 against 151.  Not with top-p for all of
@@ -1196,9 +1193,9 @@ inline bool top_p_alone(const flce_sample_params_t& q, int64_t V) {
 }
 template <typename T, bool kStats>
 void launch_pick(const RowArgs<kStats>& a, hipStream_t st) {
-  bool two = a.V <= 65536;
-  if constexpr (kStats) two = two || (!top_p_alone(a.prm, a.V) && !top_p_alone(a.prm2, a.V));
-  if (a.N > 256 && two)
+  bool any_list = false;
+  if constexpr (kStats) any_list = !top_p_alone(a.prm, a.V) && !top_p_alone(a.prm2, a.V);
+  if (picker_threads(a.N, a.V, any_list) == 512)
     sample_pick_kernel<T, 512, kStats><<<(unsigned)a.N, 512, 0, st>>>(a);
   else
     sample_pick_kernel<T, 1024, kStats><<<(unsigned)a.N, 1024, 0, st>>>(a);
