@@ -488,17 +488,18 @@ size_t flce_logits_mx_workspace_size(int64_t N, int64_t H, int x_dtype);
  *   logits    aligned to one element, ld_logits >= V when N > 1; columns from V
  *             on are not written; must not overlap an input
  * Softcap and multiplier as flce_logits.  A bf16 or fp32 x enters as sums of
- * E4M3 values under one scale for 32 columns.  bf16: exactly where it is at least
- * 2^-14 of the largest of its 32, else rounded to 2^-22 of that largest; fp32:
- * rounded to 2^-24 of that largest (and 2^-137).  Where one of the 32 is not
- * finite, all of them count as NaN.  Sums are fp32; with 8-bit and bf16 rows the
- * matrix unit cuts products below 2^-13 of the largest of the 8 that it adds at
- * a time (sums of random rows end within 4e-6 of themselves; fp32 rows, whose
- * parts are whole numbers, within 3e-7).  z is rounded once.  N <= 2^20, V <=
- * 2^24, H <= 2^21, N Kp <= 2^34 and N V <= 2^35 (else FLCE_EUNSUPPORTED); N = 0
- * does nothing.  Enqueued on `stream`; nothing is allocated, nothing synchronises.
- * Returns FLCE_OK, FLCE_EINVAL, FLCE_EUNSUPPORTED, FLCE_EWORKSPACE or
- * FLCE_EDEVICE.
+ * E4M3 values under one scale for 32 columns.  bf16 with bf16 logits: exactly where
+ * it is at least 2^-14 of the largest of its 32, else rounded to 2^-22 of that
+ * largest; fp32, and bf16 with fp32 logits: rounded to 2^-24 of that largest (and
+ * 2^-137).  Where one of the 32 is not finite, all of them count as NaN.  Sums are
+ * fp32; with 8-bit rows and with bf16 logits of bf16 rows the matrix unit cuts
+ * products below 2^-13 of the largest of the 8 that it adds at a time (sums of
+ * random rows end within 4e-6 of themselves, with a few columns 300 times the
+ * others within 1e-4; those of the other rows, whose parts are whole numbers,
+ * within 3e-7).  z is rounded once.  N <= 2^20, V <= 2^24, H <= 2^21, N Kp <= 2^34
+ * and N V <= 2^35 (else FLCE_EUNSUPPORTED); N = 0 does nothing.  Enqueued on
+ * `stream`; nothing is allocated, nothing synchronises.  Returns FLCE_OK,
+ * FLCE_EINVAL, FLCE_EUNSUPPORTED, FLCE_EWORKSPACE or FLCE_EDEVICE.
  */
 int flce_logits_mx(const void* x, int64_t ld_x, const void* x_scales, int64_t ld_xs, const void* packed,
                    const void* scales, int64_t N, int64_t H, int64_t V, float softcap_T, float multiplier,

@@ -79,7 +79,8 @@ def logits_mx4(x: Union[torch.Tensor, Mx8Rows], weight: Mx4Weight, softcap: Opti
     """Materialised logits z = cap(m x W^T) from a projection in 4 bits
     (``flce_logits_mx``), [..., V]; ``x`` [..., H] is bfloat16 or float32 (so
     are the logits), or rows in 8 bits (bfloat16 logits).  ``out``, when given,
-    is [N, ld >= V] with unit column stride, bfloat16 or float32.  As with
+    is [N, ld >= V] with unit column stride, bfloat16 or float32; float32 logits
+    of bfloat16 rows are as exact, and take as long, as those of float32 rows.  As with
     ``logits`` the returned rows may have a stride padded to 16 bytes.  A
     caller-owned ``workspace`` (uint8, ``flce_logits_mx_workspace_size``) may be
     reused by ordered calls."""
