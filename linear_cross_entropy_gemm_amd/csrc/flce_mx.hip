@@ -643,9 +643,15 @@ void launch_products(const MxArgs& p, bool raw, hipStream_t st) {
     return;
   }
   if constexpr (kParts == kDigits) {
-    // 8 x 4096 x 128256: 58, 77 by 32 tokens; 33 x 1001 x 50001: 23 by 48, 28 by 32
+    // Up to 16 tokens, 8 x 4096 x 128256: 58, by 32 tokens 77.  33 to 48 tokens:
+    // one work-group of 48 on a compute unit, or two of 32 with half the rows; a
+    // round of the former lasts as long as 1.6 of the latter.
+    // 48 x 4096 by 48 and by 32: x 32000 55 and 43 (1 round and 1), x 36000 55 and 62
+    // (1 and 2), x 80000 114 and 104 (2 and 3), x 104000 118 and 135 (2 and 4), x 150000
+    // 178 and 191 (3 and 5); 33 x 1001 x 50001 21 and 25.
+    const int64_t by48 = ceil_div(ceil_div(p.V, 256), 256), by32 = ceil_div(2 * ceil_div(p.V, 128), 512);
     if (p.N <= 16) launch_tiles<kDigits, 4, 1, 2, 1, 2, 2>(p, st);
-    else if (p.N > 32 && p.N <= 48) launch_tiles<kDigits, 8, 1, 2, 3, 1, 2>(p, st);
+    else if (p.N > 32 && p.N <= 48 && 5 * by32 >= 8 * by48) launch_tiles<kDigits, 8, 1, 2, 3, 1, 2>(p, st);
     else launch_tiles<kDigits, 4, 1, 2, 2, 1, 2>(p, st);
   } else {
     // (few tiles: rather more of them, for the other compute units)

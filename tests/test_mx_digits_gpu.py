@@ -65,3 +65,20 @@ def test_bf16_rows_count_as_the_same_fp32_rows(N, H, V):
     x[N - 1, H // 2] = float("nan")   # (and a block that is not finite)
     z = L.logits_mx4(x, q, out=torch.empty(N, V, device="cuda"))
     assert z[N - 1].isnan().all() and not z[:N - 1].isnan().any()
+
+
+@pytest.mark.parametrize("N,H,V", [(33, 130, 32768), (33, 130, 32769), (48, 1001, 40001), (40, 257, 65537), (48, 64, 80001),
+                                   (35, 129, 104003)])
+def test_tokens_by_48_and_by_32(N, H, V):
+    """Which tiles take 33 to 48 rows goes by how many rounds of work-groups they
+    make; a row's logits do not depend on it."""
+    import torch
+    import linear_cross_entropy_gemm_amd as L
+    q = L.mx4_pack(_rand((V, H), "f32", 25, 0.05))
+    x = _rand((N, H), "f32", 26)
+    z = L.logits_mx4(x, q)
+    assert torch.equal(z, torch.cat([L.logits_mx4(x[i:i + 24], q) for i in range(0, N, 24)]))
+    some = slice(V - 300, V)
+    w = _weights(L.Mx4Weight(q.data[some].contiguous(), q.scales[some].contiguous(), H))
+    ref = _np(x) @ w.T
+    assert (np.abs(_np(z)[:, some] - ref) <= _bound(_np(x), w) + 2 * U * np.abs(ref)).all()
