@@ -290,37 +290,37 @@ __host__ __device__ constexpr int code_bytes(int steps) { return (steps + 3) / 4
 // 16 rows that a wave reads at a time start in different banks.
 __host__ __device__ constexpr int part_bytes(int steps) { return steps * kStep + 16; }
 
-// A wave's ring of weights in LDS: kG groups of four steps (16 rows of 256
-// bytes), each with its scales (16 rows of 16 bytes).
+// A wave's weights in LDS: a group of four steps (16 rows of 256 bytes) with its
+// scales (16 rows of 16 bytes).
 constexpr int kGroupBytes = 4096 + 256;
-__host__ __device__ constexpr int ring_bytes(int groups) { return groups * kGroupBytes; }
 
 constexpr int kLdsMost = 160 * 1024;
 
 // Up to 16 tokens that stay in LDS as a whole, brought there once; then the
-// weights stream through every wave's own ring without a barrier, tile after
-// tile of 16 rows (tile blockIdx.x + gridDim.x (wave + waves i)).
+// weights stream through every wave's own place without a barrier, tile after
+// tile of 16 rows (tile blockIdx.x + gridDim.x (wave + waves i)): once a group is in
+// registers the next one's loads are issued, and its products hide them together
+// with the other waves'.
 //
 // The loads go straight to LDS, 16 lanes to 256 bytes of a row, four rows a
 // load: straight to the lanes that need them (a lane a row, 64 different lines
 // a load) the address units take as long as the memory.  Piece k (16 bytes) of
 // row r lands at k ^ r, so that the 16 rows that a wave reads at a time lie in
-// different banks.  Loads return in order: a group is there when no more than
-// the groups behind it are under way.
-template <int kParts, int kG, bool kInline>
+// different banks.
+template <int kParts, bool kInline>
 __global__ __launch_bounds__(1024) void mx_logits_stream_kernel(MxArgs p, int tiles) {
-  extern __shared__ __align__(16) uint8_t lds[];   // parts [kParts][N][part_bytes], codes [N][code_bytes], rings
+  extern __shared__ __align__(16) uint8_t lds[];   // parts [kParts][N][part_bytes], codes [N][code_bytes], groups
   const int threads = blockDim.x, lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = threads >> 6;
   const int N = (int)p.N, row = part_bytes(p.steps), part = N * row, crow = code_bytes(p.steps);
   uint8_t* codes = lds + kParts * part;
-  uint8_t* ring = codes + N * crow + wave * ring_bytes(kG);
-  const uint32_t ring_at = lds_address(ring);
+  uint8_t* group = codes + N * crow + wave * kGroupBytes;
+  const uint32_t to = lds_address(group);
 
   // where the next group's loads come from
   const int w_row = p.steps * 64, s_row = p.steps * 4;
   const uint32_t s_off = (uint32_t)((lane >> 2) * s_row + (lane & 3) * 4);
-  int tile_in = blockIdx.x + gridDim.x * wave, c_in = 0, slot_in = 0;
+  int tile_in = blockIdx.x + gridDim.x * wave, c_in = 0;
   const int tile_step = gridDim.x * waves;
   u32x4s from_w, from_s;
   auto set_tile = [&]() {
@@ -330,14 +330,12 @@ __global__ __launch_bounds__(1024) void mx_logits_stream_kernel(MxArgs p, int ti
     from_s = buffer_of(p.ws + (rows ? v : 0) * s_row, rows * s_row);
   };
   auto load_group = [&]() {   // (of what lies past the row's end the scales are not used, the codes not read)
-    const uint32_t to = ring_at + slot_in * kGroupBytes;
     dma4(from_s, to + 4096, s_off + c_in * 4);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int row = 4 * i + (lane >> 4), piece = (lane & 15) ^ row;
       dma16(from_w, to + i * 1024, c_in + (piece >> 2) < p.steps ? row * w_row + c_in * 64 + piece * 16 : kPastBuffer);
     }
-    if (++slot_in == kG) slot_in = 0;
     c_in += 4;
     if (c_in >= p.steps) {
       c_in = 0;
@@ -346,8 +344,7 @@ __global__ __launch_bounds__(1024) void mx_logits_stream_kernel(MxArgs p, int ti
     }
   };
   set_tile();
-#pragma unroll
-  for (int i = 0; i < kG; ++i) load_group();
+  load_group();
 
   if constexpr (kInline) {
     const int vecs = p.steps * 16;
@@ -378,20 +375,17 @@ __global__ __launch_bounds__(1024) void mx_logits_stream_kernel(MxArgs p, int ti
   const int n = r < N ? r : N - 1;
   const uint8_t* mine = lds + n * row + g * 16;
   const uint8_t* my_codes = codes + n * crow;
-  int slot = 0;
   for (int tile = blockIdx.x + gridDim.x * wave; tile < tiles; tile += tile_step) {
     f32x4 acc[1][1] = {{{0, 0, 0, 0}}};
     for (int c = 0; c < p.steps; c += 4) {
-      wait_loads<5 * (kG - 1)>();
-      const uint8_t* from = ring + slot * kGroupBytes;
-      const uint32_t scale = own_scales(*reinterpret_cast<const u32x4*>(from + 4096 + r * 16));
+      wait_loads<0>();
+      const uint32_t scale = own_scales(*reinterpret_cast<const u32x4*>(group + 4096 + r * 16));
       const uint32_t xc = own_scales(*reinterpret_cast<const u32x4*>(my_codes + c * 4));
       u32x4 a[4];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) a[s] = *reinterpret_cast<const u32x4*>(from + r * 256 + (((s * 4 + g) ^ r) * 16));
+      for (int s = 0; s < 4; ++s) a[s] = *reinterpret_cast<const u32x4*>(group + r * 256 + (((s * 4 + g) ^ r) * 16));
       wait_lds();   // what was read is in registers: its place may be loaded again
       load_group();
-      if (++slot == kG) slot = 0;
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         if (c + s < p.steps) {
@@ -581,19 +575,19 @@ __global__ __launch_bounds__(64 * kWv * kWt) void mx_logits_tile_kernel(MxArgs p
   put_logits<kRt, kNt>(p, n0 + wt * kNt * 16, v0 + wv * kRt * 16, acc);
 }
 
-// LDS of the streaming kernel beside its rings.
+// LDS of the streaming kernel's tokens.
 int64_t stream_tokens(int64_t N, int64_t steps, int parts) {
   return N * (parts * part_bytes((int)steps) + code_bytes((int)steps));
 }
 
 // One work-group on each of the 256 compute units; waves so that every one has
 // about as many tiles as the others.
-template <int kParts, int kG, bool kInline>
+template <int kParts, bool kInline>
 void launch_stream(const MxArgs& p, int waves, hipStream_t st) {
   const int64_t tiles = ceil_div(p.V, 16);
-  const int64_t bytes = stream_tokens(p.N, p.steps, kParts) + waves * ring_bytes(kG);
+  const int64_t bytes = stream_tokens(p.N, p.steps, kParts) + waves * kGroupBytes;
   const unsigned g = (unsigned)(tiles < 256 ? tiles : 256);
-  mx_logits_stream_kernel<kParts, kG, kInline><<<g, waves * 64, (size_t)bytes, st>>>(p, (int)tiles);
+  mx_logits_stream_kernel<kParts, kInline><<<g, waves * 64, (size_t)bytes, st>>>(p, (int)tiles);
 }
 
 template <int kParts, int kWv, int kWt, int kRt, int kNt, int kU, int kStages>
@@ -627,19 +621,19 @@ void launch_tiles(const MxArgs& p, hipStream_t st) {
 template <int kParts>
 void launch_products(const MxArgs& p, bool raw, hipStream_t st) {
   const int64_t left = kLdsMost - stream_tokens(p.N, p.steps, kParts);
-  if (p.N <= 16 && left >= 4 * ring_bytes(1)) {
-    int64_t most = left / ring_bytes(1);
+  if (p.N <= 16 && left >= 4 * kGroupBytes) {
+    int64_t most = left / kGroupBytes;
     if (most > 12) most = 12;
     const int64_t tiles = ceil_div(p.V, 16);
     int waves = (int)ceil_div(tiles, 256 * ceil_div(tiles, 256 * most));
     if (waves < 4) waves = 4;   // they also bring the tokens to LDS
     if constexpr (kParts > 1) {
       if (raw) {
-        launch_stream<kParts, 1, true>(p, waves, st);
+        launch_stream<kParts, true>(p, waves, st);
         return;
       }
     }
-    launch_stream<kParts, 1, false>(p, waves, st);
+    launch_stream<kParts, false>(p, waves, st);
     return;
   }
   if constexpr (kParts == kDigits) {
@@ -790,7 +784,7 @@ extern "C" int flce_logits_mx(const void* x, int64_t ld_x, const void* x_scales,
   const bool ready = mx8 && H % (4 * kStep) == 0 && ld_x <= kMostRow && ld_xs <= kMostRow && ld_x % 16 == 0 &&
                      ld_xs % 16 == 0 && addr(x) % 16 == 0 && addr(x_scales) % 16 == 0;
   const bool raw =
-      x_dtype == FLCE_DTYPE_BF16 && N <= 2 && stream_tokens(N, steps, t.parts) <= kLdsMost - 4 * ring_bytes(1);
+      x_dtype == FLCE_DTYPE_BF16 && N <= 2 && stream_tokens(N, steps, t.parts) <= kLdsMost - 4 * kGroupBytes;
   MxArgs p{parts, codes, t.ldp, t.ldc, static_cast<const uint8_t*>(packed), static_cast<const uint8_t*>(scales), logits,
            ld_logits, N, V, (int)H, (int)steps, softcap_T > 0.0f ? softcap_T : 0.0f, multiplier,
            dtype == FLCE_DTYPE_BF16};
