@@ -484,7 +484,8 @@ size_t flce_logits_mx_workspace_size(int64_t N, int64_t H, int x_dtype);
  *             [N, ceil(H / 32)], row stride ld_xs >= 0 (NULL for the others)
  *   packed    16-byte aligned; scales 4-byte aligned
  *   workspace 256-byte aligned, flce_logits_mx_workspace_size bytes (the tokens
- *             in the form that the products take); of one call at a time
+ *             in the form that the products take, for either type of logits); of
+ *             one call at a time
  *   logits    aligned to one element, ld_logits >= V when N > 1; columns from V
  *             on are not written; must not overlap an input
  * Softcap and multiplier as flce_logits.  A bf16 or fp32 x enters as sums of
@@ -600,6 +601,8 @@ size_t flce_verify_workspace_size(int64_t B, int64_t K, int64_t V, int dtype, in
  * 2^-36 of p, relative to them, or u_draw within 2^-35 of a border in weight of
  * r, either side is possible.  Weights of r go into sums in units of 2^-51: a
  * token with less is not drawn.  The same call gives the same bits.
+ * Every row is read, those behind a draft's end too.  With more than 256 rows, flat
+ * ones under top-p alone take less time with top_p as a number than as an array.
  * K <= 1024, B <= 2^21, and with R = B (2 K + 1) rows (B (K + 1) without a
  * draft) R <= 2^21, V <= 2^24, R ceil(V / 8192) <= 2^23 and B ceil(V / 4096) <
  * 2^24 (else FLCE_EUNSUPPORTED); K = 0 samples.  Enqueued on `stream`; nothing is

@@ -124,9 +124,9 @@ __device__ __forceinline__ constexpr uint32_t part_down(int q) {
 }
 
 // Their steps are summed by themselves, smallest part first, and added to the
-// sums so far by the vector unit, which rounds to nearest.  (bf16 and 8-bit
-// tokens would gain nothing: 320 x 4096 x 128256 takes 283 us and 212 that way
-// where it takes 262 and 190.)
+// sums so far by the vector unit, which rounds to nearest.  (Two parts and one
+// would gain nothing: on constant operands 320 x 4096 x 128256 takes 283 us and 212
+// that way where it takes 262 and 190.)
 template <int kParts>
 __device__ __forceinline__ f32x4 step_sums(const f32x4& acc) {
   return kParts == kDigits ? f32x4{0, 0, 0, 0} : acc;
@@ -598,26 +598,31 @@ void launch_tiles(const MxArgs& p, hipStream_t st) {
       <<<(unsigned)(ceil_div(rb, 8) * 8 * tb), 64 * S::waves, S::lds, st>>>(p, (int)rb, (int)tb);
 }
 
-// Kernels by size, as measured (us; floor: the weights' bytes at 6.1 TB/s).
-// Streaming, 1 x 6656 x 202048 bf16: 124 with one group of four steps under way
-// in each of 12 waves (floor 117), 125 with two, 130 with three; by pieces of 64
-// bytes 137; with few tiles and four waves 1 x 8192 x 1000 takes 13 with one
+// Kernels by size, as measured on random rows and weights (us; floors: the weights'
+// bytes at 6.1 TB/s; the products at the 4.0 PFLOP/s that this instruction reaches
+// on random operands, twice as many for bf16).
+// Streaming, 1 x 6656 x 202048 bf16: 121 with one group of four steps under way in
+// each of 10 waves (floor 117); two and three groups took 1 and 6 more, pieces of 64
+// bytes 13 more.  With few tiles and four waves 1 x 8192 x 1000 takes 13 with one
 // group and 14 with three or more: its time is the way from launch to sum.
 // Tiles (waves along V x along N, tiles of 16 a wave, steps x stages), in order
 // (2 parts at the first four, 1 at the others):
 //                        16 x 6656  24 x 6656  320 x 4096  64 x 8192  320 x 4096  24 x 7168
 //                        x 202048   x 202048   x 128256    x 1000     x 128256    x 129280
-//   8x1 2x1 2x3          158        221        560         30         502         131
-//   4x1 2x2 2x3          162        171        506         29         287         96
-//   4x2 4x2 1x2          200        205        260         58         194         115
-//   4x2 2x4 1x2          317        317        372         57         186         116
-//   floor                117        117        46          1          46          81
-// The large ones are bound by the matrix units, which are busy 58% of 1.98 GHz:
-// 2.57 PFLOP/s of 8-bit products at 320 bf16 tokens, two for each.  A second
-// work-group on the compute unit is worth more than deeper rings (two stages 260,
-// four stages and one work-group 334) and than the next stage's operands read
-// into registers ahead of the products (two work-groups of four waves 311, one of
-// eight 326).
+//   8x1 2x1 2x3          156        220        552         26         526         134
+//   4x1 2x2 2x3          161        170        493         25         298         98
+//   4x2 4x2 1x2          200        204        274         55         205         118
+//   4x2 2x4 1x2          315        321        377         54         203         123
+//   floor, memory        117        117        59          1          59          81
+//   floor, products      21         32         168         1          84          11
+// One part by the last two, x 4096 x 128256: 84 and 97 at 65 tokens, 129 and 125 at
+// 129, 138 and 155 at 200, 286 and 318 at 512.
+// The large ones are bound by the matrix units, which are busy 57% of 2.0 GHz: 2.47
+// PFLOP/s of 8-bit products at 320 bf16 tokens, two for each.  A second work-group
+// on the compute unit is worth more than deeper rings (two stages 260, four stages
+// and one work-group 334, on constant operands, which leave the clock higher) and
+// than the next stage's operands read into registers ahead of the products (two
+// work-groups of four waves 311, one of eight 326, likewise).
 template <int kParts>
 void launch_products(const MxArgs& p, bool raw, hipStream_t st) {
   const int64_t left = kLdsMost - stream_tokens(p.N, p.steps, kParts);
@@ -637,7 +642,7 @@ void launch_products(const MxArgs& p, bool raw, hipStream_t st) {
     return;
   }
   if constexpr (kParts == kDigits) {
-    // Up to 16 tokens, 8 x 4096 x 128256: 58, by 32 tokens 77.  33 to 48 tokens:
+    // Up to 16 tokens, 8 x 4096 x 128256: 65, by 32 tokens 85.  33 to 48 tokens:
     // one work-group of 48 on a compute unit, or two of 32 with half the rows; a
     // round of the former lasts as long as 1.6 of the latter.
     // 48 x 4096 by 48 and by 32: x 32000 55 and 43 (1 round and 1), x 36000 55 and 62
@@ -694,7 +699,9 @@ __device__ __forceinline__ uint32_t e2m1_code(float x) {
 }
 
 // Eight columns per thread, four threads per block; a row has `vecs` of them,
-// a multiple of 16.
+// a multiple of 16.  Done once for a projection; 202048 x 6656 takes 996 us from
+// bf16 and 1087 from fp32 (floors at 6.1 TB/s 558 and 999): a thread has one load of
+// 16 bytes under way, or two, which reach 3.4 and 5.6 TB/s.
 template <typename T>
 __global__ __launch_bounds__(256) void pack_mx_kernel(const T* W, int64_t ld, int64_t total, int H, int vecs,
                                                       uint32_t* packed, uint8_t* scales) {

@@ -554,9 +554,10 @@ def verify(target_logits: torch.Tensor, draft_tokens: torch.Tensor, u: torch.Ten
     and ``u_draw`` [...] are float32 random numbers in [0, 1); ``draft_lens``
     [...] (int64) says how many tokens of each sequence were drafted.  The
     sampling parameters are numbers, or tensors with one value per sequence;
-    the draft's are those of the target where not given.  A caller-owned
-    ``workspace`` (uint8, ``flce_verify_workspace_size``) may be reused by
-    ordered calls."""
+    the draft's are those of the target where not given.  (With more than 256
+    rows, flat ones under top-p alone take less time with ``top_p`` as a number
+    than as a tensor.)  A caller-owned ``workspace`` (uint8,
+    ``flce_verify_workspace_size``) may be reused by ordered calls."""
     _check_rows("target_logits", target_logits)
     if target_logits.dim() < 2 or target_logits.shape[-2] < 1:
         raise ValueError(f"target_logits must be [..., K + 1, V] (got {tuple(target_logits.shape)})")
